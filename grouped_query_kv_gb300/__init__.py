@@ -18,6 +18,8 @@ __all__ = [
     "kv_append", "kv_append_multi", "kv_append_paged", "gqa_decode_attn", "gqa_decode_step",
     "gqa_decode_attn_multi", "gqa_decode_attn_paged", "gqa_decode_step_paged",
     "kv_quantize_fp8", "kv_append_fp8", "gqa_decode_attn_fp8", "gqa_decode_step_fp8",
+    "kv_block_tables", "kv_append_slots", "gqa_prefill_attn",
+    "kv_append_paged_fp8", "gqa_decode_attn_paged_fp8",
     "check_device_error", "get_plan",
     "set_tuning", "set_wait_limit", "set_kernel_events", "release", "KvAttnError", "library_path", "lib",
     "KVATTN_OK", "KVATTN_ERR_INVALID_ARG", "KVATTN_ERR_UNSUPPORTED",
@@ -56,6 +58,7 @@ class kvattn_plan(ctypes.Structure):
 # name -> (restype, argtypes); mirrors include/kvattn.h
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
+_LL = ctypes.c_longlong
 _SIGS = {
     "kv_append": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP]),
     "kv_append_multi": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP]),
@@ -88,6 +91,14 @@ _SIGS = {
                                           _I, _I, ctypes.c_float, _I, _VP]),
     "gqa_decode_step_paged_window": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I,
                                           _I, _I, _I, _I, ctypes.c_float, _I, _VP]),
+    "kv_block_tables": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP]),
+    "kv_append_slots": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _LL, _LL, _I, _I, _VP]),
+    "gqa_prefill_attn": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _LL, _LL, _LL,
+                              ctypes.c_float, _I, _VP]),
+    "kv_append_paged_fp8": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I,
+                                 _LL, _LL, _I, _I, _I, _VP]),
+    "gqa_decode_attn_paged_fp8": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I,
+                                       _I, _I, _I, ctypes.c_float, _VP]),
     "kvattn_status_string": (ctypes.c_char_p, [_I]),
     "kvattn_last_error": (ctypes.c_char_p, []),
     "kvattn_check_device_error": (_I, [_VP]),
@@ -532,6 +543,221 @@ def gqa_decode_step_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, seq
                                      _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
                                      _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, Lmax,
                                      float(scale), _stream_ptr(stream)))
+    return out
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: all tensors must be there."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device %d (got %s)" % (dev, t.device))
+
+
+def _packed_rows(t, name, shape=None):
+    """Checks packed bf16 rows [N, H, D] whose [H, D] are contiguous (they may
+    be a slice of wider rows) and returns the elements from row to row."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (got %s)" % (name, t.device))
+    if t.dtype is not torch.bfloat16:
+        raise TypeError("%s must be %s (got %s)" % (name, torch.bfloat16, t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s must be [N, heads, D]" % name)
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s (got %s)" % (name, shape, tuple(t.shape)))
+    N, H, D = t.shape
+    row, head, one = t.stride()
+    if (one != 1 and D > 1) or (head != D and H > 1):
+        raise ValueError("%s: each row's [heads, D] must be contiguous (strides %s)" % (name, t.stride()))
+    return row if N > 1 else H * D
+
+
+def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count, block_size,
+                    num_slots, cu_seqlens=None, slots=None, free_count_out=None, stream=None):
+    """Blocks and slots for each request's new tokens, packed request after
+    request: request b keeps its ceil(cached_lens[b] / block_size) blocks and
+    takes the ones it lacks for new_lens[b] more tokens from the top of the
+    free stack (free_blocks[:free_count]); packed row cu_seqlens[b] + i gets
+    slot block * block_size + offset of position cached_lens[b] + i, rows
+    behind the last token -1.
+
+    cached_lens, new_lens: int32 [B]; block_table: int32 [B, max_blocks] (in
+    place); free_blocks: int32 [num_free]; free_count: int32 [1]; num_slots:
+    rows of the slot map.  cu_seqlens (int32 [B + 1]) and slots (int64
+    [num_slots]) are allocated if None; the count left goes to free_count_out
+    (None: back into free_count).  Returns (cu_seqlens, slots, free_count_out).
+    Requests that the free list or the table cannot serve get slot -1 and set
+    the device error word (see include/kvattn.h).
+    """
+    import torch
+    i32 = torch.int32
+    _need(cached_lens, "cached_lens", i32)
+    if cached_lens.dim() != 1:
+        raise ValueError("cached_lens must be [B]")
+    B = cached_lens.shape[0]
+    _need(new_lens, "new_lens", i32, (B,))
+    _need(block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    _need(free_blocks, "free_blocks", i32)
+    if free_blocks.dim() != 1:
+        raise ValueError("free_blocks must be [num_free]")
+    _need(free_count, "free_count", i32, (1,))
+    num_slots = int(num_slots)
+    if cu_seqlens is None:
+        cu_seqlens = torch.empty(B + 1, dtype=i32, device=cached_lens.device)
+    else:
+        _need(cu_seqlens, "cu_seqlens", i32, (B + 1,))
+    if slots is None:
+        slots = torch.empty(max(num_slots, 0), dtype=torch.int64, device=cached_lens.device)
+    else:
+        _need(slots, "slots", torch.int64, (num_slots,))
+    if free_count_out is None:
+        free_count_out = free_count
+    else:
+        _need(free_count_out, "free_count_out", i32, (1,))
+    _on_current_device(cached_lens, new_lens, block_table, free_blocks, free_count, cu_seqlens, slots,
+                       free_count_out)
+    _check(lib().kv_block_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(block_table),
+                                 _ptr(free_blocks), _ptr(free_count), _ptr(free_count_out),
+                                 _ptr(cu_seqlens), _ptr(slots), B, block_table.shape[1],
+                                 int(block_size), free_blocks.shape[0], num_slots,
+                                 _stream_ptr(stream)))
+    return cu_seqlens, slots, free_count_out
+
+
+def kv_append_slots(k_pool, v_pool, k_new, v_new, slots, stream=None):
+    """Write packed K/V rows into a paged pool: row i goes to row
+    slots[i] % block_size of block slots[i] // block_size; a negative slot
+    skips its row.
+
+    k_pool, v_pool: bf16 [num_blocks, Hkv, block_size, D] (in place); k_new,
+    v_new: bf16 [N, Hkv, D], rows contiguous or slices of wider rows; slots:
+    int64 [N], all different.
+    """
+    import torch
+    _need(k_pool, "k_pool", torch.bfloat16)
+    if k_pool.dim() != 4:
+        raise ValueError("k_pool must be [num_blocks, Hkv, block_size, D]")
+    nblk, Hkv, bs, D = k_pool.shape
+    _need(v_pool, "v_pool", torch.bfloat16, (nblk, Hkv, bs, D))
+    _need(slots, "slots", torch.int64)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [N]")
+    N = slots.shape[0]
+    ks = _packed_rows(k_new, "k_new", (N, Hkv, D))
+    vs = _packed_rows(v_new, "v_new", (N, Hkv, D))
+    _on_current_device(k_pool, v_pool, k_new, v_new, slots)
+    _check(lib().kv_append_slots(_ptr(k_pool), _ptr(v_pool), _ptr(k_new), _ptr(v_new), _ptr(slots),
+                                 N, Hkv, D, ks, vs, nblk, bs, _stream_ptr(stream)))
+
+
+def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=None):
+    """Causal attention of whole prompts packed one after the other: token i
+    of sequence b (rows [cu_seqlens[b], cu_seqlens[b + 1])) attends the tokens
+    j <= i of its sequence (j > i - window on a local attention layer).
+
+    q: bf16 [N, Hq, D]; k, v: bf16 [N, Hkv, D], rows contiguous or slices of
+    wider rows; cu_seqlens: int32 [B + 1]; out: optional bf16 [N, Hq, D] (if
+    None allocated as zeros, since rows of no sequence are not written);
+    window: None (all positions) or an int >= 1.  Returns out.
+    """
+    import torch
+    qs = _packed_rows(q, "q")
+    N, Hq, D = q.shape
+    ks = _packed_rows(k, "k")
+    Hkv = k.shape[1]
+    if k.shape[0] != N or k.shape[2] != D:
+        raise ValueError("k must be [N, Hkv, D] matching q")
+    vs = _packed_rows(v, "v", (N, Hkv, D))
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    if out is None:
+        out = torch.zeros((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, "out", torch.bfloat16, (N, Hq, D))
+    _on_current_device(q, k, v, cu_seqlens, out)
+    _check(lib().gqa_prefill_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out),
+                                  cu_seqlens.shape[0] - 1, N, Hq, Hkv, D, qs, ks, vs, float(scale),
+                                  0x7fffffff if window is None else int(window),
+                                  _stream_ptr(stream)))
+    return out
+
+
+def _pool8(k_codes, v_codes, k_scale, v_scale, block_table):
+    """Checks a paged 8-bit cache; returns (num_blocks, Hkv, block_size, D, B, max_blocks)."""
+    import torch
+    _need(k_codes, "k_codes", torch.uint8)
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [num_blocks, Hkv, block_size, D]")
+    nblk, Hkv, bs, D = k_codes.shape
+    _need(v_codes, "v_codes", torch.uint8, (nblk, Hkv, bs, D))
+    _need(k_scale, "k_scale", torch.float32, (nblk, Hkv))
+    _need(v_scale, "v_scale", torch.float32, (nblk, Hkv))
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    return nblk, Hkv, bs, D, block_table.shape[0], block_table.shape[1]
+
+
+def kv_append_paged_fp8(k_codes, v_codes, k_scale, v_scale, k_new, v_new, block_table, cached_lens,
+                        cu_seqlens, stream=None):
+    """Quantize packed K/V rows into a paged 8-bit cache with one power-of-two
+    scale per block and K/V head: token i of request b (packed row
+    cu_seqlens[b] + i) goes to position cached_lens[b] + i of its table row.  A
+    block's scale grows with its rows; earlier codes are rewritten for it.
+
+    k_codes, v_codes: uint8 [num_blocks, Hkv, block_size, D]; k_scale,
+    v_scale: fp32 [num_blocks, Hkv] (all in place); k_new, v_new: bf16
+    [N, Hkv, D], rows contiguous or slices of wider rows; block_table: int32
+    [B, max_blocks]; cached_lens: int32 [B]; cu_seqlens: int32 [B + 1].
+    """
+    import torch
+    nblk, Hkv, bs, D, B, maxb = _pool8(k_codes, v_codes, k_scale, v_scale, block_table)
+    ks = _packed_rows(k_new, "k_new")
+    N = k_new.shape[0]
+    if k_new.shape[1] != Hkv or k_new.shape[2] != D:
+        raise ValueError("k_new must be [N, Hkv, D] matching the pool")
+    vs = _packed_rows(v_new, "v_new", (N, Hkv, D))
+    _need(cached_lens, "cached_lens", torch.int32, (B,))
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _on_current_device(k_codes, v_codes, k_scale, v_scale, k_new, v_new, block_table, cached_lens,
+                       cu_seqlens)
+    _check(lib().kv_append_paged_fp8(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
+                                     _ptr(k_new), _ptr(v_new), _ptr(block_table), _ptr(cached_lens),
+                                     _ptr(cu_seqlens), B, N, Hkv, D, ks, vs, nblk, bs, maxb,
+                                     _stream_ptr(stream)))
+
+
+def gqa_decode_attn_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale,
+                              out=None, stream=None):
+    """gqa_decode_attn over a paged 8-bit cache: K = E4M3(k_codes) *
+    k_scale[block, kvh], V likewise.  q: bf16 [B, Hq, D]; pools and table as for
+    kv_append_paged_fp8; seq_lens: int32 [B], positions attended; out: optional
+    bf16 [B, Hq, D].  Returns out."""
+    import torch
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    B, Hq, D = q.shape
+    nblk, Hkv, bs, Dp, Bt, maxb = _pool8(k_codes, v_codes, k_scale, v_scale, block_table)
+    if Dp != D or Bt != B:
+        raise ValueError("k_codes / block_table do not match q")
+    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, "out", torch.bfloat16, (B, Hq, D))
+    _on_current_device(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, out)
+    _check(lib().gqa_decode_attn_paged_fp8(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
+                                           _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+                                           _ptr(out), B, Hq, Hkv, D, nblk, bs, maxb, float(scale),
+                                           _stream_ptr(stream)))
     return out
 
 

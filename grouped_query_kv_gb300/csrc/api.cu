@@ -355,6 +355,61 @@ int api_error_word(unsigned int **word) {
 
 int api_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
 
+void api_begin() { t_last_error[0] = 0; }
+
+int api_failf(int status, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_last_error, sizeof t_last_error, fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+int api_check_sizes(int B, int Hq, int Hkv, int D, int Lmax) {
+    return check_sizes(B, Hq, Hkv, D, Lmax);
+}
+
+int api_check_row_stride(long long stride, int H, int D, const char *who) {
+    if (stride < (long long)H * D || stride % 8 != 0 || stride > (1LL << 38))
+        return fail(KVATTN_ERR_INVALID_ARG,
+                    "%s: a row stride must be a multiple of 8 elements, at least heads * D = %lld "
+                    "and at most 2^38 (got %lld)", who, (long long)H * D, stride);
+    return KVATTN_OK;
+}
+
+int api_check_paged(const int32_t *table, int Hkv, int block_size, int max_blocks, int num_blocks,
+                    const char *who, int *lg, int *Lmax) {
+    return check_paged(Paged{table, block_size, max_blocks, num_blocks}, Hkv, who, lg, Lmax);
+}
+
+int api_device(int *ctas, unsigned int **err, unsigned int *wait_limit) {
+    int dev, rc;
+    if ((rc = current_device(&dev))) return rc;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState *ds;
+    if ((rc = device_state(dev, &ds))) return rc;
+    *ctas = g_force_ctas > 0 ? g_force_ctas : ds->num_sms;
+    *err = ds->err;
+    *wait_limit = g_wait_limit;
+    return KVATTN_OK;
+}
+
+int api_encode_bf16_3d(CUtensorMap *m, const void *base, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box) {
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        int rc = get_encoder();
+        if (rc) return rc;
+    }
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(KVATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return KVATTN_OK;
+}
+
 }  // namespace kvattn
 
 namespace {
@@ -612,9 +667,10 @@ int run_decode(const void *q, const void *k_cache, const void *v_cache, const vo
 int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
                    const float *v_scale, const int32_t *seq_lens, float *out, int B, int Hq,
                    int Hkv, int D, int Lmax, float scale, kvattn_stream_t stream_,
-                   const void *k_new = nullptr, const void *v_new = nullptr) {
+                   const void *k_new = nullptr, const void *v_new = nullptr,
+                   const Paged *pg = nullptr) {
     const bool fused = k_new != nullptr || v_new != nullptr;
-    const char *who = fused ? "gqa_decode_step_fp8" : "gqa_decode_attn_fp8";
+    const char *who = pg ? "gqa_decode_attn_paged_fp8" : fused ? "gqa_decode_step_fp8" : "gqa_decode_attn_fp8";
     t_last_error[0] = 0;
     if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !seq_lens || !out ||
         (fused && (!k_new || !v_new)))
@@ -625,8 +681,14 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
         (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
         return fail(KVATTN_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned (scales 4)", who);
     if (!std::isfinite(scale)) return fail(KVATTN_ERR_INVALID_ARG, "%s: scale must be finite", who);
-    int rc = check_sizes(B, Hq, Hkv, D, Lmax);
-    if (rc) return rc;
+    int rc, lg = 0;
+    if (pg) {
+        if ((rc = check_paged(*pg, Hkv, who, &lg, &Lmax))) return rc;
+        if (pg->block_size > 1024)
+            return fail(KVATTN_ERR_UNSUPPORTED, "%s: an 8-bit block holds at most 1024 positions (got %d)",
+                        who, pg->block_size);
+    }
+    if ((rc = check_sizes(B, Hq, Hkv, D, Lmax))) return rc;
     if (D != 128 && D != 256)
         return fail(KVATTN_ERR_UNSUPPORTED,
                     "%s: the 8-bit kernel reads 128-code rows per copy and needs D = 128 or 256 "
@@ -653,8 +715,11 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
     }
     const kvattn_plan &P = pl.pub;
     CUtensorMap tmk, tmv;
-    if ((rc = encode_fp8_map(&tmk, k_codes, D, Lmax, B * Hkv, P.tile_positions))) return rc;
-    if ((rc = encode_fp8_map(&tmv, v_codes, D, Lmax, B * Hkv, P.tile_positions))) return rc;
+    // (a pool is the same map, blocks in place of sequences, with boxes of at most a block's rows)
+    const int rows = pg ? pg->block_size : Lmax, boxes = pg ? pg->num_blocks * Hkv : B * Hkv;
+    const int box = pg && pg->block_size < P.tile_positions ? pg->block_size : P.tile_positions;
+    if ((rc = encode_fp8_map(&tmk, k_codes, D, rows, boxes, box))) return rc;
+    if ((rc = encode_fp8_map(&tmv, v_codes, D, rows, boxes, box))) return rc;
 
     DecodeParams p = {};
     memset(&p, 0, sizeof p);
@@ -687,6 +752,11 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.block_table = pg ? pg->table : nullptr;
+    p.block_lg = lg;
+    p.max_blocks = pg ? pg->max_blocks : 0;
+    p.num_blocks = pg ? pg->num_blocks : 0;
+    p.out_bf16 = pg ? 1 : 0;
     cudaError_t e;
     if (ev_before && (e = cudaEventRecord(ev_before, stream)) != cudaSuccess)
         return cuda_fail(e, "recording the event before the split-KV kernel");
@@ -819,6 +889,16 @@ int gqa_decode_step_fp8(const void *q, const void *k_new, const void *v_new, voi
     }
     return run_decode_fp8(q, k_codes, v_codes, k_scale, v_scale, seq_lens, out, B, Hq, Hkv, D,
                           Lmax, scale, stream, k_new, v_new);
+}
+
+int gqa_decode_attn_paged_fp8(const void *q, const void *k_codes, const void *v_codes,
+                              const float *k_scale, const float *v_scale,
+                              const int32_t *block_table, const int32_t *seq_lens, void *out, int B,
+                              int Hq, int Hkv, int D, int num_blocks, int block_size,
+                              int max_blocks, float scale, kvattn_stream_t stream) {
+    const Paged pg{block_table, block_size, max_blocks, num_blocks};
+    return run_decode_fp8(q, k_codes, v_codes, k_scale, v_scale, seq_lens, static_cast<float *>(out), B,
+                          Hq, Hkv, D, 0, scale, stream, nullptr, nullptr, &pg);
 }
 
 int kv_quantize_fp8(const void *src, void *codes, float *scales, long long rows, int D,

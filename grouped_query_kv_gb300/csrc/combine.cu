@@ -15,6 +15,8 @@
 // blocks: a large grid takes microseconds just to be placed.  Launched with
 // programmatic serialisation: it waits on the split-KV kernel with
 // griddepcontrol.wait instead of a full launch gap.
+#include <cuda_bf16.h>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "schedule.cuh"
@@ -76,6 +78,8 @@ __device__ inline void segment_pieces(const DecodeParams &p, int s, int grid, in
 // (rows whose record names none exit at once).  The host takes rows by
 // segment when there are fewer segments than CTAs: few rows, and no record
 // load between the wait and the partials' loads.
+// BF16: out holds bf16 values (the paged 8-bit cache's), else fp32.
+template <bool BF16>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeParams p, int num_ctas,
                                                            int by_segment) {
     // the next kernel in the stream may start its prologue while this one
@@ -159,8 +163,16 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeParams p,
         mrun = mx;
     }
     const float inv = (den > 0.f) ? 1.f / den : 0.f;
-    *reinterpret_cast<float4 *>(p.out + (((size_t)b * p.T + t) * p.Hq + h0 + gg) * D + d) =
-        make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+    const size_t at = (((size_t)b * p.T + t) * p.Hq + h0 + gg) * D + d;
+    if (BF16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(num.x * inv, num.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(num.z * inv, num.w * inv);
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    } else {
+        *reinterpret_cast<float4 *>(p.out + at) =
+            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+    }
 }
 
 }  // namespace
@@ -182,7 +194,8 @@ cudaError_t launch_combine(const DecodeParams &p, int num_ctas, cudaStream_t str
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, combine_kernel, p, num_ctas, by_segment);
+    return p.out_bf16 ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, p, num_ctas, by_segment)
+                      : cudaLaunchKernelEx(&cfg, combine_kernel<false>, p, num_ctas, by_segment);
 }
 
 }  // namespace kvattn

@@ -177,7 +177,12 @@ __device__ __forceinline__ float2 e4m3x2_value(uint16_t two) {
 // 2^e as a binary32 value, e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-template <int D, int NP>
+// PG: a paged pool with one scale per (block, K/V head), bf16 output.  Tiles
+// come through the block table as in the bf16 kernel (decode_tc.cuh): one TMA
+// box per block a tile spans, and a sequence's last tile ends at its length
+// -- for blocks under 128 positions the last block's rows end the tile behind
+// a hole of zero rows -- so rows past the length are never read.
+template <int D, int NP, bool PG>
 __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const DecodeParams p) {
@@ -279,13 +284,54 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
         itk.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
         itv.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
         bool ok = true;
+        // paged: boxes per tile (lanes 0 .. nbox-1 issue one each), its bytes,
+        // and this lane's box of the current K, current V and next K tile
+        const int nbox = PG ? (p.block_lg >= 7 ? 1 : kT >> p.block_lg) : 1;
+        const int box_bytes = PG ? (p.block_lg >= 7 ? kT : 1 << p.block_lg) * 128 : 0;
+        int ky = 0, kz = -1, vy = 0, vz = -1, ny = 0, nblk = -1;
+        bool nuse = false;
+        auto paged_fetch = [&](const TileIter &it) {
+            const int lg = p.block_lg;
+            const int len = seq_valid_len(it.len, p.Lmax);
+            int k;  // logical block
+            if (lg >= 7) {
+                const int r0 = it.row0();
+                k = (r0 + kT - 1) >> lg;  // the block of the tile's last row
+                ny = r0 - (k << lg);
+            } else if (!it.last_tile_of_segment()) {
+                k = (it.first_pos() >> lg) + lane;
+                ny = 0;
+            } else {
+                const int kend = (len - 1) >> lg;  // -1 for an empty sequence
+                k = kend - (nbox - 1 - lane);
+                ny = lane == nbox - 1 ? len - ((kend + 1) << lg) : 0;
+            }
+            nuse = lane < nbox && k >= 0;
+            nblk = nuse ? p.block_table[(size_t)it.b * p.max_blocks + k] : -1;
+        };
+        auto paged_row = [&](int kvh) -> int {  // the fetched box's pool row (-1: zeros)
+            if (!nuse) return -1;
+            if (nblk >= 0 && nblk < p.num_blocks) return nblk * p.Hkv + kvh;
+            set_error(p.err, DEV_ERR_BOUNDS);
+            return -1;
+        };
+        if (PG) paged_fetch(itk);
         auto issue = [&](const void *tm, const TileIter &it, uint8_t *base, uint64_t *full,
-                         uint64_t *empty, int ns, long long &n) -> bool {
+                         uint64_t *empty, int ns, long long &n, int y, int z_) -> bool {
             const int slot = (int)(n % ns);
             bool w = true;
             if (lane == 0 && n >= ns) w = wait_bar(&empty[slot], (uint32_t)(((n / ns) - 1) & 1), abort_flag);
             if (!__shfl_sync(0xffffffffu, w, 0)) return false;
-            if (lane == 0) {
+            if (PG) {
+                if (lane == 0) mbar_arrive_expect_tx(&full[slot], kStage);
+                __syncwarp();
+                if (lane < nbox) {
+#pragma unroll
+                    for (int sl = 0; sl < SL; ++sl)
+                        tma_load_3d(base + slot * kStage + sl * kBox + lane * box_bytes, tm, &full[slot],
+                                    sl * 128, y, z_, pol);
+                }
+            } else if (lane == 0) {
                 mbar_arrive_expect_tx(&full[slot], kStage);
                 const int z = it.b * p.Hkv + it.seg / p.head_groups;
 #pragma unroll
@@ -297,11 +343,13 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
             return true;
         };
         for (long long r = 0; r <= ntiles && ok; ++r) {
+            vy = ky;  // V of tile r-1 comes from the blocks of K tile r-1
+            vz = kz;
             if (r < ntiles) {
                 // fused append: this tile holds the new token's row -- its
                 // codes and scales are written (and made visible to the
                 // copies and to every SM) before the tile's copies go out
-                if (p.len_add && itk.last_tile_of_segment() && itk.len >= 1 && itk.len <= p.Lmax) {
+                if (!PG && p.len_add && itk.last_tile_of_segment() && itk.len >= 1 && itk.len <= p.Lmax) {
                     const int z = itk.b * p.Hkv + itk.seg / p.head_groups;
                     const size_t dst = (size_t)z * p.Lmax + (itk.len - 1);
                     uint8_t *kc = reinterpret_cast<uint8_t *>(p.k_cache);
@@ -314,11 +362,16 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                     __threadfence();
                     __syncwarp();
                 }
-                ok = issue(&tmk, itk, kst, kst_full, kst_empty, NSK, nk);
+                if (PG) {
+                    ky = ny;
+                    kz = paged_row(itk.seg / p.head_groups);
+                }
+                ok = issue(&tmk, itk, kst, kst_full, kst_empty, NSK, nk, ky, kz);
                 itk.next();
+                if (PG && r + 1 < ntiles) paged_fetch(itk);
             }
             if (r >= 1 && ok) {
-                ok = issue(&tmv, itv, vst, vst_full, vst_empty, NSV, nv);
+                ok = issue(&tmv, itv, vst, vst_full, vst_empty, NSV, nv, vy, vz);
                 itv.next();
             }
         }
@@ -612,17 +665,35 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
         while (true) {
             const int sb = (int)(i & 1);
             const int r0 = it.row0();
-            const int pos = r0 + row;
-            const bool valid = row >= it.first_pos() - r0 && pos < len;
+            int pos = r0 + row;
+            bool valid;
+            if (PG && p.block_lg < 7 && it.last_tile_of_segment()) {
+                // small blocks: rows before the hole hold the earlier blocks,
+                // hn positions further on
+                const int hn = ((((len - 1) >> p.block_lg) + 1) << p.block_lg) - len;
+                const int hl = kT - (1 << p.block_lg);
+                if (row < hl) pos += hn;
+                valid = !(row >= hl && row < hl + hn) && pos >= it.first_pos() && pos < len;
+            } else {
+                valid = row >= it.first_pos() - r0 && pos < len;
+            }
             // this row's scales, loaded while the scores are made -- except
             // in a segment's last tile when this call appends: that tile may
             // hold the row the copy warp has just written, so its scales are
             // read once the tile's scores exist (the copy warp fenced its
             // stores before issuing the tile's copies), past L1 (which may
             // hold the line from the tile before)
-            const bool late = p.len_add && it.last_tile_of_segment();
+            const bool late = !PG && p.len_add && it.last_tile_of_segment();
             float ksc = 0.f, vsc = 0.f;
-            if (valid && !late) {
+            if (PG) {
+                if (valid) {
+                    const int blk = p.block_table[(size_t)b * p.max_blocks + (pos >> p.block_lg)];
+                    if (blk >= 0 && blk < p.num_blocks) {  // (else zeros, as the copy warp flags)
+                        ksc = p.k_scale[(size_t)blk * p.Hkv + kvh];
+                        vsc = p.v_scale[(size_t)blk * p.Hkv + kvh];
+                    }
+                }
+            } else if (valid && !late) {
                 ksc = p.k_scale[zrow + pos];
                 vsc = p.v_scale[zrow + pos];
             }
@@ -864,7 +935,12 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                     const int g = cg0 + k;
                     if (g < gvalid) {
                         const float lt = ltot_s[g];
-                        p.out[((size_t)b * p.Hq + h0 + g) * D + d] = (lt > 0.f) ? o[k] / lt : 0.f;
+                        const size_t at = ((size_t)b * p.Hq + h0 + g) * D + d;
+                        const float x = (lt > 0.f) ? o[k] / lt : 0.f;
+                        if (PG)
+                            reinterpret_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(x);
+                        else
+                            p.out[at] = x;
                     }
                 }
             } else {
@@ -896,7 +972,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
     named_bar_sync(kBarEnd, C::END_THREADS);
 }
 
-template <int D, int NP>
+template <int D, int NP, bool PG>
 cudaError_t launch_q8(const CUtensorMap &tmk, const CUtensorMap &tmv, const DecodeParams &p,
                       int num_ctas, cudaStream_t stream) {
     static int done_for_device[64] = {0};
@@ -904,7 +980,7 @@ cudaError_t launch_q8(const CUtensorMap &tmk, const CUtensorMap &tmv, const Deco
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!(dev >= 0 && dev < 64 && done_for_device[dev])) {
-        e = cudaFuncSetAttribute(decode_q8_kernel<D, NP>,
+        e = cudaFuncSetAttribute(decode_q8_kernel<D, NP, PG>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Cfg<D, NP>::alloc);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done_for_device[dev] = 1;
@@ -919,7 +995,7 @@ cudaError_t launch_q8(const CUtensorMap &tmk, const CUtensorMap &tmv, const Deco
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_q8_kernel<D, NP>, tmk, tmv, p);
+    return cudaLaunchKernelEx(&cfg, decode_q8_kernel<D, NP, PG>, tmk, tmv, p);
 }
 
 }  // namespace
@@ -939,14 +1015,22 @@ int q8_smem_bytes(int D, int np) {
 
 cudaError_t launch_decode_q8(const CUtensorMap &tmk, const CUtensorMap &tmv,
                              const DecodeParams &p, int np, int num_ctas, cudaStream_t stream) {
+    const bool pg = p.block_table != nullptr;
     switch (p.D * 1000 + np) {
-        case 128016: return launch_q8<128, 16>(tmk, tmv, p, num_ctas, stream);
-        case 128032: return launch_q8<128, 32>(tmk, tmv, p, num_ctas, stream);
-        case 128048: return launch_q8<128, 48>(tmk, tmv, p, num_ctas, stream);
-        case 128064: return launch_q8<128, 64>(tmk, tmv, p, num_ctas, stream);
-        case 256016: return launch_q8<256, 16>(tmk, tmv, p, num_ctas, stream);
-        case 256032: return launch_q8<256, 32>(tmk, tmv, p, num_ctas, stream);
-        case 256048: return launch_q8<256, 48>(tmk, tmv, p, num_ctas, stream);
+        case 128016: return pg ? launch_q8<128, 16, true>(tmk, tmv, p, num_ctas, stream)
+                            : launch_q8<128, 16, false>(tmk, tmv, p, num_ctas, stream);
+        case 128032: return pg ? launch_q8<128, 32, true>(tmk, tmv, p, num_ctas, stream)
+                            : launch_q8<128, 32, false>(tmk, tmv, p, num_ctas, stream);
+        case 128048: return pg ? launch_q8<128, 48, true>(tmk, tmv, p, num_ctas, stream)
+                            : launch_q8<128, 48, false>(tmk, tmv, p, num_ctas, stream);
+        case 128064: return pg ? launch_q8<128, 64, true>(tmk, tmv, p, num_ctas, stream)
+                            : launch_q8<128, 64, false>(tmk, tmv, p, num_ctas, stream);
+        case 256016: return pg ? launch_q8<256, 16, true>(tmk, tmv, p, num_ctas, stream)
+                            : launch_q8<256, 16, false>(tmk, tmv, p, num_ctas, stream);
+        case 256032: return pg ? launch_q8<256, 32, true>(tmk, tmv, p, num_ctas, stream)
+                            : launch_q8<256, 32, false>(tmk, tmv, p, num_ctas, stream);
+        case 256048: return pg ? launch_q8<256, 48, true>(tmk, tmv, p, num_ctas, stream)
+                            : launch_q8<256, 48, false>(tmk, tmv, p, num_ctas, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -60,7 +60,8 @@ struct DecodeParams {
     int max_blocks;
     int num_blocks;
     // 8-bit cache (decode_fp8.cu): one fp32 scale per cached row,
-    // [B, Hkv, Lmax] for K and for V; null otherwise
+    // [B, Hkv, Lmax] for K and for V, or, paged, one per block and K/V head,
+    // [num_blocks, Hkv]; null otherwise
     const float *k_scale;
     const float *v_scale;
     // tensor-core kernel: polls before a pipeline wait gives up (the softmax
@@ -70,6 +71,7 @@ struct DecodeParams {
     int qwin;                 // positions one query attends at most (>= Lmax: all)
     int walign;               // 0, or tile - 1 (paged cache): window spans start on a tile
                               // boundary and the rows before a query's window are masked
+    int out_bf16;             // out holds bf16 values (the paged 8-bit cache), else fp32
 };
 
 // Host launchers (return cudaError_t of the launch).
@@ -140,5 +142,24 @@ int api_encode_cache_maps(CUtensorMap *tmk, CUtensorMap *tmv, const void *k_cach
                           const void *v_cache, int D, int Lmax, int BH, int tile);
 int api_error_word(unsigned int **word);
 int api_cuda_fail(cudaError_t e, const char *what);
+
+// For the entry points that live beside their kernels (prefill.cu,
+// paged_rows.cu, paged_fp8.cu).
+void api_begin();  // clears the thread's last error
+int api_failf(int status, const char *fmt, ...);
+int api_check_sizes(int B, int Hq, int Hkv, int D, int Lmax);
+// Elements from one packed row [H, D] to the next: a multiple of 8 (16
+// bytes), at least H * D.
+int api_check_row_stride(long long stride, int H, int D, const char *who);
+// A paged cache's sizes; *lg = log2(block_size), *Lmax = the positions a
+// table row can address.
+int api_check_paged(const int32_t *table, int Hkv, int block_size, int max_blocks, int num_blocks,
+                    const char *who, int *lg, int *Lmax);
+// The current device: its grid size for a persistent kernel (the SM count
+// unless the tuning knob forces another), error word and the wait-limit knob.
+int api_device(int *ctas, unsigned int **err, unsigned int *wait_limit);
+// 3-D map of bf16 values, 128-byte swizzle, out-of-range reads as zeros.
+int api_encode_bf16_3d(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+                       const cuuint32_t *box);
 
 }  // namespace kvattn

@@ -1,0 +1,883 @@
+// prefill.cu -- causal grouped-query attention over whole prompts, packed one
+// after the other ("The Basics of Transformer Inference", the prefill phase:
+// every prompt token attends itself and the tokens before it, in one pass):
+//     out[i,h,:] = sum_j softmax_j(scale q[i,h] . k[j,h/G]) v[j,h/G,:]
+// over max(first, i - window + 1) <= j <= i of the token's own sequence.
+//
+// Mathematics.  One pass over the keys with a running maximum m and sum l per
+// row (base-2 exponentials, scores scaled by |scale| log2 e):
+//     p_j = 2^(s_j - m),  l += p_j,  O += p_j v_j,   out = O / l.
+// m moves only when a score passes it by more than 2^8 (then O and l are
+// rescaled by 2^(m - m')), so O is rarely touched between products; p stays
+// below 2^8 and l in 32 bits.  p enters the second product as bf16 (the
+// output is bf16: the weights' rounding, at most 2^-9 each, averages out below
+// the output's own).
+//
+// Layout.  A tile is 128 query rows: hpg = gcd(G, 128) heads of one K/V head
+// by 128 / hpg consecutive tokens, so heads that share K/V share every key
+// tile, and the causal diagonal is only 128 / hpg tokens wide.  Rows are
+// tensor-memory lanes: thread r of a softmax warpgroup owns row r and its 128
+// scores of a key tile, so row maxima and sums need no exchange.
+//   S (tile)  = Q K^T     [128 x 128 keys]   both operands in shared memory
+//   O (tile) += P V       [128 x D]          P in tensor memory, over S
+// D = 64, 128: two query tiles per CTA, each with its S, O and warpgroup;
+// while one is in its softmax the tensor cores work for the other, and both
+// read the same K/V tiles.  D = 256: O takes 256 of the 512 columns, so one
+// query tile per CTA with two S buffers: Q K^T of the next key tile runs
+// during the softmax of this one.
+//
+// Warps: 0 walks the work list and issues the copies (TMA), 1 issues the
+// MMAs, then one softmax warpgroup per query tile.
+//
+// Work list.  A unit is (sequence, block of NQ x 128 / hpg tokens, K/V head,
+// head group); its cost grows with its block's index.  Every CTA of the
+// persistent grid sorts the blocks of all sequences into buckets of that
+// index (from cu_seqlens, in shared memory: no workspace, no atomics on
+// global memory, the same order in every run) and takes units from the
+// largest down, every second round in reverse.
+#include <cfloat>
+#include <climits>
+#include <cmath>
+#include <cuda_bf16.h>
+
+#include "../../include/kvattn.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace kvattn {
+
+namespace {
+
+constexpr int kRows = 128;      // query rows of a tile = keys of a tile
+constexpr int kSlab = 16384;    // 128 rows x 64 columns of bf16
+constexpr int kSmemMax = 232448;
+constexpr float kTauPf = 8.f;   // log2 headroom before the running max must move
+constexpr int kBuckets = 256;
+constexpr int kDesc = 4;        // units in flight between the work list and its readers
+constexpr int kBarEndPf = 1;
+
+struct PrefillParams {
+    const int32_t *cu;  // [B + 1] first rows of the sequences
+    uint16_t *out;      // bf16 [N, Hq, D]
+    unsigned int *err;
+    int B, N, Hq, Hkv, G;
+    int hpg, hpg_lg;    // query heads of a tile, a power of two
+    int tpt;            // tokens of a tile, 128 / hpg
+    int passes;         // G / hpg
+    int window;         // keys one query attends at most (N: all)
+    float sl;           // |scale| log2(e), at least the smallest normal number
+    int neg;            // scale < 0: the MMA negates q
+    unsigned int wait_limit;
+};
+
+// One unit of work as its readers see it.
+struct Unit {
+    int row0;    // first packed row of the sequence
+    int len;     // its length
+    int t0;      // first token of the unit
+    int kvh;     // K/V head
+    int h0;      // first query head
+    int kbeg;    // first key of the unit's key tiles
+    int n[2];    // key tiles of each query tile; n[0] = 0 ends the list
+};
+
+template <int D>
+struct PfCfg {
+    static constexpr int NQ = D == 256 ? 1 : 2;         // query tiles
+    static constexpr int SLABS = D / 64;
+    static constexpr int QT = SLABS * kSlab;            // one query tile
+    static constexpr int KC = D < 128 ? D : 128;        // head dims of a ring slot
+    static constexpr int CPT = D / KC;                  // slots per K (or V) tile
+    static constexpr int SLOT = KC / 64 * kSlab;
+    static constexpr int FIXED = NQ * QT + 1024 + 4096;
+    static constexpr int NS_FIT = (kSmemMax - FIXED) / SLOT;
+    static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;  // ring slots
+    static constexpr int THREADS = 64 + 128 * NQ;
+    static constexpr int off_q = 0;
+    static constexpr int off_ring = NQ * QT;
+    static constexpr int off_bar = off_ring + NS * SLOT;
+    static constexpr int nbar = 2 * NS + 2 * 2 + 3 * 2 + 2 * kDesc + 1;
+    static constexpr int off_misc = off_bar + nbar * 8;          // tmem base, abort flag
+    static constexpr int off_unit = (off_misc + 32 + 15) / 16 * 16;
+    static constexpr int off_cnt = off_unit + kDesc * (int)sizeof(Unit);
+    static constexpr int off_sum = off_cnt + 2 * kBuckets * 4;
+    static constexpr int bytes = off_sum + 64;
+    static constexpr int alloc = bytes + 1024;
+    static_assert(NS >= 2 * CPT && NS >= 4, "the ring holds one K and one V tile");
+    static_assert(alloc <= kSmemMax, "shared memory");
+    // TMEM: S0, S1 (128 columns each; P over the first 64), then O per tile
+    static constexpr int O0 = 256;
+    static_assert(O0 + NQ * D <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ void pf_error(unsigned int *err, unsigned int code) { atomicCAS(err, 0u, code); }
+
+__device__ __forceinline__ bool pf_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                        uint32_t limit = KVATTN_SPIN_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 255u && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs (A packed two to a column), fp32 accumulate.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                             uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// Warp: 32 consecutive 32-bit columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Warp: 16 packed columns.
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Length of sequence b (0 where its bounds are not 0 <= cu[b] <= cu[b+1] <= N).
+__device__ __forceinline__ int pf_len(const PrefillParams &p, int b, int *row0) {
+    const int a = p.cu[b], e = p.cu[b + 1];
+    *row0 = a;
+    return (a < 0 || e < a || e > p.N) ? -1 : e - a;
+}
+
+// The ring index of K tile j's and V tile j's first slot within a unit of n
+// key tiles: K0 V0 K1 V1 ... with two query tiles (the order the MMAs take
+// them in), K0 K1 V0 K2 V1 ... V(n-1) with one.
+template <int D>
+__device__ __forceinline__ long long k_slot(int j) {
+    using C = PfCfg<D>;
+    if (C::NQ == 2) return 2 * j;
+    return j == 0 ? 0 : (2 * j - 1) * C::CPT;
+}
+template <int D>
+__device__ __forceinline__ long long v_slot(int j, int n) {
+    using C = PfCfg<D>;
+    if (C::NQ == 2) return 2 * j + 1;
+    return (j == n - 1 ? 2 * n - 1 : 2 * j + 2) * C::CPT;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                   const __grid_constant__ CUtensorMap tmv, const PrefillParams p) {
+    using C = PfCfg<D>;
+    constexpr int NQ = C::NQ, NS = C::NS, CPT = C::CPT;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *qbuf = smem + C::off_q;
+    uint8_t *ring = smem + C::off_ring;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::off_bar);
+    uint64_t *slot_full = bars, *slot_empty = slot_full + NS;
+    uint64_t *q_full = slot_empty + NS, *q_empty = q_full + 2;
+    // s_full, p_full, pv_done: of query tile s (two tiles) or of S buffer s (one)
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2;
+    uint64_t *u_full = pv_done + 2, *u_empty = u_full + kDesc, *drain = u_empty + kDesc;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::off_misc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::off_misc + 16);
+    Unit *units = reinterpret_cast<Unit *>(smem + C::off_unit);
+    int *cnt = reinterpret_cast<int *>(smem + C::off_cnt);  // [kBuckets] full, [kBuckets] rest
+    unsigned long long *sum_pairs = reinterpret_cast<unsigned long long *>(smem + C::off_sum);
+    int *max_nb = reinterpret_cast<int *>(sum_pairs + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tpu = NQ * p.tpt;          // tokens of a unit
+    const int heads = p.Hkv * p.passes;  // units of one block of tokens
+
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&slot_full[s], 1);
+            mbar_init(&slot_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 4);
+            mbar_init(&pv_done[s], 1);
+        }
+        for (int s = 0; s < kDesc; ++s) {
+            mbar_init(&u_full[s], 1);
+            mbar_init(&u_empty[s], 1 + 4 * NQ);  // the MMA thread and the softmax warps
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *sum_pairs = 0;
+        *max_nb = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tmq);
+        prefetch_tmap(&tmk);
+        prefetch_tmap(&tmv);
+    }
+    for (int i = tid; i < 2 * kBuckets; i += C::THREADS) cnt[i] = 0;
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_prior();  // inputs and lengths may come from the previous kernel
+
+    // ------------------------------------------------ the work list's buckets
+    {
+        unsigned long long s = 0;
+        int m = 0;
+        for (int b = tid; b < p.B; b += C::THREADS) {
+            int row0;
+            const int len = pf_len(p, b, &row0);
+            if (len < 0) {
+                if (blockIdx.x == 0) pf_error(p.err, DEV_ERR_BOUNDS);
+                continue;
+            }
+            const int nb = (len + tpu - 1) / tpu;
+            s += nb;
+            m = max(m, nb);
+        }
+        if (m > 0) {
+            atomicAdd(sum_pairs, s);
+            atomicMax(max_nb, m);
+        }
+    }
+    __syncthreads();
+    const long long total = (long long)*sum_pairs * heads;
+    const int mnb = *max_nb;
+    // one wave of units: any order does
+    const int width = total <= gridDim.x ? max(mnb, 1) : (mnb + kBuckets - 1) / kBuckets;
+    const int nbk = width > 0 ? (mnb + width - 1) / width : 0;
+    if (nbk > 1) {
+        for (int b = tid; b < p.B; b += C::THREADS) {
+            int row0;
+            const int len = pf_len(p, b, &row0);
+            if (len <= 0) continue;
+            const int nb = (len + tpu - 1) / tpu;
+            const int k = nb / width;
+            // buckets below k hold `width` blocks of this sequence, bucket k the rest
+            if (k > 0) atomicAdd(&cnt[k - 1], 1);
+            if (nb % width) atomicAdd(&cnt[kBuckets + k], nb % width);
+        }
+        __syncthreads();
+    }
+
+    const uint32_t ring_s = smem_u32(ring), qbuf_s = smem_u32(qbuf);
+
+    // ============================================================ work list, TMA
+    if (warp == 0) {
+        bool ok = true;
+        long long nslot = 0;         // ring slots issued
+        uint32_t qn[2] = {0, 0};     // query tiles issued
+        // the walk: bucket kb holds pairs [pb0, pb0 + its count), `cover` sequences reach past it
+        int kb = nbk;
+        long long pb0 = 0, pbn = 0;
+        int cover = 0;
+        int sb = 0;                  // the bucket's scan: sequences before sb hold sp pairs
+        long long sp = 0;
+        auto find = [&](long long k, Unit *u) {
+            const long long rank = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (rank >= total) {
+                u->n[0] = 0;
+                return;
+            }
+            const long long pair = rank / heads;
+            const int hh = (int)(rank - pair * heads);
+            while (pair >= pb0 + pbn) {  // the next bucket down
+                pb0 += pbn;
+                --kb;
+                if (nbk == 1) {
+                    pbn = (long long)*sum_pairs;
+                } else {
+                    cover += cnt[kb];
+                    pbn = (long long)cover * width + cnt[kBuckets + kb];
+                }
+                sb = 0;
+                sp = 0;
+            }
+            const long long off = pair - pb0;
+            for (;; sb += 32) {  // the chunk of 32 sequences that holds the pair
+                const int b = sb + lane;
+                int row0 = 0, len = 0, mine = 0;
+                if (b < p.B) {
+                    len = max(pf_len(p, b, &row0), 0);
+                    mine = min(max((len + tpu - 1) / tpu - kb * width, 0), width);
+                }
+                int incl = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                const long long before = sp + incl - mine;
+                const unsigned hit = __ballot_sync(0xffffffffu, off >= before && off < before + mine);
+                if (hit) {
+                    const int src = __ffs(hit) - 1;
+                    u->row0 = __shfl_sync(0xffffffffu, row0, src);
+                    u->len = __shfl_sync(0xffffffffu, len, src);
+                    const int blk = kb * width + (int)(off - __shfl_sync(0xffffffffu, before, src));
+                    u->t0 = blk * tpu;
+                    break;
+                }
+                sp += __shfl_sync(0xffffffffu, incl, 31);
+                if (sb + 32 >= p.B) {  // (not reached: every pair has a sequence)
+                    u->n[0] = 0;
+                    return;
+                }
+            }
+            u->kvh = hh / p.passes;
+            u->h0 = u->kvh * p.G + (hh - u->kvh * p.passes) * p.hpg;
+            u->kbeg = max(0, u->t0 + 1 - p.window);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int a = u->t0 + s * p.tpt, e = min(a + p.tpt, u->len);
+                u->n[s] = (s < NQ && a < e) ? (e - u->kbeg + kRows - 1) / kRows : 0;
+            }
+        };
+        auto publish = [&](long long k, const Unit &u) -> bool {
+            const int slot = (int)(k % kDesc);
+            bool w = true;
+            if (lane == 0) {
+                if (k >= kDesc) w = pf_wait(&u_empty[slot], (uint32_t)((k / kDesc - 1) & 1), abort_flag);
+                if (w) {
+                    units[slot] = u;
+                    mbar_arrive(&u_full[slot]);
+                }
+            }
+            return __shfl_sync(0xffffffffu, w, 0);
+        };
+        auto issue = [&](const void *tm, int c, int head, int row) -> bool {
+            const int slot = (int)(nslot % NS);
+            bool w = true;
+            if (nslot >= NS)
+                w = pf_wait(&slot_empty[slot], (uint32_t)((nslot / NS - 1) & 1), abort_flag);
+            if (!w) return false;
+            mbar_arrive_expect_tx(&slot_full[slot], C::SLOT);
+#pragma unroll
+            for (int sl = 0; sl < C::KC / 64; ++sl)
+                tma_load_3d_plain(ring + slot * C::SLOT + sl * kSlab, tm, &slot_full[slot],
+                                  c * C::KC + sl * 64, head, row);
+            ++nslot;
+            return true;
+        };
+        Unit cur, nxt;
+        find(0, &nxt);
+        ok = publish(0, nxt);
+        for (long long k = 0; ok; ++k) {
+            cur = nxt;
+            if (cur.n[0] == 0) break;
+            find(k + 1, &nxt);
+            ok = publish(k + 1, nxt);
+            if (ok && lane == 0) {
+                const int n = max(cur.n[0], cur.n[1]);
+                const int kv0 = cur.row0 + cur.kbeg;
+                auto load_q = [&]() -> bool {
+                    for (int s = 0; s < NQ; ++s) {
+                        if (cur.n[s] == 0) continue;
+                        if (qn[s] && !pf_wait(&q_empty[s], (qn[s] - 1) & 1, abort_flag)) return false;
+                        mbar_arrive_expect_tx(&q_full[s], C::QT);
+                        for (int sl = 0; sl < C::SLABS; ++sl)
+                            tma_load_3d_plain(qbuf + s * C::QT + sl * kSlab, &tmq, &q_full[s], sl * 64,
+                                              cur.h0, cur.row0 + cur.t0 + s * p.tpt);
+                        ++qn[s];
+                    }
+                    return true;
+                };
+                if (NQ == 2) {
+                    for (int j = 0; j < n && ok; ++j) {
+                        ok = issue(&tmk, 0, cur.kvh, kv0 + j * kRows);
+                        if (ok && j == 0) ok = load_q();
+                        if (ok) ok = issue(&tmv, 0, cur.kvh, kv0 + j * kRows);
+                    }
+                } else {
+                    for (int j = 0; j <= n && ok; ++j) {
+                        for (int c = 0; c < CPT && ok && j < n; ++c)
+                            ok = issue(&tmk, c, cur.kvh, kv0 + j * kRows);
+                        if (ok && j == 0) ok = load_q();
+                        for (int c = 0; c < CPT && ok && j > 0; ++c)
+                            ok = issue(&tmv, c, cur.kvh, kv0 + (j - 1) * kRows);
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (!ok && lane == 0) {
+            pf_error(p.err, DEV_ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+        pdl_launch_dependents();
+        named_bar_sync(kBarEndPf, C::THREADS);
+        if (*abort_flag && lane == 0) {
+            // a role gave up: let the copies in flight land before the CTA exits
+            volatile int never = 0;
+            for (long long i = nslot > NS ? nslot - NS : 0; i < nslot; ++i)
+                pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), &never);
+            for (int s = 0; s < NQ; ++s)
+                if (qn[s]) pf_wait(&q_full[s], (qn[s] - 1) & 1, &never);
+        }
+        return;
+    }
+
+    const uint32_t wlim = p.wait_limit ? p.wait_limit : KVATTN_SPIN_LIMIT;
+
+    // ================================================================== MMA
+    if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, C::KC, false, true);
+            // bit 13: A enters negated (a negative scale)
+            const uint32_t idesc_qk = IDESC_QK | (p.neg ? 1u << 13 : 0u);
+            bool ok = true;
+            uint32_t qc[2] = {0, 0};      // query tiles consumed
+            uint32_t pc[2] = {0, 0};      // probability tiles consumed, by tile / S buffer
+            long long base = 0;           // ring slots of the units before this one
+
+            auto slot_ready = [&](long long i) {
+                return pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), abort_flag);
+            };
+            // S[buf] = Q_s K_j^T; keys past the tile's last are left out, 16 at a time
+            auto qk = [&](int s, int buf, long long i0, int keys, bool last_use) {
+                tc_fence_after();
+                const uint32_t idesc = (idesc_qk & ~(0x3fu << 17)) | ((uint32_t)((keys + 15) / 16 * 2) << 17);
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) {
+                    const int slot = (int)((i0 + c) % NS);
+                    const uint32_t kb = ring_s + slot * C::SLOT;
+                    const uint32_t qb = qbuf_s + s * C::QT + c * (C::KC / 64) * kSlab;
+#pragma unroll
+                    for (int kk = 0; kk < C::KC / 16; ++kk) {
+                        const uint32_t o = (kk >> 2) * kSlab + (kk & 3) * 32;
+                        umma_bf16(tmem + buf * 128, smem_desc(qb + o, 16, 1024, 2),
+                                  smem_desc(kb + o, 16, 1024, 2), idesc, c != 0 || kk != 0);
+                    }
+                    if (last_use) umma_commit(&slot_empty[slot]);
+                }
+                umma_commit(&s_full[buf]);
+            };
+            // O_s (+)= P[buf] V_j
+            auto pv = [&](int s, int buf, long long i0, int keys, bool first, bool last_use) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) {
+                    const int slot = (int)((i0 + c) % NS);
+                    const uint32_t vb = ring_s + slot * C::SLOT;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        if (kk * 16 < keys)
+                            umma_bf16_ts(tmem + C::O0 + s * D + c * C::KC, tmem + buf * 128 + kk * 8,
+                                         smem_desc(vb + kk * 2048, kSlab, 1024, 2), IDESC_PV,
+                                         !(first && kk == 0));
+                    }
+                    if (last_use) umma_commit(&slot_empty[slot]);
+                }
+                umma_commit(&pv_done[buf]);
+            };
+            // keys of key tile j that query tile s attends at most (from the tile's start)
+            auto keys_of = [&](const Unit &u, int s, int j) {
+                const int e = min(u.t0 + (s + 1) * p.tpt, u.len);
+                return min(kRows, e - u.kbeg - j * kRows);
+            };
+            auto get = [&](long long k, Unit *u) {
+                if (!pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag)) return false;
+                *u = units[k % kDesc];
+                mbar_arrive(&u_empty[k % kDesc]);
+                return true;
+            };
+
+            Unit cur, nxt;
+            ok = get(0, &nxt);
+            if (NQ == 2) {
+                // step (unit, j): for each tile, P V of j, then Q K^T of the next step
+                bool fresh = true;  // the first unit's Q K^T of step 0 is not issued yet
+                for (long long k = 0; ok; ++k) {
+                    cur = nxt;
+                    if (cur.n[0] == 0) break;
+                    const int n = max(cur.n[0], cur.n[1]);
+                    if (fresh) {
+                        fresh = false;
+                        for (int s = 0; s < 2 && ok; ++s) {
+                            if (cur.n[s] == 0) continue;
+                            ok = slot_ready(base) && pf_wait(&q_full[s], qc[s] & 1, abort_flag);
+                            if (!ok) break;
+                            qk(s, s, base, keys_of(cur, s, 0), s == (cur.n[1] > 0 ? 1 : 0));
+                            ++qc[s];
+                            if (cur.n[s] == 1) umma_commit(&q_empty[s]);
+                        }
+                    }
+                    for (int j = 0; j < n && ok; ++j) {
+                        const bool last = j == n - 1;
+                        if (last && !(ok = get(k + 1, &nxt))) break;
+                        const long long iv = base + 2 * j + 1, ik = base + 2 * j + 2;
+                        ok = slot_ready(iv);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (!ok) break;
+                            if (j < cur.n[s]) {
+                                ok = pf_wait(&p_full[s], pc[s] & 1, abort_flag, wlim);
+                                if (!ok) break;
+                                ++pc[s];
+                                pv(s, s, iv, keys_of(cur, s, j), j == 0, s == (j < cur.n[1] ? 1 : 0));
+                            }
+                            if (!last) {
+                                if (j + 1 < cur.n[s]) {
+                                    ok = slot_ready(ik);
+                                    if (!ok) break;
+                                    qk(s, s, ik, keys_of(cur, s, j + 1), s == (j + 1 < cur.n[1] ? 1 : 0));
+                                    if (j + 1 == cur.n[s] - 1) umma_commit(&q_empty[s]);
+                                }
+                            } else if (nxt.n[0] > 0 && nxt.n[s] > 0) {
+                                ok = slot_ready(ik) && pf_wait(&q_full[s], qc[s] & 1, abort_flag);
+                                if (!ok) break;
+                                qk(s, s, ik, keys_of(nxt, s, 0), s == (nxt.n[1] > 0 ? 1 : 0));
+                                ++qc[s];
+                                if (nxt.n[s] == 1) umma_commit(&q_empty[s]);
+                            }
+                        }
+                    }
+                    base += 2 * n;
+                }
+            } else {
+                // Q K^T of key tile j + 1 goes out before P V of tile j
+                long long g = 0;  // key tiles so far: S buffer g & 1
+                for (long long k = 0; ok; ++k) {
+                    cur = nxt;
+                    if (cur.n[0] == 0) break;
+                    const int n = cur.n[0];
+                    auto scores = [&](int j, int buf) -> bool {
+                        const long long i0 = base + k_slot<D>(j);
+                        for (int c = 0; c < CPT; ++c)
+                            if (!slot_ready(i0 + c)) return false;
+                        qk(0, buf, i0, keys_of(cur, 0, j), true);
+                        if (j == n - 1) umma_commit(&q_empty[0]);
+                        return true;
+                    };
+                    ok = pf_wait(&q_full[0], qc[0] & 1, abort_flag);
+                    ++qc[0];
+                    if (ok) ok = scores(0, (int)(g & 1));
+                    for (int j = 0; j < n && ok; ++j, ++g) {
+                        const int buf = (int)(g & 1);
+                        if (j + 1 < n) ok = scores(j + 1, buf ^ 1);
+                        if (ok) ok = pf_wait(&p_full[buf], pc[buf] & 1, abort_flag, wlim);
+                        if (!ok) break;
+                        ++pc[buf];
+                        const long long iv = base + v_slot<D>(j, n);
+                        for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(iv + c);
+                        if (ok) pv(0, buf, iv, keys_of(cur, 0, j), j == 0, true);
+                    }
+                    base += 2 * n * CPT;
+                    if (ok) ok = get(k + 1, &nxt);
+                }
+            }
+            if (!ok) {
+                pf_error(p.err, DEV_ERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every MMA issued so far has finished before tensor memory is freed
+            umma_commit(drain);
+            volatile int never = 0;
+            pf_wait(drain, 0, &never);
+        }
+        __syncwarp();
+        named_bar_sync(kBarEndPf, C::THREADS);
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+        return;
+    }
+
+    // ============================================================== softmax
+    const int s = (warp - 2) >> 2;                 // query tile
+    const int q4 = warp & 3;                       // TMEM lane quarter this warp may access
+    const int row = q4 * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t o_t = lanes + C::O0 + s * D;
+    const int r_tok = row >> p.hpg_lg, r_head = row & (p.hpg - 1);
+    long long g = 0;      // key tiles so far
+    long long base = 0;   // ring slots of the units before this one
+    bool ok = true;
+
+    for (long long k = 0;; ++k) {
+        ok = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+        }
+        const Unit u = units[k % kDesc];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
+        if (u.n[0] == 0) break;
+        const int n = u.n[s], nmax = max(u.n[0], u.n[1]);
+        const int first_tok = u.t0 + s * p.tpt;
+        const int end_tok = min(first_tok + p.tpt, u.len);
+        const int tok = first_tok + r_tok;
+        const int tq = min(tok, u.len - 1);
+        float m = -INFINITY, l = 0.f;
+
+        for (int j = 0; j < n; ++j, ++g) {
+            const int buf = NQ == 2 ? s : (int)(g & 1);
+            const uint32_t par = (uint32_t)((NQ == 2 ? g : g >> 1) & 1);
+            ok = pf_wait(&s_full[buf], par, abort_flag, wlim);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t s_t = lanes + buf * 128;
+            float v[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, v + c * 32);
+            tmem_ld_wait();
+            const int kb = u.kbeg + j * kRows;
+            // keys [lo, hi) of this tile are the row's; only the tiles at the
+            // diagonal and at the window's edge hide any
+            if (kb + kRows > first_tok + 1 || kb < end_tok - p.window) {
+                const int hi = tq + 1 - kb, lo = tq + 1 - p.window - kb;
+#pragma unroll
+                for (int c = 0; c < 128; ++c) v[c] = (c < hi && c >= lo) ? v[c] : -INFINITY;
+            }
+            float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int c = 4; c < 128; c += 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], v[c + i]);
+            }
+            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            const bool grow = (mn - m) * p.sl > kTauPf;  // (both -inf: no)
+            if (__any_sync(0xffffffffu, grow)) {
+                const float alpha = (grow && m != -INFINITY) ? fast_exp2((m - mn) * p.sl) : 1.f;
+                if (grow) m = mn;
+                l *= alpha;
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // O holds the tiles up to j - 1
+                    const int pb = NQ == 2 ? s : buf ^ 1;
+                    const uint32_t pp = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
+                    ok = pf_wait(&pv_done[pb], pp, abort_flag, wlim);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        tmem_ld16(o_t + c * 16, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                        tmem_st16(o_t + c * 16, o);
+                    }
+                }
+            }
+            const float neg_m = m == -INFINITY ? 0.f : -m * p.sl;
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = fast_exp2(fmaf(v[c * 32 + 2 * i], p.sl, neg_m));
+                    const float p1 = fast_exp2(fmaf(v[c * 32 + 2 * i + 1], p.sl, neg_m));
+                    ls[(2 * i) & 3] += p0;
+                    ls[(2 * i + 1) & 3] += p1;
+                    pk[i] = bf16x2_of(p0, p1);
+                }
+                tmem_st16u(s_t + c * 16, pk);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            // rows past the sequence's end that the last 16 keys of P V would
+            // read belong to another sequence (or to none) and may hold
+            // anything, which a weight of zero does not hide: they are zeroed
+            const int keys = min(kRows, end_tok - kb);
+            const int stop = (keys + 15) / 16 * 16, past = u.len - kb;
+            if (past < stop) {
+                const long long iv = base + v_slot<D>(j, nmax);
+                for (int c = 0; c < CPT && ok; ++c) {
+                    const int slot = (int)((iv + c) % NS);
+                    ok = pf_wait(&slot_full[slot], (uint32_t)(((iv + c) / NS) & 1), abort_flag);
+                    if (ok)
+                        for (int i = row; i < (stop - past) * (C::KC / 64) * 8; i += 128) {
+                            const int r = past + (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
+                            *reinterpret_cast<uint4 *>(ring + slot * C::SLOT + sl * kSlab + r * 128 +
+                                                       (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                }
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                fence_proxy_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[buf]);
+        }
+        if (!ok) break;
+        if (n > 0) {
+            const int buf = NQ == 2 ? s : (int)((g - 1) & 1);
+            const uint32_t par = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
+            ok = pf_wait(&pv_done[buf], par, abort_flag, wlim);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float inv = 1.f / l;  // (every row attends itself)
+            uint16_t *dst = p.out + ((size_t)(u.row0 + tok) * p.Hq + u.h0 + r_head) * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tmem_ld32(o_t + c * 32, o);
+                tmem_ld_wait();
+                if (tok < end_tok) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4 *>(dst)[c * 4 + i] = make_uint4(
+                            bf16x2_of(o[8 * i] * inv, o[8 * i + 1] * inv),
+                            bf16x2_of(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                            bf16x2_of(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                            bf16x2_of(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+        }
+        base += 2 * nmax * CPT;
+    }
+    if (!ok) {
+        pf_error(p.err, DEV_ERR_TIMEOUT);
+        *abort_flag = 1;
+    }
+    tc_fence_before();
+    named_bar_sync(kBarEndPf, C::THREADS);
+}
+
+template <int D>
+cudaError_t launch_pf(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                      const PrefillParams &p, int num_ctas, cudaStream_t stream) {
+    static int done_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(dev >= 0 && dev < 64 && done_for_device[dev])) {
+        e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PfCfg<D>::alloc);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) done_for_device[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_ctas);
+    cfg.blockDim = dim3(PfCfg<D>::THREADS);
+    cfg.dynamicSmemBytes = PfCfg<D>::alloc;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_kernel<D>, tmq, tmk, tmv, p);
+}
+
+// 3-D map over packed rows [N, H, D] with `stride` elements from token to
+// token: dims (D, H, N), box (64, heads, tokens), 128-byte swizzle; tokens
+// past N read as zeros.
+int encode_rows_map(CUtensorMap *m, const void *base, int D, int H, int N, long long stride, int heads,
+                    int tokens) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)N};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+    return api_encode_bf16_3d(m, base, dims, strides, box);
+}
+
+}  // namespace
+
+}  // namespace kvattn
+
+using namespace kvattn;
+
+extern "C" int gqa_prefill_attn(const void *q, const void *k, const void *v,
+                                const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv,
+                                int D, long long q_stride, long long k_stride, long long v_stride,
+                                float scale, int window, kvattn_stream_t stream) {
+    const char *who = "gqa_prefill_attn";
+    api_begin();
+    if (!q || !k || !v || !cu_seqlens || !out) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+          reinterpret_cast<uintptr_t>(out)) & 15u) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+        return api_failf(KVATTN_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+    if (!std::isfinite(scale)) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: scale must be finite", who);
+    if (window < 1) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: window must be >= 1 (got %d)", who, window);
+    int rc = api_check_sizes(B, Hq, Hkv, D, 1);
+    if (rc) return rc;
+    if (N < 1) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: N must be positive (got %d)", who, N);
+    if (N > (1 << 28)) return api_failf(KVATTN_ERR_UNSUPPORTED, "%s: N = %d rows beyond 2^28", who, N);
+    if ((rc = api_check_row_stride(q_stride, Hq, D, who)) || (rc = api_check_row_stride(k_stride, Hkv, D, who)) ||
+        (rc = api_check_row_stride(v_stride, Hkv, D, who)))
+        return rc;
+    int num_sms;
+    PrefillParams p = {};
+    if ((rc = api_device(&num_sms, &p.err, &p.wait_limit))) return rc;
+
+    p.cu = cu_seqlens;
+    p.out = static_cast<uint16_t *>(out);
+    p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.hpg = 1;
+    while (p.hpg < kRows && p.G % (2 * p.hpg) == 0) p.hpg *= 2, ++p.hpg_lg;
+    p.tpt = kRows / p.hpg;
+    p.passes = p.G / p.hpg;
+    p.window = window < N ? window : N;
+    const float sl = (float)(std::fabs((double)scale) * 1.4426950408889634);
+    p.sl = std::isfinite(sl) ? std::fmax(sl, FLT_MIN) : FLT_MAX;  // (masked scores stay -inf at scale 0)
+    p.neg = scale < 0.f;
+    CUtensorMap tmq, tmk, tmv;
+    if ((rc = encode_rows_map(&tmq, q, D, Hq, N, q_stride, p.hpg, p.tpt)) ||
+        (rc = encode_rows_map(&tmk, k, D, Hkv, N, k_stride, 1, kRows)) ||
+        (rc = encode_rows_map(&tmv, v, D, Hkv, N, v_stride, 1, kRows)))
+        return rc;
+    // at most one unit per NQ tiles of tokens and one more per sequence
+    const int tpu = (D == 256 ? 1 : 2) * p.tpt;
+    const long long most = ((long long)N / tpu + B) * Hkv * p.passes;
+    const int ctas = (int)(most < num_sms ? most : num_sms);
+    cudaError_t e;
+    switch (D) {
+        case 64: e = launch_pf<64>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
+        case 128: e = launch_pf<128>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
+        default: e = launch_pf<256>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
+    }
+    if (e != cudaSuccess) return api_cuda_fail(e, "prefill kernel launch");
+    return KVATTN_OK;
+}

@@ -405,6 +405,170 @@ KVATTN_API int gqa_decode_step_fp8(const void *q, const void *k_new, const void 
                                    int D, int Lmax, float scale, kvattn_stream_t stream);
 
 /*
+ * Prompts into a paged cache.  A serving step takes its requests' new tokens
+ * packed one request after the other -- whole prompts and single tokens
+ * alike, request b's rows at [cu_seqlens[b], cu_seqlens[b+1]) -- and
+ * kv_block_tables gives them blocks and slots, kv_append_slots (bf16 pool)
+ * or kv_append_paged_fp8 (8-bit pool) writes their K/V rows, and
+ * gqa_prefill_attn computes the prompts' own attention ("The Basics of
+ * Transformer Inference", prefill and generation; "Machine Learning
+ * Engineering and AI Systems at Scale", section "The key and value cache",
+ * on PagedAttention).  None of the five calls below allocates or keeps
+ * device memory, so a captured graph holds nothing of the library's and may
+ * replay beside any other.  Packed rows k_new, v_new (and q, k, v) may be
+ * slices of wider rows, as of one fused projection: *_stride counts the
+ * elements from one token's [H, D] row to the next, a multiple of 8, at
+ * least H * D.  The calls run on the current device; every pointer belongs
+ * to it.
+ */
+
+/*
+ * kv_block_tables -- blocks and slots for each request's new tokens.
+ *
+ *   cached_lens : int32 [B], tokens request b has cached (c_b)
+ *   new_lens    : int32 [B], tokens it adds now (n_b; 0: none)
+ *   block_table : int32 [B, max_blocks], updated in place: entries
+ *                 [0, ceil(c_b / block_size)) are the blocks it has,
+ *                 the next ones, up to ceil((c_b + n_b) / block_size), are
+ *                 taken from the free list; all others stay as they are
+ *   free_blocks : int32 [num_free], a stack of free block ids of which the
+ *                 first free_count[0] are left; ids are taken from its top
+ *                 (entry free_count[0] - 1 first) in request order
+ *   free_count, free_count_out : int32 [1], ids left before and after; the
+ *                 two may be the same word
+ *   cu_seqlens  : int32 [B + 1], written: cu_seqlens[b] = sum of n before b
+ *   slots       : int64 [num_slots], written in full: token i of request b,
+ *                 at packed row cu_seqlens[b] + i, gets slot
+ *                 block_table[b, p / block_size] * block_size + p % block_size
+ *                 with p = c_b + i; rows behind the last token get -1
+ *   block_size  : a power of two in [16, 2^20]
+ *
+ * A request whose lengths are negative or do not fit max_blocks blocks sets
+ * KVATTN_ERR_DEVICE_BOUNDS, takes no block and its rows get slot -1 (a
+ * negative n counts as 0).  When the free list runs out, the first request
+ * that it cannot serve whole and every later one that needs a block take
+ * none: the entries they lack become -1, their rows get slot -1, and the
+ * error word is set.  So it is when free_count[0] is outside [0, num_free]
+ * (taken as 0) or num_slots is less than the sum of n (the rows past it have
+ * no slot; cu_seqlens is capped at 2^31 - 1).
+ * Limits: B <= 65535, max_blocks * block_size <= 2^24, num_slots <= 2^28.
+ */
+KVATTN_API int kv_block_tables(const int32_t *cached_lens, const int32_t *new_lens,
+                               int32_t *block_table, const int32_t *free_blocks,
+                               const int32_t *free_count, int32_t *free_count_out,
+                               int32_t *cu_seqlens, int64_t *slots, int B, int max_blocks,
+                               int block_size, int num_free, int num_slots,
+                               kvattn_stream_t stream);
+
+/*
+ * kv_append_slots -- write packed K/V rows to the pool rows that a slot map
+ * names: row i goes to position slots[i] % block_size of block
+ * slots[i] / block_size.
+ *
+ *   k_pool, v_pool : bf16 [num_blocks, Hkv, block_size, D], in place
+ *   k_new, v_new   : bf16, N rows [Hkv, D]
+ *   slots          : int64 [N] (8-byte aligned); a negative slot skips its row
+ * Bit-exact; rows no slot names stay as they are.  A slot at or past
+ * num_blocks * block_size skips its row and sets KVATTN_ERR_DEVICE_BOUNDS.
+ * Slots must differ: of two rows with one slot either may land, in pieces of
+ * 16 bytes.  D in {64, 128, 256}; N <= 2^28.
+ */
+KVATTN_API int kv_append_slots(void *k_pool, void *v_pool, const void *k_new, const void *v_new,
+                               const int64_t *slots, int N, int Hkv, int D, long long k_stride,
+                               long long v_stride, int num_blocks, int block_size,
+                               kvattn_stream_t stream);
+
+/*
+ * gqa_prefill_attn -- causal attention of whole prompts, packed.
+ *
+ * For every sequence b, token i of its n_b = cu_seqlens[b+1] - cu_seqlens[b]
+ * and query head h (kvh = h / (Hq / Hkv)):
+ *     out[i,h,:] = softmax_j(scale * q[i,h,:] . k[j,kvh,:]) . v[j,kvh,:]
+ * over max(0, i - window + 1) <= j <= i of its own sequence.
+ *
+ *   q          : bf16, N rows [Hq, D]; k, v: bf16, N rows [Hkv, D]
+ *   cu_seqlens : int32 [B + 1] (device), non-decreasing, within [0, N]
+ *   out        : bf16 [N, Hq, D], contiguous; rows of no sequence (behind the
+ *                last one, or between two) stay as they are
+ *   scale      : finite; window >= 1 (>= N: the whole prompt)
+ *
+ * Scores, maxima and sums are held in fp32; the weights enter the second
+ * product as bf16, unnormalised, and the result is rounded once more.  A
+ * sequence's own q, k and v rows must hold finite values; all other rows may
+ * hold anything.  A sequence whose bounds are not
+ * 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <= N is skipped and sets
+ * KVATTN_ERR_DEVICE_BOUNDS; of sequences that overlap either may have
+ * written the shared rows.  The single-token form is gqa_decode_attn
+ * (gqa_decode_attn_paged).  D in {64, 128, 256}; N <= 2^28.
+ */
+KVATTN_API int gqa_prefill_attn(const void *q, const void *k, const void *v,
+                                const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv,
+                                int D, long long q_stride, long long k_stride, long long v_stride,
+                                float scale, int window, kvattn_stream_t stream);
+
+/*
+ * A paged 8-bit cache with one scale per block and K/V head ("The Basics of
+ * Transformer Inference", item "Quantization"; "Machine Learning Engineering
+ * and AI Systems at Scale", section "Quantization").  The pages give no
+ * rule; this library's:
+ *     row_d = E4M3(code_d) * scale[block, kvh]
+ *     scale = the smallest power of two, 2^-100 at least, with
+ *             absmax <= 448 * scale over the block's rows of that head
+ *     code_d = E4M3(row_d / scale)      nearest, ties to even
+ * The rows of a block are written over many steps, so a scale can only be
+ * final once its block is full: a row that needs a larger one raises it, and
+ * the codes already there are rewritten for it (E4M3(code value * old / new),
+ * exact but for results below 2^-6, whose last bits are rounded away: the
+ * scales are powers of two for this).  Rows must be finite.
+ *
+ *   codes  : uint8 [num_blocks, Hkv, block_size, D] (K and V separately)
+ *   scales : fp32  [num_blocks, Hkv]                (K and V separately)
+ *   block_size: a power of two in [16, 1024]; otherwise as the paged cache above
+ */
+
+/*
+ * kv_append_paged_fp8 -- quantize packed K/V rows into a paged 8-bit cache:
+ * token i of request b goes to position cached_lens[b] + i of its block
+ * table row.
+ *
+ *   k_new, v_new : bf16, N rows [Hkv, D]
+ *   block_table  : int32 [B, max_blocks]; cached_lens: int32 [B], tokens
+ *                  cached before (not modified); cu_seqlens: int32 [B + 1]
+ * A block's scale counts its first min(cached_lens[b] - start, block_size)
+ * rows and the new ones: a block that starts empty forgets what it held.
+ * Rows past the new ones keep their codes.  Blocks written by one call must
+ * belong to one request each.  A request with negative lengths, rows outside
+ * [0, N) or positions outside its table row is skipped, a table entry outside
+ * [0, num_blocks) skips its block; both set KVATTN_ERR_DEVICE_BOUNDS.
+ * Deterministic, codes and scales exact by the rule above.
+ * D in {64, 128, 256}; N <= 2^28.
+ */
+KVATTN_API int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                                   const void *k_new, const void *v_new,
+                                   const int32_t *block_table, const int32_t *cached_lens,
+                                   const int32_t *cu_seqlens, int B, int N, int Hkv, int D,
+                                   long long k_stride, long long v_stride, int num_blocks,
+                                   int block_size, int max_blocks, kvattn_stream_t stream);
+
+/*
+ * gqa_decode_attn_paged_fp8 -- gqa_decode_attn over a paged 8-bit cache.
+ *
+ *   q   : bf16 [B, Hq, D]; seq_lens: int32 [B] (device), positions attended,
+ *         0 <= seq_lens[b] <= max_blocks * block_size
+ *   out : bf16 [B, Hq, D] (the 8-bit products carry the weights' 11
+ *         significant bits, bf16 has 8)
+ * Scales may be any finite values >= 0.  Pool rows at and past a length are
+ * never read; table entries, lengths, workspaces and device-side errors are
+ * those of gqa_decode_attn_paged.  D = 128 or 256.
+ */
+KVATTN_API int gqa_decode_attn_paged_fp8(const void *q, const void *k_codes, const void *v_codes,
+                                         const float *k_scale, const float *v_scale,
+                                         const int32_t *block_table, const int32_t *seq_lens,
+                                         void *out, int B, int Hq, int Hkv, int D, int num_blocks,
+                                         int block_size, int max_blocks, float scale,
+                                         kvattn_stream_t stream);
+
+/*
  * gqa_decode_attn_noalloc -- the same computation as gqa_decode_attn, for
  * callers that must not have the library allocate device memory (for
  * example a server that gives all free GPU memory to its own pool at
