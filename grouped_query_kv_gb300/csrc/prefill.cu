@@ -26,8 +26,8 @@
 // query tile per CTA with two S buffers: Q K^T of the next key tile runs
 // during the softmax of this one.
 //
-// Warps: 0 walks the work list and issues the copies (TMA), 1 issues the
-// MMAs, then one softmax warpgroup per query tile.
+// Warps: 0 walks the work list and issues the copies (TMA), 1 and 2 issue the
+// MMAs, then (from 4) one softmax warpgroup per query tile.
 //
 // Work list.  A unit is (sequence, block of NQ x 128 / hpg tokens, K/V head,
 // head group); its cost grows with its block's index.  Every CTA of the
@@ -92,11 +92,15 @@ struct PfCfg {
     static constexpr int FIXED = NQ * QT + 1024 + 4096;
     static constexpr int NS_FIT = (kSmemMax - FIXED) / SLOT;
     static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;  // ring slots
-    static constexpr int THREADS = 64 + 128 * NQ;
+    // the copy and MMA warps are a warpgroup of their own (one of its warps
+    // idle); with two query tiles it hands registers to the softmax warpgroups
+    static constexpr int SOFT0 = 4;                     // first softmax warp
+    static constexpr int THREADS = 32 * SOFT0 + 128 * NQ;
+    static constexpr int REGS_SERVICE = 88, REGS_SOFT = 208;
     static constexpr int off_q = 0;
     static constexpr int off_ring = NQ * QT;
     static constexpr int off_bar = off_ring + NS * SLOT;
-    static constexpr int nbar = 2 * NS + 2 * 2 + 3 * 2 + 2 * kDesc + 1;
+    static constexpr int nbar = 2 * NS + 2 * 2 + 3 * 2 + 2 * kDesc + 1 + 2;
     static constexpr int off_misc = off_bar + nbar * 8;          // tmem base, abort flag
     static constexpr int off_unit = (off_misc + 32 + 15) / 16 * 16;
     static constexpr int off_cnt = off_unit + kDesc * (int)sizeof(Unit);
@@ -112,10 +116,13 @@ struct PfCfg {
 
 __device__ __forceinline__ void pf_error(unsigned int *err, unsigned int code) { atomicCAS(err, 0u, code); }
 
+// Bounded wait that also gives up once another role has.  A poll sleeps until
+// the phase ends or a hardware limit passes; under the shortened limit of the
+// failure tests it does not, so that few polls are sure to give up.
 __device__ __forceinline__ bool pf_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                         uint32_t limit = KVATTN_SPIN_LIMIT) {
     for (uint32_t it = 0; it < limit; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((it & 255u) == 255u && *abort_flag) return false;
     }
     *abort_flag = 1;
@@ -167,6 +174,49 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Pairs of binary32 values in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
+    return r != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Length of sequence b (0 where its bounds are not 0 <= cu[b] <= cu[b+1] <= N).
 __device__ __forceinline__ int pf_len(const PrefillParams &p, int b, int *row0) {
     const int a = p.cu[b], e = p.cu[b + 1];
@@ -208,6 +258,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     // s_full, p_full, pv_done: of query tile s (two tiles) or of S buffer s (one)
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2;
     uint64_t *u_full = pv_done + 2, *u_empty = u_full + kDesc, *drain = u_empty + kDesc;
+    uint64_t *turn = drain + 1;  // the MMA warps' turns
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::off_misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::off_misc + 16);
     Unit *units = reinterpret_cast<Unit *>(smem + C::off_unit);
@@ -222,7 +273,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&slot_full[s], 1);
-            mbar_init(&slot_empty[s], 1);
+            mbar_init(&slot_empty[s], NQ);  // K and V tiles serve every query tile
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1);
@@ -230,12 +281,13 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 4);
             mbar_init(&pv_done[s], 1);
+            mbar_init(&turn[s], 1);
         }
         for (int s = 0; s < kDesc; ++s) {
             mbar_init(&u_full[s], 1);
-            mbar_init(&u_empty[s], 1 + 4 * NQ);  // the MMA thread and the softmax warps
+            mbar_init(&u_empty[s], 2 + 4 * NQ);  // the MMA and the softmax warps
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, 2);  // both MMA warps
         *abort_flag = 0;
         *sum_pairs = 0;
         *max_nb = 0;
@@ -296,6 +348,10 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     }
 
     const uint32_t ring_s = smem_u32(ring), qbuf_s = smem_u32(qbuf);
+
+    const uint32_t wlim = p.wait_limit ? p.wait_limit : KVATTN_SPIN_LIMIT;
+    if (warp < C::SOFT0) {
+    if constexpr (NQ == 2) regs_dec<C::REGS_SERVICE>();
 
     // ============================================================ work list, TMA
     if (warp == 0) {
@@ -452,174 +508,184 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         return;
     }
 
-    const uint32_t wlim = p.wait_limit ? p.wait_limit : KVATTN_SPIN_LIMIT;
-
     // ================================================================== MMA
-    if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, C::KC, false, true);
-            // bit 13: A enters negated (a negative scale)
-            const uint32_t idesc_qk = IDESC_QK | (p.neg ? 1u << 13 : 0u);
-            bool ok = true;
-            uint32_t qc[2] = {0, 0};      // query tiles consumed
-            uint32_t pc[2] = {0, 0};      // probability tiles consumed, by tile / S buffer
-            long long base = 0;           // ring slots of the units before this one
+    // Two warps issue, so that one's waits do not drain the tensor pipe: with
+    // two query tiles a warp per tile (P V of key tile j - 1, then Q K^T of
+    // j), with one a warp for Q K^T and one for P V.
+    if (warp <= 2) {
+        constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, C::KC, false, true);
+        // bit 13: A enters negated (a negative scale)
+        const uint32_t idesc_qk = (IDESC_QK | (p.neg ? 1u << 13 : 0u)) & ~(0x3fu << 17);
+        const int s = NQ == 2 ? warp - 1 : 0;  // query tile
+        bool ok = true;
+        uint32_t units_q = 0;         // query tiles consumed
+        long long g = 0;              // key tiles so far
+        long long base = 0;           // ring slots of the units before this one
+        uint32_t it = 0;              // turns taken (two query tiles)
 
-            auto slot_ready = [&](long long i) {
-                return pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), abort_flag);
-            };
-            // S[buf] = Q_s K_j^T; keys past the tile's last are left out, 16 at a time
-            auto qk = [&](int s, int buf, long long i0, int keys, bool last_use) {
-                tc_fence_after();
-                const uint32_t idesc = (idesc_qk & ~(0x3fu << 17)) | ((uint32_t)((keys + 15) / 16 * 2) << 17);
+        // The two query tiles' MMAs go out in turns, the products of one key
+        // tile together: the tiles then keep half a period apart, each in its
+        // softmax while the other's products run (left to share the tensor
+        // cores, both finish together and both wait for both: 8192 tokens, 64
+        // heads over 8 of 128, took 1009 us against ... with turns).
+        auto take_turn = [&]() {
+            return s == 0 ? it == 0 || pf_wait(&turn[0], (it - 1) & 1, abort_flag)
+                          : pf_wait(&turn[1], it & 1, abort_flag);
+        };
+        auto slot_ready = [&](long long i) {
+            return pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), abort_flag);
+        };
+        // S[buf] = Q_s K_j^T; keys past the tile's last are left out, 16 at a time
+        auto qk = [&](int buf, long long i0, int keys, bool last) {
+            const uint32_t idesc = idesc_qk | ((uint32_t)((keys + 15) / 16 * 2) << 17);
+            const uint32_t d = tmem + buf * 128;
+            if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < CPT; ++c) {
                     const int slot = (int)((i0 + c) % NS);
-                    const uint32_t kb = ring_s + slot * C::SLOT;
-                    const uint32_t qb = qbuf_s + s * C::QT + c * (C::KC / 64) * kSlab;
+                    const uint64_t kd = smem_desc(ring_s + slot * C::SLOT, 16, 1024, 2);
+                    const uint64_t qd = smem_desc(qbuf_s + s * C::QT + c * (C::KC / 64) * kSlab, 16, 1024, 2);
 #pragma unroll
                     for (int kk = 0; kk < C::KC / 16; ++kk) {
-                        const uint32_t o = (kk >> 2) * kSlab + (kk & 3) * 32;
-                        umma_bf16(tmem + buf * 128, smem_desc(qb + o, 16, 1024, 2),
-                                  smem_desc(kb + o, 16, 1024, 2), idesc, c != 0 || kk != 0);
+                        const uint64_t o = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
+                        umma_bf16(d, qd + o, kd + o, idesc, c != 0 || kk != 0);
                     }
-                    if (last_use) umma_commit(&slot_empty[slot]);
+                    umma_commit(&slot_empty[slot]);
                 }
                 umma_commit(&s_full[buf]);
-            };
-            // O_s (+)= P[buf] V_j
-            auto pv = [&](int s, int buf, long long i0, int keys, bool first, bool last_use) {
-                tc_fence_after();
+                if (last) umma_commit(&q_empty[s]);
+            }
+            __syncwarp();
+        };
+        // O_s (+)= P[buf] V_j
+        auto pv = [&](int buf, long long i0, int keys, bool first) {
+            const uint32_t a = tmem + buf * 128, d = tmem + C::O0 + s * D;
+            if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < CPT; ++c) {
                     const int slot = (int)((i0 + c) % NS);
-                    const uint32_t vb = ring_s + slot * C::SLOT;
+                    const uint64_t vd = smem_desc(ring_s + slot * C::SLOT, kSlab, 1024, 2);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         if (kk * 16 < keys)
-                            umma_bf16_ts(tmem + C::O0 + s * D + c * C::KC, tmem + buf * 128 + kk * 8,
-                                         smem_desc(vb + kk * 2048, kSlab, 1024, 2), IDESC_PV,
+                            umma_bf16_ts(d + c * C::KC, a + kk * 8, vd + kk * (2048 >> 4), IDESC_PV,
                                          !(first && kk == 0));
                     }
-                    if (last_use) umma_commit(&slot_empty[slot]);
+                    umma_commit(&slot_empty[slot]);
                 }
                 umma_commit(&pv_done[buf]);
-            };
-            // keys of key tile j that query tile s attends at most (from the tile's start)
-            auto keys_of = [&](const Unit &u, int s, int j) {
-                const int e = min(u.t0 + (s + 1) * p.tpt, u.len);
-                return min(kRows, e - u.kbeg - j * kRows);
-            };
-            auto get = [&](long long k, Unit *u) {
-                if (!pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag)) return false;
-                *u = units[k % kDesc];
-                mbar_arrive(&u_empty[k % kDesc]);
-                return true;
-            };
+            }
+            __syncwarp();
+        };
 
-            Unit cur, nxt;
-            ok = get(0, &nxt);
+        for (long long k = 0; ok; ++k) {
+            ok = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            const Unit u = units[k % kDesc];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
+            if (u.n[0] == 0) break;
+            const int n = u.n[s], nmax = max(u.n[0], u.n[1]);
+            // keys of key tile j that the query tile attends at most
+            const int end = min(u.t0 + (s + 1) * p.tpt, u.len) - u.kbeg;
             if (NQ == 2) {
-                // step (unit, j): for each tile, P V of j, then Q K^T of the next step
-                bool fresh = true;  // the first unit's Q K^T of step 0 is not issued yet
-                for (long long k = 0; ok; ++k) {
-                    cur = nxt;
-                    if (cur.n[0] == 0) break;
-                    const int n = max(cur.n[0], cur.n[1]);
-                    if (fresh) {
-                        fresh = false;
-                        for (int s = 0; s < 2 && ok; ++s) {
-                            if (cur.n[s] == 0) continue;
-                            ok = slot_ready(base) && pf_wait(&q_full[s], qc[s] & 1, abort_flag);
-                            if (!ok) break;
-                            qk(s, s, base, keys_of(cur, s, 0), s == (cur.n[1] > 0 ? 1 : 0));
-                            ++qc[s];
-                            if (cur.n[s] == 1) umma_commit(&q_empty[s]);
+                for (int j = 0; j <= nmax; ++j, ++it) {
+                    const long long iv = base + 2 * j - 1, ik = base + 2 * j;
+                    if (j > n || n == 0) {
+                        // key tiles of the other query tile alone
+                        if (j > 0) ok = slot_ready(iv);
+                        if (ok && j < nmax) ok = slot_ready(ik);
+                        if (ok) ok = take_turn();
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
                         }
-                    }
-                    for (int j = 0; j < n && ok; ++j) {
-                        const bool last = j == n - 1;
-                        if (last && !(ok = get(k + 1, &nxt))) break;
-                        const long long iv = base + 2 * j + 1, ik = base + 2 * j + 2;
-                        ok = slot_ready(iv);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            if (!ok) break;
-                            if (j < cur.n[s]) {
-                                ok = pf_wait(&p_full[s], pc[s] & 1, abort_flag, wlim);
-                                if (!ok) break;
-                                ++pc[s];
-                                pv(s, s, iv, keys_of(cur, s, j), j == 0, s == (j < cur.n[1] ? 1 : 0));
-                            }
-                            if (!last) {
-                                if (j + 1 < cur.n[s]) {
-                                    ok = slot_ready(ik);
-                                    if (!ok) break;
-                                    qk(s, s, ik, keys_of(cur, s, j + 1), s == (j + 1 < cur.n[1] ? 1 : 0));
-                                    if (j + 1 == cur.n[s] - 1) umma_commit(&q_empty[s]);
-                                }
-                            } else if (nxt.n[0] > 0 && nxt.n[s] > 0) {
-                                ok = slot_ready(ik) && pf_wait(&q_full[s], qc[s] & 1, abort_flag);
-                                if (!ok) break;
-                                qk(s, s, ik, keys_of(nxt, s, 0), s == (nxt.n[1] > 0 ? 1 : 0));
-                                ++qc[s];
-                                if (nxt.n[s] == 1) umma_commit(&q_empty[s]);
-                            }
+                        if (lane == 0) {
+                            if (j > 0) mbar_arrive(&slot_empty[iv % NS]);
+                            if (j < nmax) mbar_arrive(&slot_empty[ik % NS]);
+                            mbar_arrive(&turn[s ^ 1]);
                         }
+                        continue;
                     }
-                    base += 2 * n;
+                    if (j == 0) ok = pf_wait(&q_full[s], units_q++ & 1, abort_flag);
+                    if (ok && j > 0) ok = pf_wait(&p_full[s], (uint32_t)((g - 1) & 1), abort_flag, wlim) && slot_ready(iv);
+                    if (ok && j < nmax) ok = slot_ready(ik);
+                    if (ok) ok = take_turn();
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (j > 0) pv(s, iv, min(kRows, end - (j - 1) * kRows), j == 1);
+                    if (j < n) {
+                        qk(s, ik, min(kRows, end - j * kRows), j == n - 1);
+                        ++g;
+                    } else if (j < nmax && lane == 0) {
+                        mbar_arrive(&slot_empty[ik % NS]);
+                    }
+                    if (lane == 0) mbar_arrive(&turn[s ^ 1]);
+                }
+            } else if (warp == 1) {
+                ok = pf_wait(&q_full[0], units_q++ & 1, abort_flag);
+                for (int j = 0; j < n && ok; ++j, ++g) {
+                    const int buf = (int)(g & 1);
+                    const long long ik = base + k_slot<D>(j);
+                    for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(ik + c);
+                    // S[buf] still holds the P of two tiles ago
+                    if (ok && g >= 2) ok = pf_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    qk(buf, ik, min(kRows, end - j * kRows), j == n - 1);
                 }
             } else {
-                // Q K^T of key tile j + 1 goes out before P V of tile j
-                long long g = 0;  // key tiles so far: S buffer g & 1
-                for (long long k = 0; ok; ++k) {
-                    cur = nxt;
-                    if (cur.n[0] == 0) break;
-                    const int n = cur.n[0];
-                    auto scores = [&](int j, int buf) -> bool {
-                        const long long i0 = base + k_slot<D>(j);
-                        for (int c = 0; c < CPT; ++c)
-                            if (!slot_ready(i0 + c)) return false;
-                        qk(0, buf, i0, keys_of(cur, 0, j), true);
-                        if (j == n - 1) umma_commit(&q_empty[0]);
-                        return true;
-                    };
-                    ok = pf_wait(&q_full[0], qc[0] & 1, abort_flag);
-                    ++qc[0];
-                    if (ok) ok = scores(0, (int)(g & 1));
-                    for (int j = 0; j < n && ok; ++j, ++g) {
-                        const int buf = (int)(g & 1);
-                        if (j + 1 < n) ok = scores(j + 1, buf ^ 1);
-                        if (ok) ok = pf_wait(&p_full[buf], pc[buf] & 1, abort_flag, wlim);
-                        if (!ok) break;
-                        ++pc[buf];
-                        const long long iv = base + v_slot<D>(j, n);
-                        for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(iv + c);
-                        if (ok) pv(0, buf, iv, keys_of(cur, 0, j), j == 0, true);
+                for (int j = 0; j < n && ok; ++j, ++g) {
+                    const int buf = (int)(g & 1);
+                    const long long iv = base + v_slot<D>(j, n);
+                    ok = pf_wait(&p_full[buf], (uint32_t)((g >> 1) & 1), abort_flag, wlim);
+                    for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(iv + c);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
                     }
-                    base += 2 * n * CPT;
-                    if (ok) ok = get(k + 1, &nxt);
+                    tc_fence_after();
+                    pv(buf, iv, min(kRows, end - j * kRows), j == 0);
                 }
             }
-            if (!ok) {
-                pf_error(p.err, DEV_ERR_TIMEOUT);
-                *abort_flag = 1;
-            }
-            // every MMA issued so far has finished before tensor memory is freed
-            umma_commit(drain);
-            volatile int never = 0;
-            pf_wait(drain, 0, &never);
+            ok = __all_sync(0xffffffffu, ok);
+            base += 2 * nmax * CPT;
         }
+        if (!ok) {
+            pf_error(p.err, DEV_ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        // every MMA issued so far has finished before tensor memory is freed
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        volatile int never = 0;
+        pf_wait(drain, 0, &never);
         __syncwarp();
         named_bar_sync(kBarEndPf, C::THREADS);
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc(tmem, 512);
+        }
         return;
     }
 
+    named_bar_sync(kBarEndPf, C::THREADS);  // the warpgroup's idle warp
+    return;
+    }
+
     // ============================================================== softmax
-    const int s = (warp - 2) >> 2;                 // query tile
+    if constexpr (NQ == 2) regs_inc<C::REGS_SOFT>();
+    const int s = (warp - C::SOFT0) >> 2;          // query tile
     const int q4 = warp & 3;                       // TMEM lane quarter this warp may access
     const int row = q4 * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
@@ -668,13 +734,17 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 128; ++c) v[c] = (c < hi && c >= lo) ? v[c] : -INFINITY;
             }
-            float mx[4] = {v[0], v[1], v[2], v[3]};
+            float mx[8];
 #pragma unroll
-            for (int c = 4; c < 128; c += 4) {
+            for (int i = 0; i < 8; ++i) mx[i] = max3(v[i], v[8 + i], v[16 + i]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], v[c + i]);
+            for (int c = 24; c < 120; c += 16) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], v[c + i], v[c + 8 + i]);
             }
-            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], v[120 + i]);
+            const float mn = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), max3(mx[6], mx[7], m));
             const bool grow = (mn - m) * p.sl > kTauPf;  // (both -inf: no)
             if (__any_sync(0xffffffffu, grow)) {
                 const float alpha = (grow && m != -INFINITY) ? fast_exp2((m - mn) * p.sl) : 1.f;
@@ -702,21 +772,22 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 }
             }
             const float neg_m = m == -INFINITY ? 0.f : -m * p.sl;
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(neg_m, neg_m);
+            float2 ls[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p0 = fast_exp2(fmaf(v[c * 32 + 2 * i], p.sl, neg_m));
-                    const float p1 = fast_exp2(fmaf(v[c * 32 + 2 * i + 1], p.sl, neg_m));
-                    ls[(2 * i) & 3] += p0;
-                    ls[(2 * i + 1) & 3] += p1;
-                    pk[i] = bf16x2_of(p0, p1);
+                    const float2 x = fma2(make_float2(v[c * 32 + 2 * i], v[c * 32 + 2 * i + 1]), sl2, nm2);
+                    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    ls[i & 1] = add2(ls[i & 1], e);
+                    pk[i] = bf16x2_of(e.x, e.y);
                 }
                 tmem_st16u(s_t + c * 16, pk);
             }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            ls[0] = add2(ls[0], ls[1]);
+            l = ls[0].x + ls[0].y;
             // rows past the sequence's end that the last 16 keys of P V would
             // read belong to another sequence (or to none) and may hold
             // anything, which a weight of zero does not hide: they are zeroed
