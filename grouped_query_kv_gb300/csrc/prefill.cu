@@ -26,8 +26,8 @@
 // query tile per CTA with two S buffers: Q K^T of the next key tile runs
 // during the softmax of this one.
 //
-// Warps: 0 walks the work list and issues the copies (TMA), 1 and 2 issue the
-// MMAs, then (from 4) one softmax warpgroup per query tile.
+// Warps: 0 issues the copies (TMA), 1 and 2 the MMAs, 3 walks the work list,
+// then one softmax warpgroup per query tile.
 //
 // Work list.  A unit is (sequence, block of NQ x 128 / hpg tokens, K/V head,
 // head group); its cost grows with its block's index.  Every CTA of the
@@ -92,8 +92,8 @@ struct PfCfg {
     static constexpr int FIXED = NQ * QT + 1024 + 4096;
     static constexpr int NS_FIT = (kSmemMax - FIXED) / SLOT;
     static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;  // ring slots
-    // the copy and MMA warps are a warpgroup of their own (one of its warps
-    // idle); with two query tiles it hands registers to the softmax warpgroups
+    // the first four warps are a warpgroup of their own; with two query tiles
+    // it hands registers to the softmax warpgroups
     static constexpr int SOFT0 = 4;                     // first softmax warp
     static constexpr int THREADS = 32 * SOFT0 + 128 * NQ;
     static constexpr int REGS_SERVICE = 88, REGS_SOFT = 208;
@@ -199,6 +199,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// 32 bytes, a whole sector, from one thread (dst 32-byte aligned).
+__device__ __forceinline__ void st_global_32b(uint16_t *dst, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         }
         for (int s = 0; s < kDesc; ++s) {
             mbar_init(&u_full[s], 1);
-            mbar_init(&u_empty[s], 2 + 4 * NQ);  // the MMA and the softmax warps
+            mbar_init(&u_empty[s], 3 + 4 * NQ);  // the copy, MMA and softmax warps
         }
         mbar_init(drain, 2);  // both MMA warps
         *abort_flag = 0;
@@ -353,11 +360,9 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     if (warp < C::SOFT0) {
     if constexpr (NQ == 2) regs_dec<C::REGS_SERVICE>();
 
-    // ============================================================ work list, TMA
-    if (warp == 0) {
+    // ============================================================ work list
+    if (warp == 3) {
         bool ok = true;
-        long long nslot = 0;         // ring slots issued
-        uint32_t qn[2] = {0, 0};     // query tiles issued
         // the walk: bucket kb holds pairs [pb0, pb0 + its count), `cover` sequences reach past it
         int kb = nbk;
         long long pb0 = 0, pbn = 0;
@@ -435,6 +440,26 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             }
             return __shfl_sync(0xffffffffu, w, 0);
         };
+        Unit u = {};
+        for (long long k = 0; ok; ++k) {
+            find(k, &u);
+            ok = publish(k, u);
+            if (u.n[0] == 0) break;
+        }
+        if (!ok && lane == 0) {
+            pf_error(p.err, DEV_ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+        named_bar_sync(kBarEndPf, C::THREADS);
+        return;
+    }
+
+    // ================================================================== TMA
+    if (warp == 0) {
+        bool ok = true;
+        long long nslot = 0;         // ring slots issued
+        uint32_t qn[2] = {0, 0};     // query tiles issued
         auto issue = [&](const void *tm, int c, int head, int row) -> bool {
             const int slot = (int)(nslot % NS);
             bool w = true;
@@ -449,15 +474,17 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             ++nslot;
             return true;
         };
-        Unit cur, nxt;
-        find(0, &nxt);
-        ok = publish(0, nxt);
-        for (long long k = 0; ok; ++k) {
-            cur = nxt;
+        for (long long k = 0;; ++k) {
+            ok = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            const Unit cur = units[k % kDesc];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
             if (cur.n[0] == 0) break;
-            find(k + 1, &nxt);
-            ok = publish(k + 1, nxt);
-            if (ok && lane == 0) {
+            if (lane == 0) {
                 const int n = max(cur.n[0], cur.n[1]);
                 const int kv0 = cur.row0 + cur.kbeg;
                 auto load_q = [&]() -> bool {
@@ -489,6 +516,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
         }
         if (!ok && lane == 0) {
             pf_error(p.err, DEV_ERR_TIMEOUT);
@@ -679,8 +707,6 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         return;
     }
 
-    named_bar_sync(kBarEndPf, C::THREADS);  // the warpgroup's idle warp
-    return;
     }
 
     // ============================================================== softmax
@@ -834,13 +860,11 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 tmem_ld32(o_t + c * 32, o);
                 tmem_ld_wait();
                 if (tok < end_tok) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        reinterpret_cast<uint4 *>(dst)[c * 4 + i] = make_uint4(
-                            bf16x2_of(o[8 * i] * inv, o[8 * i + 1] * inv),
-                            bf16x2_of(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                            bf16x2_of(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                            bf16x2_of(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    for (int i = 0; i < 16; ++i) w[i] = bf16x2_of(o[2 * i] * inv, o[2 * i + 1] * inv);
+                    st_global_32b(dst + c * 32, w);
+                    st_global_32b(dst + c * 32 + 16, w + 8);
                 }
             }
             tc_fence_before();
@@ -906,9 +930,9 @@ extern "C" int gqa_prefill_attn(const void *q, const void *k, const void *v,
     const char *who = "gqa_prefill_attn";
     api_begin();
     if (!q || !k || !v || !cu_seqlens || !out) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: null pointer", who);
-    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
-          reinterpret_cast<uintptr_t>(out)) & 15u) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
-        return api_failf(KVATTN_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u) ||
+        (reinterpret_cast<uintptr_t>(out) & 31u) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+        return api_failf(KVATTN_ERR_INVALID_ARG, "%s: q, k and v must be 16-byte, out 32-byte aligned", who);
     if (!std::isfinite(scale)) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: scale must be finite", who);
     if (window < 1) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: window must be >= 1 (got %d)", who, window);
     int rc = api_check_sizes(B, Hq, Hkv, D, 1);

@@ -488,8 +488,9 @@ KVATTN_API int kv_append_slots(void *k_pool, void *v_pool, const void *k_new, co
  *
  *   q          : bf16, N rows [Hq, D]; k, v: bf16, N rows [Hkv, D]
  *   cu_seqlens : int32 [B + 1] (device), non-decreasing, within [0, N]
- *   out        : bf16 [N, Hq, D], contiguous; rows of no sequence (behind the
- *                last one, or between two) stay as they are
+ *   out        : bf16 [N, Hq, D], contiguous, 32-byte aligned; rows of no
+ *                sequence (behind the last one, or between two) stay as they
+ *                are
  *   scale      : finite; window >= 1 (>= N: the whole prompt)
  *
  * Scores, maxima and sums are held in fp32; the weights enter the second

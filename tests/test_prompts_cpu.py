@@ -65,6 +65,7 @@ def _cases():
     yield "kv_block_tables", TABLES, dict(slots=P + 4), INV
     yield "kv_append_slots", SLOTS, dict(slots=P + 4), INV
     yield "kv_append_slots", SLOTS, dict(num_blocks=1 << 30, Hkv=4, k_stride=256, v_stride=256), UNS
+    yield "gqa_prefill_attn", PREFILL, dict(out=P + 16), INV
     yield "gqa_prefill_attn", PREFILL, dict(window=0), INV
     yield "gqa_prefill_attn", PREFILL, dict(Hq=5, q_stride=640), INV
     yield "kv_append_paged_fp8", APPEND8, dict(block_size=2048), UNS
