@@ -607,87 +607,97 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             __syncwarp();
         };
 
-        for (long long k = 0; ok; ++k) {
-            ok = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            const Unit u = units[k % kDesc];
+        auto next_unit = [&](long long k, Unit *u) {
+            const bool got = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
+            if (!__all_sync(0xffffffffu, got)) return false;
+            *u = units[k % kDesc];
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
-            if (u.n[0] == 0) break;
-            const int n = u.n[s], nmax = max(u.n[0], u.n[1]);
-            // keys of key tile j that the query tile attends at most
-            const int end = min(u.t0 + (s + 1) * p.tpt, u.len) - u.kbeg;
-            if (NQ == 2) {
-                for (int j = 0; j <= nmax; ++j, ++it) {
-                    const long long iv = base + 2 * j - 1, ik = base + 2 * j;
-                    if (j > n || n == 0) {
-                        // key tiles of the other query tile alone
-                        if (j > 0) ok = slot_ready(iv);
-                        if (ok && j < nmax) ok = slot_ready(ik);
-                        if (ok) ok = take_turn();
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) {
-                            if (j > 0) mbar_arrive(&slot_empty[iv % NS]);
-                            if (j < nmax) mbar_arrive(&slot_empty[ik % NS]);
-                            mbar_arrive(&turn[s ^ 1]);
-                        }
-                        continue;
-                    }
-                    if (j == 0) ok = pf_wait(&q_full[s], units_q++ & 1, abort_flag);
-                    if (ok && j > 0) ok = pf_wait(&p_full[s], (uint32_t)((g - 1) & 1), abort_flag, wlim) && slot_ready(iv);
-                    if (ok && j < nmax) ok = slot_ready(ik);
-                    if (ok) ok = take_turn();
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (j > 0) pv(s, iv, min(kRows, end - (j - 1) * kRows), j == 1);
-                    if (j < n) {
-                        qk(s, ik, min(kRows, end - j * kRows), j == n - 1);
-                        ++g;
-                    } else if (j < nmax && lane == 0) {
-                        mbar_arrive(&slot_empty[ik % NS]);
-                    }
-                    if (lane == 0) mbar_arrive(&turn[s ^ 1]);
+            return true;
+        };
+
+        Unit u;
+        if (NQ == 2) {
+            // A turn: P V of the step before, then Q K^T of this one (of the
+            // next unit's first key tile, too).  Everything else is waited for
+            // before the probabilities, the last to come.
+            int owed = 0;            // the step before: 1 its P V is due, 2 its V tile was not needed
+            long long owed_iv = 0;
+            int owed_keys = 0;
+            bool owed_first = false;
+            auto turn_of = [&](int n, int nmax, int j, int end) {  // j = nmax: the last P V alone
+                const long long ik = base + 2 * j;
+                bool go = true;
+                if (owed) go = slot_ready(owed_iv);
+                if (go && j < nmax) go = slot_ready(ik);
+                if (go && j == 0 && n > 0) go = pf_wait(&q_full[s], units_q++ & 1, abort_flag);
+                if (go) go = take_turn();
+                if (go && owed == 1) go = pf_wait(&p_full[s], (uint32_t)((g - 1) & 1), abort_flag, wlim);
+                if (!__all_sync(0xffffffffu, go)) return false;
+                tc_fence_after();
+                if (owed == 1)
+                    pv(s, owed_iv, owed_keys, owed_first);
+                else if (owed == 2 && lane == 0)
+                    mbar_arrive(&slot_empty[owed_iv % NS]);
+                owed = 0;
+                if (j < n) {
+                    const int keys = min(kRows, end - j * kRows);
+                    qk(s, ik, keys, j == n - 1);
+                    ++g;
+                    owed = 1;
+                    owed_keys = keys;
+                    owed_first = j == 0;
+                } else if (j < nmax) {
+                    if (lane == 0) mbar_arrive(&slot_empty[ik % NS]);
+                    owed = 2;
                 }
-            } else if (warp == 1) {
-                ok = pf_wait(&q_full[0], units_q++ & 1, abort_flag);
-                for (int j = 0; j < n && ok; ++j, ++g) {
-                    const int buf = (int)(g & 1);
-                    const long long ik = base + k_slot<D>(j);
-                    for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(ik + c);
-                    // S[buf] still holds the P of two tiles ago
-                    if (ok && g >= 2) ok = pf_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    qk(buf, ik, min(kRows, end - j * kRows), j == n - 1);
+                owed_iv = ik + 1;
+                if (lane == 0) mbar_arrive(&turn[s ^ 1]);
+                ++it;
+                return true;
+            };
+            for (long long k = 0; ok; ++k) {
+                ok = next_unit(k, &u);
+                if (!ok) break;
+                if (u.n[0] == 0) {
+                    if (owed) ok = turn_of(0, 0, 0, 0);
+                    break;
                 }
-            } else {
-                for (int j = 0; j < n && ok; ++j, ++g) {
-                    const int buf = (int)(g & 1);
-                    const long long iv = base + v_slot<D>(j, n);
-                    ok = pf_wait(&p_full[buf], (uint32_t)((g >> 1) & 1), abort_flag, wlim);
-                    for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(iv + c);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    pv(buf, iv, min(kRows, end - j * kRows), j == 0);
-                }
+                const int n = u.n[s], nmax = max(u.n[0], u.n[1]);
+                // keys of the unit's key tiles that the query tile attends at most
+                const int end = min(u.t0 + (s + 1) * p.tpt, u.len) - u.kbeg;
+                for (int j = 0; j < nmax && ok; ++j) ok = turn_of(n, nmax, j, end);
+                base += 2 * nmax;
             }
-            ok = __all_sync(0xffffffffu, ok);
-            base += 2 * nmax * CPT;
+        } else {
+            for (long long k = 0; ok; ++k) {
+                ok = next_unit(k, &u);
+                if (!ok || u.n[0] == 0) break;
+                const int n = u.n[0];
+                const int end = min(u.t0 + p.tpt, u.len) - u.kbeg;
+                if (warp == 1) ok = pf_wait(&q_full[0], units_q++ & 1, abort_flag);
+                for (int j = 0; j < n && ok; ++j, ++g) {
+                    const int buf = (int)(g & 1);
+                    const long long i0 = base + (warp == 1 ? k_slot<D>(j) : v_slot<D>(j, n));
+                    for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(i0 + c);
+                    if (warp == 1) {
+                        // S[buf] still holds the P of two tiles ago
+                        if (ok && g >= 2) ok = pf_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
+                    } else if (ok) {
+                        ok = pf_wait(&p_full[buf], (uint32_t)((g >> 1) & 1), abort_flag, wlim);
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int keys = min(kRows, end - j * kRows);
+                    if (warp == 1)
+                        qk(buf, i0, keys, j == n - 1);
+                    else
+                        pv(buf, i0, keys, j == 0);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                base += 2 * n * CPT;
+            }
         }
         if (!ok) {
             pf_error(p.err, DEV_ERR_TIMEOUT);
@@ -748,29 +758,59 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             }
             tc_fence_after();
             const uint32_t s_t = lanes + buf * 128;
+            // The tile's keys in four parts of 32: parts past the last key that
+            // any row attends are left out (the MMAs stop there too), and only
+            // parts at the diagonal or the window's edge hide some keys from
+            // some rows: a row's are [lo, hi).
             float v[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, v + c * 32);
-            tmem_ld_wait();
             const int kb = u.kbeg + j * kRows;
-            // keys [lo, hi) of this tile are the row's; only the tiles at the
-            // diagonal and at the window's edge hide any
-            if (kb + kRows > first_tok + 1 || kb < end_tok - p.window) {
-                const int hi = tq + 1 - kb, lo = tq + 1 - p.window - kb;
+            const int keys = min(kRows, end_tok - kb);
+            const int hi = tq + 1 - kb, lo = tq + 1 - p.window - kb;
+            const int sure_hi = first_tok + 1 - kb, sure_lo = end_tok - p.window - kb;
+            // (a whole tile that hides nothing takes the straight path)
+            const bool whole = keys == kRows && kRows <= sure_hi && sure_lo <= 0;
+            float mn;
+            if (whole) {
 #pragma unroll
-                for (int c = 0; c < 128; ++c) v[c] = (c < hi && c >= lo) ? v[c] : -INFINITY;
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, v + c * 32);
+                tmem_ld_wait();
+                float mx[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx[i] = max3(v[i], v[8 + i], v[16 + i]);
+#pragma unroll
+                for (int c = 24; c < 120; c += 16) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], v[c + i], v[c + 8 + i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], v[120 + i]);
+                mn = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), max3(mx[6], mx[7], m));
+            } else {
+                mn = m;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float *x = v + c * 32;
+                    if (c * 32 < keys) {
+                        tmem_ld32(s_t + c * 32, x);
+                        tmem_ld_wait();
+                        if (c * 32 + 32 > sure_hi || c * 32 < sure_lo) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                x[i] = (c * 32 + i < hi && c * 32 + i >= lo) ? x[i] : -INFINITY;
+                        }
+                        float mx[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = max3(x[i], x[4 + i], x[8 + i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], x[12 + i], x[16 + i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], x[20 + i], x[24 + i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[28 + i]);
+                        mn = max3(mn, max3(mx[0], mx[1], mx[2]), mx[3]);
+                    }
+                }
             }
-            float mx[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mx[i] = max3(v[i], v[8 + i], v[16 + i]);
-#pragma unroll
-            for (int c = 24; c < 120; c += 16) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], v[c + i], v[c + 8 + i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], v[120 + i]);
-            const float mn = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), max3(mx[6], mx[7], m));
             const bool grow = (mn - m) * p.sl > kTauPf;  // (both -inf: no)
             if (__any_sync(0xffffffffu, grow)) {
                 const float alpha = (grow && m != -INFINITY) ? fast_exp2((m - mn) * p.sl) : 1.f;
@@ -800,8 +840,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             const float neg_m = m == -INFINITY ? 0.f : -m * p.sl;
             const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(neg_m, neg_m);
             float2 ls[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            auto weights = [&](int c) {  // of the part's 32 keys
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -811,13 +850,20 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                     pk[i] = bf16x2_of(e.x, e.y);
                 }
                 tmem_st16u(s_t + c * 16, pk);
+            };
+            if (whole) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) weights(c);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c * 32 < keys) weights(c);
             }
             ls[0] = add2(ls[0], ls[1]);
             l = ls[0].x + ls[0].y;
             // rows past the sequence's end that the last 16 keys of P V would
             // read belong to another sequence (or to none) and may hold
             // anything, which a weight of zero does not hide: they are zeroed
-            const int keys = min(kRows, end_tok - kb);
             const int stop = (keys + 15) / 16 * 16, past = u.len - kb;
             if (past < stop) {
                 const long long iv = base + v_slot<D>(j, nmax);
