@@ -129,6 +129,19 @@ __device__ __forceinline__ bool pf_wait(uint64_t *bar, uint32_t parity, volatile
     return false;
 }
 
+// The same by a whole warp, which leaves it together (a uniform branch: with
+// each lane leaving on its own the wait took some 90 cycles, so 36).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                          uint32_t limit = KVATTN_SPIN_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
+        const bool done = limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], bf16 inputs (A packed two to a column), fp32 accumulate.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                              uint32_t idesc, bool accumulate) {
@@ -224,6 +237,16 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A published unit, the same in every lane.
+__device__ __forceinline__ Unit read_unit(const Unit &from) {
+    Unit u;
+    const int *src = reinterpret_cast<const int *>(&from);
+    int *dst = reinterpret_cast<int *>(&u);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Unit) / 4); ++i) dst[i] = __shfl_sync(0xffffffffu, src[i], 0);
+    return u;
+}
+
 // Length of sequence b (0 where its bounds are not 0 <= cu[b] <= cu[b+1] <= N).
 __device__ __forceinline__ int pf_len(const PrefillParams &p, int b, int *row0) {
     const int a = p.cu[b], e = p.cu[b + 1];
@@ -273,7 +296,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     unsigned long long *sum_pairs = reinterpret_cast<unsigned long long *>(smem + C::off_sum);
     int *max_nb = reinterpret_cast<int *>(sum_pairs + 1);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int tpu = NQ * p.tpt;          // tokens of a unit
     const int heads = p.Hkv * p.passes;  // units of one block of tokens
 
@@ -475,12 +498,9 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             return true;
         };
         for (long long k = 0;; ++k) {
-            ok = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            const Unit cur = units[k % kDesc];
+            ok = warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
+            if (!ok) break;
+            const Unit cur = read_unit(units[k % kDesc]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
             if (cur.n[0] == 0) break;
@@ -558,11 +578,11 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         // cores, both finish together and both wait for both: 8192 tokens, 64
         // heads over 8 of 128, took 1009 us against ... with turns).
         auto take_turn = [&]() {
-            return s == 0 ? it == 0 || pf_wait(&turn[0], (it - 1) & 1, abort_flag)
-                          : pf_wait(&turn[1], it & 1, abort_flag);
+            return s == 0 ? it == 0 || warp_wait(&turn[0], (it - 1) & 1, abort_flag)
+                          : warp_wait(&turn[1], it & 1, abort_flag);
         };
         auto slot_ready = [&](long long i) {
-            return pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), abort_flag);
+            return warp_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), abort_flag);
         };
         // S[buf] = Q_s K_j^T; keys past the tile's last are left out, 16 at a time
         auto qk = [&](int buf, long long i0, int keys, bool last) {
@@ -608,9 +628,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         };
 
         auto next_unit = [&](long long k, Unit *u) {
-            const bool got = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
-            if (!__all_sync(0xffffffffu, got)) return false;
-            *u = units[k % kDesc];
+            if (!warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag)) return false;
+            *u = read_unit(units[k % kDesc]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
             return true;
@@ -630,10 +649,10 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 bool go = true;
                 if (owed) go = slot_ready(owed_iv);
                 if (go && j < nmax) go = slot_ready(ik);
-                if (go && j == 0 && n > 0) go = pf_wait(&q_full[s], units_q++ & 1, abort_flag);
+                if (go && j == 0 && n > 0) go = warp_wait(&q_full[s], units_q++ & 1, abort_flag);
                 if (go) go = take_turn();
-                if (go && owed == 1) go = pf_wait(&p_full[s], (uint32_t)((g - 1) & 1), abort_flag, wlim);
-                if (!__all_sync(0xffffffffu, go)) return false;
+                if (go && owed == 1) go = warp_wait(&p_full[s], (uint32_t)((g - 1) & 1), abort_flag, wlim);
+                if (!go) return false;
                 tc_fence_after();
                 if (owed == 1)
                     pv(s, owed_iv, owed_keys, owed_first);
@@ -675,18 +694,17 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 if (!ok || u.n[0] == 0) break;
                 const int n = u.n[0];
                 const int end = min(u.t0 + p.tpt, u.len) - u.kbeg;
-                if (warp == 1) ok = pf_wait(&q_full[0], units_q++ & 1, abort_flag);
+                if (warp == 1) ok = warp_wait(&q_full[0], units_q++ & 1, abort_flag);
                 for (int j = 0; j < n && ok; ++j, ++g) {
                     const int buf = (int)(g & 1);
                     const long long i0 = base + (warp == 1 ? k_slot<D>(j) : v_slot<D>(j, n));
                     for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(i0 + c);
                     if (warp == 1) {
                         // S[buf] still holds the P of two tiles ago
-                        if (ok && g >= 2) ok = pf_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
+                        if (ok && g >= 2) ok = warp_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
                     } else if (ok) {
-                        ok = pf_wait(&p_full[buf], (uint32_t)((g >> 1) & 1), abort_flag, wlim);
+                        ok = warp_wait(&p_full[buf], (uint32_t)((g >> 1) & 1), abort_flag, wlim);
                     }
-                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
                     const int keys = min(kRows, end - j * kRows);
@@ -695,7 +713,6 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                     else
                         pv(buf, i0, keys, j == 0);
                 }
-                ok = __all_sync(0xffffffffu, ok);
                 base += 2 * n * CPT;
             }
         }
@@ -707,7 +724,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         if (elect_one()) umma_commit(drain);
         __syncwarp();
         volatile int never = 0;
-        pf_wait(drain, 0, &never);
+        warp_wait(drain, 0, &never);
         __syncwarp();
         named_bar_sync(kBarEndPf, C::THREADS);
         if (warp == 1) {
@@ -732,12 +749,9 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     bool ok = true;
 
     for (long long k = 0;; ++k) {
-        ok = pf_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-        }
-        const Unit u = units[k % kDesc];
+        ok = warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
+        if (!ok) break;
+        const Unit u = read_unit(units[k % kDesc]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
         if (u.n[0] == 0) break;
@@ -751,11 +765,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         for (int j = 0; j < n; ++j, ++g) {
             const int buf = NQ == 2 ? s : (int)(g & 1);
             const uint32_t par = (uint32_t)((NQ == 2 ? g : g >> 1) & 1);
-            ok = pf_wait(&s_full[buf], par, abort_flag, wlim);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+            ok = warp_wait(&s_full[buf], par, abort_flag, wlim);
+            if (!ok) break;
             tc_fence_after();
             const uint32_t s_t = lanes + buf * 128;
             // The tile's keys in four parts of 32: parts past the last key that
@@ -820,11 +831,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                     // O holds the tiles up to j - 1
                     const int pb = NQ == 2 ? s : buf ^ 1;
                     const uint32_t pp = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
-                    ok = pf_wait(&pv_done[pb], pp, abort_flag, wlim);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = warp_wait(&pv_done[pb], pp, abort_flag, wlim);
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
@@ -869,7 +877,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 const long long iv = base + v_slot<D>(j, nmax);
                 for (int c = 0; c < CPT && ok; ++c) {
                     const int slot = (int)((iv + c) % NS);
-                    ok = pf_wait(&slot_full[slot], (uint32_t)(((iv + c) / NS) & 1), abort_flag);
+                    ok = warp_wait(&slot_full[slot], (uint32_t)(((iv + c) / NS) & 1), abort_flag);
                     if (ok)
                         for (int i = row; i < (stop - past) * (C::KC / 64) * 8; i += 128) {
                             const int r = past + (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
@@ -877,10 +885,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                                                        (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                 }
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                if (!ok) break;
                 fence_proxy_async_smem();
             }
             tmem_st_wait();
@@ -892,11 +897,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         if (n > 0) {
             const int buf = NQ == 2 ? s : (int)((g - 1) & 1);
             const uint32_t par = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
-            ok = pf_wait(&pv_done[buf], par, abort_flag, wlim);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+            ok = warp_wait(&pv_done[buf], par, abort_flag, wlim);
+            if (!ok) break;
             tc_fence_after();
             const float inv = 1.f / l;  // (every row attends itself)
             uint16_t *dst = p.out + ((size_t)(u.row0 + tok) * p.Hq + u.h0 + r_head) * D;
