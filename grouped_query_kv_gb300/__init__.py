@@ -14,6 +14,8 @@ import ctypes
 import os
 import threading
 
+import torch
+
 __all__ = [
     "kv_append", "kv_append_multi", "kv_append_paged", "gqa_decode_attn", "gqa_decode_step",
     "gqa_decode_attn_multi", "gqa_decode_attn_paged", "gqa_decode_step_paged",
@@ -148,9 +150,15 @@ def _check(status: int):
         raise KvAttnError(status, lib().kvattn_last_error().decode())
 
 
+# the current stream's handle without building a torch.cuda.Stream (several
+# microseconds of a decode step's host time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(stream):
     if stream is None:
-        import torch
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream  # a plain int: ctypes converts it for the c_void_p argument
 
@@ -162,7 +170,6 @@ def _ptr(t):
 def _need(t, name, dtype, shape=None):
     # the checks run on every call of a decode loop, so they use the cheapest
     # torch attributes (is_cuda, dtype identity, torch.Size == tuple)
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
@@ -182,7 +189,6 @@ def kv_append(k_cache, v_cache, k_new, v_new, seq_lens, stream=None):
     [B, Hkv, D]; seq_lens: int32 [B], tokens cached before this one (not
     modified).
     """
-    import torch
     _need(k_cache, "k_cache", torch.bfloat16)
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [B, Hkv, Lmax, D]")
@@ -202,7 +208,6 @@ def kv_append_multi(k_cache, v_cache, k_new, v_new, seq_lens, stream=None):
     [B, T, Hkv, D]; seq_lens: int32 [B], tokens cached before them (not
     modified).
     """
-    import torch
     _need(k_cache, "k_cache", torch.bfloat16)
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [B, Hkv, Lmax, D]")
@@ -228,7 +233,6 @@ def gqa_decode_attn(q, k_cache, v_cache, seq_lens, scale, out=None, stream=None,
     out: optional fp32 [B, Hq, D] (allocated if None); window: None (all
     positions) or an int >= 1.  Returns out.
     """
-    import torch
     _need(q, "q", torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
@@ -263,7 +267,6 @@ def gqa_decode_step(q, k_new, v_new, k_cache, v_cache, seq_lens, scale, out=None
     [B, Hkv, Lmax, D] (modified in place); seq_lens: int32 [B], tokens cached
     before this step (not modified); out: optional fp32 [B, Hq, D].
     """
-    import torch
     _need(q, "q", torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
@@ -302,7 +305,6 @@ def gqa_decode_attn_multi(q, k_cache, v_cache, seq_lens, scale, out=None, stream
     new ones; out: optional fp32 [B, T, Hq, D]; window: None (all positions)
     or an int >= 1.  Returns out.
     """
-    import torch
     _need(q, "q", torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, D]")
@@ -330,7 +332,6 @@ def gqa_decode_attn_multi(q, k_cache, v_cache, seq_lens, scale, out=None, stream
 
 def _pool_shape(k_pool, block_table, name="k_pool"):
     """(num_blocks, Hkv, block_size, D, B, max_blocks) of a paged cache."""
-    import torch
     _need(k_pool, name, torch.bfloat16)
     if k_pool.dim() != 4:
         raise ValueError("%s must be [num_blocks, Hkv, block_size, D]" % name)
@@ -350,7 +351,6 @@ def kv_append_paged(k_pool, v_pool, k_new, v_new, block_table, seq_lens, stream=
     block_table: int32 [B, max_blocks]; seq_lens: int32 [B], tokens cached
     before the new ones (not modified).
     """
-    import torch
     nblk, Hkv, bs, D, B, maxb = _pool_shape(k_pool, block_table)
     _need(v_pool, "v_pool", torch.bfloat16, (nblk, Hkv, bs, D))
     _need(k_new, "k_new", torch.bfloat16)
@@ -380,7 +380,6 @@ def gqa_decode_attn_paged(q, k_pool, v_pool, block_table, seq_lens, scale, out=N
     window: None (all positions) or an int >= 1, each query's local window.
     Returns out.
     """
-    import torch
     _need(q, "q", torch.bfloat16)
     if q.dim() not in (3, 4):
         raise ValueError("q must be [B, Hq, D] or [B, T, Hq, D]")
@@ -417,7 +416,6 @@ def gqa_decode_step_paged(q, k_new, v_new, k_pool, v_pool, block_table, seq_lens
     q: bf16 [B, Hq, D]; k_new, v_new: bf16 [B, Hkv, D]; pools and table as
     for gqa_decode_attn_paged; seq_lens: tokens cached before this step.
     """
-    import torch
     _need(q, "q", torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
@@ -450,7 +448,6 @@ def kv_quantize_fp8(src, codes=None, scales=None, stream=None):
     """Quantize bf16 rows [..., D] into E4M3 codes (uint8 [..., D]) and one
     fp32 scale per row ([...]): scale = absmax / 448, code = E4M3(x / scale).
     Returns (codes, scales)."""
-    import torch
     _need(src, "src", torch.bfloat16)
     D = src.shape[-1]
     rows = src.numel() // D if D else 0
@@ -469,7 +466,6 @@ def kv_append_fp8(k_codes, v_codes, k_scale, v_scale, k_new, v_new, seq_lens, st
     """Quantize the new token's K/V rows into position seq_lens[b] of an
     8-bit cache (codes uint8 [B, Hkv, Lmax, D], scales fp32 [B, Hkv, Lmax];
     k_new, v_new bf16 [B, Hkv, D])."""
-    import torch
     _need(k_codes, "k_codes", torch.uint8)
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [B, Hkv, Lmax, D]")
@@ -491,7 +487,6 @@ def gqa_decode_attn_fp8(q, k_codes, v_codes, k_scale, v_scale, seq_lens, scale, 
     row, V likewise.  q bf16 [B, Hq, D]; codes uint8 [B, Hkv, Lmax, D];
     scales fp32 [B, Hkv, Lmax]; seq_lens int32 [B]; out optional fp32
     [B, Hq, D].  Returns out."""
-    import torch
     _need(q, "q", torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
@@ -521,7 +516,6 @@ def gqa_decode_step_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, seq
     [B, Hkv, Lmax, D] and scales fp32 [B, Hkv, Lmax], updated in place;
     seq_lens int32 [B] (tokens cached before this step, not modified);
     out optional fp32 [B, Hq, D].  Returns out."""
-    import torch
     _need(q, "q", torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
@@ -546,23 +540,40 @@ def gqa_decode_step_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, seq
     return out
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: all tensors must be there."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError("tensors must be on the current CUDA device %d (got %s)" % (dev, t.device))
-
-
-def _packed_rows(t, name, shape=None):
-    """Checks packed bf16 rows [N, H, D] whose [H, D] are contiguous (they may
-    be a slice of wider rows) and returns the elements from row to row."""
-    import torch
+def _home(t, name):
+    """The current CUDA device, which is where tensor t must be (the library
+    launches there)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("%s must be a CUDA tensor (got %s)" % (name, t.device))
+    if dev != torch.cuda.current_device():
+        raise ValueError("%s is on %s, not on the current CUDA device %d"
+                         % (name, t.device, torch.cuda.current_device()))
+    return dev
+
+
+def _want(t, name, dtype, dev, shape=None):
+    """_need, and on CUDA device `dev`; one pass over the cheap attributes when
+    all is well."""
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and (shape is None or t.shape == shape)
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape)
+    raise ValueError("%s must be on the current CUDA device %d (got %s)" % (name, dev, t.device))
+
+
+def _packed_rows(t, name, dev, shape=None):
+    """Checks packed bf16 rows [N, H, D] whose [H, D] are contiguous (they may
+    be a slice of wider rows) and returns the elements from row to row."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the current device %d (got %s)" % (name, dev, t.device))
     if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be %s (got %s)" % (name, torch.bfloat16, t.dtype))
     if t.dim() != 3:
@@ -593,35 +604,32 @@ def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count,
     Requests that the free list or the table cannot serve get slot -1 and set
     the device error word (see include/kvattn.h).
     """
-    import torch
-    i32 = torch.int32
-    _need(cached_lens, "cached_lens", i32)
+    i32, dev = torch.int32, _home(cached_lens, "cached_lens")
+    _want(cached_lens, "cached_lens", i32, dev)
     if cached_lens.dim() != 1:
         raise ValueError("cached_lens must be [B]")
     B = cached_lens.shape[0]
-    _need(new_lens, "new_lens", i32, (B,))
-    _need(block_table, "block_table", i32)
+    _want(new_lens, "new_lens", i32, dev, (B,))
+    _want(block_table, "block_table", i32, dev)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_blocks]")
-    _need(free_blocks, "free_blocks", i32)
+    _want(free_blocks, "free_blocks", i32, dev)
     if free_blocks.dim() != 1:
         raise ValueError("free_blocks must be [num_free]")
-    _need(free_count, "free_count", i32, (1,))
+    _want(free_count, "free_count", i32, dev, (1,))
     num_slots = int(num_slots)
     if cu_seqlens is None:
-        cu_seqlens = torch.empty(B + 1, dtype=i32, device=cached_lens.device)
+        cu_seqlens = cached_lens.new_empty(B + 1)
     else:
-        _need(cu_seqlens, "cu_seqlens", i32, (B + 1,))
+        _want(cu_seqlens, "cu_seqlens", i32, dev, (B + 1,))
     if slots is None:
-        slots = torch.empty(max(num_slots, 0), dtype=torch.int64, device=cached_lens.device)
+        slots = cached_lens.new_empty(max(num_slots, 0), dtype=torch.int64)
     else:
-        _need(slots, "slots", torch.int64, (num_slots,))
+        _want(slots, "slots", torch.int64, dev, (num_slots,))
     if free_count_out is None:
         free_count_out = free_count
     else:
-        _need(free_count_out, "free_count_out", i32, (1,))
-    _on_current_device(cached_lens, new_lens, block_table, free_blocks, free_count, cu_seqlens, slots,
-                       free_count_out)
+        _want(free_count_out, "free_count_out", i32, dev, (1,))
     _check(lib().kv_block_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(block_table),
                                  _ptr(free_blocks), _ptr(free_count), _ptr(free_count_out),
                                  _ptr(cu_seqlens), _ptr(slots), B, block_table.shape[1],
@@ -639,19 +647,18 @@ def kv_append_slots(k_pool, v_pool, k_new, v_new, slots, stream=None):
     v_new: bf16 [N, Hkv, D], rows contiguous or slices of wider rows; slots:
     int64 [N], all different.
     """
-    import torch
-    _need(k_pool, "k_pool", torch.bfloat16)
+    dev = _home(k_pool, "k_pool")
+    _want(k_pool, "k_pool", torch.bfloat16, dev)
     if k_pool.dim() != 4:
         raise ValueError("k_pool must be [num_blocks, Hkv, block_size, D]")
     nblk, Hkv, bs, D = k_pool.shape
-    _need(v_pool, "v_pool", torch.bfloat16, (nblk, Hkv, bs, D))
-    _need(slots, "slots", torch.int64)
+    _want(v_pool, "v_pool", torch.bfloat16, dev, (nblk, Hkv, bs, D))
+    _want(slots, "slots", torch.int64, dev)
     if slots.dim() != 1:
         raise ValueError("slots must be [N]")
     N = slots.shape[0]
-    ks = _packed_rows(k_new, "k_new", (N, Hkv, D))
-    vs = _packed_rows(v_new, "v_new", (N, Hkv, D))
-    _on_current_device(k_pool, v_pool, k_new, v_new, slots)
+    ks = _packed_rows(k_new, "k_new", dev, (N, Hkv, D))
+    vs = _packed_rows(v_new, "v_new", dev, (N, Hkv, D))
     _check(lib().kv_append_slots(_ptr(k_pool), _ptr(v_pool), _ptr(k_new), _ptr(v_new), _ptr(slots),
                                  N, Hkv, D, ks, vs, nblk, bs, _stream_ptr(stream)))
 
@@ -666,22 +673,21 @@ def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=N
     None allocated as zeros, since rows of no sequence are not written);
     window: None (all positions) or an int >= 1.  Returns out.
     """
-    import torch
-    qs = _packed_rows(q, "q")
+    dev = _home(q, "q")
+    qs = _packed_rows(q, "q", dev)
     N, Hq, D = q.shape
-    ks = _packed_rows(k, "k")
+    ks = _packed_rows(k, "k", dev)
     Hkv = k.shape[1]
     if k.shape[0] != N or k.shape[2] != D:
         raise ValueError("k must be [N, Hkv, D] matching q")
-    vs = _packed_rows(v, "v", (N, Hkv, D))
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    vs = _packed_rows(v, "v", dev, (N, Hkv, D))
+    _want(cu_seqlens, "cu_seqlens", torch.int32, dev)
     if cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be [B + 1]")
     if out is None:
         out = torch.zeros((N, Hq, D), dtype=torch.bfloat16, device=q.device)
     else:
-        _need(out, "out", torch.bfloat16, (N, Hq, D))
-    _on_current_device(q, k, v, cu_seqlens, out)
+        _want(out, "out", torch.bfloat16, dev, (N, Hq, D))
     _check(lib().gqa_prefill_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out),
                                   cu_seqlens.shape[0] - 1, N, Hq, Hkv, D, qs, ks, vs, float(scale),
                                   0x7fffffff if window is None else int(window),
@@ -689,17 +695,16 @@ def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=N
     return out
 
 
-def _pool8(k_codes, v_codes, k_scale, v_scale, block_table):
+def _pool8(k_codes, v_codes, k_scale, v_scale, block_table, dev):
     """Checks a paged 8-bit cache; returns (num_blocks, Hkv, block_size, D, B, max_blocks)."""
-    import torch
-    _need(k_codes, "k_codes", torch.uint8)
+    _want(k_codes, "k_codes", torch.uint8, dev)
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [num_blocks, Hkv, block_size, D]")
     nblk, Hkv, bs, D = k_codes.shape
-    _need(v_codes, "v_codes", torch.uint8, (nblk, Hkv, bs, D))
-    _need(k_scale, "k_scale", torch.float32, (nblk, Hkv))
-    _need(v_scale, "v_scale", torch.float32, (nblk, Hkv))
-    _need(block_table, "block_table", torch.int32)
+    _want(v_codes, "v_codes", torch.uint8, dev, (nblk, Hkv, bs, D))
+    _want(k_scale, "k_scale", torch.float32, dev, (nblk, Hkv))
+    _want(v_scale, "v_scale", torch.float32, dev, (nblk, Hkv))
+    _want(block_table, "block_table", torch.int32, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     return nblk, Hkv, bs, D, block_table.shape[0], block_table.shape[1]
@@ -717,17 +722,15 @@ def kv_append_paged_fp8(k_codes, v_codes, k_scale, v_scale, k_new, v_new, block_
     [N, Hkv, D], rows contiguous or slices of wider rows; block_table: int32
     [B, max_blocks]; cached_lens: int32 [B]; cu_seqlens: int32 [B + 1].
     """
-    import torch
-    nblk, Hkv, bs, D, B, maxb = _pool8(k_codes, v_codes, k_scale, v_scale, block_table)
-    ks = _packed_rows(k_new, "k_new")
+    dev = _home(k_codes, "k_codes")
+    nblk, Hkv, bs, D, B, maxb = _pool8(k_codes, v_codes, k_scale, v_scale, block_table, dev)
+    ks = _packed_rows(k_new, "k_new", dev)
     N = k_new.shape[0]
     if k_new.shape[1] != Hkv or k_new.shape[2] != D:
         raise ValueError("k_new must be [N, Hkv, D] matching the pool")
-    vs = _packed_rows(v_new, "v_new", (N, Hkv, D))
-    _need(cached_lens, "cached_lens", torch.int32, (B,))
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    _on_current_device(k_codes, v_codes, k_scale, v_scale, k_new, v_new, block_table, cached_lens,
-                       cu_seqlens)
+    vs = _packed_rows(v_new, "v_new", dev, (N, Hkv, D))
+    _want(cached_lens, "cached_lens", torch.int32, dev, (B,))
+    _want(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
     _check(lib().kv_append_paged_fp8(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
                                      _ptr(k_new), _ptr(v_new), _ptr(block_table), _ptr(cached_lens),
                                      _ptr(cu_seqlens), B, N, Hkv, D, ks, vs, nblk, bs, maxb,
@@ -740,20 +743,19 @@ def gqa_decode_attn_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table
     k_scale[block, kvh], V likewise.  q: bf16 [B, Hq, D]; pools and table as for
     kv_append_paged_fp8; seq_lens: int32 [B], positions attended; out: optional
     bf16 [B, Hq, D].  Returns out."""
-    import torch
-    _need(q, "q", torch.bfloat16)
+    dev = _home(q, "q")
+    _want(q, "q", torch.bfloat16, dev)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
     B, Hq, D = q.shape
-    nblk, Hkv, bs, Dp, Bt, maxb = _pool8(k_codes, v_codes, k_scale, v_scale, block_table)
+    nblk, Hkv, bs, Dp, Bt, maxb = _pool8(k_codes, v_codes, k_scale, v_scale, block_table, dev)
     if Dp != D or Bt != B:
         raise ValueError("k_codes / block_table do not match q")
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _want(seq_lens, "seq_lens", torch.int32, dev, (B,))
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty((B, Hq, D))
     else:
-        _need(out, "out", torch.bfloat16, (B, Hq, D))
-    _on_current_device(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, out)
+        _want(out, "out", torch.bfloat16, dev, (B, Hq, D))
     _check(lib().gqa_decode_attn_paged_fp8(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
                                            _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
                                            _ptr(out), B, Hq, Hkv, D, nblk, bs, maxb, float(scale),

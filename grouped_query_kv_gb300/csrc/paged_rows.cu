@@ -6,12 +6,12 @@
 // Block tables.  With c_b tokens cached and n_b new ones, request b has
 // have_b = ceil(c_b / bs) blocks and needs up to upto_b = ceil((c_b + n_b) /
 // bs); before_b = sum of (upto - have) over the requests before it places it
-// in the free stack.  Two prefix sums over B lengths and one write per new
-// block and per token: the bytes are few (8 per token), so what bounds a
-// call is the chain of launch, length loads, scans and dependent loads.  One
-// block of 1024 threads does the sums, the tables and (up to
-// kOneBlockSlots slots) the slot map; larger maps get a second launch of
-// many blocks, which starts its prologue under the first.
+// in the free stack.  The bytes are few (8 per token), so what bounds a call
+// is the chain of launch, length loads, two prefix sums over the requests and
+// one dependent load per token.  Every block of the grid does the prefix sums
+// itself (B lengths from L2, no workspace, nothing to wait for), then takes
+// tiles of 4096 packed rows, a row's thread also writing the table entry of
+// the block that starts at it; up to one tile the call is one block.
 //
 // Row write.  A copy of 16-byte vectors, four K and four V vectors of a
 // thread in flight; both sides are contiguous per (token, head), so it runs
@@ -25,9 +25,8 @@ namespace kvattn {
 namespace {
 
 constexpr int kTblThreads = 1024;
-constexpr int kOneBlockSlots = 4096;  // slots that the table kernel writes itself
-constexpr int kSlotThreads = 256;
-constexpr int kSlotsPerThread = 4;
+constexpr int kTblRows = 4;                        // consecutive rows per thread
+constexpr int kTblTile = kTblThreads * kTblRows;
 
 struct TableParams {
     const int32_t *cached, *fresh;
@@ -37,193 +36,170 @@ struct TableParams {
     long long *slots;
     unsigned int *err;
     int B, max_blocks, lg, num_free, num_slots;
+    int rows, count;  // write the slots and tables; write the count
 };
 
-// Lengths of one request; false if they are negative or do not fit its table row.
-__device__ __forceinline__ bool request_ok(int c, int n, int max_blocks, int lg) {
-    return c >= 0 && n >= 0 && (long long)c + n <= ((long long)max_blocks << lg);
-}
+// One request: its new rows and the blocks it lacks for them.
+struct Request {
+    int c, n, have, need;
+    bool ok;  // lengths that are not negative and fit its table row
+};
 
-// Slot of packed row t of request b (-1: none).  A request whose first
-// missing block is -1 got no blocks.
-__device__ __forceinline__ long long slot_of(const TableParams &p, int b, int c, int n, long long i) {
-    if (!request_ok(c, n, p.max_blocks, p.lg)) return -1;
+__device__ __forceinline__ Request get_request(const TableParams &p, int b) {
+    Request r;
+    r.c = p.cached[b];
+    r.n = p.fresh[b];
+    r.ok = r.c >= 0 && r.n >= 0 && (long long)r.c + r.n <= ((long long)p.max_blocks << p.lg);
     const int bs1 = (1 << p.lg) - 1;
-    const int have = (c + bs1) >> p.lg, upto = (c + n + bs1) >> p.lg;
-    const int32_t *row = p.table + (size_t)b * p.max_blocks;
-    if (upto > have && row[have] < 0) return -1;
-    const int pos = c + (int)i;
-    const int blk = row[pos >> p.lg];
-    return blk < 0 ? -1 : ((long long)blk << p.lg) + (pos & bs1);
+    r.have = r.ok ? (r.c + bs1) >> p.lg : 0;
+    r.need = r.ok ? ((r.c + r.n + bs1) >> p.lg) - r.have : 0;
+    r.n = max(r.n, 0);
+    return r;
 }
 
-// Exclusive prefix sums of two values over the block; *ta, *tb the totals.
-__device__ __forceinline__ void block_scan2(long long a, long long b, long long *ea, long long *eb,
-                                            long long *ta, long long *tb, longlong2 *warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long ia = a, ib = b;
+__device__ __forceinline__ int cap32(long long x) { return (int)min(x, 0x7fffffffLL); }
+
+__global__ void __launch_bounds__(kTblThreads) block_table_kernel(const TableParams p) {
+    __shared__ longlong2 warps[32];
+    __shared__ int s_rows[kTblThreads], s_blocks[kTblThreads];  // before each thread's requests
+    __shared__ int s_taken;
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int count = p.free_count[0];
+    bool bad = count < 0 || count > p.num_free;
+    if (bad) count = 0;
+    if (tid == 0) s_taken = 0;
+
+    // prefix sums of rows and blocks: `per` consecutive requests per thread
+    const int per = (p.B + kTblThreads - 1) / kTblThreads;
+    const int b0 = tid * per, b1 = min(p.B, b0 + per);
+    long long rows = 0, blocks = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = get_request(p, b);
+        rows += r.n;
+        blocks += r.need;
+        bad |= !r.ok;
+    }
+    long long ir = rows, ib = blocks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long va = __shfl_up_sync(0xffffffffu, ia, o), vb = __shfl_up_sync(0xffffffffu, ib, o);
+        const long long vr = __shfl_up_sync(0xffffffffu, ir, o), vb = __shfl_up_sync(0xffffffffu, ib, o);
         if (lane >= o) {
-            ia += va;
+            ir += vr;
             ib += vb;
         }
     }
-    if (lane == 31) warps[warp] = make_longlong2(ia, ib);
+    if (lane == 31) warps[warp] = make_longlong2(ir, ib);
     __syncthreads();
     if (warp == 0) {
         longlong2 w = warps[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long va = __shfl_up_sync(0xffffffffu, w.x, o), vb = __shfl_up_sync(0xffffffffu, w.y, o);
+            const long long vr = __shfl_up_sync(0xffffffffu, w.x, o), vb = __shfl_up_sync(0xffffffffu, w.y, o);
             if (lane >= o) {
-                w.x += va;
+                w.x += vr;
                 w.y += vb;
             }
         }
         warps[lane] = w;
     }
     __syncthreads();
-    const longlong2 before = warp ? warps[warp - 1] : make_longlong2(0, 0);
-    *ea = before.x + ia - a;
-    *eb = before.y + ib - b;
-    *ta = warps[31].x;
-    *tb = warps[31].y;
+    if (warp > 0) {
+        ir += warps[warp - 1].x;
+        ib += warps[warp - 1].y;
+    }
+    long long at_row = ir - rows, at_block = ib - blocks;
+    s_rows[tid] = cap32(at_row);
+    s_blocks[tid] = cap32(at_block);
+    const long long all_rows = warps[31].x;
+
+    if (blockIdx.x == 0) {
+        // cu_seqlens, and the blocks taken: by the requests up to the last that
+        // is served
+        int taken = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Request r = get_request(p, b);
+            if (p.rows) {
+                p.cu[b] = cap32(at_row);
+                if (b == p.B - 1) p.cu[p.B] = cap32(at_row + r.n);
+            }
+            at_row += r.n;
+            at_block += r.need;
+            if (r.need > 0) {
+                if (at_block <= count && at_row <= p.num_slots)
+                    taken = (int)at_block;
+                else
+                    bad = true;
+            }
+        }
+        if (taken) atomicMax(&s_taken, taken);
+        if (all_rows > p.num_slots) bad = true;
+        if (bad) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
+    }
     __syncthreads();
-}
+    if (blockIdx.x == 0 && p.count && tid == 0) p.free_out[0] = count - s_taken;
+    if (!p.rows) return;
 
-__global__ void __launch_bounds__(kTblThreads) block_table_kernel(const TableParams p) {
-    __shared__ longlong2 warps[32];
-    __shared__ int s_first[kTblThreads + 1];  // first new block of each request of a chunk
-    __shared__ int s_have[kTblThreads];
-    __shared__ int s_cut;                     // requests from here on are not served
-    pdl_launch_dependents();
-    pdl_wait_prior();
-    const int tid = threadIdx.x;
-    int count = p.free_count[0];
-    bool bad = false;
-    if (count < 0 || count > p.num_free) {
-        count = 0;
-        bad = true;
-    }
-    long long rows = 0, taken = 0;  // of the requests before this chunk
-    long long wanted = 0;
-    bool out = false;  // the free list has run out
-    for (int b0 = 0; b0 < p.B; b0 += kTblThreads) {
-        const int b = b0 + tid;
-        int c = 0, n = 0, have = 0, need = 0;
-        if (b < p.B) {
-            c = p.cached[b];
-            n = p.fresh[b];
-            if (request_ok(c, n, p.max_blocks, p.lg)) {
-                const int bs1 = (1 << p.lg) - 1;
-                have = (c + bs1) >> p.lg;
-                need = ((c + n + bs1) >> p.lg) - have;
-            } else {
-                bad = true;
-                n = max(n, 0);
-            }
-        }
-        long long er, eb, tr, tb;
-        block_scan2(n, need, &er, &eb, &tr, &tb, warps);
-        if (b < p.B) {
-            const long long at = rows + er;
-            p.cu[b] = (int)min(at, 0x7fffffffLL);
-            if (b == p.B - 1) p.cu[p.B] = (int)min(at + n, 0x7fffffffLL);
-        }
-        rows += tr;
-        // served: every request whose blocks end within the list (a prefix of those that need any)
-        const bool fits = !out && wanted + eb + need <= count;
-        const int chunk = min(kTblThreads, p.B - b0);
-        if (tid == 0) s_cut = chunk;
-        s_first[tid] = (int)min(eb, 0x7fffffffLL);
-        s_have[tid] = have;
-        if (tid == 0) s_first[chunk] = (int)min(tb, 0x7fffffffLL);
-        __syncthreads();
-        if (b < p.B && need > 0 && !fits) atomicMin(&s_cut, tid);
-        __syncthreads();
-        const int cut = s_cut;
-        const int blocks = s_first[chunk], good = s_first[cut];
-        // one new block per thread: its request by bisection over s_first
-        for (int e = tid; e < blocks; e += kTblThreads) {
-            int lo = 0, hi = chunk - 1;  // the last request whose first block is <= e
+    for (long long tile = (long long)blockIdx.x * kTblTile; tile < p.num_slots; tile += (long long)gridDim.x * kTblTile) {
+        const int t0 = (int)tile + tid * kTblRows;
+        if (t0 >= p.num_slots) continue;
+        long long slot[kTblRows];
+        int b = 0, first = 0, before = 0, blk = -1, blk_of = -1;
+        Request r = {};
+        bool served = false;
+        // the request after `b` starts at first + r.n
+        auto enter = [&](int nb) {
+            b = nb;
+            r = get_request(p, b);
+            served = r.ok && (long long)first + r.n <= p.num_slots &&
+                     (r.need == 0 || (long long)before + r.need <= count);
+            blk_of = -1;
+        };
+        if (t0 < all_rows) {
+            int lo = 0, hi = (p.B - 1) / per;  // the last thread whose requests start at or before t0
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (s_first[mid] <= e) lo = mid;
+                if (s_rows[mid] <= t0) lo = mid;
                 else hi = mid - 1;
             }
-            const int id = e < good ? p.free_ids[count - 1 - (int)(taken + e)] : -1;
-            p.table[(size_t)(b0 + lo) * p.max_blocks + s_have[lo] + (e - s_first[lo])] = id;
+            first = s_rows[lo];
+            before = s_blocks[lo];
+            enter(lo * per);
         }
-        if (cut < chunk) {
-            out = true;
-            bad = true;
-        }
-        taken += good;
-        wanted += tb;
-        __syncthreads();
-    }
-    if (rows > p.num_slots) bad = true;
-    if (tid == 0) p.free_out[0] = count - (int)taken;
-    if (bad) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
-    if (p.num_slots > kOneBlockSlots) return;
-    // (this block wrote the table and cu_seqlens: visible after the barrier above)
-    for (int t = tid; t < p.num_slots; t += kTblThreads) {
-        long long s = -1;
-        if (t < rows) {
-            int lo = 0, hi = p.B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (p.cu[mid] <= t) lo = mid;
-                else hi = mid - 1;
-            }
-            s = slot_of(p, lo, p.cached[lo], p.fresh[lo], t - p.cu[lo]);
-        }
-        p.slots[t] = s;
-    }
-}
-
-// Slots of many rows: kSlotsPerThread consecutive ones per thread.
-__global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const TableParams p) {
-    pdl_launch_dependents();
-    pdl_wait_prior();
-    const int t0 = (blockIdx.x * kSlotThreads + threadIdx.x) * kSlotsPerThread;
-    if (t0 >= p.num_slots) return;
-    const int rows = p.cu[p.B];
-    int b = 0, next = 0, c = 0, n = 0, first = 0;
-    if (t0 < rows) {
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.cu[mid] <= t0) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
-        first = p.cu[b];
-        next = p.cu[b + 1];
-        c = p.cached[b];
-        n = p.fresh[b];
-    }
-    long long s[kSlotsPerThread];
 #pragma unroll
-    for (int i = 0; i < kSlotsPerThread; ++i) {
-        const int t = t0 + i;
-        s[i] = -1;
-        if (t < rows) {
-            while (t >= next) {  // (ends: t < cu[B])
-                ++b;
-                first = next;
-                next = p.cu[b + 1];
-                c = p.cached[b];
-                n = p.fresh[b];
+        for (int i = 0; i < kTblRows; ++i) {
+            const int t = t0 + i;
+            slot[i] = -1;
+            if (t < all_rows && t < p.num_slots) {
+                while (t >= first + r.n) {  // (ends: t is before the last request's end)
+                    first += r.n;
+                    before = cap32((long long)before + r.need);
+                    enter(b + 1);
+                }
+                if (r.ok) {
+                    const int pos = r.c + (t - first), e = pos >> p.lg;
+                    int32_t *entry = p.table + (size_t)b * p.max_blocks + e;
+                    if (e != blk_of) {
+                        blk_of = e;
+                        blk = !served ? -1 : e < r.have ? *entry : p.free_ids[count - 1 - (before + e - r.have)];
+                    }
+                    // the block's first row writes its entry (-1: none was left)
+                    if (e >= r.have && (pos & ((1 << p.lg) - 1)) == 0) *entry = blk;
+                    if (blk >= 0) slot[i] = ((long long)blk << p.lg) + (pos & ((1 << p.lg) - 1));
+                }
             }
-            s[i] = slot_of(p, b, c, n, t - first);
+        }
+        if ((reinterpret_cast<uintptr_t>(p.slots) & 15u) == 0 && t0 + kTblRows <= p.num_slots) {
+#pragma unroll
+            for (int i = 0; i < kTblRows; i += 2)
+                *reinterpret_cast<longlong2 *>(p.slots + t0 + i) = make_longlong2(slot[i], slot[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTblRows; ++i)
+                if (t0 + i < p.num_slots) p.slots[t0 + i] = slot[i];
         }
     }
-#pragma unroll
-    for (int i = 0; i < kSlotsPerThread; ++i)
-        if (t0 + i < p.num_slots) p.slots[t0 + i] = s[i];
 }
 
 constexpr int kRowThreads = 256;
@@ -339,13 +315,20 @@ int kv_block_tables(const int32_t *cached_lens, const int32_t *new_lens, int32_t
     p.num_free = num_free;
     p.num_slots = num_slots;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_pdl(block_table_kernel, 1, kTblThreads, st, p);
-    if (e != cudaSuccess) return api_cuda_fail(e, "block table launch");
-    if (num_slots > kOneBlockSlots) {
-        const unsigned per = kSlotThreads * kSlotsPerThread;
-        e = launch_pdl(slot_map_kernel, (num_slots + per - 1) / per, kSlotThreads, st, p);
-        if (e != cudaSuccess) return api_cuda_fail(e, "slot map launch");
+    // one block per tile of rows, two to an SM; the count, where it goes back
+    // into the word that every block reads, is written by a launch of its own
+    const int tiles = (num_slots + kTblTile - 1) / kTblTile;
+    const int grid = tiles < 2 * ctas ? tiles : 2 * ctas;
+    const bool apart = grid > 1 && free_count == free_count_out;
+    p.rows = 1;
+    p.count = apart ? 0 : 1;
+    cudaError_t e = launch_pdl(block_table_kernel, grid, kTblThreads, st, p);
+    if (e == cudaSuccess && apart) {
+        p.rows = 0;
+        p.count = 1;
+        e = launch_pdl(block_table_kernel, 1, kTblThreads, st, p);
     }
+    if (e != cudaSuccess) return api_cuda_fail(e, "block table launch");
     return KVATTN_OK;
 }
 

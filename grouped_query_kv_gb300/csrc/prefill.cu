@@ -108,6 +108,7 @@ struct PfCfg {
     static constexpr int bytes = off_sum + 64;
     static constexpr int alloc = bytes + 1024;
     static_assert(NS >= 2 * CPT && NS >= 4, "the ring holds one K and one V tile");
+    static_assert(NQ == 2 || NS == 2 * CPT, "the slots' order that the MMA warps' waits count on");
     static_assert(alloc <= kSmemMax, "shared memory");
     // TMEM: S0, S1 (128 columns each; P over the first 64), then O per tile
     static constexpr int O0 = 256;
@@ -698,12 +699,18 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 for (int j = 0; j < n && ok; ++j, ++g) {
                     const int buf = (int)(g & 1);
                     const long long i0 = base + (warp == 1 ? k_slot<D>(j) : v_slot<D>(j, n));
-                    for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(i0 + c);
+                    // S[buf] holds the P of two tiles ago until its P V is done.  That
+                    // is waited for before the slots: a parity says something only
+                    // once the slot's fill before has landed, and the tile before
+                    // a K tile in its slot may be the V tile of that P V.  (P V
+                    // waits for none whose predecessor is not its own or a K tile
+                    // whose scores its probabilities came from.)
                     if (warp == 1) {
-                        // S[buf] still holds the P of two tiles ago
-                        if (ok && g >= 2) ok = warp_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
-                    } else if (ok) {
+                        if (g >= 2) ok = warp_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
+                        for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(i0 + c);
+                    } else {
                         ok = warp_wait(&p_full[buf], (uint32_t)((g >> 1) & 1), abort_flag, wlim);
+                        for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(i0 + c);
                     }
                     if (!ok) break;
                     tc_fence_after();

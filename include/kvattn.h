@@ -443,14 +443,13 @@ KVATTN_API int gqa_decode_step_fp8(const void *q, const void *k_new, const void 
  *                 with p = c_b + i; rows behind the last token get -1
  *   block_size  : a power of two in [16, 2^20]
  *
- * A request whose lengths are negative or do not fit max_blocks blocks sets
- * KVATTN_ERR_DEVICE_BOUNDS, takes no block and its rows get slot -1 (a
- * negative n counts as 0).  When the free list runs out, the first request
- * that it cannot serve whole and every later one that needs a block take
- * none: the entries they lack become -1, their rows get slot -1, and the
- * error word is set.  So it is when free_count[0] is outside [0, num_free]
- * (taken as 0) or num_slots is less than the sum of n (the rows past it have
- * no slot; cu_seqlens is capped at 2^31 - 1).
+ * A request is served if its lengths are not negative and fit max_blocks
+ * blocks, its rows end within num_slots, and the blocks wanted by it and all
+ * requests before it are no more than free_count[0].  One that is not takes
+ * no block, its rows get slot -1, the table entries it lacks become -1 (those
+ * of its first num_slots rows), and KVATTN_ERR_DEVICE_BOUNDS is set; a
+ * negative n counts as 0 rows.  free_count[0] outside [0, num_free] sets it
+ * too and counts as 0.  cu_seqlens is capped at 2^31 - 1.
  * Limits: B <= 65535, max_blocks * block_size <= 2^24, num_slots <= 2^28.
  */
 KVATTN_API int kv_block_tables(const int32_t *cached_lens, const int32_t *new_lens,

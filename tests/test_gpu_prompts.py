@@ -177,6 +177,24 @@ def test_prefill_many_sequences_and_one_long():
     run_prefill([2500] + rng.integers(0, 40, 90).tolist(), 16, 1, 256, seed=11)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 16, 4), (128, 16, 2), (256, 16, 1)])
+def test_prefill_ragged_launches_back_to_back(D, Hq, Hkv):
+    # many units of every number of key tiles in a CTA's list, three batches in
+    # flight one behind the other: the copy ring turns over across all of them
+    rng = np.random.default_rng(D)
+    runs = []
+    for i in range(3):
+        lens = rng.permutation([0, 1, 130, 257, 700, 1400, 2049, 2900])
+        cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+        q, k, v = (_normal((cu[-1], h, D), 7 * i + j) for j, h in enumerate((Hq, Hkv, Hkv)))
+        runs.append((q, k, v, cu, _i32(cu)))
+    for _ in range(3):
+        outs = [g.gqa_prefill_attn(q, k, v, dcu, D ** -0.5) for q, k, v, _, dcu in runs]
+    g.check_device_error()
+    for (q, k, v, cu, _), out in zip(runs, outs):
+        check_prefill(out, *prefill_ref(q, k, v, cu, D ** -0.5))
+
+
 def test_prefill_neighbours_do_not_meet():
     # a sequence of NaN and infinities between two others: they come out as without it
     for D, Hq, Hkv in ((64, 4, 1), (128, 16, 2), (256, 4, 1)):
@@ -262,7 +280,7 @@ def tables_ref(cached, new, table, free, count, bs, num_slots):
     bad = not 0 <= count <= len(free)
     if bad:
         count = 0
-    cu, slots, taken, wanted, out = [0], [], 0, 0, False
+    cu, slots, taken, wanted = [0], [], 0, 0
     for b, (c, n) in enumerate(zip(cached, new)):
         ok = c >= 0 and n >= 0 and c + n <= maxb * bs
         rows = max(n, 0)
@@ -273,9 +291,11 @@ def tables_ref(cached, new, table, free, count, bs, num_slots):
             continue
         have, upto = -(-c // bs), -(-(c + n) // bs)
         wanted += upto - have
-        if upto > have and (out or wanted > count):
-            out = bad = True
-            table[b, have:upto] = -1
+        if cu[-1] > num_slots or (upto > have and wanted > count):
+            bad = True
+            for e in range(have, upto):  # entries of rows that the slot map holds
+                if cu[b] + e * bs - c < num_slots:
+                    table[b, e] = -1
             slots += [-1] * rows
             continue
         for e in range(have, upto):
