@@ -52,7 +52,7 @@ constexpr int kRows = 128;      // query rows of a tile = keys of a tile
 constexpr int kSlab = 16384;    // 128 rows x 64 columns of bf16
 constexpr int kSmemMax = 232448;
 constexpr float kTauPf = 8.f;   // log2 headroom before the running max must move
-constexpr int kBuckets = 256;
+constexpr int kBuckets = 128;
 constexpr int kDesc = 4;        // units in flight between the work list and its readers
 constexpr int kBarEndPf = 1;
 
@@ -89,9 +89,9 @@ struct PfCfg {
     static constexpr int KC = D < 128 ? D : 128;        // head dims of a ring slot
     static constexpr int CPT = D / KC;                  // slots per K (or V) tile
     static constexpr int SLOT = KC / 64 * kSlab;
-    static constexpr int FIXED = NQ * QT + 1024 + 4096;
+    static constexpr int FIXED = NQ * QT + 1024 + 2048;
     static constexpr int NS_FIT = (kSmemMax - FIXED) / SLOT;
-    static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;  // ring slots
+    static constexpr int NS = NS_FIT > 10 ? 10 : NS_FIT;  // ring slots
     // the first four warps are a warpgroup of their own; with two query tiles
     // it hands registers to the softmax warpgroups
     static constexpr int SOFT0 = 4;                     // first softmax warp
@@ -107,8 +107,7 @@ struct PfCfg {
     static constexpr int off_sum = off_cnt + 2 * kBuckets * 4;
     static constexpr int bytes = off_sum + 64;
     static constexpr int alloc = bytes + 1024;
-    static_assert(NS >= 2 * CPT && NS >= 4, "the ring holds one K and one V tile");
-    static_assert(NQ == 2 || NS == 2 * CPT, "the slots' order that the MMA warps' waits count on");
+    static_assert(NS > 2 * CPT && NS >= 4, "the ring holds more than one K and one V tile");
     static_assert(alloc <= kSmemMax, "shared memory");
     // TMEM: S0, S1 (128 columns each; P over the first 64), then O per tile
     static constexpr int O0 = 256;
@@ -136,6 +135,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
                                           uint32_t limit = KVATTN_SPIN_LIMIT) {
     for (uint32_t it = 0; it < limit; ++it) {
         const bool done = limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
+// A whole warp waits for one barrier per lane (bar null: for nothing) in one
+// loop: each wait of its own cost an issuing warp 190 to 370 cycles, ready or
+// not, in which the tensor pipe ran dry.
+__device__ __forceinline__ bool warp_wait_each(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                               uint32_t limit) {
+    for (uint32_t it = 0; it < limit; ++it) {
+        bool done = true;
+        if (bar) done = limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity);
         if (__all_sync(0xffffffffu, done)) return true;
         if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
     }
@@ -238,6 +252,20 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A place in the ring of NS slots: the slot and the parity of its present fill
+// (counted up: a division by NS of every place took a tenth of the time).
+template <int NS>
+struct Ring {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == NS) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 // A published unit, the same in every lane.
 __device__ __forceinline__ Unit read_unit(const Unit &from) {
     Unit u;
@@ -255,21 +283,13 @@ __device__ __forceinline__ int pf_len(const PrefillParams &p, int b, int *row0) 
     return (a < 0 || e < a || e > p.N) ? -1 : e - a;
 }
 
-// The ring index of K tile j's and V tile j's first slot within a unit of n
-// key tiles: K0 V0 K1 V1 ... with two query tiles (the order the MMAs take
-// them in), K0 K1 V0 K2 V1 ... V(n-1) with one.
-template <int D>
-__device__ __forceinline__ long long k_slot(int j) {
-    using C = PfCfg<D>;
-    if (C::NQ == 2) return 2 * j;
-    return j == 0 ? 0 : (2 * j - 1) * C::CPT;
-}
-template <int D>
-__device__ __forceinline__ long long v_slot(int j, int n) {
-    using C = PfCfg<D>;
-    if (C::NQ == 2) return 2 * j + 1;
-    return (j == n - 1 ? 2 * n - 1 : 2 * j + 2) * C::CPT;
-}
+// Ring order.  Two query tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 K3 ...,
+// counted over all units of a CTA (g).  It is the order the MMA warps take the
+// tiles in, each of them every tile, so that a slot's fill before has always
+// been seen to land when its parity is looked at (a parity alone cannot tell
+// a fill from the one two before).
+__device__ __forceinline__ long long k_tile1(long long g) { return g == 0 ? 0 : 2 * g - 1; }
+__device__ __forceinline__ long long v_tile1(long long g) { return 2 * g + 2; }
 
 template <int D>
 __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
@@ -316,9 +336,10 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         }
         for (int s = 0; s < kDesc; ++s) {
             mbar_init(&u_full[s], 1);
-            mbar_init(&u_empty[s], 3 + 4 * NQ);  // the copy, MMA and softmax warps
+            // readers of a unit: copies (of K and of V), MMAs (twice), softmax warps
+            mbar_init(&u_empty[s], (NQ == 2 ? 3 : 4) + 4 * NQ);
         }
-        mbar_init(drain, 2);  // both MMA warps
+        mbar_init(drain, 2);  // warps 1 and 2
         *abort_flag = 0;
         *sum_pairs = 0;
         *max_nb = 0;
@@ -381,6 +402,29 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     const uint32_t ring_s = smem_u32(ring), qbuf_s = smem_u32(qbuf);
 
     const uint32_t wlim = p.wait_limit ? p.wait_limit : KVATTN_SPIN_LIMIT;
+    // (by a whole warp) unit k of this CTA's list
+    auto next_unit = [&](int k, Unit *u) {
+        if (!warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag)) return false;
+        *u = read_unit(units[k % kDesc]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
+        return true;
+    };
+    // A walk over the key tiles of all units (one query tile).
+    struct Walk {
+        Unit u;
+        int k = -1, g = -1;  // unit, key tile of the CTA
+        int j = 0;           // key tile of the unit
+        bool done = false;
+    };
+    auto step = [&](Walk &w) -> bool {
+        ++w.g;
+        if (w.k >= 0 && ++w.j < w.u.n[0]) return true;
+        w.j = 0;
+        if (!next_unit(++w.k, &w.u)) return false;
+        w.done = w.u.n[0] == 0;
+        return true;
+    };
     if (warp < C::SOFT0) {
     if constexpr (NQ == 2) regs_dec<C::REGS_SERVICE>();
 
@@ -483,61 +527,74 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     if (warp == 0) {
         bool ok = true;
         long long nslot = 0;         // ring slots issued
+        long long left_out = -1;     // (one query tile) the place of a K tile past the last
         uint32_t qn[2] = {0, 0};     // query tiles issued
+        Ring<NS> rc;
+        // (by the whole warp: a uniform wait, then one lane's copies)
         auto issue = [&](const void *tm, int c, int head, int row) -> bool {
-            const int slot = (int)(nslot % NS);
-            bool w = true;
-            if (nslot >= NS)
-                w = pf_wait(&slot_empty[slot], (uint32_t)((nslot / NS - 1) & 1), abort_flag);
-            if (!w) return false;
-            mbar_arrive_expect_tx(&slot_full[slot], C::SLOT);
+            const int slot = rc.slot;
+            if (nslot >= NS && !warp_wait(&slot_empty[slot], rc.parity ^ 1, abort_flag)) return false;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&slot_full[slot], C::SLOT);
 #pragma unroll
-            for (int sl = 0; sl < C::KC / 64; ++sl)
-                tma_load_3d_plain(ring + slot * C::SLOT + sl * kSlab, tm, &slot_full[slot],
-                                  c * C::KC + sl * 64, head, row);
+                for (int sl = 0; sl < C::KC / 64; ++sl)
+                    tma_load_3d_plain(ring + slot * C::SLOT + sl * kSlab, tm, &slot_full[slot],
+                                      c * C::KC + sl * 64, head, row);
+            }
+            __syncwarp();
             ++nslot;
+            rc.next();
             return true;
         };
-        for (long long k = 0;; ++k) {
-            ok = warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
-            if (!ok) break;
-            const Unit cur = read_unit(units[k % kDesc]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
-            if (cur.n[0] == 0) break;
-            if (lane == 0) {
-                const int n = max(cur.n[0], cur.n[1]);
-                const int kv0 = cur.row0 + cur.kbeg;
-                auto load_q = [&]() -> bool {
-                    for (int s = 0; s < NQ; ++s) {
-                        if (cur.n[s] == 0) continue;
-                        if (qn[s] && !pf_wait(&q_empty[s], (qn[s] - 1) & 1, abort_flag)) return false;
-                        mbar_arrive_expect_tx(&q_full[s], C::QT);
-                        for (int sl = 0; sl < C::SLABS; ++sl)
-                            tma_load_3d_plain(qbuf + s * C::QT + sl * kSlab, &tmq, &q_full[s], sl * 64,
-                                              cur.h0, cur.row0 + cur.t0 + s * p.tpt);
-                        ++qn[s];
-                    }
-                    return true;
-                };
-                if (NQ == 2) {
-                    for (int j = 0; j < n && ok; ++j) {
-                        ok = issue(&tmk, 0, cur.kvh, kv0 + j * kRows);
-                        if (ok && j == 0) ok = load_q();
-                        if (ok) ok = issue(&tmv, 0, cur.kvh, kv0 + j * kRows);
-                    }
-                } else {
-                    for (int j = 0; j <= n && ok; ++j) {
-                        for (int c = 0; c < CPT && ok && j < n; ++c)
-                            ok = issue(&tmk, c, cur.kvh, kv0 + j * kRows);
-                        if (ok && j == 0) ok = load_q();
-                        for (int c = 0; c < CPT && ok && j > 0; ++c)
-                            ok = issue(&tmv, c, cur.kvh, kv0 + (j - 1) * kRows);
-                    }
+        auto load_q = [&](const Unit &u) -> bool {
+            for (int s = 0; s < NQ; ++s) {
+                if (u.n[s] == 0) continue;
+                if (qn[s] && !warp_wait(&q_empty[s], (qn[s] - 1) & 1, abort_flag)) return false;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&q_full[s], C::QT);
+#pragma unroll
+                    for (int sl = 0; sl < C::SLABS; ++sl)
+                        tma_load_3d_plain(qbuf + s * C::QT + sl * kSlab, &tmq, &q_full[s], sl * 64, u.h0,
+                                          u.row0 + u.t0 + s * p.tpt);
+                }
+                __syncwarp();
+                ++qn[s];
+            }
+            return true;
+        };
+        if (NQ == 2) {
+            Unit u;
+            for (int k = 0; ok; ++k) {
+                ok = next_unit(k, &u);
+                if (!ok || u.n[0] == 0) break;
+                const int n = max(u.n[0], u.n[1]);
+                const int kv0 = u.row0 + u.kbeg;
+                for (int j = 0; j < n && ok; ++j) {
+                    ok = issue(&tmk, 0, u.kvh, kv0 + j * kRows);
+                    if (ok && j == 0) ok = load_q(u);
+                    if (ok) ok = issue(&tmv, 0, u.kvh, kv0 + j * kRows);
                 }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
+        } else {
+            Walk wk, wv;
+            auto tile = [&](const void *tm, const Walk &w) -> bool {
+                bool go = true;
+                for (int c = 0; c < CPT && go; ++c)
+                    go = issue(tm, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows);
+                return go;
+            };
+            auto put_k = [&]() -> bool {
+                if (wk.done) {  // behind the last K tile its place stays empty
+                    left_out = nslot;
+                    nslot += CPT;
+                    for (int c = 0; c < CPT; ++c) rc.next();
+                    return true;
+                }
+                return tile(&tmk, wk) && (wk.j > 0 || load_q(wk.u)) && step(wk);
+            };
+            ok = step(wk) && step(wv);
+            if (ok && !wk.done) ok = put_k() && put_k();
+            while (ok && !wv.done) ok = tile(&tmv, wv) && step(wv) && (wv.done || put_k());
         }
         if (!ok && lane == 0) {
             pf_error(p.err, DEV_ERR_TIMEOUT);
@@ -550,7 +607,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             // a role gave up: let the copies in flight land before the CTA exits
             volatile int never = 0;
             for (long long i = nslot > NS ? nslot - NS : 0; i < nslot; ++i)
-                pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), &never);
+                if (left_out < 0 || i < left_out || i >= left_out + CPT)
+                    pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), &never);
             for (int s = 0; s < NQ; ++s)
                 if (qn[s]) pf_wait(&q_full[s], (qn[s] - 1) & 1, &never);
         }
@@ -558,9 +616,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     }
 
     // ================================================================== MMA
-    // Two warps issue, so that one's waits do not drain the tensor pipe: with
-    // two query tiles a warp per tile (P V of key tile j - 1, then Q K^T of
-    // j), with one a warp for Q K^T and one for P V.
+    // With two query tiles a warp for each, so that one's waits do not drain the
+    // tensor pipe of the other's MMAs.
     if (warp <= 2) {
         constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, C::KC, false, true);
@@ -569,114 +626,105 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         const int s = NQ == 2 ? warp - 1 : 0;  // query tile
         bool ok = true;
         uint32_t units_q = 0;         // query tiles consumed
-        long long g = 0;              // key tiles so far
-        long long base = 0;           // ring slots of the units before this one
-        uint32_t it = 0;              // turns taken (two query tiles)
+        uint32_t g = 0;               // key tiles so far, its last bit
+        uint32_t it = 0;              // turns taken, the last bit
+        bool first_turn = true;
 
-        // The two query tiles' MMAs go out in turns, the products of one key
-        // tile together: the tiles then keep half a period apart, each in its
-        // softmax while the other's products run (left to share the tensor
-        // cores, both finish together and both wait for both: 8192 tokens, 64
-        // heads over 8 of 128, took 1009 us against ... with turns).
-        auto take_turn = [&]() {
-            return s == 0 ? it == 0 || warp_wait(&turn[0], (it - 1) & 1, abort_flag)
-                          : warp_wait(&turn[1], it & 1, abort_flag);
+        Ring<NS> rc;                  // the next slot that this warp has not waited for
+        auto slot_ready = [&]() {
+            const bool go = warp_wait(&slot_full[rc.slot], rc.parity, abort_flag);
+            rc.next();
+            return go;
         };
-        auto slot_ready = [&](long long i) {
-            return warp_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), abort_flag);
-        };
-        // S[buf] = Q_s K_j^T; keys past the tile's last are left out, 16 at a time
-        auto qk = [&](int buf, long long i0, int keys, bool last) {
+        // S[buf] = Q_s K_j^T from the slots at r; keys past the tile's last are
+        // left out, 16 at a time
+        auto qk = [&](int buf, Ring<NS> r, int keys, bool last) {
             const uint32_t idesc = idesc_qk | ((uint32_t)((keys + 15) / 16 * 2) << 17);
             const uint32_t d = tmem + buf * 128;
             if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const int slot = (int)((i0 + c) % NS);
-                    const uint64_t kd = smem_desc(ring_s + slot * C::SLOT, 16, 1024, 2);
+                for (int c = 0; c < CPT; ++c, r.next()) {
+                    const uint64_t kd = smem_desc(ring_s + r.slot * C::SLOT, 16, 1024, 2);
                     const uint64_t qd = smem_desc(qbuf_s + s * C::QT + c * (C::KC / 64) * kSlab, 16, 1024, 2);
 #pragma unroll
                     for (int kk = 0; kk < C::KC / 16; ++kk) {
                         const uint64_t o = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
                         umma_bf16(d, qd + o, kd + o, idesc, c != 0 || kk != 0);
                     }
-                    umma_commit(&slot_empty[slot]);
+                    umma_commit(&slot_empty[r.slot]);
                 }
                 umma_commit(&s_full[buf]);
                 if (last) umma_commit(&q_empty[s]);
             }
             __syncwarp();
         };
-        // O_s (+)= P[buf] V_j
-        auto pv = [&](int buf, long long i0, int keys, bool first) {
+        // O_s (+)= P[buf] V_j from the slots at r
+        auto pv = [&](int buf, Ring<NS> r, int keys, bool first) {
             const uint32_t a = tmem + buf * 128, d = tmem + C::O0 + s * D;
             if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const int slot = (int)((i0 + c) % NS);
-                    const uint64_t vd = smem_desc(ring_s + slot * C::SLOT, kSlab, 1024, 2);
+                for (int c = 0; c < CPT; ++c, r.next()) {
+                    const uint64_t vd = smem_desc(ring_s + r.slot * C::SLOT, kSlab, 1024, 2);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         if (kk * 16 < keys)
                             umma_bf16_ts(d + c * C::KC, a + kk * 8, vd + kk * (2048 >> 4), IDESC_PV,
                                          !(first && kk == 0));
                     }
-                    umma_commit(&slot_empty[slot]);
+                    umma_commit(&slot_empty[r.slot]);
                 }
                 umma_commit(&pv_done[buf]);
             }
             __syncwarp();
         };
 
-        auto next_unit = [&](long long k, Unit *u) {
-            if (!warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag)) return false;
-            *u = read_unit(units[k % kDesc]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
-            return true;
-        };
-
         Unit u;
         if (NQ == 2) {
-            // A turn: P V of the step before, then Q K^T of this one (of the
-            // next unit's first key tile, too).  Everything else is waited for
-            // before the probabilities, the last to come.
+            // The two query tiles' MMAs go out in turns, the products of one key
+            // tile together: P V of the step before, then Q K^T of this one (of
+            // the next unit's first key tile, too).  The query tiles then keep
+            // half a period apart, each in its softmax while the other's
+            // products run.  Measured at 8192 tokens, 64 heads over 8 of 128:
+            // left to share the tensor cores, both finish together and both
+            // wait for both, 1009 us; in turns 869 us.
             int owed = 0;            // the step before: 1 its P V is due, 2 its V tile was not needed
-            long long owed_iv = 0;
             int owed_keys = 0;
             bool owed_first = false;
             auto turn_of = [&](int n, int nmax, int j, int end) {  // j = nmax: the last P V alone
-                const long long ik = base + 2 * j;
+                // (one uniform wait after the other: what comes early is waited for
+                // while the other tile's MMAs are still running)
                 bool go = true;
-                if (owed) go = slot_ready(owed_iv);
-                if (go && j < nmax) go = slot_ready(ik);
+                const Ring<NS> rv = rc;
+                if (owed) go = slot_ready();
+                const Ring<NS> rk = rc;
+                if (go && j < nmax) go = slot_ready();
                 if (go && j == 0 && n > 0) go = warp_wait(&q_full[s], units_q++ & 1, abort_flag);
-                if (go) go = take_turn();
-                if (go && owed == 1) go = warp_wait(&p_full[s], (uint32_t)((g - 1) & 1), abort_flag, wlim);
+                if (go && (s == 1 || !first_turn)) go = warp_wait(&turn[s], s == 0 ? it ^ 1 : it, abort_flag);
+                if (go && owed == 1) go = warp_wait(&p_full[s], g ^ 1, abort_flag, wlim);
                 if (!go) return false;
                 tc_fence_after();
                 if (owed == 1)
-                    pv(s, owed_iv, owed_keys, owed_first);
+                    pv(s, rv, owed_keys, owed_first);
                 else if (owed == 2 && lane == 0)
-                    mbar_arrive(&slot_empty[owed_iv % NS]);
+                    mbar_arrive(&slot_empty[rv.slot]);
                 owed = 0;
                 if (j < n) {
                     const int keys = min(kRows, end - j * kRows);
-                    qk(s, ik, keys, j == n - 1);
-                    ++g;
+                    qk(s, rk, keys, j == n - 1);
+                    g ^= 1;
                     owed = 1;
                     owed_keys = keys;
                     owed_first = j == 0;
                 } else if (j < nmax) {
-                    if (lane == 0) mbar_arrive(&slot_empty[ik % NS]);
+                    if (lane == 0) mbar_arrive(&slot_empty[rk.slot]);
                     owed = 2;
                 }
-                owed_iv = ik + 1;
                 if (lane == 0) mbar_arrive(&turn[s ^ 1]);
-                ++it;
+                it ^= 1;
+                first_turn = false;
                 return true;
             };
-            for (long long k = 0; ok; ++k) {
+            for (int k = 0; ok; ++k) {
                 ok = next_unit(k, &u);
                 if (!ok) break;
                 if (u.n[0] == 0) {
@@ -687,40 +735,60 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 // keys of the unit's key tiles that the query tile attends at most
                 const int end = min(u.t0 + (s + 1) * p.tpt, u.len) - u.kbeg;
                 for (int j = 0; j < nmax && ok; ++j) ok = turn_of(n, nmax, j, end);
-                base += 2 * nmax;
             }
-        } else {
-            for (long long k = 0; ok; ++k) {
-                ok = next_unit(k, &u);
-                if (!ok || u.n[0] == 0) break;
-                const int n = u.n[0];
-                const int end = min(u.t0 + p.tpt, u.len) - u.kbeg;
-                if (warp == 1) ok = warp_wait(&q_full[0], units_q++ & 1, abort_flag);
-                for (int j = 0; j < n && ok; ++j, ++g) {
-                    const int buf = (int)(g & 1);
-                    const long long i0 = base + (warp == 1 ? k_slot<D>(j) : v_slot<D>(j, n));
-                    // S[buf] holds the P of two tiles ago until its P V is done.  That
-                    // is waited for before the slots: a parity says something only
-                    // once the slot's fill before has landed, and the tile before
-                    // a K tile in its slot may be the V tile of that P V.  (P V
-                    // waits for none whose predecessor is not its own or a K tile
-                    // whose scores its probabilities came from.)
-                    if (warp == 1) {
-                        if (g >= 2) ok = warp_wait(&pv_done[buf], (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
-                        for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(i0 + c);
-                    } else {
-                        ok = warp_wait(&p_full[buf], (uint32_t)((g >> 1) & 1), abort_flag, wlim);
-                        for (int c = 0; c < CPT && ok; ++c) ok = slot_ready(i0 + c);
-                    }
-                    if (!ok) break;
-                    tc_fence_after();
-                    const int keys = min(kRows, end - j * kRows);
-                    if (warp == 1)
-                        qk(buf, i0, keys, j == n - 1);
-                    else
-                        pv(buf, i0, keys, j == 0);
+        } else if (warp == 1) {
+            // One warp issues P V of key tile g, then Q K^T of g + 2 into the S
+            // buffer that P V has just read (the same thread's MMAs run in
+            // order), with the probabilities the last thing waited for.
+            Walk wq, wp;
+            auto keys_of = [&](const Walk &w) {
+                return min(kRows, min(w.u.t0 + p.tpt, w.u.len) - w.u.kbeg - w.j * kRows);
+            };
+            auto scores = [&](Ring<NS> r) -> bool {
+                qk(wq.g & 1, r, keys_of(wq), wq.j == wq.u.n[0] - 1);
+                return step(wq);
+            };
+            // Waits, a barrier a lane, for the V tile at rv and the
+            // probabilities (with_p) and for the K tile at rk and a unit's
+            // first q (with_k).
+            auto ready = [&](Ring<NS> rv, Ring<NS> rk, bool with_p, bool with_k) {
+                uint64_t *bar = nullptr;
+                uint32_t parity = 0;
+#pragma unroll
+                for (int c = 0; c < CPT; ++c, rv.next(), rk.next()) {
+                    if (lane == c && with_p) bar = &slot_full[rv.slot], parity = rv.parity;
+                    if (lane == CPT + c && with_k) bar = &slot_full[rk.slot], parity = rk.parity;
                 }
-                base += 2 * n * CPT;
+                const bool with_q = with_k && wq.j == 0;
+                if (lane == 2 * CPT && with_q) bar = &q_full[0], parity = units_q & 1;
+                if (lane == 2 * CPT + 1 && with_p) bar = &p_full[wp.g & 1], parity = (wp.g >> 1) & 1;
+                if (with_q) ++units_q;
+                return warp_wait_each(bar, parity, abort_flag, with_p ? wlim : KVATTN_SPIN_LIMIT);
+            };
+            auto pass_tile = [&]() {
+                const Ring<NS> r = rc;
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) rc.next();
+                return r;
+            };
+            ok = step(wq) && step(wp);
+            for (int i = 0; i < 2 && ok; ++i) {
+                const Ring<NS> rk = pass_tile();
+                if (wq.done) break;  // (no second key tile: its place stays empty)
+                ok = ready(rk, rk, false, true);
+                if (!ok) break;
+                tc_fence_after();
+                ok = scores(rk);
+            }
+            while (ok && !wp.done) {
+                const Ring<NS> rv = pass_tile(), rk = pass_tile();
+                const bool more = !wq.done;
+                ok = ready(rv, rk, true, more);
+                if (!ok) break;
+                tc_fence_after();
+                pv(wp.g & 1, rv, keys_of(wp), wp.j == 0);
+                if (more) ok = scores(rk);
+                if (ok) ok = step(wp);
             }
         }
         if (!ok) {
@@ -755,13 +823,10 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     long long base = 0;   // ring slots of the units before this one
     bool ok = true;
 
-    for (long long k = 0;; ++k) {
-        ok = warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag);
-        if (!ok) break;
-        const Unit u = read_unit(units[k % kDesc]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
-        if (u.n[0] == 0) break;
+    Unit u;
+    for (int k = 0;; ++k) {
+        ok = next_unit(k, &u);
+        if (!ok || u.n[0] == 0) break;
         const int n = u.n[s], nmax = max(u.n[0], u.n[1]);
         const int first_tok = u.t0 + s * p.tpt;
         const int end_tok = min(first_tok + p.tpt, u.len);
@@ -881,7 +946,10 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             // anything, which a weight of zero does not hide: they are zeroed
             const int stop = (keys + 15) / 16 * 16, past = u.len - kb;
             if (past < stop) {
-                const long long iv = base + v_slot<D>(j, nmax);
+                const long long iv = NQ == 2 ? base + 2 * j + 1 : v_tile1(g) * CPT;
+                // (one query tile: the scores may be two tiles ahead of P V, and
+                // the slot's parity says something once the V tile before is done with)
+                if (NQ == 1 && g > 0) ok = warp_wait(&pv_done[buf ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abort_flag);
                 for (int c = 0; c < CPT && ok; ++c) {
                     const int slot = (int)((iv + c) % NS);
                     ok = warp_wait(&slot_full[slot], (uint32_t)(((iv + c) / NS) & 1), abort_flag);
@@ -925,7 +993,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             tc_fence_before();
             __syncwarp();
         }
-        base += 2 * nmax * CPT;
+        base += 2 * nmax;
     }
     if (!ok) {
         pf_error(p.err, DEV_ERR_TIMEOUT);
