@@ -10,13 +10,16 @@
 // a code written before its scale grew is the code it would have had, unless
 // its value fell below E4M3's normal range).
 //
-// A block of 128 threads writes one (pool block, K/V head) of K or of V: it
-// owns the scale, so nothing is shared between blocks and no atomic decides
-// an order.  Blocks of the grid are candidates: x < B is request x's first
-// touched pool block (the one that may hold earlier rows), x >= B the pool
-// blocks that start inside the bs packed rows from (x - B) bs.  What bounds
-// it is the copy: 2 bytes read and 1 written per value; the rows are read
-// twice (largest magnitude, then codes), the second time from L1.
+// A block of 128 threads writes (pool block, K/V head) pairs of K and of V one
+// after the other: it owns their scales, so nothing is shared between blocks
+// and no atomic decides an order.  Blocks of the grid are candidates: x < B is
+// request x's first touched pool block (the one that may hold earlier rows),
+// x >= B the pool blocks that start inside the bs packed rows from (x - B) bs;
+// y takes every gridDim.y-th head, K and V (few where there are many
+// candidates: a candidate's search for its request then serves all heads).
+// What bounds it is the copy: 2 bytes read and 1 written per value.  Up to
+// kHeld 16-byte vectors a thread the new rows stay in registers between the
+// search for the largest and the rounding; longer blocks read them again.
 #include <cuda_fp16.h>
 
 #include "../../include/kvattn.h"
@@ -68,11 +71,30 @@ __device__ __forceinline__ uint32_t rescale2(uint32_t two, float f) {
     return e4m3x2_from_f32(v.x * f, v.y * f);
 }
 
-// Writes rows [r0, r0 + m) of the pool block at positions pos.. of request b
-// from packed rows t.. ; called by the whole block.
+constexpr int kHeld = 8;
+
+__device__ __forceinline__ float absmax8(uint4 raw, float a) {
+    float x[8];
+    unpack8(raw, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));
+    return a;
+}
+__device__ __forceinline__ uint2 codes8(uint4 raw, float inv) {
+    float x[8];
+    unpack8(raw, x);
+    return make_uint2((uint32_t)e4m3x2_from_f32(x[0] * inv, x[1] * inv) |
+                          ((uint32_t)e4m3x2_from_f32(x[2] * inv, x[3] * inv) << 16),
+                      (uint32_t)e4m3x2_from_f32(x[4] * inv, x[5] * inv) |
+                          ((uint32_t)e4m3x2_from_f32(x[6] * inv, x[7] * inv) << 16));
+}
+
+// Writes m packed rows from row t to positions pos.. (of one pool block) of
+// request b, for head h of K (kv = 0) or V; called by the whole block, `turn`
+// counting its calls.
 template <int D>
 __device__ __forceinline__ void write_block(const Append8Params &p, int kv, int h, int b, int pos, int t,
-                                            int m, float *red) {
+                                            int m, float (*red)[4], int turn) {
     constexpr int VPR = D / 8;               // 16-byte vectors of a new row
     constexpr int RPP = kThreads / VPR;      // rows per pass
     const int tid = threadIdx.x;
@@ -85,29 +107,37 @@ __device__ __forceinline__ void write_block(const Append8Params &p, int kv, int 
     const size_t bh = (size_t)blk * p.Hkv + h;
     uint8_t *codes = p.codes[kv] + (bh << p.lg) * D;
     float *scale = p.scales[kv] + bh;
-    const uint16_t *src = p.rows[kv] + (long long)t * p.stride[kv] + (size_t)h * D + (tid % VPR) * 8;
+    const int row = tid / VPR;
+    const long long stride = p.stride[kv];
+    const uint16_t *src = p.rows[kv] + (t + row) * stride + (size_t)h * D + (tid % VPR) * 8;
     const float old = r0 > 0 ? *scale : 0.f;
+    const bool held = m <= kHeld * RPP;
 
+    uint4 raw[kHeld];
     float a = 0.f;
-    for (int r = tid / VPR; r < m; r += 4 * RPP) {
-        uint4 raw[4];
+    if (held) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            raw[i] = r + i * RPP < m ? *reinterpret_cast<const uint4 *>(src + (r + i * RPP) * p.stride[kv])
-                                     : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < kHeld; ++i)
+            raw[i] = row + i * RPP < m ? __ldcs(reinterpret_cast<const uint4 *>(src + i * RPP * stride))
+                                       : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x[8];
-            unpack8(raw[i], x);
+        for (int i = 0; i < kHeld; ++i) a = absmax8(raw[i], a);
+    } else {
+        for (int r = 0; row + r < m; r += kHeld * RPP) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));
+            for (int i = 0; i < kHeld; ++i)
+                raw[i] = row + r + i * RPP < m ? *reinterpret_cast<const uint4 *>(src + (r + i * RPP) * stride)
+                                               : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) a = absmax8(raw[i], a);
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if ((tid & 31) == 0) red[tid >> 5] = a;
-    __syncthreads();  // (every thread has read the old scale, too)
-    a = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    float *mine = red[turn & 1];  // (the barrier of the next call keeps the one after from this buffer)
+    if ((tid & 31) == 0) mine[tid >> 5] = a;
+    __syncthreads();              // (every thread has read the old scale, too)
+    a = fmaxf(fmaxf(mine[0], mine[1]), fmaxf(mine[2], mine[3]));
     const float now = fmaxf(old, __uint_as_float((uint32_t)(127 + scale_exponent(a)) << 23));
     if (tid == 0) *scale = now;
     if (r0 > 0 && now > old) {
@@ -125,23 +155,22 @@ __device__ __forceinline__ void write_block(const Append8Params &p, int kv, int 
         }
     }
     const float inv = 1.f / now;  // exact: 2^-120 .. 2^100
-    uint8_t *dst = codes + (size_t)r0 * D + (tid % VPR) * 8;
-    for (int r = tid / VPR; r < m; r += 4 * RPP) {
-        uint4 raw[4];
+    uint8_t *dst = codes + (size_t)(r0 + row) * D + (tid % VPR) * 8;
+    if (held) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (r + i * RPP < m) raw[i] = *reinterpret_cast<const uint4 *>(src + (r + i * RPP) * p.stride[kv]);
+        for (int i = 0; i < kHeld; ++i)
+            if (row + i * RPP < m) *reinterpret_cast<uint2 *>(dst + i * RPP * D) = codes8(raw[i], inv);
+    } else {
+        for (int r = 0; row + r < m; r += kHeld * RPP) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (r + i * RPP < m) {
-                float x[8];
-                unpack8(raw[i], x);
-                const uint32_t lo = (uint32_t)e4m3x2_from_f32(x[0] * inv, x[1] * inv) |
-                                    ((uint32_t)e4m3x2_from_f32(x[2] * inv, x[3] * inv) << 16);
-                const uint32_t hi = (uint32_t)e4m3x2_from_f32(x[4] * inv, x[5] * inv) |
-                                    ((uint32_t)e4m3x2_from_f32(x[6] * inv, x[7] * inv) << 16);
-                *reinterpret_cast<uint2 *>(dst + (size_t)(r + i * RPP) * D) = make_uint2(lo, hi);
-            }
+            for (int i = 0; i < kHeld; ++i)
+                if (row + r + i * RPP < m)
+                    raw[i] = *reinterpret_cast<const uint4 *>(src + (r + i * RPP) * stride);
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                if (row + r + i * RPP < m)
+                    *reinterpret_cast<uint2 *>(dst + (size_t)(r + i * RPP) * D) = codes8(raw[i], inv);
+        }
     }
 }
 
@@ -158,30 +187,35 @@ __device__ __forceinline__ bool request(const Append8Params &p, int b, int *firs
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_paged8_kernel(const Append8Params p) {
-    __shared__ float red[4];
+    __shared__ float red[2][4];
     __shared__ int found;
     __shared__ int s_b[kMaxBlock], s_t[kMaxBlock];
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int kv = blockIdx.y & 1, h = blockIdx.y >> 1;
     const int bs = 1 << p.lg;
-    int first, n, c;
+    int first, n, c, turn = 0;
     bool bad;
     if ((int)blockIdx.x < p.B) {
         const int b = blockIdx.x;
         const bool some = request(p, b, &first, &n, &c, &bad);
         if (bad && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
-        if (some) write_block<D>(p, kv, h, b, c, first, min(n, bs - (c & (bs - 1))), red);
+        if (some)
+            for (int hk = blockIdx.y; hk < 2 * p.Hkv; hk += gridDim.y)
+                write_block<D>(p, hk & 1, hk >> 1, b, c, first, min(n, bs - (c & (bs - 1))), red, turn++);
         return;
     }
     // pool blocks that start at packed rows [t0, t1), the requests' first
     // touched ones aside: of bs consecutive rows of a request one starts a block
     const int t0 = (int)(blockIdx.x - p.B) << p.lg, t1 = min(t0 + bs, p.N);
-    int lo = 0, hi = p.B - 1;  // the last request that starts at or before t0
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cu[mid] <= t0) lo = mid;
-        else hi = mid - 1;
+    // the last request that starts at or before t0, 32 probes at a time
+    int lo = 0, span = p.B;  // it is in [lo, lo + span)
+    while (span > 1) {
+        const int each = (span + 31) / 32, at = lo + (int)(threadIdx.x & 31) * each;
+        const bool before = (threadIdx.x & 31) * each < span && p.cu[at] <= t0;
+        const int past = __popc(__ballot_sync(0xffffffffu, before));  // (cu does not decrease)
+        const int step = max(past - 1, 0) * each;
+        lo += step;
+        span = min(each, span - step);
     }
     if (threadIdx.x == 0) found = 0;
     __syncthreads();
@@ -202,8 +236,8 @@ __global__ void __launch_bounds__(kThreads) append_paged8_kernel(const Append8Pa
     for (int i = 0; i < blocks; ++i) {
         const int b = s_b[i], t = s_t[i];
         request(p, b, &first, &n, &c, &bad);
-        write_block<D>(p, kv, h, b, c + t - first, t, min(bs, first + n - t), red);
-        __syncthreads();  // `red` again
+        for (int hk = blockIdx.y; hk < 2 * p.Hkv; hk += gridDim.y)
+            write_block<D>(p, hk & 1, hk >> 1, b, c + t - first, t, min(bs, first + n - t), red, turn++);
     }
 }
 
@@ -263,7 +297,10 @@ extern "C" int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)B + (unsigned)((N + block_size - 1) / block_size), 2u * (unsigned)Hkv);
+    // candidates, and enough splits of the heads to give every SM eight blocks
+    const long long cand = (long long)B + ((long long)N + block_size - 1) / block_size;
+    const long long split = (8LL * ctas + cand - 1) / cand;
+    cfg.gridDim = dim3((unsigned)cand, (unsigned)(split < 2 * Hkv ? split : 2 * Hkv));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
