@@ -619,11 +619,11 @@ def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count,
     _want(free_count, "free_count", i32, dev, (1,))
     num_slots = int(num_slots)
     if cu_seqlens is None:
-        cu_seqlens = cached_lens.new_empty(B + 1)
+        cu_seqlens = torch.empty(B + 1, dtype=i32, device=cached_lens.device)
     else:
         _want(cu_seqlens, "cu_seqlens", i32, dev, (B + 1,))
     if slots is None:
-        slots = cached_lens.new_empty(max(num_slots, 0), dtype=torch.int64)
+        slots = torch.empty(max(num_slots, 0), dtype=torch.int64, device=cached_lens.device)
     else:
         _want(slots, "slots", torch.int64, dev, (num_slots,))
     if free_count_out is None:
@@ -753,7 +753,7 @@ def gqa_decode_attn_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table
         raise ValueError("k_codes / block_table do not match q")
     _want(seq_lens, "seq_lens", torch.int32, dev, (B,))
     if out is None:
-        out = q.new_empty((B, Hq, D))
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
     else:
         _want(out, "out", torch.bfloat16, dev, (B, Hq, D))
     _check(lib().gqa_decode_attn_paged_fp8(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),

@@ -297,9 +297,10 @@ extern "C" int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     cudaLaunchConfig_t cfg = {};
-    // candidates, and enough splits of the heads to give every SM eight blocks
+    // candidates, and enough splits of the heads to give every SM 32 blocks (65 thousand
+    // rows of 8 heads of 128: 8 blocks 80 us, 16 76, 32 73.6, 64 73)
     const long long cand = (long long)B + ((long long)N + block_size - 1) / block_size;
-    const long long split = (8LL * ctas + cand - 1) / cand;
+    const long long split = (32LL * ctas + cand - 1) / cand;
     cfg.gridDim = dim3((unsigned)cand, (unsigned)(split < 2 * Hkv ? split : 2 * Hkv));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
