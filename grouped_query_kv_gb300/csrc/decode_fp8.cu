@@ -76,6 +76,25 @@ constexpr float kTauQ8 = 2.f;    // rescale once a score passes the running max 
 constexpr float kVHi = 64.f;     // v_scale[j] 2^cv stays <= 64
 constexpr int kCvNone = 1 << 20; // cv not chosen yet (piece start)
 
+// wait_bar by a whole warp, which leaves it together.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    for (uint32_t it = 0; it < KVATTN_SPIN_LIMIT; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
+    return r != 0;
+}
+
 template <int D, int NP>
 struct Q8Cfg {
     static constexpr int SL = D / 128;        // 128-code slabs per row
@@ -124,8 +143,7 @@ struct Q8Cfg {
     // TMEM: S0, S1 (side by side: 2 NP columns each, hi part then lo part),
     // then per 128 head dims an O^T accumulator (3 NP columns: hi, mid, lo
     // parts of P)
-    static constexpr bool SBS = true;
-    static constexpr int SW = SBS ? 2 * NP : NP;
+    static constexpr int SW = 2 * NP;
     static constexpr int OA = 2 * SW;
     static constexpr int TMEM_COLS = pow2_at_least(OA + SL * 3 * NP);
     static constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, SW, false, false);
@@ -319,9 +337,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
         auto issue = [&](const void *tm, const TileIter &it, uint8_t *base, uint64_t *full,
                          uint64_t *empty, int ns, long long &n, int y, int z_) -> bool {
             const int slot = (int)(n % ns);
-            bool w = true;
-            if (lane == 0 && n >= ns) w = wait_bar(&empty[slot], (uint32_t)(((n / ns) - 1) & 1), abort_flag);
-            if (!__shfl_sync(0xffffffffu, w, 0)) return false;
+            if (n >= ns && !wait_bar_warp(&empty[slot], (uint32_t)(((n / ns) - 1) & 1), abort_flag))
+                return false;
             if (PG) {
                 if (lane == 0) mbar_arrive_expect_tx(&full[slot], kStage);
                 __syncwarp();
@@ -501,113 +518,110 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
     }
 
     // ================================================================== MMA
+    // The whole warp walks the tiles; a poll tests every barrier that either
+    // product is waiting for at once, a lane each (one lane testing them one
+    // after the other took some 90 cycles apiece, as long as the MMAs).
     if (warp == 1) {
-        if (lane == 0) {
-            TileIter itq, itp;
-            itq.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
-            itp.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
-            long long iq = 0, ip = 0;
-            int piece_q = 0, piece_pv = 0, qcur = 0;
-            uint32_t idle = 0;
-            bool ok = true;
-            while (ip < ntiles) {
-                bool did = false;
-                if (ip < iq) {  // P V of tile ip: 32 positions per MMA, the 3 P parts side by side
-                    const long long j = ip;
-                    const int pb = (int)(j & 1);
-                    const bool first_pv = (j == 0) || (itp.t == 0);
-                    bool ready = mbar_test(&p_full[pb], (uint32_t)((j >> 1) & 1));
-                    if (ready && first_pv && piece_pv > 0)
-                        ready = mbar_test(o_free, (uint32_t)((piece_pv - 1) & 1));
-                    const int slot = (int)(j % NSV);
-                    if (ready) ready = mbar_test(&vst_full[slot], (uint32_t)((j / NSV) & 1));
-                    if (ready) {
-                        if (first_pv) ++piece_pv;
-                        tc_fence_after();
-                        const uint32_t pstage = pbuf_s + (int)(j % C::PST) * C::PB;
-                        const uint32_t v0 = vst_s + slot * kStage;
+        TileIter itq, itp;
+        itq.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
+        itp.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
+        const int nt = (int)ntiles;
+        int iq = 0, ip = 0;
+        int kslot = 0, vslot = 0;            // iq % NSK, ip % NSV
+        uint32_t kpar = 0, vpar = 0;         // (iq / NSK) & 1, (ip / NSV) & 1
+        int piece_q = 0, piece_pv = 0, qcur = 0;
+        uint32_t idle = 0;
+        bool ok = true;
+        while (ip < nt) {
+            const int pb = ip & 1, sb = iq & 1;
+            const bool first_pv = ip == 0 || itp.t == 0, first_q = iq == 0 || itq.t == 0;
+            const bool want_pv = ip < iq, want_q = iq < nt;
+            uint64_t *bar = nullptr;
+            uint32_t par = 0;
+            if (lane == 0 && want_pv) bar = &p_full[pb], par = (ip >> 1) & 1;
+            if (lane == 1 && want_pv && first_pv && piece_pv > 0) bar = o_free, par = (piece_pv - 1) & 1;
+            if (lane == 2 && want_pv) bar = &vst_full[vslot], par = vpar;
+            if (lane == 3 && want_q && first_q) bar = &q_full[piece_q & 1], par = (piece_q >> 1) & 1;
+            if (lane == 4 && want_q && iq >= 2) bar = &s_empty[sb], par = ((iq >> 1) - 1) & 1;
+            if (lane == 5 && want_q) bar = &kst_full[kslot], par = kpar;
+            bool there = true;
+            if (bar) there = mbar_test(bar, par);
+            const uint32_t ready = __ballot_sync(0xffffffffu, there);
+            bool did = false;
+            if (want_pv && (ready & 7u) == 7u) {  // P V of tile ip: 32 positions per MMA, the 3 P parts side by side
+                if (first_pv) ++piece_pv;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t pstage = pbuf_s + (ip % C::PST) * C::PB;
+                    const uint32_t v0 = vst_s + vslot * kStage;
 #pragma unroll
-                        for (int sl = 0; sl < SL; ++sl) {  // head dims 128 sl .. 128 sl + 127
+                    for (int sl = 0; sl < SL; ++sl) {  // head dims 128 sl .. 128 sl + 127
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                // A = V^T: the staged box read position-major (SW128);
-                                // B = P: position-major, no swizzle, 16-column blocks
-                                const uint64_t ad = smem_desc(v0 + sl * kBox + kk * 4096, 16384, 1024, 2);
-                                const uint64_t bd = smem_desc(pstage + kk * 512, 128, 2048, 0);
-                                umma_f8(tmem + C::OA + sl * 3 * NP, ad, bd, C::IDESC_PV,
-                                        !(first_pv && kk == 0));
-                            }
+                        for (int kk = 0; kk < 4; ++kk) {
+                            // A = V^T: the staged box read position-major (SW128);
+                            // B = P: position-major, no swizzle, 16-column blocks
+                            const uint64_t ad = smem_desc(v0 + sl * kBox + kk * 4096, 16384, 1024, 2);
+                            const uint64_t bd = smem_desc(pstage + kk * 512, 128, 2048, 0);
+                            umma_f8(tmem + C::OA + sl * 3 * NP, ad, bd, C::IDESC_PV, !(first_pv && kk == 0));
                         }
-                        umma_commit(&vst_empty[slot]);
-                        umma_commit(&pv_done[pb]);
-                        if (j < ntiles - 1) itp.next();
-                        ++ip;
-                        did = true;
                     }
+                    umma_commit(&vst_empty[vslot]);
+                    umma_commit(&pv_done[pb]);
                 }
-                if (iq < ntiles) {  // Q K^T of tile iq
-                    const long long i = iq;
-                    const int sb = (int)(i & 1);
-                    const bool first_q = (i == 0) || (itq.t == 0);
-                    bool ready = true;
-                    if (first_q) ready = mbar_test(&q_full[piece_q & 1], (uint32_t)((piece_q >> 1) & 1));
-                    if (ready && i >= 2) ready = mbar_test(&s_empty[sb], (uint32_t)(((i >> 1) - 1) & 1));
-                    const int slot = (int)(i % NSK);
-                    if (ready) ready = mbar_test(&kst_full[slot], (uint32_t)((i / NSK) & 1));
-                    if (ready) {
-                        if (first_q) {
-                            qcur = piece_q & 1;
-                            ++piece_q;
+                __syncwarp();
+                if (ip < nt - 1) itp.next();
+                ++ip;
+                if (++vslot == NSV) vslot = 0, vpar ^= 1;
+                did = true;
+            }
+            if (want_q && (ready & 56u) == 56u) {  // Q K^T of tile iq
+                if (first_q) {
+                    qcur = piece_q & 1;
+                    ++piece_q;
+                }
+                tc_fence_after();
+                const bool piece_end = itq.last_tile_of_segment() || iq == nt - 1;
+                if (elect_one()) {
+                    const uint32_t a0 = kst_s + kslot * kStage;
+                    const uint32_t b0 = qbuf_s + qcur * C::QB;
+                    // 32 codes per MMA, the hi and lo rows one operand of 2 NP rows
+#pragma unroll
+                    for (int sl = 0; sl < SL; ++sl)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t ad = smem_desc(a0 + sl * kBox + kk * 32, 16, 1024, 2);
+                            const uint64_t bd = smem_desc(b0 + sl * C::QSL + kk * 32, 16, 1024, 2);
+                            umma_f8(tmem + sb * C::SW, ad, bd, C::IDESC_QK, sl != 0 || kk != 0);
                         }
-                        tc_fence_after();
-                        const uint32_t a0 = kst_s + slot * kStage;
-                        const uint32_t b0 = qbuf_s + qcur * C::QB;
-                        // 32 codes per MMA; side by side the hi and lo rows are one
-                        // operand of 2 NP rows, else the lo part follows the hi part
-#pragma unroll
-                        for (int part = 0; part < (C::SBS ? 1 : 2); ++part)
-#pragma unroll
-                            for (int sl = 0; sl < SL; ++sl)
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) {
-                                    const uint64_t ad = smem_desc(a0 + sl * kBox + kk * 32, 16, 1024, 2);
-                                    const uint64_t bd = smem_desc(
-                                        b0 + sl * C::QSL + part * (NP * 128) + kk * 32, 16, 1024, 2);
-                                    umma_f8(tmem + sb * C::SW, ad, bd, C::IDESC_QK,
-                                            part != 0 || sl != 0 || kk != 0);
-                                }
-                        umma_commit(&kst_empty[slot]);
-                        umma_commit(&s_full[sb]);
-                        if (itq.last_tile_of_segment() || i == ntiles - 1) umma_commit(&q_empty[qcur]);
-                        if (i < ntiles - 1) itq.next();
-                        ++iq;
-                        did = true;
-                    }
+                    umma_commit(&kst_empty[kslot]);
+                    umma_commit(&s_full[sb]);
+                    if (piece_end) umma_commit(&q_empty[qcur]);
                 }
-                if (did) {
-                    idle = 0;
-                    continue;
-                }
-                ++idle;
-                if ((idle & 255u) == 0 && *abort_flag) {
-                    ok = false;
-                    break;
-                }
-                if (idle >= kMmaIdleLimit) {
-                    ok = false;
-                    *abort_flag = 1;
-                    break;
-                }
-                if (idle > 16) __nanosleep(64);
+                __syncwarp();
+                if (iq < nt - 1) itq.next();
+                ++iq;
+                if (++kslot == NSK) kslot = 0, kpar ^= 1;
+                did = true;
             }
-            if (!ok) {
-                set_error(p.err, DEV_ERR_TIMEOUT);
-                *abort_flag = 1;
+            if (did) {
+                idle = 0;
+                continue;
             }
-            umma_commit(drain);
-            volatile int never = 0;
-            wait_bar(drain, 0, &never);
+            ++idle;
+            if (((idle & 255u) == 0 && __any_sync(0xffffffffu, *abort_flag)) || idle >= kMmaIdleLimit) {
+                ok = false;
+                break;
+            }
+            if (idle > 64) __nanosleep(64);
         }
+        if (!ok) {
+            set_error(p.err, DEV_ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        volatile int never = 0;
+        wait_bar_warp(drain, 0, &never);
         __syncwarp();
         named_bar_sync(kBarEnd, C::END_THREADS);
         tc_fence_after();
@@ -659,7 +673,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
         for (int g = 0; g < NPH; ++g) l[g] = 0.f;
         if (row < NPH) mref_s[cg0 + row] = -INFINITY;
         // the piece's 2^-c (written by the q warps)
-        carry_fail = carry_fail || !wait_bar(&q_full[qs], (uint32_t)((spiece >> 1) & 1), abort_flag);
+        carry_fail = carry_fail || !wait_bar_warp(&q_full[qs], (uint32_t)((spiece >> 1) & 1), abort_flag);
         named_bar_sync(bar_grp, 128);
 
         while (true) {
@@ -697,7 +711,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                 ksc = p.k_scale[zrow + pos];
                 vsc = p.v_scale[zrow + pos];
             }
-            bool fail = carry_fail || !wait_bar(&s_full[sb], (uint32_t)((i >> 1) & 1), abort_flag);
+            bool fail = carry_fail || !wait_bar_warp(&s_full[sb], (uint32_t)((i >> 1) & 1), abort_flag);
             if (valid && late) {
                 ksc = __ldcg(p.k_scale + zrow + pos);
                 vsc = __ldcg(p.v_scale + zrow + pos);
@@ -782,7 +796,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                 for (int g = 0; g < NPH; ++g) l[g] *= alpha_s[cg0 + g];
                 if (i > i0) {
                     const long long j = i - 1;
-                    if (!wait_bar(&pv_done[j & 1], (uint32_t)((j >> 1) & 1), abort_flag))
+                    if (!wait_bar_warp(&pv_done[j & 1], (uint32_t)((j >> 1) & 1), abort_flag))
                         fail = true;
                     tc_fence_after();
                     // the group's columns of every part of every O^T block
@@ -837,7 +851,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
             }
             if (i >= C::PST) {
                 const long long jp = i - C::PST;
-                if (!wait_bar(&pv_done[jp & 1], (uint32_t)((jp >> 1) & 1), abort_flag))
+                if (!wait_bar_warp(&pv_done[jp & 1], (uint32_t)((jp >> 1) & 1), abort_flag))
                     fail = true;
             }
             // P stage: column n's byte at 2048 (n / 16) + n mod 16 of its
@@ -873,7 +887,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
 
         // ---- piece end
         const long long e = i - 1;
-        bool fail = carry_fail || !wait_bar(&pv_done[e & 1], (uint32_t)((e >> 1) & 1), abort_flag);
+        bool fail = carry_fail || !wait_bar_warp(&pv_done[e & 1], (uint32_t)((e >> 1) & 1), abort_flag);
         carry_fail = false;
         tc_fence_after();
         warp_cols_n<NPH>(l, redg + q4 * 64, lane, OpSum());
