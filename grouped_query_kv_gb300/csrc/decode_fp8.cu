@@ -68,8 +68,7 @@ constexpr int kBox = 16384;      // one TMA box: 128 positions x 128 codes
 // Warps: 0 copies, 1 issues the MMAs, then the softmax in SG groups of four
 // (group sg = (warp - 2) / 4 takes NP / SG of the pass's columns, so SG
 // softmax warps share each SM sub-partition), then two that write the q
-// parts (Q8Cfg: SG, THREADS).
-constexpr int kQWarps = 2;
+// parts, or, paged, one that does and one that copies V (Q8Cfg: SG, THREADS).
 constexpr int kBarQ8All = 1;     // named barrier: all softmax threads
 constexpr int kBarQ8Grp = 3;     // named barriers 3, 4, ...: the 128 threads of group 0, 1, ...
 constexpr float kTauQ8 = 2.f;    // rescale once a score passes the running max by 2 (log2 units)
@@ -95,7 +94,7 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-template <int D, int NP>
+template <int D, int NP, bool PG>
 struct Q8Cfg {
     static constexpr int SL = D / 128;        // 128-code slabs per row
     static constexpr int kStage = SL * kBox;  // one staged tile: 128 positions x D codes
@@ -105,22 +104,33 @@ struct Q8Cfg {
     static constexpr int PST = 2;
     static constexpr int NS_MAX = 12;
     static constexpr int NBAR_MAX = 2 * NS_MAX + 14;
+    // paged: the scales of the last SCR tiles, eight of K and of V each.  The
+    // copy warp is at most NSK tiles ahead of Q K^T and that two of the softmax.
+    static constexpr int SCR = 16;
+    static_assert(NS_MAX / 2 + 3 <= SCR, "a tile's scales outlive their use");
+    static constexpr int SCB = PG ? SCR * 16 * 4 : 0;
     static constexpr int FIXED = 2 * QB + PST * PB + (NP == 48 ? 3 : 2) * 4 * 64 * 4 +
-                                 3 * 64 * 4 + 2 * 64 * 4 + 64 + 64 + 1024 + NBAR_MAX * 8;
+                                 3 * 64 * 4 + 2 * 64 * 4 + 64 + 64 + 1024 + NBAR_MAX * 8 + SCB;
     static constexpr int NS_FIT = (kSmemLimit - FIXED) / kStage;
     static constexpr int NS = NS_FIT > NS_MAX ? NS_MAX : NS_FIT;   // staging slots, both rings
     static constexpr int NSK = NS / 2;                             // K staging slots
     static constexpr int NSV = NS - NSK;                           // V staging slots
     static_assert(NSV >= 2 && NSK >= 2, "staging rings must hold two tiles each");
-    static_assert(NP % (4 * kQWarps) == 0, "the q warps convert four heads at a time each");
+    // warps that write the q parts; the paged kernel gives one of the two to
+    // the copies of V (one warp for both took some 2150 cycles a tile, 2800 in
+    // blocks of 16 positions, as long as the softmax)
+    static constexpr int QW = PG ? 1 : 2;
+    static_assert(NP % (4 * QW) == 0, "the q warps convert four heads at a time each");
     // softmax groups: three at 48 columns (16 each), else two
     static constexpr int SG = NP == 48 ? 3 : 2;
     static constexpr int NPH = NP / SG;  // columns of one softmax group
     static_assert(NPH % 8 == 0, "a group's columns come in tensor-memory loads of 8");
     static constexpr int SOFTW = 4 * SG;              // softmax warps
     static constexpr int QWARP0 = 2 + SOFTW;          // first q-part warp
-    static constexpr int THREADS = 32 * (QWARP0 + kQWarps);
-    static constexpr int END_THREADS = 32 * QWARP0;   // warps that meet before TMEM is freed
+    static constexpr int VWARP = QWARP0 + QW;         // paged: copies V
+    static constexpr int THREADS = 32 * (QWARP0 + 2);
+    // warps that meet before TMEM is freed: all but those that write the q parts
+    static constexpr int END_THREADS = 32 * (QWARP0 + (PG ? 1 : 0));
 
     static constexpr int off_kst = 0;
     static constexpr int off_vst = off_kst + NSK * kStage;
@@ -135,7 +145,8 @@ struct Q8Cfg {
     static constexpr int off_bar = off_vred + 64;
     static constexpr int nbar = 2 * NS + 14;
     static constexpr int off_misc = off_bar + nbar * 8;
-    static constexpr int bytes = off_misc + 64;
+    static constexpr int off_sc = off_misc + 64;          // paged: float [SCR][K, V][8]
+    static constexpr int bytes = off_sc + SCB;
     static constexpr int alloc = bytes + 1024;
     static_assert(alloc <= kSmemLimit, "shared memory");
     static_assert(off_q % 1024 == 0 && off_p % 1024 == 0 && QB % 1024 == 0, "swizzle atoms");
@@ -201,10 +212,10 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // -- for blocks under 128 positions the last block's rows end the tile behind
 // a hole of zero rows -- so rows past the length are never read.
 template <int D, int NP, bool PG>
-__global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
+__global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const DecodeParams p) {
-    using C = Q8Cfg<D, NP>;
+    using C = Q8Cfg<D, NP, PG>;
     constexpr int SL = C::SL;
     constexpr int kStage = C::kStage;
     constexpr int NSK = C::NSK;
@@ -223,6 +234,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
     float *alpha_s = reinterpret_cast<float *>(smem + C::off_alpha);
     float *qinv_s = reinterpret_cast<float *>(smem + C::off_qinv);
     float *vred_s = reinterpret_cast<float *>(smem + C::off_vred);
+    float *sc_s = reinterpret_cast<float *>(smem + C::off_sc);
     uint64_t *bar_base = reinterpret_cast<uint64_t *>(smem + C::off_bar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::off_misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::off_misc + 16);
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
             mbar_init(&vst_empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&q_full[s], kQWarps);
+            mbar_init(&q_full[s], C::QW);
             mbar_init(&q_empty[s], 1 + C::SOFTW);  // the MMA commit and the softmax warps
             mbar_init(&s_full[s], 1);
             mbar_init(&s_empty[s], C::SOFTW);
@@ -291,64 +303,131 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
     const uint32_t qbuf_s = smem_u32(qbuf);
     const uint32_t pbuf_s = smem_u32(pbuf);
 
+    // ========================================================== paged copies
+    // Warp 0 brings K, VWARP brings V: a TMA box per block that a tile spans
+    // (lanes 0 .. nbox-1 issue one each).  The table entry of a box is read two
+    // tiles ahead and its scales (by the K warp) one, so neither is waited for.
+    if (PG && (warp == 0 || warp == C::VWARP)) {
+        const bool is_v = warp != 0;
+        const CUtensorMap *tm = is_v ? &tmv : &tmk;
+        uint8_t *base = is_v ? vst : kst;
+        uint64_t *full = is_v ? vst_full : kst_full, *empty = is_v ? vst_empty : kst_empty;
+        const int ns = is_v ? NSV : NSK, nt = (int)ntiles;
+        const int lg = p.block_lg;
+        const int nbox = lg >= 7 ? 1 : kT >> lg;
+        const int box_bytes = (lg >= 7 ? kT : 1 << lg) * 128;
+        const uint64_t pol = l2_policy_evict_first();
+        TileIter it;
+        it.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
+        int fy = 0, fblk = -1, fkvh = it.seg / p.head_groups;  // a box: first row in its block, its entry
+        bool fused = false;                                    // (there is one)
+        auto fetch = [&]() {
+            const int len = seq_valid_len(it.len, p.Lmax);
+            if (it.t == 0) fkvh = it.seg / p.head_groups;
+            int k;  // logical block
+            if (lg >= 7) {
+                const int r0 = it.row0();
+                k = (r0 + kT - 1) >> lg;  // the block of the tile's last row
+                fy = r0 - (k << lg);
+            } else if (!it.last_tile_of_segment()) {
+                k = (it.first_pos() >> lg) + lane;
+                fy = 0;
+            } else {
+                const int kend = (len - 1) >> lg;  // -1 for an empty sequence
+                k = kend - (nbox - 1 - lane);
+                fy = lane == nbox - 1 ? len - ((kend + 1) << lg) : 0;
+            }
+            fused = lane < nbox && k >= 0;
+            fblk = fused ? p.block_table[(size_t)it.b * p.max_blocks + k] : -1;
+        };
+        int y = 0, z = -1;            // the next tile's box: its row, and its pool row (-1: zeros)
+        float ksc = 0.f, vsc = 0.f;   // its scales
+        auto take = [&]() {
+            y = fy;
+            z = -1;
+            ksc = vsc = 0.f;
+            if (!fused) return;
+            if (fblk >= 0 && fblk < p.num_blocks) {
+                z = fblk * p.Hkv + fkvh;
+                if (!is_v) {
+                    ksc = p.k_scale[z];
+                    vsc = p.v_scale[z];
+                }
+            } else {
+                set_error(p.err, DEV_ERR_BOUNDS);
+            }
+        };
+        fetch();
+        take();
+        if (nt > 1) {
+            it.next();
+            fetch();
+        }
+        int slot = 0, n = 0;
+        uint32_t par = 1;  // of the slot's release before its fill
+        bool ok = true;
+        for (; n < nt; ++n) {
+            if (n >= ns && !wait_bar_warp(&empty[slot], par, abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (!is_v && lane < 8) {  // before the tile's arrival: the softmax reads them behind it
+                float *sc = sc_s + (n & (C::SCR - 1)) * 16 + lane;
+                sc[0] = ksc;
+                sc[8] = vsc;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], kStage);
+            __syncwarp();
+            if (lane < nbox) {
+#pragma unroll
+                for (int sl = 0; sl < SL; ++sl)
+                    tma_load_3d(base + slot * kStage + sl * kBox + lane * box_bytes, tm, &full[slot],
+                                sl * 128, y, z, pol);
+            }
+            if (++slot == ns) slot = 0, par ^= 1;
+            if (n + 1 < nt) {
+                take();
+                if (n + 2 < nt) {
+                    it.next();
+                    fetch();
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.err, DEV_ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+        if (!is_v) pdl_launch_dependents();
+        named_bar_sync(kBarEnd, C::END_THREADS);
+        if (*abort_flag && lane == 0) {
+            // a role gave up, so copies may still be in flight that no one
+            // consumed: let them land before the CTA exits
+            volatile int never = 0;
+            for (int k = n > ns ? n - ns : 0; k < n; ++k)
+                wait_bar(&full[k % ns], (uint32_t)((k / ns) & 1), &never);
+        }
+        return;
+    }
+
     // ================================================================ producer
     // Issue order K_0, K_1, V_0, K_2, V_1, ... (each ring in its own order).
     // The whole warp walks the tiles (the fused append quantizes a row with
     // all 32 lanes); lane 0 alone waits on staging slots and issues copies.
-    if (warp == 0) {
+    if (!PG && warp == 0) {
         long long nk = 0, nv = 0;  // K and V stage copies issued
         const uint64_t pol = l2_policy_evict_first();
         TileIter itk, itv;
         itk.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
         itv.init(lens, p.B, p.Lmax, kT, segs_per_b, st);
         bool ok = true;
-        // paged: boxes per tile (lanes 0 .. nbox-1 issue one each), its bytes,
-        // and this lane's box of the current K, current V and next K tile
-        const int nbox = PG ? (p.block_lg >= 7 ? 1 : kT >> p.block_lg) : 1;
-        const int box_bytes = PG ? (p.block_lg >= 7 ? kT : 1 << p.block_lg) * 128 : 0;
-        int ky = 0, kz = -1, vy = 0, vz = -1, ny = 0, nblk = -1;
-        bool nuse = false;
-        auto paged_fetch = [&](const TileIter &it) {
-            const int lg = p.block_lg;
-            const int len = seq_valid_len(it.len, p.Lmax);
-            int k;  // logical block
-            if (lg >= 7) {
-                const int r0 = it.row0();
-                k = (r0 + kT - 1) >> lg;  // the block of the tile's last row
-                ny = r0 - (k << lg);
-            } else if (!it.last_tile_of_segment()) {
-                k = (it.first_pos() >> lg) + lane;
-                ny = 0;
-            } else {
-                const int kend = (len - 1) >> lg;  // -1 for an empty sequence
-                k = kend - (nbox - 1 - lane);
-                ny = lane == nbox - 1 ? len - ((kend + 1) << lg) : 0;
-            }
-            nuse = lane < nbox && k >= 0;
-            nblk = nuse ? p.block_table[(size_t)it.b * p.max_blocks + k] : -1;
-        };
-        auto paged_row = [&](int kvh) -> int {  // the fetched box's pool row (-1: zeros)
-            if (!nuse) return -1;
-            if (nblk >= 0 && nblk < p.num_blocks) return nblk * p.Hkv + kvh;
-            set_error(p.err, DEV_ERR_BOUNDS);
-            return -1;
-        };
-        if (PG) paged_fetch(itk);
         auto issue = [&](const void *tm, const TileIter &it, uint8_t *base, uint64_t *full,
-                         uint64_t *empty, int ns, long long &n, int y, int z_) -> bool {
+                         uint64_t *empty, int ns, long long &n) -> bool {
             const int slot = (int)(n % ns);
             if (n >= ns && !wait_bar_warp(&empty[slot], (uint32_t)(((n / ns) - 1) & 1), abort_flag))
                 return false;
-            if (PG) {
-                if (lane == 0) mbar_arrive_expect_tx(&full[slot], kStage);
-                __syncwarp();
-                if (lane < nbox) {
-#pragma unroll
-                    for (int sl = 0; sl < SL; ++sl)
-                        tma_load_3d(base + slot * kStage + sl * kBox + lane * box_bytes, tm, &full[slot],
-                                    sl * 128, y, z_, pol);
-                }
-            } else if (lane == 0) {
+            if (lane == 0) {
                 mbar_arrive_expect_tx(&full[slot], kStage);
                 const int z = it.b * p.Hkv + it.seg / p.head_groups;
 #pragma unroll
@@ -360,13 +439,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
             return true;
         };
         for (long long r = 0; r <= ntiles && ok; ++r) {
-            vy = ky;  // V of tile r-1 comes from the blocks of K tile r-1
-            vz = kz;
             if (r < ntiles) {
                 // fused append: this tile holds the new token's row -- its
                 // codes and scales are written (and made visible to the
                 // copies and to every SM) before the tile's copies go out
-                if (!PG && p.len_add && itk.last_tile_of_segment() && itk.len >= 1 && itk.len <= p.Lmax) {
+                if (p.len_add && itk.last_tile_of_segment() && itk.len >= 1 && itk.len <= p.Lmax) {
                     const int z = itk.b * p.Hkv + itk.seg / p.head_groups;
                     const size_t dst = (size_t)z * p.Lmax + (itk.len - 1);
                     uint8_t *kc = reinterpret_cast<uint8_t *>(p.k_cache);
@@ -379,16 +456,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                     __threadfence();
                     __syncwarp();
                 }
-                if (PG) {
-                    ky = ny;
-                    kz = paged_row(itk.seg / p.head_groups);
-                }
-                ok = issue(&tmk, itk, kst, kst_full, kst_empty, NSK, nk, ky, kz);
+                ok = issue(&tmk, itk, kst, kst_full, kst_empty, NSK, nk);
                 itk.next();
-                if (PG && r + 1 < ntiles) paged_fetch(itk);
             }
             if (r >= 1 && ok) {
-                ok = issue(&tmv, itv, vst, vst_full, vst_empty, NSV, nv, vy, vz);
+                ok = issue(&tmv, itv, vst, vst_full, vst_empty, NSV, nv);
                 itv.next();
             }
         }
@@ -438,13 +510,16 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                 // head it converts, so their reads overlap
                 constexpr int VPL = D / 8;              // head dims per lane
                 constexpr int NV = VPL / 8;             // 16-byte loads per lane and head
-                constexpr int HPW = NP / kQWarps;       // heads per warp
-                constexpr int NIT = HPW / 4;            // four heads per pass of the warp
+                constexpr int HPW = NP / C::QW;         // heads per warp
+                constexpr int NALL = HPW / 4;           // four heads per pass of the warp
+                constexpr int NIT = NALL > 6 ? 4 : NALL;  // passes whose loads are in flight together
+                static_assert(NALL % NIT == 0, "whole batches of passes");
                 const int sub = lane & 7, d0 = sub * VPL;
+                for (int it0 = 0; it0 < NALL; it0 += NIT) {
                 uint4 raw[NIT][NV];
 #pragma unroll
                 for (int it4 = 0; it4 < NIT; ++it4) {
-                    const int g = (it4 * kQWarps + qw) * 4 + (lane >> 3);
+                    const int g = ((it0 + it4) * C::QW + qw) * 4 + (lane >> 3);
 #pragma unroll
                     for (int v = 0; v < NV; ++v) raw[it4][v] = make_uint4(0u, 0u, 0u, 0u);
                     if (g < gvalid) {
@@ -456,7 +531,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                 }
 #pragma unroll
                 for (int it4 = 0; it4 < NIT; ++it4) {
-                    const int g = (it4 * kQWarps + qw) * 4 + (lane >> 3);
+                    const int g = ((it0 + it4) * C::QW + qw) * 4 + (lane >> 3);
                     float x[VPL];
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
@@ -502,6 +577,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
                             make_uint4(lw[0], lw[1], lw[2], lw[3]);
                     }
                     if (sub == 0) qinv_s[qs * 64 + g] = (g < gvalid) ? pow2i(e - 7) : 0.f;
+                }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -699,20 +775,17 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP>::THREADS, 1)
             // hold the line from the tile before)
             const bool late = !PG && p.len_add && it.last_tile_of_segment();
             float ksc = 0.f, vsc = 0.f;
-            if (PG) {
-                if (valid) {
-                    const int blk = p.block_table[(size_t)b * p.max_blocks + (pos >> p.block_lg)];
-                    if (blk >= 0 && blk < p.num_blocks) {  // (else zeros, as the copy warp flags)
-                        ksc = p.k_scale[(size_t)blk * p.Hkv + kvh];
-                        vsc = p.v_scale[(size_t)blk * p.Hkv + kvh];
-                    }
-                }
-            } else if (valid && !late) {
+            if (!PG && valid && !late) {
                 ksc = p.k_scale[zrow + pos];
                 vsc = p.v_scale[zrow + pos];
             }
             bool fail = carry_fail || !wait_bar_warp(&s_full[sb], (uint32_t)((i >> 1) & 1), abort_flag);
-            if (valid && late) {
+            if (PG && valid) {  // the copy warp's: row r of the tile came in box r / block size
+                const float *sc = sc_s + ((int)i & (C::SCR - 1)) * 16 + (p.block_lg >= 7 ? 0 : row >> p.block_lg);
+                ksc = sc[0];
+                vsc = sc[8];
+            }
+            if (!PG && valid && late) {
                 ksc = __ldcg(p.k_scale + zrow + pos);
                 vsc = __ldcg(p.v_scale + zrow + pos);
             }
@@ -995,14 +1068,14 @@ cudaError_t launch_q8(const CUtensorMap &tmk, const CUtensorMap &tmv, const Deco
     if (e != cudaSuccess) return e;
     if (!(dev >= 0 && dev < 64 && done_for_device[dev])) {
         e = cudaFuncSetAttribute(decode_q8_kernel<D, NP, PG>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Cfg<D, NP>::alloc);
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Cfg<D, NP, PG>::alloc);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done_for_device[dev] = 1;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_ctas);
-    cfg.blockDim = dim3(Q8Cfg<D, NP>::THREADS);
-    cfg.dynamicSmemBytes = Q8Cfg<D, NP>::alloc;
+    cfg.blockDim = dim3(Q8Cfg<D, NP, PG>::THREADS);
+    cfg.dynamicSmemBytes = Q8Cfg<D, NP, PG>::alloc;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1016,13 +1089,13 @@ cudaError_t launch_q8(const CUtensorMap &tmk, const CUtensorMap &tmv, const Deco
 
 int q8_smem_bytes(int D, int np) {
     switch (D * 1000 + np) {
-        case 128016: return Q8Cfg<128, 16>::alloc;
-        case 128032: return Q8Cfg<128, 32>::alloc;
-        case 128048: return Q8Cfg<128, 48>::alloc;
-        case 128064: return Q8Cfg<128, 64>::alloc;
-        case 256016: return Q8Cfg<256, 16>::alloc;
-        case 256032: return Q8Cfg<256, 32>::alloc;
-        case 256048: return Q8Cfg<256, 48>::alloc;
+        case 128016: return Q8Cfg<128, 16, false>::alloc;
+        case 128032: return Q8Cfg<128, 32, false>::alloc;
+        case 128048: return Q8Cfg<128, 48, false>::alloc;
+        case 128064: return Q8Cfg<128, 64, false>::alloc;
+        case 256016: return Q8Cfg<256, 16, false>::alloc;
+        case 256032: return Q8Cfg<256, 32, false>::alloc;
+        case 256048: return Q8Cfg<256, 48, false>::alloc;
         default: return -1;
     }
 }
