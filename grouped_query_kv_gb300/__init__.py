@@ -567,6 +567,14 @@ def _want(t, name, dtype, dev, shape=None):
     raise ValueError("%s must be on the current CUDA device %d (got %s)" % (name, dev, t.device))
 
 
+def _int32(x, name):
+    """x as an int that a C int holds."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError("%s is beyond 32 bits (%d)" % (name, x))
+    return x
+
+
 def _packed_rows(t, name, dev, shape=None):
     """Checks packed bf16 rows [N, H, D] whose [H, D] are contiguous (they may
     be a slice of wider rows) and returns the elements from row to row."""
@@ -617,7 +625,7 @@ def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count,
     if free_blocks.dim() != 1:
         raise ValueError("free_blocks must be [num_free]")
     _want(free_count, "free_count", i32, dev, (1,))
-    num_slots = int(num_slots)
+    num_slots = _int32(num_slots, "num_slots")
     if cu_seqlens is None:
         cu_seqlens = torch.empty(B + 1, dtype=i32, device=cached_lens.device)
     else:
@@ -633,7 +641,7 @@ def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count,
     _check(lib().kv_block_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(block_table),
                                  _ptr(free_blocks), _ptr(free_count), _ptr(free_count_out),
                                  _ptr(cu_seqlens), _ptr(slots), B, block_table.shape[1],
-                                 int(block_size), free_blocks.shape[0], num_slots,
+                                 _int32(block_size, "block_size"), free_blocks.shape[0], num_slots,
                                  _stream_ptr(stream)))
     return cu_seqlens, slots, free_count_out
 
@@ -690,7 +698,7 @@ def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=N
         _want(out, "out", torch.bfloat16, dev, (N, Hq, D))
     _check(lib().gqa_prefill_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out),
                                   cu_seqlens.shape[0] - 1, N, Hq, Hkv, D, qs, ks, vs, float(scale),
-                                  0x7fffffff if window is None else int(window),
+                                  0x7fffffff if window is None else min(int(window), 0x7fffffff),
                                   _stream_ptr(stream)))
     return out
 

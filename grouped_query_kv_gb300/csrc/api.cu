@@ -59,6 +59,9 @@ struct Workspace {
     std::vector<void *> retired;
 };
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+// workspaces of captures, each its own (gqa_decode_attn_paged_fp8): by device,
+// stream and capture
+std::map<std::pair<std::pair<int, cudaStream_t>, unsigned long long>, Workspace> g_ws_captured;
 
 // cuTensorMapEncodeTiled, fetched through the runtime so the library needs no
 // link-time dependency on the driver library.
@@ -289,8 +292,7 @@ int check_sizes(int B, int Hq, int Hkv, int D, int Lmax) {
     return KVATTN_OK;
 }
 
-int get_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
-    Workspace &w = g_ws[std::make_pair(dev, stream)];
+int grow_workspace(Workspace &w, size_t bytes, void **ptr) {
     if (w.bytes < bytes) {
         // grow at least twofold; the old buffer is retired, not freed
         size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
@@ -307,6 +309,29 @@ int get_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
     }
     *ptr = w.ptr;
     return KVATTN_OK;
+}
+
+int get_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
+    return grow_workspace(g_ws[std::make_pair(dev, stream)], bytes, ptr);
+}
+
+// The same, but a call that is being captured gets a workspace of its
+// capture's own, so that graphs captured on one stream may replay side by
+// side, and a first call may be a captured one: the thread's capture mode is
+// relaxed around the allocation, which is no part of the graph.
+int get_call_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    cudaError_t e = cudaStreamGetCaptureInfo(stream, &st, &id);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetCaptureInfo");
+    if (st != cudaStreamCaptureStatusActive) return get_workspace(dev, stream, bytes, ptr);
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
+    const int rc = grow_workspace(g_ws_captured[std::make_pair(std::make_pair(dev, stream), id)], bytes, ptr);
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (rc == KVATTN_OK && e != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
+    return rc;
 }
 
 }  // namespace
@@ -711,7 +736,9 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
         rc = make_plan(B, Hq, Hkv, D, Lmax, ds->num_sms, &pl);
         g_force_path = saved;
         if (rc) return rc;
-        if ((rc = get_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws))) return rc;
+        rc = pg ? get_call_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws)
+                : get_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws);
+        if (rc) return rc;
     }
     const kvattn_plan &P = pl.pub;
     CUtensorMap tmk, tmv;
@@ -971,6 +998,12 @@ void kvattn_release(void) {
         for (void *old : kv.second.retired) cudaFree(old);
     }
     g_ws.clear();
+    for (auto &kv : g_ws_captured) {
+        cudaSetDevice(kv.first.first.first);
+        if (kv.second.ptr) cudaFree(kv.second.ptr);
+        for (void *old : kv.second.retired) cudaFree(old);
+    }
+    g_ws_captured.clear();
     cudaSetDevice(cur);
 }
 

@@ -91,10 +91,10 @@ __device__ __forceinline__ uint2 codes8(uint4 raw, float inv) {
 
 // Writes m packed rows from row t to positions pos.. (of one pool block) of
 // request b, for head h of K (kv = 0) or V; called by the whole block, `turn`
-// counting its calls.
+// counting the blocks that it wrote.
 template <int D>
 __device__ __forceinline__ void write_block(const Append8Params &p, int kv, int h, int b, int pos, int t,
-                                            int m, float (*red)[4], int turn) {
+                                            int m, float (*red)[4], int &turn) {
     constexpr int VPR = D / 8;               // 16-byte vectors of a new row
     constexpr int RPP = kThreads / VPR;      // rows per pass
     const int tid = threadIdx.x;
@@ -134,7 +134,9 @@ __device__ __forceinline__ void write_block(const Append8Params &p, int kv, int 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    float *mine = red[turn & 1];  // (the barrier of the next call keeps the one after from this buffer)
+    // (two buffers in turn: the barrier of the next block written keeps the one
+    // after it from this buffer until every thread has read it)
+    float *mine = red[turn++ & 1];
     if ((tid & 31) == 0) mine[tid >> 5] = a;
     __syncthreads();              // (every thread has read the old scale, too)
     a = fmaxf(fmaxf(mine[0], mine[1]), fmaxf(mine[2], mine[3]));
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) append_paged8_kernel(const Append8Pa
         if (bad && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
         if (some)
             for (int hk = blockIdx.y; hk < 2 * p.Hkv; hk += gridDim.y)
-                write_block<D>(p, hk & 1, hk >> 1, b, c, first, min(n, bs - (c & (bs - 1))), red, turn++);
+                write_block<D>(p, hk & 1, hk >> 1, b, c, first, min(n, bs - (c & (bs - 1))), red, turn);
         return;
     }
     // pool blocks that start at packed rows [t0, t1), the requests' first
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) append_paged8_kernel(const Append8Pa
         const int b = s_b[i], t = s_t[i];
         request(p, b, &first, &n, &c, &bad);
         for (int hk = blockIdx.y; hk < 2 * p.Hkv; hk += gridDim.y)
-            write_block<D>(p, hk & 1, hk >> 1, b, c + t - first, t, min(bs, first + n - t), red, turn++);
+            write_block<D>(p, hk & 1, hk >> 1, b, c + t - first, t, min(bs, first + n - t), red, turn);
     }
 }
 

@@ -413,9 +413,11 @@ KVATTN_API int gqa_decode_step_fp8(const void *q, const void *k_new, const void 
  * gqa_prefill_attn computes the prompts' own attention ("The Basics of
  * Transformer Inference", prefill and generation; "Machine Learning
  * Engineering and AI Systems at Scale", section "The key and value cache",
- * on PagedAttention).  None of the five calls below allocates or keeps
- * device memory, so a captured graph holds nothing of the library's and may
- * replay beside any other.  Packed rows k_new, v_new (and q, k, v) may be
+ * on PagedAttention); gqa_decode_attn_paged_fp8 then takes single tokens
+ * over the 8-bit pool.  The first four keep no device memory: a captured
+ * graph of them holds nothing of the library's and may replay beside any
+ * other.  Outputs must not overlap inputs, but where that is said.  Packed
+ * rows k_new, v_new (and q, k, v) may be
  * slices of wider rows, as of one fused projection: *_stride counts the
  * elements from one token's [H, D] row to the next, a multiple of 8, at
  * least H * D.  The calls run on the current device; every pointer belongs
@@ -492,7 +494,8 @@ KVATTN_API int kv_append_slots(void *k_pool, void *v_pool, const void *k_new, co
  *                are
  *   scale      : finite; window >= 1 (>= N: the whole prompt)
  *
- * Scores, maxima and sums are held in fp32; the weights enter the second
+ * Scores, maxima and sums are held in fp32 (scale * q . k must stay finite
+ * there); the weights enter the second
  * product as bf16, unnormalised, and the result is rounded once more.  A
  * sequence's own q, k and v rows must hold finite values; all other rows may
  * hold anything.  A sequence whose bounds are not
@@ -558,8 +561,12 @@ KVATTN_API int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
  *   out : bf16 [B, Hq, D] (the 8-bit products carry the weights' 11
  *         significant bits, bf16 has 8)
  * Scales may be any finite values >= 0.  Pool rows at and past a length are
- * never read; table entries, lengths, workspaces and device-side errors are
- * those of gqa_decode_attn_paged.  D = 128 or 256.
+ * never read; table entries, lengths and device-side errors are those of
+ * gqa_decode_attn_paged.  Its workspace is the stream's, as for the other
+ * attention calls, but a call that is being captured gets one of that
+ * capture's own (allocated then, kept until kvattn_release): graphs captured
+ * on one stream may replay side by side, and the first call on a stream may
+ * be a captured one.  D = 128 or 256.
  */
 KVATTN_API int gqa_decode_attn_paged_fp8(const void *q, const void *k_codes, const void *v_codes,
                                          const float *k_scale, const float *v_scale,

@@ -532,6 +532,29 @@ def test_append8_extremes():
         assert same_values(values(kc), ref[0])
 
 
+def test_append8_bad_entries_between_good_ones():
+    # blocks outside the pool between blocks inside, many heads in one block's turn
+    D, Hkv, bs, nblk, B = 64, 8, 16, 300, 60
+    rng = np.random.default_rng(8)
+    table = rng.permutation(nblk)[:B * 5].reshape(B, 5).astype(np.int32)
+    bad = rng.random((B, 5)) < 0.3
+    t = np.where(bad, 1000, table)
+    new = rng.integers(0, 5 * bs + 1, B)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    kv = _normal((int(cu[-1]), 2 * Hkv, D), 3)
+    pools = [new_pool8(nblk, Hkv, bs, D, 85 + i) for i in range(2)]
+    refs = [(values(c), s.cpu().numpy().astype(np.float64)) for c, s in pools]
+    g.kv_append_paged_fp8(pools[0][0], pools[1][0], pools[0][1], pools[1][1], kv[:, :Hkv], kv[:, Hkv:], _i32(t),
+                          _i32([0] * B), _i32(cu))
+    _raises(g.KVATTN_ERR_DEVICE_BOUNDS)
+    for (c, s), (rc, rs), x in zip(pools, refs, (kv[:, :Hkv], kv[:, Hkv:])):
+        wc, ws = append8_ref(rc, rs, x.double().cpu().numpy(), table, [0] * B, cu, bs)
+        skipped = table[bad]
+        wc[skipped], ws[skipped] = rc[skipped], rs[skipped]
+        assert np.array_equal(s.cpu().numpy().astype(np.float64), ws)
+        assert same_values(values(c), wc)
+
+
 def test_append8_flags_and_skips_bad_requests():
     D, Hkv, bs, nblk = 128, 2, 16, 9
     table = np.array([[0, 1], [2, 99], [3, 4], [5, 6], [-1, 7]], np.int32)
@@ -640,6 +663,39 @@ def test_attn8_small_and_large_grids(ctas):
         g.set_tuning(0, 0)
 
 
+def test_attn8_graphs_of_one_stream_replay_side_by_side():
+    # two graphs captured on one stream (the first calls there), with segments that
+    # several CTAs share, replayed on two streams: each has a workspace of its own
+    Hq, Hkv, D, bs = 16, 1, 128, 16
+    g.release()
+    stream, runs = torch.cuda.Stream(), []
+    for seed, lens in ((1, [5000, 3000]), (2, [7000, 10])):
+        table, nblk = make_table(lens, bs, seed)
+        kc, ks = new_pool8(nblk, Hkv, bs, D, seed)
+        vc, vs = new_pool8(nblk, Hkv, bs, D, seed + 10)
+        ks.fill_(2.0 ** -8)
+        vs.fill_(2.0 ** -8)
+        q = _normal((2, Hq, D), seed)
+        args = (q, kc, vc, ks, vs, _i32(table), _i32(lens), 0.1)
+        out = torch.zeros((2, Hq, D), dtype=torch.bfloat16, device="cuda")
+        want = g.gqa_decode_attn_paged_fp8(*args).clone()
+        gr = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr, stream=stream):
+            for _ in range(20):
+                g.gqa_decode_attn_paged_fp8(*args, out=out)
+        runs.append((gr, out, want, args))
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(30):
+        for st, (gr, _, _, _) in zip(streams, runs):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    g.check_device_error()
+    for _, out, want, _ in runs:
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
 def test_attn8_flags_bad_lengths_and_entries():
     Hq, Hkv, D, bs = 16, 2, 128, 16
     table, nblk = make_table([40, 40, 40], bs, 1)
@@ -731,12 +787,9 @@ def test_the_path_captured_and_replayed():
     q, k, v = _normal((B, Hq, D), 1), _normal((B, Hkv, D), 2), _normal((B, Hkv, D), 3)
     cu, slots = torch.zeros(B + 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int64, device="cuda")
     out = torch.zeros((B, Hq, D), dtype=torch.bfloat16, device="cuda")
-    s = torch.cuda.Stream()
-    with torch.cuda.stream(s):  # the attention's workspace for this stream
-        g.gqa_decode_attn_paged_fp8(q, kc, vc, ks, vs, table, _i32([0] * B), 0.1, out=out)
-    torch.cuda.synchronize()
     gr = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(gr, stream=s):
+    torch.cuda.synchronize()
+    with torch.cuda.graph(gr):
         g.kv_block_tables(lens, one, table, free, count, bs, B, cu_seqlens=cu, slots=slots)
         g.kv_append_slots(kp, vp, k, v, slots)
         g.kv_append_paged_fp8(kc, vc, ks, vs, k, v, table, lens, cu)
