@@ -39,6 +39,7 @@
 #include <climits>
 #include <cmath>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "../../include/kvattn.h"
 #include "internal.h"
@@ -81,6 +82,22 @@ struct Unit {
     int n[2];    // key tiles of each query tile; n[0] = 0 ends the list
 };
 
+// A place in a ring of N slots from slot OFF: the slot and the parity of its
+// present fill (counted up: a division by N of every place took a tenth of the
+// time).
+template <int N_, int OFF>
+struct Ring {
+    static constexpr int N = N_;
+    int slot = OFF;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == OFF + N) {
+            slot = OFF;
+            parity ^= 1;
+        }
+    }
+};
+
 template <int D>
 struct PfCfg {
     static constexpr int NQ = D == 256 ? 1 : 2;         // query tiles
@@ -96,7 +113,7 @@ struct PfCfg {
     // it hands registers to the softmax warpgroups
     static constexpr int SOFT0 = 4;                     // first softmax warp
     static constexpr int THREADS = 32 * SOFT0 + 128 * NQ;
-    static constexpr int REGS_SERVICE = 88, REGS_SOFT = 208;
+    [[maybe_unused]] static constexpr int REGS_SERVICE = 88, REGS_SOFT = 208;  // 128 x 88 + 256 x 208 = 384 x 168
     static constexpr int off_q = 0;
     static constexpr int off_ring = NQ * QT;
     static constexpr int off_bar = off_ring + NS * SLOT;
@@ -107,6 +124,14 @@ struct PfCfg {
     static constexpr int off_sum = off_cnt + 2 * kBuckets * 4;
     static constexpr int bytes = off_sum + 64;
     static constexpr int alloc = bytes + 1024;
+    // Two query tiles: one ring, K0 V0 K1 V1 ..., which each MMA warp takes
+    // whole.  One: a ring of K and one of V, each with a copy warp and an MMA
+    // warp of its own (one copy warp for both took some 2700 cycles a key tile,
+    // longer than its MMAs).  Either way a slot's waits see every fill in
+    // order: a barrier's parity cannot tell a fill from the one two before.
+    static constexpr int KN = NQ == 2 ? NS : CPT, VN = NQ == 2 ? NS : NS - CPT;
+    using KRing = Ring<KN, 0>;
+    using VRing = Ring<VN, NQ == 2 ? 0 : CPT>;
     static_assert(NS > 2 * CPT && NS >= 4, "the ring holds more than one K and one V tile");
     static_assert(alloc <= kSmemMax, "shared memory");
     // TMEM: S0, S1 (128 columns each; P over the first 64), then O per tile
@@ -135,21 +160,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
                                           uint32_t limit = KVATTN_SPIN_LIMIT) {
     for (uint32_t it = 0; it < limit; ++it) {
         const bool done = limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity);
-        if (__all_sync(0xffffffffu, done)) return true;
-        if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
-    }
-    *abort_flag = 1;
-    return false;
-}
-
-// A whole warp waits for one barrier per lane (bar null: for nothing) in one
-// loop: each wait of its own cost an issuing warp 190 to 370 cycles, ready or
-// not, in which the tensor pipe ran dry.
-__device__ __forceinline__ bool warp_wait_each(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                               uint32_t limit) {
-    for (uint32_t it = 0; it < limit; ++it) {
-        bool done = true;
-        if (bar) done = limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity);
         if (__all_sync(0xffffffffu, done)) return true;
         if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
     }
@@ -252,20 +262,6 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A place in the ring of NS slots: the slot and the parity of its present fill
-// (counted up: a division by NS of every place took a tenth of the time).
-template <int NS>
-struct Ring {
-    int slot = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == NS) {
-            slot = 0;
-            parity ^= 1;
-        }
-    }
-};
-
 // A published unit, the same in every lane.
 __device__ __forceinline__ Unit read_unit(const Unit &from) {
     Unit u;
@@ -282,14 +278,6 @@ __device__ __forceinline__ int pf_len(const PrefillParams &p, int b, int *row0) 
     *row0 = a;
     return (a < 0 || e < a || e > p.N) ? -1 : e - a;
 }
-
-// Ring order.  Two query tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 K3 ...,
-// counted over all units of a CTA (g).  It is the order the MMA warps take the
-// tiles in, each of them every tile, so that a slot's fill before has always
-// been seen to land when its parity is looked at (a parity alone cannot tell
-// a fill from the one two before).
-__device__ __forceinline__ long long k_tile1(long long g) { return g == 0 ? 0 : 2 * g - 1; }
-__device__ __forceinline__ long long v_tile1(long long g) { return 2 * g + 2; }
 
 template <int D>
 __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
@@ -336,7 +324,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         }
         for (int s = 0; s < kDesc; ++s) {
             mbar_init(&u_full[s], 1);
-            // readers of a unit: copies (of K and of V), MMAs (twice), softmax warps
+            // readers of a unit: the copy warps, the MMA warps, the softmax warps
             mbar_init(&u_empty[s], (NQ == 2 ? 3 : 4) + 4 * NQ);
         }
         mbar_init(drain, 2);  // warps 1 and 2
@@ -409,6 +397,29 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
         return true;
+    };
+    // (by a whole warp) one slot's copies: a uniform wait, then one lane issues
+    int fills = 0;  // slots filled by this warp
+    auto issue = [&](const void *tm, int c, int head, int row, auto &r) -> bool {
+        const int slot = r.slot;
+        if (fills >= r.N && !warp_wait(&slot_empty[slot], r.parity ^ 1, abort_flag)) return false;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&slot_full[slot], C::SLOT);
+#pragma unroll
+            for (int sl = 0; sl < C::KC / 64; ++sl)
+                tma_load_3d_plain(ring + slot * C::SLOT + sl * kSlab, tm, &slot_full[slot],
+                                  c * C::KC + sl * 64, head, row);
+        }
+        __syncwarp();
+        ++fills;
+        r.next();
+        return true;
+    };
+    // (by one lane) the last fills of a ring of n slots from slot `off` have landed
+    auto landed = [&](int n, int off) {
+        volatile int never = 0;
+        for (int i = fills > n ? fills - n : 0; i < fills; ++i)
+            pf_wait(&slot_full[off + i % n], (uint32_t)((i / n) & 1), &never);
     };
     // A walk over the key tiles of all units (one query tile).
     struct Walk {
@@ -496,23 +507,50 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 u->n[s] = (s < NQ && a < e) ? (e - u->kbeg + kRows - 1) / kRows : 0;
             }
         };
-        auto publish = [&](long long k, const Unit &u) -> bool {
-            const int slot = (int)(k % kDesc);
-            bool w = true;
-            if (lane == 0) {
-                if (k >= kDesc) w = pf_wait(&u_empty[slot], (uint32_t)((k / kDesc - 1) & 1), abort_flag);
-                if (w) {
-                    units[slot] = u;
-                    mbar_arrive(&u_full[slot]);
-                }
+        // publishes unit k; with one query tile only if its place is free, unless it must
+        auto publish = [&](int k, const Unit &u, bool must, bool *done) -> bool {
+            uint64_t *place = &u_empty[k % kDesc];
+            const uint32_t parity = (uint32_t)((k / kDesc - 1) & 1);
+            *done = false;
+            if (k >= kDesc) {
+                if (!must && !__all_sync(0xffffffffu, mbar_test(place, parity))) return true;
+                if (!warp_wait(place, parity, abort_flag)) return false;
             }
-            return __shfl_sync(0xffffffffu, w, 0);
+            if (lane == 0) {
+                units[k % kDesc] = u;
+                mbar_arrive(&u_full[k % kDesc]);
+            }
+            __syncwarp();
+            *done = true;
+            return true;
         };
         Unit u = {};
-        for (long long k = 0; ok; ++k) {
-            find(k, &u);
-            ok = publish(k, u);
-            if (u.n[0] == 0) break;
+        int k = 0;
+        bool more = true, done;  // the last unit published does not end the list
+        find(0, &u);
+        auto pump = [&](bool must) {  // publishes the next unit and finds the one after
+            if (!more) return true;
+            if (!publish(k, u, must, &done)) return false;
+            if (done) {
+                more = u.n[0] != 0;
+                ++k;
+                if (more) find(k, &u);
+            }
+            return true;
+        };
+        if (NQ == 2) {
+            while (ok && more) ok = pump(true);
+        } else {
+            // this warp copies V, too, and publishes units as their places come free
+            typename C::VRing rc;
+            Walk w;
+            ok = pump(true) && pump(true) && pump(true) && step(w);
+            while (ok && !w.done) {
+                for (int c = 0; c < CPT && ok; ++c)
+                    ok = issue(&tmv, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows, rc);
+                if (ok) ok = pump(w.j + 1 == w.u.n[0] && w.k + 1 >= k);
+                if (ok) ok = step(w);
+            }
         }
         if (!ok && lane == 0) {
             pf_error(p.err, DEV_ERR_TIMEOUT);
@@ -520,32 +558,15 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         }
         __syncwarp();
         named_bar_sync(kBarEndPf, C::THREADS);
+        if (NQ == 1 && *abort_flag && lane == 0) landed(C::VN, CPT);
         return;
     }
 
     // ================================================================== TMA
     if (warp == 0) {
         bool ok = true;
-        long long nslot = 0;         // ring slots issued
-        long long left_out = -1;     // (one query tile) the place of a K tile past the last
         uint32_t qn[2] = {0, 0};     // query tiles issued
-        Ring<NS> rc;
-        // (by the whole warp: a uniform wait, then one lane's copies)
-        auto issue = [&](const void *tm, int c, int head, int row) -> bool {
-            const int slot = rc.slot;
-            if (nslot >= NS && !warp_wait(&slot_empty[slot], rc.parity ^ 1, abort_flag)) return false;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&slot_full[slot], C::SLOT);
-#pragma unroll
-                for (int sl = 0; sl < C::KC / 64; ++sl)
-                    tma_load_3d_plain(ring + slot * C::SLOT + sl * kSlab, tm, &slot_full[slot],
-                                      c * C::KC + sl * 64, head, row);
-            }
-            __syncwarp();
-            ++nslot;
-            rc.next();
-            return true;
-        };
+        typename C::KRing rc;
         auto load_q = [&](const Unit &u) -> bool {
             for (int s = 0; s < NQ; ++s) {
                 if (u.n[s] == 0) continue;
@@ -570,31 +591,20 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 const int n = max(u.n[0], u.n[1]);
                 const int kv0 = u.row0 + u.kbeg;
                 for (int j = 0; j < n && ok; ++j) {
-                    ok = issue(&tmk, 0, u.kvh, kv0 + j * kRows);
+                    ok = issue(&tmk, 0, u.kvh, kv0 + j * kRows, rc);
                     if (ok && j == 0) ok = load_q(u);
-                    if (ok) ok = issue(&tmv, 0, u.kvh, kv0 + j * kRows);
+                    if (ok) ok = issue(&tmv, 0, u.kvh, kv0 + j * kRows, rc);
                 }
             }
         } else {
-            Walk wk, wv;
-            auto tile = [&](const void *tm, const Walk &w) -> bool {
-                bool go = true;
-                for (int c = 0; c < CPT && go; ++c)
-                    go = issue(tm, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows);
-                return go;
-            };
-            auto put_k = [&]() -> bool {
-                if (wk.done) {  // behind the last K tile its place stays empty
-                    left_out = nslot;
-                    nslot += CPT;
-                    for (int c = 0; c < CPT; ++c) rc.next();
-                    return true;
-                }
-                return tile(&tmk, wk) && (wk.j > 0 || load_q(wk.u)) && step(wk);
-            };
-            ok = step(wk) && step(wv);
-            if (ok && !wk.done) ok = put_k() && put_k();
-            while (ok && !wv.done) ok = tile(&tmv, wv) && step(wv) && (wv.done || put_k());
+            Walk w;
+            ok = step(w);
+            while (ok && !w.done) {
+                for (int c = 0; c < CPT && ok; ++c)
+                    ok = issue(&tmk, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows, rc);
+                if (ok && w.j == 0) ok = load_q(w.u);
+                if (ok) ok = step(w);
+            }
         }
         if (!ok && lane == 0) {
             pf_error(p.err, DEV_ERR_TIMEOUT);
@@ -605,10 +615,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         named_bar_sync(kBarEndPf, C::THREADS);
         if (*abort_flag && lane == 0) {
             // a role gave up: let the copies in flight land before the CTA exits
+            landed(C::KN, 0);
             volatile int never = 0;
-            for (long long i = nslot > NS ? nslot - NS : 0; i < nslot; ++i)
-                if (left_out < 0 || i < left_out || i >= left_out + CPT)
-                    pf_wait(&slot_full[i % NS], (uint32_t)((i / NS) & 1), &never);
             for (int s = 0; s < NQ; ++s)
                 if (qn[s]) pf_wait(&q_full[s], (qn[s] - 1) & 1, &never);
         }
@@ -630,15 +638,9 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         uint32_t it = 0;              // turns taken, the last bit
         bool first_turn = true;
 
-        Ring<NS> rc;                  // the next slot that this warp has not waited for
-        auto slot_ready = [&]() {
-            const bool go = warp_wait(&slot_full[rc.slot], rc.parity, abort_flag);
-            rc.next();
-            return go;
-        };
         // S[buf] = Q_s K_j^T from the slots at r; keys past the tile's last are
         // left out, 16 at a time
-        auto qk = [&](int buf, Ring<NS> r, int keys, bool last) {
+        auto qk = [&](int buf, typename C::KRing r, int keys, bool last) {
             const uint32_t idesc = idesc_qk | ((uint32_t)((keys + 15) / 16 * 2) << 17);
             const uint32_t d = tmem + buf * 128;
             if (elect_one()) {
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             __syncwarp();
         };
         // O_s (+)= P[buf] V_j from the slots at r
-        auto pv = [&](int buf, Ring<NS> r, int keys, bool first) {
+        auto pv = [&](int buf, typename C::VRing r, int keys, bool first) {
             const uint32_t a = tmem + buf * 128, d = tmem + C::O0 + s * D;
             if (elect_one()) {
 #pragma unroll
@@ -678,8 +680,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             __syncwarp();
         };
 
-        Unit u;
-        if (NQ == 2) {
+        if constexpr (NQ == 2) {
+            Unit u;
             // The two query tiles' MMAs go out in turns, the products of one key
             // tile together: P V of the step before, then Q K^T of this one (of
             // the next unit's first key tile, too).  The query tiles then keep
@@ -687,6 +689,12 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             // products run.  Measured at 8192 tokens, 64 heads over 8 of 128:
             // left to share the tensor cores, both finish together and both
             // wait for both, 1009 us; in turns 869 us.
+            typename C::KRing rc;    // the next slot that this warp has not waited for
+            auto slot_ready = [&]() {
+                const bool go = warp_wait(&slot_full[rc.slot], rc.parity, abort_flag);
+                rc.next();
+                return go;
+            };
             int owed = 0;            // the step before: 1 its P V is due, 2 its V tile was not needed
             int owed_keys = 0;
             bool owed_first = false;
@@ -694,9 +702,9 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 // (one uniform wait after the other: what comes early is waited for
                 // while the other tile's MMAs are still running)
                 bool go = true;
-                const Ring<NS> rv = rc;
+                const auto rv = rc;
                 if (owed) go = slot_ready();
-                const Ring<NS> rk = rc;
+                const auto rk = rc;
                 if (go && j < nmax) go = slot_ready();
                 if (go && j == 0 && n > 0) go = warp_wait(&q_full[s], units_q++ & 1, abort_flag);
                 if (go && (s == 1 || !first_turn)) go = warp_wait(&turn[s], s == 0 ? it ^ 1 : it, abort_flag);
@@ -736,59 +744,48 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 const int end = min(u.t0 + (s + 1) * p.tpt, u.len) - u.kbeg;
                 for (int j = 0; j < nmax && ok; ++j) ok = turn_of(n, nmax, j, end);
             }
-        } else if (warp == 1) {
-            // One warp issues P V of key tile g, then Q K^T of g + 2 into the S
-            // buffer that P V has just read (the same thread's MMAs run in
-            // order), with the probabilities the last thing waited for.
-            Walk wq, wp;
-            auto keys_of = [&](const Walk &w) {
-                return min(kRows, min(w.u.t0 + p.tpt, w.u.len) - w.u.kbeg - w.j * kRows);
-            };
-            auto scores = [&](Ring<NS> r) -> bool {
-                qk(wq.g & 1, r, keys_of(wq), wq.j == wq.u.n[0] - 1);
-                return step(wq);
-            };
-            // Waits, a barrier a lane, for the V tile at rv and the
-            // probabilities (with_p) and for the K tile at rk and a unit's
-            // first q (with_k).
-            auto ready = [&](Ring<NS> rv, Ring<NS> rk, bool with_p, bool with_k) {
-                uint64_t *bar = nullptr;
-                uint32_t parity = 0;
+        } else {
+            // One warp issues Q K^T, the other P V, so that each one's waits pass
+            // under the other's MMAs.  Q K^T of key tile g goes into the S buffer
+            // that P V of g - 2 reads its P from: it is issued behind that (a
+            // fence on both sides of the barrier keeps the MMAs' order).
+            Walk w;
+            auto tile = [&](auto &rc) {
+                ok = step(w);
+                while (ok && !w.done) {
+                    const int buf = w.g & 1;
+                    const uint32_t parity = (w.g >> 1) & 1;
+                    const auto r = rc;
+                    if (warp == 1 && w.j == 0) ok = warp_wait(&q_full[0], units_q++ & 1, abort_flag);
 #pragma unroll
-                for (int c = 0; c < CPT; ++c, rv.next(), rk.next()) {
-                    if (lane == c && with_p) bar = &slot_full[rv.slot], parity = rv.parity;
-                    if (lane == CPT + c && with_k) bar = &slot_full[rk.slot], parity = rk.parity;
+                    for (int c = 0; c < CPT; ++c, rc.next())
+                        ok = ok && warp_wait(&slot_full[rc.slot], rc.parity, abort_flag);
+                    if (ok && warp == 1 && w.g >= 2) ok = warp_wait(&turn[buf], parity ^ 1, abort_flag);
+                    if (ok && warp == 2) ok = warp_wait(&p_full[buf], parity, abort_flag, wlim);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int keys = min(kRows, min(w.u.t0 + p.tpt, w.u.len) - w.u.kbeg - w.j * kRows);
+                    if constexpr (std::is_same_v<std::remove_const_t<decltype(r)>, typename C::KRing>) {
+                        qk(buf, r, keys, w.j == w.u.n[0] - 1);
+                    } else {
+                        pv(buf, r, keys, w.j == 0);
+                        if (elect_one()) {  // (the lane that issued)
+                            tc_fence_before();
+                            mbar_arrive(&turn[buf]);
+                        }
+                        __syncwarp();
+                    }
+                    ok = step(w);
                 }
-                const bool with_q = with_k && wq.j == 0;
-                if (lane == 2 * CPT && with_q) bar = &q_full[0], parity = units_q & 1;
-                if (lane == 2 * CPT + 1 && with_p) bar = &p_full[wp.g & 1], parity = (wp.g >> 1) & 1;
-                if (with_q) ++units_q;
-                return warp_wait_each(bar, parity, abort_flag, with_p ? wlim : KVATTN_SPIN_LIMIT);
             };
-            auto pass_tile = [&]() {
-                const Ring<NS> r = rc;
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) rc.next();
-                return r;
-            };
-            ok = step(wq) && step(wp);
-            for (int i = 0; i < 2 && ok; ++i) {
-                const Ring<NS> rk = pass_tile();
-                if (wq.done) break;  // (no second key tile: its place stays empty)
-                ok = ready(rk, rk, false, true);
-                if (!ok) break;
-                tc_fence_after();
-                ok = scores(rk);
-            }
-            while (ok && !wp.done) {
-                const Ring<NS> rv = pass_tile(), rk = pass_tile();
-                const bool more = !wq.done;
-                ok = ready(rv, rk, true, more);
-                if (!ok) break;
-                tc_fence_after();
-                pv(wp.g & 1, rv, keys_of(wp), wp.j == 0);
-                if (more) ok = scores(rk);
-                if (ok) ok = step(wp);
+            if constexpr (NQ == 1) {
+                if (warp == 1) {
+                    typename C::KRing rc;
+                    tile(rc);
+                } else {
+                    typename C::VRing rc;
+                    tile(rc);
+                }
             }
         }
         if (!ok) {
@@ -946,13 +943,13 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             // anything, which a weight of zero does not hide: they are zeroed
             const int stop = (keys + 15) / 16 * 16, past = u.len - kb;
             if (past < stop) {
-                const long long iv = NQ == 2 ? base + 2 * j + 1 : v_tile1(g) * CPT;
+                const long long iv = NQ == 2 ? base + 2 * j + 1 : g * CPT;  // (of the ring that V is in)
                 // (one query tile: the scores may be two tiles ahead of P V, and
                 // the slot's parity says something once the V tile before is done with)
                 if (NQ == 1 && g > 0) ok = warp_wait(&pv_done[buf ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abort_flag);
                 for (int c = 0; c < CPT && ok; ++c) {
-                    const int slot = (int)((iv + c) % NS);
-                    ok = warp_wait(&slot_full[slot], (uint32_t)(((iv + c) / NS) & 1), abort_flag);
+                    const int slot = (NQ == 2 ? 0 : CPT) + (int)((iv + c) % C::VN);
+                    ok = warp_wait(&slot_full[slot], (uint32_t)(((iv + c) / C::VN) & 1), abort_flag);
                     if (ok)
                         for (int i = row; i < (stop - past) * (C::KC / 64) * 8; i += 128) {
                             const int r = past + (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
