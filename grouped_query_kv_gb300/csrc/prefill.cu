@@ -129,9 +129,9 @@ struct PfCfg {
     // warp of its own (one copy warp for both took some 2700 cycles a key tile,
     // longer than its MMAs).  Either way a slot's waits see every fill in
     // order: a barrier's parity cannot tell a fill from the one two before.
-    static constexpr int KN = NQ == 2 ? NS : CPT, VN = NQ == 2 ? NS : NS - CPT;
+    static constexpr int KN = NQ == 2 ? NS : NS - CPT, VN = NQ == 2 ? NS : CPT;
     using KRing = Ring<KN, 0>;
-    using VRing = Ring<VN, NQ == 2 ? 0 : CPT>;
+    using VRing = Ring<VN, NQ == 2 ? 0 : KN>;
     static_assert(NS > 2 * CPT && NS >= 4, "the ring holds more than one K and one V tile");
     static_assert(alloc <= kSmemMax, "shared memory");
     // TMEM: S0, S1 (128 columns each; P over the first 64), then O per tile
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         }
         __syncwarp();
         named_bar_sync(kBarEndPf, C::THREADS);
-        if (NQ == 1 && *abort_flag && lane == 0) landed(C::VN, CPT);
+        if (NQ == 1 && *abort_flag && lane == 0) landed(C::VN, C::KN);
         return;
     }
 
@@ -948,7 +948,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 // the slot's parity says something once the V tile before is done with)
                 if (NQ == 1 && g > 0) ok = warp_wait(&pv_done[buf ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abort_flag);
                 for (int c = 0; c < CPT && ok; ++c) {
-                    const int slot = (NQ == 2 ? 0 : CPT) + (int)((iv + c) % C::VN);
+                    const int slot = (NQ == 2 ? 0 : C::KN) + (int)((iv + c) % C::VN);
                     ok = warp_wait(&slot_full[slot], (uint32_t)(((iv + c) / C::VN) & 1), abort_flag);
                     if (ok)
                         for (int i = row; i < (stop - past) * (C::KC / 64) * 8; i += 128) {
