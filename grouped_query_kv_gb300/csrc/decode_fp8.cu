@@ -125,6 +125,11 @@ struct Q8Cfg {
     static constexpr int SG = NP == 48 ? 3 : 2;
     static constexpr int NPH = NP / SG;  // columns of one softmax group
     static_assert(NPH % 8 == 0, "a group's columns come in tensor-memory loads of 8");
+    // paged: the softmax takes two tiles in one turn, with one vote, where their
+    // scores fit the registers: the turn's waits and barriers, not its
+    // arithmetic, are what a tile takes (32 ragged requests, 64 heads over 8 of
+    // 128: one tile a turn 62.2 us, two 57.7)
+    static constexpr bool PAIR = PG && NP <= 32;
     static constexpr int SOFTW = 4 * SG;              // softmax warps
     static constexpr int QWARP0 = 2 + SOFTW;          // first q-part warp
     static constexpr int VWARP = QWARP0 + QW;         // paged: copies V
@@ -711,6 +716,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
     // Votes (the running-max refresh, aborts) are taken by all softmax
     // threads, so the groups move their maxima and the V unit together.
     constexpr int NPH = C::NPH;
+    constexpr int U = C::PAIR ? 2 : 1;  // tiles of one turn of the loop
     const int sg = (warp - 2) >> 2;
     const int cg0 = sg * NPH;
     const int bar_grp = kBarQ8Grp + sg;
@@ -753,86 +759,122 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
         named_bar_sync(bar_grp, 128);
 
         while (true) {
-            const int sb = (int)(i & 1);
-            const int r0 = it.row0();
-            int pos = r0 + row;
-            bool valid;
-            if (PG && p.block_lg < 7 && it.last_tile_of_segment()) {
-                // small blocks: rows before the hole hold the earlier blocks,
-                // hn positions further on
-                const int hn = ((((len - 1) >> p.block_lg) + 1) << p.block_lg) - len;
-                const int hl = kT - (1 << p.block_lg);
-                if (row < hl) pos += hn;
-                valid = !(row >= hl && row < hl + hn) && pos >= it.first_pos() && pos < len;
-            } else {
-                valid = row >= it.first_pos() - r0 && pos < len;
-            }
-            // this row's scales, loaded while the scores are made -- except
-            // in a segment's last tile when this call appends: that tile may
-            // hold the row the copy warp has just written, so its scales are
-            // read once the tile's scores exist (the copy warp fenced its
-            // stores before issuing the tile's copies), past L1 (which may
-            // hold the line from the tile before)
-            const bool late = !PG && p.len_add && it.last_tile_of_segment();
-            float ksc = 0.f, vsc = 0.f;
-            if (!PG && valid && !late) {
-                ksc = p.k_scale[zrow + pos];
-                vsc = p.v_scale[zrow + pos];
-            }
-            bool fail = carry_fail || !wait_bar_warp(&s_full[sb], (uint32_t)((i >> 1) & 1), abort_flag);
-            if (PG && valid) {  // the copy warp's: row r of the tile came in box r / block size
-                const float *sc = sc_s + ((int)i & (C::SCR - 1)) * 16 + (p.block_lg >= 7 ? 0 : row >> p.block_lg);
-                ksc = sc[0];
-                vsc = sc[8];
-            }
-            if (!PG && valid && late) {
-                ksc = __ldcg(p.k_scale + zrow + pos);
-                vsc = __ldcg(p.v_scale + zrow + pos);
-            }
-            tc_fence_after();
-            // the group's scores: hi-part plus lo-part columns
-            float s[NPH];
-            tmem_ld_n<NPH>(lane_base + sb * C::SW + cg0, s);
-            tmem_ld_wait();
+            // the tiles of this turn: two where the piece has them (Q8Cfg::PAIR)
+            const int nu = U == 2 && i + 1 < ntiles && !it.last_tile_of_segment() ? 2 : 1;
+            const int t_first = it.t;
+            bool valid[U], late[U];
+            int pos[U];
+            float ksc[U], vsc[U];
 #pragma unroll
-            for (int c = 0; c + 16 <= NPH; c += 16) {
-                float v[16];
-                tmem_ld16(lane_base + sb * C::SW + NP + cg0 + c, v);
+            for (int u = 0; u < U; ++u) {
+                valid[u] = late[u] = false;
+                pos[u] = 0;
+                ksc[u] = vsc[u] = 0.f;
+                if (u >= nu) continue;
+                const int r0 = it.row0();
+                const bool last = it.last_tile_of_segment();
+                pos[u] = r0 + row;
+                if (PG && p.block_lg < 7 && last) {
+                    // small blocks: rows before the hole hold the earlier blocks,
+                    // hn positions further on
+                    const int hn = ((((len - 1) >> p.block_lg) + 1) << p.block_lg) - len;
+                    const int hl = kT - (1 << p.block_lg);
+                    if (row < hl) pos[u] += hn;
+                    valid[u] = !(row >= hl && row < hl + hn) && pos[u] >= it.first_pos() && pos[u] < len;
+                } else {
+                    valid[u] = row >= it.first_pos() - r0 && pos[u] < len;
+                }
+                // this row's scales, loaded while the scores are made -- except
+                // in a segment's last tile when this call appends: that tile may
+                // hold the row the copy warp has just written, so its scales are
+                // read once the tile's scores exist (the copy warp fenced its
+                // stores before issuing the tile's copies), past L1 (which may
+                // hold the line from the tile before)
+                late[u] = !PG && p.len_add && last;
+                if (!PG && valid[u] && !late[u]) {
+                    ksc[u] = p.k_scale[zrow + pos[u]];
+                    vsc[u] = p.v_scale[zrow + pos[u]];
+                }
+                if (u + 1 < nu) ++it.t;  // (the same segment)
+            }
+            it.t = t_first;
+            bool fail = carry_fail;
+            float s[U][NPH];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u >= nu) {
+#pragma unroll
+                    for (int g = 0; g < NPH; ++g) s[u][g] = -INFINITY;
+                    continue;
+                }
+                const int iu = (int)i + u, sb = iu & 1;
+                fail = fail || !wait_bar_warp(&s_full[sb], (uint32_t)((iu >> 1) & 1), abort_flag);
+                if (PG && valid[u]) {  // the copy warp's: row r of the tile came in box r / block size
+                    const float *sc = sc_s + (iu & (C::SCR - 1)) * 16 + (p.block_lg >= 7 ? 0 : row >> p.block_lg);
+                    ksc[u] = sc[0];
+                    vsc[u] = sc[8];
+                }
+                if (!PG && valid[u] && late[u]) {
+                    ksc[u] = __ldcg(p.k_scale + zrow + pos[u]);
+                    vsc[u] = __ldcg(p.v_scale + zrow + pos[u]);
+                }
+                tc_fence_after();
+                // the group's scores: hi-part plus lo-part columns
+                tmem_ld_n<NPH>(lane_base + sb * C::SW + cg0, s[u]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) s[c + k] += v[k];
-            }
-            if constexpr (NPH % 16 == 8) {
-                float v[8];
-                tmem_ld8(lane_base + sb * C::SW + NP + cg0 + NPH - 8, v);
-                tmem_ld_wait();
+                for (int c = 0; c + 16 <= NPH; c += 16) {
+                    float v[16];
+                    tmem_ld16(lane_base + sb * C::SW + NP + cg0 + c, v);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) s[NPH - 8 + k] += v[k];
+                    for (int k = 0; k < 16; ++k) s[u][c + k] += v[k];
+                }
+                if constexpr (NPH % 16 == 8) {
+                    float v[8];
+                    tmem_ld8(lane_base + sb * C::SW + NP + cg0 + NPH - 8, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) s[u][NPH - 8 + k] += v[k];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[sb]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[sb]);
 
-            const float sl = p.scale_log2 * ksc;
-            bool over = vsc * vsf > kVHi;
+            bool over = false;
 #pragma unroll
-            for (int g = 0; g < NPH; g += 4) {
-                const float4 m4 = *reinterpret_cast<const float4 *>(mref_s + cg0 + g);
-                const float4 c4 = *reinterpret_cast<const float4 *>(qinv + g);
-                s[g] = valid ? s[g] * (c4.x * sl) : -INFINITY;
-                s[g + 1] = valid ? s[g + 1] * (c4.y * sl) : -INFINITY;
-                s[g + 2] = valid ? s[g + 2] * (c4.z * sl) : -INFINITY;
-                s[g + 3] = valid ? s[g + 3] * (c4.w * sl) : -INFINITY;
-                over |= (s[g] > m4.x + kTauQ8) | (s[g + 1] > m4.y + kTauQ8) |
-                        (s[g + 2] > m4.z + kTauQ8) | (s[g + 3] > m4.w + kTauQ8);
+            for (int u = 0; u < U; ++u) {
+                if (u >= nu) continue;
+                const float sl = p.scale_log2 * ksc[u];
+                over |= vsc[u] * vsf > kVHi;
+#pragma unroll
+                for (int g = 0; g < NPH; g += 4) {
+                    const float4 m4 = *reinterpret_cast<const float4 *>(mref_s + cg0 + g);
+                    const float4 c4 = *reinterpret_cast<const float4 *>(qinv + g);
+                    float *x = s[u];
+                    x[g] = valid[u] ? x[g] * (c4.x * sl) : -INFINITY;
+                    x[g + 1] = valid[u] ? x[g + 1] * (c4.y * sl) : -INFINITY;
+                    x[g + 2] = valid[u] ? x[g + 2] * (c4.z * sl) : -INFINITY;
+                    x[g + 3] = valid[u] ? x[g + 3] * (c4.w * sl) : -INFINITY;
+                    over |= (x[g] > m4.x + kTauQ8) | (x[g + 1] > m4.y + kTauQ8) |
+                            (x[g + 2] > m4.z + kTauQ8) | (x[g + 3] > m4.w + kTauQ8);
+                }
             }
             if (named_bar_sync_or(kBarQ8All, 128 * C::SG, over || fail)) {
                 if (named_bar_sync_or(kBarQ8All, 128 * C::SG, fail || *abort_flag != 0)) {
                     aborted = true;
                     break;
                 }
-                warp_cols_n<NPH>(s, redg + q4 * 64, lane, OpMax());
-                const float vm = warp_max(vsc);  // 0 on rows past the length
+                if constexpr (U == 2) {
+                    float mx[NPH];
+#pragma unroll
+                    for (int g = 0; g < NPH; ++g) mx[g] = fmaxf(s[0][g], s[U - 1][g]);
+                    warp_cols_n<NPH>(mx, redg + q4 * 64, lane, OpMax());
+                } else {
+                    warp_cols_n<NPH>(s[0], redg + q4 * 64, lane, OpMax());
+                }
+                const float vm = warp_max(U == 2 ? fmaxf(vsc[0], vsc[U - 1]) : vsc[0]);  // 0 on rows past the length
                 if (lane == 0) vredg[q4] = vm;
                 named_bar_sync(bar_grp, 128);
                 if (row < NPH) {
@@ -890,65 +932,72 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
             // probabilities p (summed into l); the weights p v_scale 2^cv in
             // binary16 as three E4M3 parts, each the rounded remainder of the
             // previous
-            const float vs2 = vsc * vsf;
-            uint32_t ph[NPH / 4], pm[NPH / 4], pl[NPH / 4];
 #pragma unroll
-            for (int g4 = 0; g4 < NPH; g4 += 4) {
-                const float4 m4 = *reinterpret_cast<const float4 *>(mref_s + cg0 + g4);
-                const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+            for (int u = 0; u < U; ++u) {
+                if (u >= nu) continue;
+                const int iu = (int)i + u;
+                const float *x = s[u];
+                const float vs2 = vsc[u] * vsf;
+                uint32_t ph[NPH / 4], pm[NPH / 4], pl[NPH / 4];
 #pragma unroll
-                for (int h = 0; h < 4; h += 2) {
-                    const int g = g4 + h;
-                    const float p0 = (s[g] == -INFINITY) ? 0.f : fast_exp2(s[g] - mm[h]);
-                    const float p1 = (s[g + 1] == -INFINITY) ? 0.f : fast_exp2(s[g + 1] - mm[h + 1]);
-                    l[g] += p0;
-                    l[g + 1] += p1;
-                    // w rounded to binary16; its 11 significant bits split
-                    // exactly into three 4-bit E4M3 parts (each remainder is
-                    // a binary16 value, so the subtractions are exact)
-                    const uint32_t w = f16x2_of(p0 * vs2, p1 * vs2);
-                    const uint16_t c1 = e4m3x2_of_f16x2(w);
-                    const uint32_t r1 = f16x2_sub(w, e4m3x2_to_f16x2(c1));
-                    const uint16_t c2 = e4m3x2_of_f16x2(r1);
-                    const uint16_t c3 = e4m3x2_of_f16x2(f16x2_sub(r1, e4m3x2_to_f16x2(c2)));
-                    if (h == 0) {
-                        ph[g4 / 4] = c1;
-                        pm[g4 / 4] = c2;
-                        pl[g4 / 4] = c3;
-                    } else {
-                        ph[g4 / 4] |= (uint32_t)c1 << 16;
-                        pm[g4 / 4] |= (uint32_t)c2 << 16;
-                        pl[g4 / 4] |= (uint32_t)c3 << 16;
+                for (int g4 = 0; g4 < NPH; g4 += 4) {
+                    const float4 m4 = *reinterpret_cast<const float4 *>(mref_s + cg0 + g4);
+                    const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                    for (int h = 0; h < 4; h += 2) {
+                        const int g = g4 + h;
+                        const float p0 = (x[g] == -INFINITY) ? 0.f : fast_exp2(x[g] - mm[h]);
+                        const float p1 = (x[g + 1] == -INFINITY) ? 0.f : fast_exp2(x[g + 1] - mm[h + 1]);
+                        l[g] += p0;
+                        l[g + 1] += p1;
+                        // w rounded to binary16; its 11 significant bits split
+                        // exactly into three 4-bit E4M3 parts (each remainder is
+                        // a binary16 value, so the subtractions are exact)
+                        const uint32_t w = f16x2_of(p0 * vs2, p1 * vs2);
+                        const uint16_t c1 = e4m3x2_of_f16x2(w);
+                        const uint32_t r1 = f16x2_sub(w, e4m3x2_to_f16x2(c1));
+                        const uint16_t c2 = e4m3x2_of_f16x2(r1);
+                        const uint16_t c3 = e4m3x2_of_f16x2(f16x2_sub(r1, e4m3x2_to_f16x2(c2)));
+                        if (h == 0) {
+                            ph[g4 / 4] = c1;
+                            pm[g4 / 4] = c2;
+                            pl[g4 / 4] = c3;
+                        } else {
+                            ph[g4 / 4] |= (uint32_t)c1 << 16;
+                            pm[g4 / 4] |= (uint32_t)c2 << 16;
+                            pl[g4 / 4] |= (uint32_t)c3 << 16;
+                        }
                     }
                 }
-            }
-            if (i >= C::PST) {
-                const long long jp = i - C::PST;
-                if (!wait_bar_warp(&pv_done[jp & 1], (uint32_t)((jp >> 1) & 1), abort_flag))
-                    fail = true;
-            }
-            // P stage: column n's byte at 2048 (n / 16) + n mod 16 of its
-            // position row, rows at 128 (row / 8) + 16 (row mod 8); columns
-            // hi 0..NP-1, mid NP.., lo 2 NP..; the group's columns go in as
-            // 8-byte runs (column starts are multiples of 8)
-            uint8_t *pdst = pbuf + (int)(i % C::PST) * C::PB + (row >> 3) * 128 + (row & 7) * 16;
+                if (iu >= C::PST) {
+                    const int jp = iu - C::PST;
+                    if (!wait_bar_warp(&pv_done[jp & 1], (uint32_t)((jp >> 1) & 1), abort_flag))
+                        fail = true;
+                }
+                // P stage: column n's byte at 2048 (n / 16) + n mod 16 of its
+                // position row, rows at 128 (row / 8) + 16 (row mod 8); columns
+                // hi 0..NP-1, mid NP.., lo 2 NP..; the group's columns go in as
+                // 8-byte runs (column starts are multiples of 8)
+                uint8_t *pdst = pbuf + (iu % C::PST) * C::PB + (row >> 3) * 128 + (row & 7) * 16;
 #pragma unroll
-            for (int u = 0; u < NPH / 8; ++u) {
-                const int ch = cg0 + 8 * u, cm = NP + cg0 + 8 * u, cl = 2 * NP + cg0 + 8 * u;
-                *reinterpret_cast<uint2 *>(pdst + (ch >> 4) * 2048 + (ch & 15)) =
-                    make_uint2(ph[2 * u], ph[2 * u + 1]);
-                *reinterpret_cast<uint2 *>(pdst + (cm >> 4) * 2048 + (cm & 15)) =
-                    make_uint2(pm[2 * u], pm[2 * u + 1]);
-                *reinterpret_cast<uint2 *>(pdst + (cl >> 4) * 2048 + (cl & 15)) =
-                    make_uint2(pl[2 * u], pl[2 * u + 1]);
+                for (int e = 0; e < NPH / 8; ++e) {
+                    const int ch = cg0 + 8 * e, cm = NP + cg0 + 8 * e, cl = 2 * NP + cg0 + 8 * e;
+                    *reinterpret_cast<uint2 *>(pdst + (ch >> 4) * 2048 + (ch & 15)) =
+                        make_uint2(ph[2 * e], ph[2 * e + 1]);
+                    *reinterpret_cast<uint2 *>(pdst + (cm >> 4) * 2048 + (cm & 15)) =
+                        make_uint2(pm[2 * e], pm[2 * e + 1]);
+                    *reinterpret_cast<uint2 *>(pdst + (cl >> 4) * 2048 + (cl & 15)) =
+                        make_uint2(pl[2 * e], pl[2 * e + 1]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[iu & 1]);
             }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[sb]);
             carry_fail = fail;
 
-            ++i;
+            i += nu;
+            it.t += nu - 1;
             if (it.last_tile_of_segment() || i == ntiles) break;
             it.next();
         }
