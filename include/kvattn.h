@@ -624,7 +624,9 @@ KVATTN_API void kvattn_release(void);
  * Test and ablation knobs (process-wide; 0 restores the automatic choice).
  *   force_path : 0 auto, 1 CUDA-core FMA kernel, 2 tensor-core kernel
  *   num_ctas   : 0 auto, else the persistent grid size of the attention
- *                kernel (a small value forces long multi-CTA splits)
+ *                kernel (a small value forces long multi-CTA splits); also that
+ *                of gqa_prefill_attn, kv_block_tables and the split of
+ *                kv_append_paged_fp8
  * Returns KVATTN_ERR_INVALID_ARG for values out of range.
  */
 KVATTN_API int kvattn_set_tuning(int force_path, int num_ctas);
@@ -639,8 +641,10 @@ KVATTN_API int kvattn_set_tuning(int force_path, int num_ctas);
  * lets every copy and MMA it already issued finish, frees its tensor memory
  * and returns; the output of that call is undefined.  Waits for work already
  * issued keep their default limit.  With a very small value (1) a call is
- * sure to give up, which is how the tests exercise this path.  Always
- * returns KVATTN_OK.
+ * sure to give up, which is how the tests exercise this path.  It shortens
+ * gqa_prefill_attn's waits for scores, probabilities and P.V products the
+ * same way; the 8-bit kernels' waits keep their limit.  Always returns
+ * KVATTN_OK.
  */
 KVATTN_API int kvattn_set_wait_limit(unsigned int polls);
 
@@ -649,7 +653,8 @@ KVATTN_API int kvattn_set_wait_limit(unsigned int polls);
  * handles, owned by the caller), every later attention call records
  * `before` on its stream just before its split-KV kernel and `after` just
  * after it, so that cudaEventElapsedTime(before, after) is that kernel's
- * duration alone.  The records sit between the kernel and its neighbours on
+ * duration alone (gqa_prefill_attn has no such kernel and records nothing).
+ * The records sit between the kernel and its neighbours on
  * the stream, so they also end the programmatic overlap with them: use it to
  * time, not in production.  Pass (NULL, NULL) to stop; one NULL alone is
  * KVATTN_ERR_INVALID_ARG.
