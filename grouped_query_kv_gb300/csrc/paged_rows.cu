@@ -11,11 +11,14 @@
 // one dependent load per token.  Every block of the grid does the prefix sums
 // itself (B lengths from L2, no workspace, nothing to wait for), then takes
 // tiles of 4096 packed rows, a row's thread also writing the table entry of
-// the block that starts at it; up to one tile the call is one block.
+// the block that starts at it; up to one tile the call is one block.  On the
+// device 64 requests of one token take 4.4 us, 1024 requests of 1.0 M rows
+// 8.6 (their 8.4 MB of slots are 1.3).
 //
 // Row write.  A copy of 16-byte vectors, four K and four V vectors of a
 // thread in flight; both sides are contiguous per (token, head), so it runs
-// at the copy's bandwidth.
+// at the copy's bandwidth: 65 536 rows of 8 x 128 (537 MB read and written)
+// 80.4 us, 0.98 of the measured copy rate; 64 rows 2.5 us, a launch.
 #include "../../include/kvattn.h"
 #include "internal.h"
 #include "ptx.cuh"
