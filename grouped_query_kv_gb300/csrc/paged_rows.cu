@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kTblThreads) block_table_kernel(const TablePar
             const int t = t0 + i;
             slot[i] = -1;
             if (t < all_rows && t < p.num_slots) {
-                while (t >= first + r.n) {  // (ends: t is before the last request's end)
+                // (ends: t is before the last request's end; first + n may pass 32 bits)
+                while (t - first >= r.n) {
                     first += r.n;
                     before = cap32((long long)before + r.need);
                     enter(b + 1);

@@ -372,6 +372,14 @@ def test_block_tables_bad_requests():
     run_tables([3000, 7], [3000, 4000], 16, 600, 700, 700, num_slots=5000)  # the same with a large map
 
 
+def test_block_tables_row_counts_that_add_up_past_32_bits():
+    big = 2 ** 31 - 1
+    run_tables([5, 7], [3, big], 16, 8, 9, 9, num_slots=30)          # behind other rows, last
+    run_tables([5, 7, 1, 2], [29, big, big, 4], 16, 8, 9, 9, num_slots=30)
+    run_tables([5, 7], [5000, big], 16, 400, 400, 400, num_slots=9001)  # from the second tile on
+    run_tables([0] * 1500, [2] * 1499 + [big], 16, 8, 1500, 1500, num_slots=3001)
+
+
 def test_append_slots_moves_bits():
     for D, Hkv, bs, N in ((64, 1, 16, 1), (64, 3, 32, 77), (128, 8, 16, 500), (256, 1, 128, 300), (256, 8, 16, 33)):
         rng = np.random.default_rng(D + N)
