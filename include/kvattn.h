@@ -560,7 +560,9 @@ KVATTN_API int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
  *         0 <= seq_lens[b] <= max_blocks * block_size
  *   out : bf16 [B, Hq, D] (the 8-bit products carry the weights' 11
  *         significant bits, bf16 has 8)
- * Scales may be any finite values >= 0.  Pool rows at and past a length are
+ * Scales may be any finite values >= 0 (scale * q . K must stay finite in
+ * fp32, and a value scale's weight counts down to 2^-15 of the largest one
+ * its head's positions meet).  Pool rows at and past a length are
  * never read; table entries, lengths and device-side errors are those of
  * gqa_decode_attn_paged.  Its workspace is the stream's, as for the other
  * attention calls, but a call that is being captured gets one of that

@@ -271,6 +271,21 @@ def test_prefill_captured_replayed_and_on_two_streams():
     check_prefill(outs[0][:651], *(x[:651] for x in prefill_ref(*ts[0], [0, 650, 651], 0.1)))
 
 
+def test_prefill_past_32_bits():
+    # the last rows of a projection of 2^32 elements and more, out as well
+    N, Hq, Hkv, D = 530000, 64, 8, 128
+    qkv = torch.zeros((N, Hq + 2 * Hkv, D), dtype=torch.bfloat16, device="cuda")
+    qkv[N - 300:] = _normal((300, Hq + 2 * Hkv, D), 1)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    out = g.gqa_prefill_attn(q, k, v, _i32([N - 300, N - 170, N]), 0.1)
+    g.check_device_error()
+    last = [t[N - 300:].contiguous() for t in (q, k, v)]
+    check_prefill(out[N - 300:], *prefill_ref(*last, [0, 130, 300], 0.1))
+    assert not bool(out[:1000].any()) and not bool(out[N - 1000:N - 300].any())
+    del qkv, q, k, v, out
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------ tables and slots
 
 def tables_ref(cached, new, table, free, count, bs, num_slots):
@@ -727,6 +742,116 @@ def test_attn8_flags_bad_lengths_and_entries():
 
 
 # --------------------------------------------------------------- the whole path
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (256, 16, 1)])
+@pytest.mark.parametrize("order", [1, -1, 0])
+def test_attn8_scales_far_apart(D, Hq, Hkv, order):
+    # value scales that rise, fall or jump over 200 binary orders from block to
+    # block (the unit of the weights has to follow), zeros and a single head
+    # without any; key scales of zero
+    bs, lens = 16, [700, 16, 130, 1]
+    table, nblk = make_table(lens, bs, 5)
+    kc, _ = new_pool8(nblk, Hkv, bs, D, 6)
+    vc, _ = new_pool8(nblk, Hkv, bs, D, 7)
+    ks = torch.full((nblk, Hkv), 2.0 ** -8, device="cuda")
+    vs = torch.zeros((nblk, Hkv), device="cuda")
+    rng = np.random.default_rng(8)
+    for b, n in enumerate(lens):
+        ids = torch.as_tensor(table[b, :-(-n // bs)].astype(np.int64), device="cuda")
+        e = np.linspace(-100, 100, len(ids))
+        e = rng.permutation(e) if order == 0 else e[::order].copy()
+        vs[ids] = torch.exp2(torch.as_tensor(np.round(e), device="cuda").float())[:, None]
+        vs[ids[len(ids) // 2:][:1], 0] = 0.0
+        ks[ids[:2], Hkv - 1] = 0.0
+    q = _normal((len(lens), Hq, D), 9)
+    out = torch.full((len(lens), Hq, D), NAN, dtype=torch.bfloat16, device="cuda")
+    g.gqa_decode_attn_paged_fp8(q, kc, vc, ks, vs, _i32(table), _i32(lens), 1 / math.sqrt(D), out=out)
+    g.check_device_error()
+    ref, bound = attn8_ref(q, kc, vc, ks, vs, table, lens, 1 / math.sqrt(D), bs)
+    o = out.double().cpu().numpy()
+    assert np.isfinite(o).all()
+    assert (np.abs(o - ref) <= bound).all()
+
+
+def test_attn8_requests_that_share_blocks():
+    # one prefix's blocks in many table rows, read to different lengths
+    bs, Hkv, D = 16, 2, 128
+    table, nblk = make_table([400], bs, 3)
+    kc, _ = new_pool8(nblk, Hkv, bs, D, 1)
+    vc, _ = new_pool8(nblk, Hkv, bs, D, 2)
+    ks, vs = (torch.full((nblk, Hkv), 2.0 ** -7, device="cuda") for _ in range(2))
+    lens = [400, 399, 128, 129, 1, 0, 400]
+    table = np.repeat(table, len(lens), 0)
+    q = _normal((len(lens), 16, D), 4)
+    out = g.gqa_decode_attn_paged_fp8(q, kc, vc, ks, vs, _i32(table), _i32(lens), 0.1)
+    g.check_device_error()
+    ref, bound = attn8_ref(q, kc, vc, ks, vs, table, lens, 0.1, bs)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+
+
+def test_pool8_past_32_bits():
+    bs, D, nblk = 1024, 256, 16400  # 4.3 GB of K codes, as many of V
+    codes = [torch.zeros((nblk, 1, bs, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((nblk, 1), device="cuda") for _ in range(2)]
+    table = np.array([[nblk - 1, 16384, 0], [16383, 1, 2]], np.int32)  # block 16384 starts at byte 2^32
+    lens, cu = [2100, 700], [0, 2100, 2800]
+    q = _normal((2, 16, D), 1)
+    k, v = (_normal((2800, 1, D), i) for i in (2, 3))
+    g.kv_append_paged_fp8(*codes, *scales, k, v, _i32(table), _i32([0, 0]), _i32(cu))
+    out = g.gqa_decode_attn_paged_fp8(q, *codes, *scales, _i32(table), _i32(lens), 1 / 16)
+    g.check_device_error()
+    ids = table.ravel()
+    at = torch.as_tensor(ids.astype(np.int64), device="cuda")
+    kc, vc = (c[at] for c in codes)
+    ks, vs = (s[at] for s in scales)
+    near = np.arange(6, dtype=np.int32).reshape(2, 3)
+    for c, s, x in ((kc, ks, k), (vc, vs, v)):
+        empty = np.zeros((6, 1, bs, D))
+        rc, rs = append8_ref(empty, np.zeros((6, 1)), x.double().cpu().numpy(), near, [0, 0], cu, bs)
+        used = [0, 1, 2, 3]
+        assert np.array_equal(s.cpu().numpy()[used], rs[used])
+        assert same_values(values(c)[used], rc[used])
+    assert not any(bool(c[5].any()) for c in codes)
+    ref, bound = attn8_ref(q, kc, vc, ks, vs, near, lens, 1 / 16, bs)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+    del codes
+    torch.cuda.empty_cache()
+
+
+def test_the_largest_batch():
+    # 65535 requests of one token each: attention gives its value row back, exactly
+    # (a weight of one; a power of two times a code)
+    B, D, bs = 65535, 128, 16
+    zeros = torch.zeros(B, dtype=torch.int32, device="cuda")
+    table = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(B, dtype=torch.int32, device="cuda")
+    cu, slots, left = g.kv_block_tables(zeros, zeros + 1, table, free, _i32([B]), bs, B + 1)
+    g.check_device_error()
+    want = torch.arange(B - 1, -1, -1, device="cuda")
+    assert int(left) == 0 and torch.equal(table[:, 0].long(), want)
+    assert torch.equal(cu.long(), torch.arange(B + 1, device="cuda"))
+    assert torch.equal(slots[:B], want * bs) and int(slots[B]) == -1
+
+    q, k, v = (_normal((B, 1, D), i) for i in range(3))
+    out = g.gqa_prefill_attn(q, k, v, cu, 0.1)
+    g.check_device_error()
+    assert torch.equal(out, v)
+
+    codes = [torch.zeros((B, 1, bs, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((B, 1), device="cuda") for _ in range(2)]
+    g.kv_append_paged_fp8(*codes, *scales, k, v, table, zeros, cu)
+    g.check_device_error()
+    for c, s, x in zip(codes, scales, (k, v)):
+        x = x[:, 0].double()
+        need = torch.exp2(torch.ceil(torch.log2(x.abs().amax(1) / 448)))
+        assert torch.equal(s[want, 0].double(), need)
+        rows = (x / need[:, None]).to(torch.float32).to(torch.float8_e4m3fn)
+        assert torch.equal(c[want, 0, 0].view(torch.float8_e4m3fn).float(), rows.float())
+    out = g.gqa_decode_attn_paged_fp8(q, *codes, *scales, table, zeros + 1, 0.1)
+    g.check_device_error()
+    row = codes[1][want, 0, 0].view(torch.float8_e4m3fn).float() * scales[1][want]
+    assert torch.equal(out[:, 0].float(), row)
+
 
 def test_prompts_then_steps_through_bf16_and_8_bit_pools():
     """Admission, prompt attention and single-token steps: after each step the
