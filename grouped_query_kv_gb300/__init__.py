@@ -567,6 +567,15 @@ def _want(t, name, dtype, dev, shape=None):
     raise ValueError("%s must be on the current CUDA device %d (got %s)" % (name, dev, t.device))
 
 
+def _new(make, shape, dtype, like, stream):
+    """An output made by torch.empty or torch.zeros on the stream that the call
+    launches on, so that what fills it, or used its memory before, comes first."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
 def _int32(x, name):
     """x as an int that a C int holds."""
     x = int(x)
@@ -627,11 +636,11 @@ def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count,
     _want(free_count, "free_count", i32, dev, (1,))
     num_slots = _int32(num_slots, "num_slots")
     if cu_seqlens is None:
-        cu_seqlens = torch.empty(B + 1, dtype=i32, device=cached_lens.device)
+        cu_seqlens = _new(torch.empty, (B + 1,), i32, cached_lens, stream)
     else:
         _want(cu_seqlens, "cu_seqlens", i32, dev, (B + 1,))
     if slots is None:
-        slots = torch.empty(max(num_slots, 0), dtype=torch.int64, device=cached_lens.device)
+        slots = _new(torch.empty, (max(num_slots, 0),), torch.int64, cached_lens, stream)
     else:
         _want(slots, "slots", torch.int64, dev, (num_slots,))
     if free_count_out is None:
@@ -693,7 +702,7 @@ def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=N
     if cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be [B + 1]")
     if out is None:
-        out = torch.zeros((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _new(torch.zeros, (N, Hq, D), torch.bfloat16, q, stream)
     else:
         _want(out, "out", torch.bfloat16, dev, (N, Hq, D))
     _check(lib().gqa_prefill_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out),
@@ -761,7 +770,7 @@ def gqa_decode_attn_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table
         raise ValueError("k_codes / block_table do not match q")
     _want(seq_lens, "seq_lens", torch.int32, dev, (B,))
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _new(torch.empty, (B, Hq, D), torch.bfloat16, q, stream)
     else:
         _want(out, "out", torch.bfloat16, dev, (B, Hq, D))
     _check(lib().gqa_decode_attn_paged_fp8(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),

@@ -907,6 +907,31 @@ def test_prompts_then_steps_through_bf16_and_8_bit_pools():
     assert len(set(used)) == len(used) == nblk - int(count)
 
 
+def test_calls_on_another_stream_than_the_current_one():
+    # outputs that a call makes belong to its stream: nothing of the current
+    # stream, busy here, may come behind them
+    side = torch.cuda.Stream()
+    qkv = _normal((200, 10, 128), 1)
+    q, k, v = qkv[:, :8], qkv[:, 8:9], qkv[:, 9:]
+    cu, cached, new = _i32([0, 150, 200]), _i32([0, 0]), _i32([150, 50])
+    table, free, count = torch.full((2, 16), -1, dtype=torch.int32, device="cuda"), _i32(range(20)), _i32([20])
+    pool = [torch.zeros((20, 1, 16, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((20, 1), device="cuda") for _ in range(2)]
+    last = qkv[[149, 199], :8].contiguous()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # the current stream, for some 0.1 s
+    out = g.gqa_prefill_attn(q, k, v, cu, 0.1, stream=side)
+    rows, slots, left = g.kv_block_tables(cached, new, table, free, count, 16, 200, stream=side)
+    g.kv_append_paged_fp8(*pool, *scales, k, v, table, cached, rows, stream=side)
+    step = g.gqa_decode_attn_paged_fp8(last, *pool, *scales, table, new, 0.1, stream=side)
+    torch.cuda.synchronize()
+    g.check_device_error()
+    check_prefill(out, *prefill_ref(q, k, v, [0, 150, 200], 0.1))
+    assert rows.tolist() == [0, 150, 200] and int(left) == 20 - 10 - 4 and int((slots < 0).sum()) == 0
+    ref, bound = attn8_ref(last, *pool, *scales, table.cpu().numpy(), [150, 50], 0.1, 16)
+    assert (np.abs(step.double().cpu().numpy() - ref) <= bound).all()
+
+
 def test_the_path_captured_and_replayed():
     """One decode step of every call in a graph, replayed: lengths and the free
     list advance on the device."""
