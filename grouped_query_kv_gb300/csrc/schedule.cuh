@@ -98,26 +98,27 @@ __device__ __forceinline__ int warp_incl_scan(int v) {
     return v;
 }
 
-// A tile found by its start cost.
+// A tile found by its start cost (I: an integer that holds the total cost).
+template <class I>
 struct SchedHit {
-    long long g;      // tile index (the total if the cost is past the end)
-    long long cost0;  // start cost of its segment
+    I g;      // tile index (the total if the cost is past the end)
+    I cost0;  // start cost of its segment
     int b, seg, t;
 };
 
 // Where cost T falls in a sequence whose cost starts at ec (segments of segc,
 // nt tiles each): the tile, its segment's start cost and coordinates.
-__device__ __forceinline__ SchedHit sched_hit_in(long long T, long long ec, int segc, int nt,
-                                                 long long tiles_before, int b, int segs_per_b,
-                                                 int P) {
+template <class I>
+__device__ __forceinline__ SchedHit<I> sched_hit_in(I T, I ec, int segc, int nt, I tiles_before, int b,
+                                                    int segs_per_b, int P) {
     const unsigned long long rb = (unsigned long long)(T - ec);
-    int seg = (int)(rb <= 0xffffffffull ? (unsigned)rb / (unsigned)segc
-                                        : rb / (unsigned long long)segc);
+    int seg = (int)(sizeof(I) == 4 || rb <= 0xffffffffull ? (unsigned)rb / (unsigned)segc
+                                                          : rb / (unsigned long long)segc);
     const int rem = (int)(rb - (unsigned long long)seg * segc);
     int t = rem == 0 ? 0 : max(1, (rem - P + kCostTile - 1) >> kCostTileShift);
-    SchedHit h;
-    h.g = tiles_before + (long long)seg * nt + t;
-    h.cost0 = ec + (long long)seg * segc;
+    SchedHit<I> h;
+    h.g = tiles_before + (I)seg * nt + t;
+    h.cost0 = ec + (I)seg * segc;
     h.b = b;
     if (t >= nt) {  // the next segment's first tile
         t = 0;
@@ -132,7 +133,8 @@ __device__ __forceinline__ SchedHit sched_hit_in(long long T, long long ec, int 
     return h;
 }
 
-__device__ __forceinline__ void sched_take(SchedHit *h, const SchedHit &mine, int src) {
+template <class I>
+__device__ __forceinline__ void sched_take(SchedHit<I> *h, const SchedHit<I> &mine, int src) {
     h->g = __shfl_sync(0xffffffffu, mine.g, src);
     h->cost0 = __shfl_sync(0xffffffffu, mine.cost0, src);
     h->b = __shfl_sync(0xffffffffu, mine.b, src);
@@ -144,11 +146,11 @@ __device__ __forceinline__ void sched_take(SchedHit *h, const SchedHit &mine, in
 // (NT = 2) >= T1, T0 <= T1.  The cost before sequence b is
 // segs_per_b * (W * (tiles of the sequences before b) + P * b).  Every lane
 // evaluates its own sequence for both bounds at once; a ballot picks the
-// lane that holds each.
-template <int NT>
+// lane that holds each.  KEPT: nt_first holds the tiles of sequence `lane`.
+template <int NT, class I, bool KEPT>
 __device__ inline void sched_find(LenView lens, int B, int Lmax, int tile, int segs_per_b,
-                                  SchedCost w, long long T0, long long T1, long long total,
-                                  SchedHit *h0, SchedHit *h1) {
+                                  SchedCost w, int nt_first, I T0, I T1, I total,
+                                  SchedHit<I> *h0, SchedHit<I> *h1) {
     const int lane = threadIdx.x & 31;
     h0->g = h1->g = total;
     h0->cost0 = h1->cost0 = 0;
@@ -157,19 +159,21 @@ __device__ inline void sched_find(LenView lens, int B, int Lmax, int tile, int s
     int tcarry = 0;  // tiles of one segment of every sequence so far
     for (int base = 0; base < B && !(got0 && got1); base += 32) {
         const int b = base + lane;
-        const int nt = (b < B) ? seq_ntiles(lens[b], Lmax, tile, lens.window, lens.walign) : 0;
+        const int nt = KEPT && base == 0 ? nt_first
+                       : b < B           ? seq_ntiles(lens[b], Lmax, tile, lens.window, lens.walign)
+                                         : 0;
         const int incl = warp_incl_scan(nt);
         const int before = tcarry + incl - nt;
         const int segc = nt * kCostTile + w.P;  // one segment of sequence b
-        const long long ec = (long long)segs_per_b * ((long long)before * kCostTile + (long long)w.P * b);
-        const long long vc = (b < B) ? (long long)segs_per_b * segc : 0;
-        const long long tb = (long long)before * segs_per_b;
+        const I ec = (I)segs_per_b * ((I)before * kCostTile + (I)w.P * (KEPT ? min(b, B) : b));
+        const I vc = (b < B) ? (I)segs_per_b * segc : 0;
+        const I tb = (I)before * segs_per_b;
         const bool in0 = (b < B) && ec <= T0 && T0 < ec + vc;
         const bool in1 = NT > 1 && (b < B) && ec <= T1 && T1 < ec + vc;
-        const SchedHit m0 = sched_hit_in(in0 ? T0 : ec, ec, segc > 0 ? segc : 1, nt, tb, b,
-                                         segs_per_b, w.P);
-        SchedHit m1 = m0;
-        if (NT > 1) m1 = sched_hit_in(in1 ? T1 : ec, ec, segc > 0 ? segc : 1, nt, tb, b, segs_per_b, w.P);
+        const SchedHit<I> m0 = sched_hit_in<I>(in0 ? T0 : ec, ec, segc > 0 ? segc : 1, nt, tb, b,
+                                               segs_per_b, w.P);
+        SchedHit<I> m1 = m0;
+        if (NT > 1) m1 = sched_hit_in<I>(in1 ? T1 : ec, ec, segc > 0 ? segc : 1, nt, tb, b, segs_per_b, w.P);
         const unsigned b0 = __ballot_sync(0xffffffffu, in0);
         const unsigned b1 = __ballot_sync(0xffffffffu, in1);
         if (b0 && !got0) {
@@ -185,20 +189,27 @@ __device__ inline void sched_find(LenView lens, int B, int Lmax, int tile, int s
 }
 
 // Called by a whole warp: totals (tiles, cost) and the CTA count that the
-// split uses.
+// split uses; KEPT: and the tiles of one segment of sequence `lane`.
+template <bool KEPT = false>
 __device__ inline void sched_totals(LenView lens, int B, int Lmax, int tile, int segs_per_b,
                                     SchedCost w, int grid, long long *total, long long *cost,
-                                    int *ctas_eff) {
+                                    int *ctas_eff, int *nt_first = nullptr) {
     const int lane = threadIdx.x & 31;
     int nt_lane = 0;
-    for (int b = lane; b < B; b += 32) nt_lane += seq_ntiles(lens[b], Lmax, tile, lens.window, lens.walign);
+    if (KEPT) *nt_first = 0;
+    for (int b = lane; b < B; b += 32) {
+        const int nt = seq_ntiles(lens[b], Lmax, tile, lens.window, lens.walign);
+        if (KEPT && b == lane) *nt_first = nt;
+        nt_lane += nt;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) nt_lane += __shfl_xor_sync(0xffffffffu, nt_lane, o);
     const long long nt_sum = nt_lane;  // tiles of one segment of every sequence
     *total = nt_sum * segs_per_b;
     *cost = (long long)segs_per_b * (nt_sum * kCostTile + (long long)w.P * B);
     long long ce = *total < (long long)grid ? *total : (long long)grid;
-    if (*cost < (long long)(kCostTile + w.P) * ce) ce = *cost / (kCostTile + w.P);
+    if (*cost < (long long)(kCostTile + w.P) * ce)
+        ce = KEPT && *cost <= 0x7fffffff ? (int)*cost / (kCostTile + w.P) : *cost / (kCostTile + w.P);
     *ctas_eff = (int)(ce < 1 ? 1 : ce);
 }
 
@@ -217,29 +228,60 @@ __device__ __forceinline__ long long sched_bound(long long cost, int ctas_eff, i
     return (long long)c * q + ((unsigned)c * rem + C - 1) / C;
 }
 
-// Locate CTA `c`'s tile range; called by a whole warp (every warp of a CTA
-// can do it on its own, so the TMA producer starts as soon as the lengths
-// have been read).
-__device__ inline SchedStart warp_locate(LenView lens, int B, int Lmax, int tile,
-                                         int segs_per_b, SchedCost w, int c, int grid) {
-    SchedStart r;
-    sched_totals(lens, B, Lmax, tile, segs_per_b, w, grid, &r.total, &r.cost, &r.ctas_eff);
-    r.found = 0;
-    r.b = r.seg = r.t = 0;
-    r.g_begin = r.g_end = r.total;
-    r.cost0 = 0;
-    if (c >= r.ctas_eff) return r;
-    const long long T0 = sched_bound(r.cost, r.ctas_eff, c);
-    const long long T1 = sched_bound(r.cost, r.ctas_eff, c + 1);
-    SchedHit h0, h1;
-    sched_find<2>(lens, B, Lmax, tile, segs_per_b, w, T0, T1, r.total, &h0, &h1);
+// T(c) and T(c + 1), whose quotients differ by the carry of the remainder.
+template <class I>
+__device__ __forceinline__ void sched_bounds(I cost, int ctas_eff, int c, I *T0, I *T1) {
+    const unsigned C = (unsigned)ctas_eff;
+    const I q = cost / ctas_eff;
+    const unsigned rem = (unsigned)(cost - q * ctas_eff);
+    const unsigned x = (unsigned)c * rem + C - 1, d = x / C;
+    *T0 = (I)c * q + (I)d;
+    *T1 = *T0 + q + (x - d * C + rem >= C ? 1 : 0);
+}
+
+template <class I, bool KEPT>
+__device__ __forceinline__ void sched_range(LenView lens, int B, int Lmax, int tile, int segs_per_b,
+                                            SchedCost w, int nt_first, I T0, I T1, SchedStart &r) {
+    SchedHit<I> h0, h1;
+    sched_find<2, I, KEPT>(lens, B, Lmax, tile, segs_per_b, w, nt_first, T0, T1, (I)r.total, &h0, &h1);
     r.g_end = h1.g;
     r.g_begin = h0.g;
     r.cost0 = h0.cost0;
     r.b = h0.b;
     r.seg = h0.seg;
     r.t = h0.t;
-    r.found = h0.g < r.total ? 1 : 0;
+    r.found = h0.g < (I)r.total ? 1 : 0;
+}
+
+// Locate CTA `c`'s tile range; called by a whole warp (every warp of a CTA
+// can do it on its own, so the TMA producer starts as soon as the lengths
+// have been read).  NARROW: in 32 bits where the total cost fits them, and with
+// the first lengths kept -- some 3000 cycles from the lengths being readable
+// instead of 3700 (five requests over a paged 8-bit pool 11.5 -> 11.2 us); the
+// kernels whose registers are all taken keep the other form (with this one the
+// 48-column 8-bit pass at D = 256 went from 39.2 to 39.7 us).
+template <bool NARROW = false>
+__device__ inline SchedStart warp_locate(LenView lens, int B, int Lmax, int tile,
+                                         int segs_per_b, SchedCost w, int c, int grid) {
+    SchedStart r;
+    int nt_first = 0;
+    sched_totals<NARROW>(lens, B, Lmax, tile, segs_per_b, w, grid, &r.total, &r.cost, &r.ctas_eff, &nt_first);
+    r.found = 0;
+    r.b = r.seg = r.t = 0;
+    r.g_begin = r.g_end = r.total;
+    r.cost0 = 0;
+    if (c >= r.ctas_eff) return r;
+    if constexpr (NARROW) {
+        if (r.cost <= 0x7fffffff) {
+            int T0, T1;
+            sched_bounds<int>((int)r.cost, r.ctas_eff, c, &T0, &T1);
+            sched_range<int, true>(lens, B, Lmax, tile, segs_per_b, w, nt_first, T0, T1, r);
+            return r;
+        }
+    }
+    const long long T0 = sched_bound(r.cost, r.ctas_eff, c);
+    const long long T1 = sched_bound(r.cost, r.ctas_eff, c + 1);
+    sched_range<long long, false>(lens, B, Lmax, tile, segs_per_b, w, 0, T0, T1, r);
     return r;
 }
 
@@ -260,8 +302,9 @@ __device__ inline void sched_split_record(LenView lens, int B, int Lmax, int til
         // below T(c-1)
         const long long Tp = sched_bound(st.cost, st.ctas_eff, c - 1);
         if (st.cost0 >= Tp) {
-            SchedHit hp, unused;
-            sched_find<1>(lens, B, Lmax, tile, segs_per_b, w, Tp, Tp, st.total, &hp, &unused);
+            SchedHit<long long> hp, unused;
+            sched_find<1, long long, false>(lens, B, Lmax, tile, segs_per_b, w, 0, Tp, Tp, st.total, &hp,
+                                            &unused);
             const int nt = seq_ntiles(lens[st.b], Lmax, tile, lens.window, lens.walign);
             const long long last_cost = st.cost0 + (nt == 1 ? 0 : w.P + (long long)kCostTile * (nt - 1));
             const int c_last = sched_owner(last_cost, st.cost, st.ctas_eff);

@@ -818,6 +818,22 @@ def test_pool8_past_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_attn8_schedule_past_32_bits():
+    # so many segments that their cost passes 2^31; all read one block's first row
+    B, H, D, bs = 65535, 384, 128, 16
+    codes = torch.randint(0, 120, (1, H, bs, D), generator=_gen(1), device="cuda", dtype=torch.uint8)
+    scale = torch.full((1, H), 0.25, device="cuda")
+    q = torch.ones((B, H, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((B, H, D), NAN, dtype=torch.bfloat16, device="cuda")
+    g.gqa_decode_attn_paged_fp8(q, codes, codes, scale, scale, torch.zeros((B, 1), dtype=torch.int32, device="cuda"),
+                                torch.ones(B, dtype=torch.int32, device="cuda"), 0.1, out=out)
+    g.check_device_error()
+    row = (codes[0, :, 0].view(torch.float8_e4m3fn).float() * 0.25).to(torch.bfloat16)
+    assert bool((out == row).all())
+    del q, out
+    torch.cuda.empty_cache()
+
+
 def test_the_largest_batch():
     # 65535 requests of one token each: attention gives its value row back, exactly
     # (a weight of one; a power of two times a code)
@@ -913,23 +929,25 @@ def test_calls_on_another_stream_than_the_current_one():
     side = torch.cuda.Stream()
     qkv = _normal((200, 10, 128), 1)
     q, k, v = qkv[:, :8], qkv[:, 8:9], qkv[:, 9:]
-    cu, cached, new = _i32([0, 150, 200]), _i32([0, 0]), _i32([150, 50])
-    table, free, count = torch.full((2, 16), -1, dtype=torch.int32, device="cuda"), _i32(range(20)), _i32([20])
-    pool = [torch.zeros((20, 1, 16, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
-    scales = [torch.zeros((20, 1), device="cuda") for _ in range(2)]
     last = qkv[[149, 199], :8].contiguous()
-    torch.cuda.synchronize()
-    torch.cuda._sleep(200_000_000)  # the current stream, for some 0.1 s
-    out = g.gqa_prefill_attn(q, k, v, cu, 0.1, stream=side)
-    rows, slots, left = g.kv_block_tables(cached, new, table, free, count, 16, 200, stream=side)
-    g.kv_append_paged_fp8(*pool, *scales, k, v, table, cached, rows, stream=side)
-    step = g.gqa_decode_attn_paged_fp8(last, *pool, *scales, table, new, 0.1, stream=side)
-    torch.cuda.synchronize()
-    g.check_device_error()
-    check_prefill(out, *prefill_ref(q, k, v, [0, 150, 200], 0.1))
-    assert rows.tolist() == [0, 150, 200] and int(left) == 20 - 10 - 4 and int((slots < 0).sum()) == 0
-    ref, bound = attn8_ref(last, *pool, *scales, table.cpu().numpy(), [150, 50], 0.1, 16)
-    assert (np.abs(step.double().cpu().numpy() - ref) <= bound).all()
+    cu, cached, new = _i32([0, 150, 200]), _i32([0, 0]), _i32([150, 50])
+    for busy in (False, True):  # (a first call may wait for the device by itself)
+        table, free, count = torch.full((2, 16), -1, dtype=torch.int32, device="cuda"), _i32(range(20)), _i32([20])
+        pool = [torch.zeros((20, 1, 16, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros((20, 1), device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        if busy:
+            torch.cuda._sleep(200_000_000)  # some 0.1 s
+        out = g.gqa_prefill_attn(q, k, v, cu, 0.1, stream=side)
+        rows, slots, left = g.kv_block_tables(cached, new, table, free, count, 16, 200, stream=side)
+        g.kv_append_paged_fp8(*pool, *scales, k, v, table, cached, rows, stream=side)
+        step = g.gqa_decode_attn_paged_fp8(last, *pool, *scales, table, new, 0.1, stream=side)
+        torch.cuda.synchronize()
+        g.check_device_error()
+        check_prefill(out, *prefill_ref(q, k, v, [0, 150, 200], 0.1))
+        assert rows.tolist() == [0, 150, 200] and int(left) == 20 - 10 - 4 and int((slots < 0).sum()) == 0
+        ref, bound = attn8_ref(last, *pool, *scales, table.cpu().numpy(), [150, 50], 0.1, 16)
+        assert (np.abs(step.double().cpu().numpy() - ref) <= bound).all()
 
 
 def test_the_path_captured_and_replayed():
