@@ -783,7 +783,7 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
     p.block_lg = lg;
     p.max_blocks = pg ? pg->max_blocks : 0;
     p.num_blocks = pg ? pg->num_blocks : 0;
-    p.out_bf16 = pg ? 1 : 0;
+    p.out_bf16 = p.even_small = pg ? 1 : 0;
     cudaError_t e;
     if (ev_before && (e = cudaEventRecord(ev_before, stream)) != cudaSuccess)
         return cuda_fail(e, "recording the event before the split-KV kernel");

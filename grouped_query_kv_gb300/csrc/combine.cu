@@ -45,10 +45,11 @@ __device__ inline void segment_pieces(const DecodeParams &p, int s, int grid, in
     const int lane = threadIdx.x & 31;
     const LenView lens{p.seq_lens, p.len_add, p.window, p.walign};
     const int segs_per_b = p.Hkv * p.head_groups;
-    const SchedCost w{p.cost_piece};
+    SchedCost w{p.cost_piece};
     long long total, cost;
     int ctas_eff;
     sched_totals(lens, p.B, p.Lmax, p.tile, segs_per_b, w, grid, &total, &cost, &ctas_eff);
+    if (p.even_small) sched_even(grid, p.B * segs_per_b, total, &cost, &ctas_eff, &w);
     const int b = s / segs_per_b, sg = s % segs_per_b;
     int before = 0;  // tiles of one segment of every sequence before b
     for (int bb = lane; bb < b; bb += 32) before += seq_ntiles(lens[bb], p.Lmax, p.tile, lens.window, lens.walign);

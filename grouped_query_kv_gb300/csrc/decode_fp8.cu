@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
     const LenView lens{p.seq_lens, p.len_add, p.window, 0};  // contiguous: no window alignment
     const SchedCost wcost{p.cost_piece};
     const SchedStart st = warp_locate<PG>(lens, p.B, p.Lmax, kT, segs_per_b, wcost, blockIdx.x, gridDim.x);
-    if (warp == 2) sched_split_record(lens, p.B, p.Lmax, kT, segs_per_b, wcost, blockIdx.x, st, p.split);
+    if (warp == 2) sched_split_record(lens, p.B, p.Lmax, kT, segs_per_b, PG ? SchedCost{st.P} : wcost, blockIdx.x, st, p.split);
     if (!st.found) {
         if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
         pdl_launch_dependents();

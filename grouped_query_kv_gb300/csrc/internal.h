@@ -72,6 +72,7 @@ struct DecodeParams {
     int walign;               // 0, or tile - 1 (paged cache): window spans start on a tile
                               // boundary and the rows before a query's window are masked
     int out_bf16;             // out holds bf16 values (the paged 8-bit cache), else fp32
+    int even_small;           // small calls are split in equal runs of tiles (the same cache)
 };
 
 // Host launchers (return cudaError_t of the launch).

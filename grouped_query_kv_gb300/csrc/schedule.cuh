@@ -80,6 +80,7 @@ struct SchedStart {
     int ctas_eff;
     int found;          // 1 if this CTA has work
     int b, seg, t;      // coordinates of g_begin: sequence, segment within b, tile
+    int P;              // the piece weight that the split used
 };
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
@@ -213,6 +214,30 @@ __device__ inline void sched_totals(LenView lens, int B, int Lmax, int tile, int
     *ctas_eff = (int)(ce < 1 ? 1 : ce);
 }
 
+// Calls too small for the equal-cost split to use every CTA (TC / (W + P) below
+// the grid: a piece is charged more than the work it would share): equal runs of
+// tiles instead, whatever a piece costs, as short as the grid allows -- the other
+// CTAs' SMs would be idle, and a second piece of a CTA is the longer wait -- but
+// no more than kPiecesEach pieces of a segment, which are merged in a chain of
+// batches.  A whole number of tiles each: 192 tiles on 152 CTAs are 96 pairs
+// (one segment of 4096 in each of six requests at D = 256 13.5 us by cost, 16.9
+// cut 152 ways, 12.8 in pairs).  Paged 8-bit calls, by cost and by this rule:
+// five requests of up to 301 (40 segments, 64 tiles) 11.1 and 9.0 us; one of 2048
+// with 8 K/V heads 12.7 and 10.1, of 4096 13.6 and 11.5; eight of 4096, 48 query
+// heads over one 24.0 and 16.5; a segment of 64 tiles, 16 heads, 13.9 and 13.0 (a
+// tile each 14.9); the worst found, eight ragged ones of 256 tiles together, 15.0
+// and 15.8.
+constexpr int kPiecesEach = 32;
+__device__ __forceinline__ void sched_even(int grid, int segments, long long total, long long *cost,
+                                                int *ctas_eff, SchedCost *w) {
+    if (total > grid && *ctas_eff >= grid) return;
+    w->P = 0;
+    *cost = total * kCostTile;
+    const int n = (int)total, most = (int)min((long long)grid, (long long)segments * kPiecesEach);
+    const int each = (n + most - 1) / most;
+    *ctas_eff = (n + each - 1) / each;
+}
+
 // Owner of a tile with start cost s.
 __device__ __forceinline__ int sched_owner(long long s, long long cost, int ctas_eff) {
     const long long c = s * ctas_eff / cost;
@@ -266,6 +291,8 @@ __device__ inline SchedStart warp_locate(LenView lens, int B, int Lmax, int tile
     SchedStart r;
     int nt_first = 0;
     sched_totals<NARROW>(lens, B, Lmax, tile, segs_per_b, w, grid, &r.total, &r.cost, &r.ctas_eff, &nt_first);
+    if (NARROW) sched_even(grid, B * segs_per_b, r.total, &r.cost, &r.ctas_eff, &w);
+    r.P = w.P;
     r.found = 0;
     r.b = r.seg = r.t = 0;
     r.g_begin = r.g_end = r.total;

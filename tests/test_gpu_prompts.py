@@ -686,6 +686,21 @@ def test_attn8_small_and_large_grids(ctas):
         g.set_tuning(0, 0)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (128, 48, 1), (256, 16, 1)])
+@pytest.mark.parametrize("ctas", [0, 3, 40])
+def test_attn8_tile_counts_about_the_grid(D, Hq, Hkv, ctas):
+    # one segment per head and many: fewer tiles than CTAs, as many, a few more,
+    # and more pieces than a merge takes in a batch
+    g.set_tuning(0, ctas)
+    try:
+        for n in (1, 2, 31, 33, 39, 40, 41, 79, 81, 161):
+            run_attn8([128 * n - 5], Hq, Hkv, D, 64, seed=n)
+        for n in (13, 14, 20, 40, 41, 152 // Hkv, 153 // Hkv + 1):
+            run_attn8([0, 129] + [100] * n + [300], Hq, Hkv, D, 32, seed=n)
+    finally:
+        g.set_tuning(0, 0)
+
+
 def test_attn8_graphs_of_one_stream_replay_side_by_side():
     # two graphs captured on one stream (the first calls there), with segments that
     # several CTAs share, replayed on two streams: each has a workspace of its own
