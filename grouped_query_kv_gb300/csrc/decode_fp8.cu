@@ -212,9 +212,9 @@ __device__ __forceinline__ float2 e4m3x2_value(uint16_t two) {
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // What bounds it: bandwidth at long caches, a chain of latencies at short
-// ones.  PG, 64 heads over 8 of 128: 11.4 us for five requests of up to 301
-// (the second kernel among them), then 5.7 TB/s, 0.84 of the copy rate, from
-// one batch size to the next; so 32 ragged requests of up to 8192 take 57 us.
+// ones.  PG, 64 heads over 8 of 128: one request of 1024 takes 8.8 us (the
+// second kernel among them), and from 64 requests of 4096 to 128 a byte comes
+// at 5.7 TB/s, 0.84 of the copy rate; 32 ragged ones of up to 8192 take 57 us.
 //
 // PG: a paged pool with one scale per (block, K/V head), bf16 output.  Tiles
 // come through the block table as in the bf16 kernel (decode_tc.cuh): one TMA
