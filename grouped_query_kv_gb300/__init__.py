@@ -153,6 +153,8 @@ def _check(status: int):
 # the current stream's handle without building a torch.cuda.Stream (several
 # microseconds of a decode step's host time)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device without torch.cuda's own call around it
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream_ptr(stream):
@@ -548,10 +550,14 @@ def _home(t, name):
     dev = t.get_device()
     if dev < 0:
         raise ValueError("%s must be a CUDA tensor (got %s)" % (name, t.device))
-    if dev != torch.cuda.current_device():
-        raise ValueError("%s is on %s, not on the current CUDA device %d"
-                         % (name, t.device, torch.cuda.current_device()))
+    if dev != _device():
+        raise ValueError("%s is on %s, not on the current CUDA device %d" % (name, t.device, _device()))
     return dev
+
+
+def _on(stream, dev):
+    """The handle of the stream to launch on, of device `dev` if None."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream_ptr(stream)
 
 
 def _want(t, name, dtype, dev, shape=None):
@@ -593,11 +599,13 @@ def _packed_rows(t, name, dev, shape=None):
         raise ValueError("%s must be a CUDA tensor on the current device %d (got %s)" % (name, dev, t.device))
     if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be %s (got %s)" % (name, torch.bfloat16, t.dtype))
-    if t.dim() != 3:
-        raise ValueError("%s must be [N, heads, D]" % name)
-    if shape is not None and t.shape != shape:
+    if shape is None:
+        if t.dim() != 3:
+            raise ValueError("%s must be [N, heads, D]" % name)
+        shape = t.shape
+    elif t.shape != shape:
         raise ValueError("%s must have shape %s (got %s)" % (name, shape, tuple(t.shape)))
-    N, H, D = t.shape
+    N, H, D = shape
     row, head, one = t.stride()
     if (one != 1 and D > 1) or (head != D and H > 1):
         raise ValueError("%s: each row's [heads, D] must be contiguous (strides %s)" % (name, t.stride()))
@@ -647,11 +655,11 @@ def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count,
         free_count_out = free_count
     else:
         _want(free_count_out, "free_count_out", i32, dev, (1,))
-    _check(lib().kv_block_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(block_table),
-                                 _ptr(free_blocks), _ptr(free_count), _ptr(free_count_out),
-                                 _ptr(cu_seqlens), _ptr(slots), B, block_table.shape[1],
+    _check(lib().kv_block_tables(cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                                 free_blocks.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),
+                                 cu_seqlens.data_ptr(), slots.data_ptr(), B, block_table.shape[1],
                                  _int32(block_size, "block_size"), free_blocks.shape[0], num_slots,
-                                 _stream_ptr(stream)))
+                                 _on(stream, dev)))
     return cu_seqlens, slots, free_count_out
 
 
@@ -676,8 +684,8 @@ def kv_append_slots(k_pool, v_pool, k_new, v_new, slots, stream=None):
     N = slots.shape[0]
     ks = _packed_rows(k_new, "k_new", dev, (N, Hkv, D))
     vs = _packed_rows(v_new, "v_new", dev, (N, Hkv, D))
-    _check(lib().kv_append_slots(_ptr(k_pool), _ptr(v_pool), _ptr(k_new), _ptr(v_new), _ptr(slots),
-                                 N, Hkv, D, ks, vs, nblk, bs, _stream_ptr(stream)))
+    _check(lib().kv_append_slots(k_pool.data_ptr(), v_pool.data_ptr(), k_new.data_ptr(),
+                                 v_new.data_ptr(), slots.data_ptr(), N, Hkv, D, ks, vs, nblk, bs, _on(stream, dev)))
 
 
 def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=None):
@@ -705,10 +713,10 @@ def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=N
         out = _new(torch.zeros, (N, Hq, D), torch.bfloat16, q, stream)
     else:
         _want(out, "out", torch.bfloat16, dev, (N, Hq, D))
-    _check(lib().gqa_prefill_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out),
+    _check(lib().gqa_prefill_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
                                   cu_seqlens.shape[0] - 1, N, Hq, Hkv, D, qs, ks, vs, float(scale),
                                   0x7fffffff if window is None else min(int(window), 0x7fffffff),
-                                  _stream_ptr(stream)))
+                                  _on(stream, dev)))
     return out
 
 
@@ -748,10 +756,10 @@ def kv_append_paged_fp8(k_codes, v_codes, k_scale, v_scale, k_new, v_new, block_
     vs = _packed_rows(v_new, "v_new", dev, (N, Hkv, D))
     _want(cached_lens, "cached_lens", torch.int32, dev, (B,))
     _want(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
-    _check(lib().kv_append_paged_fp8(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
-                                     _ptr(k_new), _ptr(v_new), _ptr(block_table), _ptr(cached_lens),
-                                     _ptr(cu_seqlens), B, N, Hkv, D, ks, vs, nblk, bs, maxb,
-                                     _stream_ptr(stream)))
+    _check(lib().kv_append_paged_fp8(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                     k_new.data_ptr(), v_new.data_ptr(), block_table.data_ptr(), cached_lens.data_ptr(),
+                                     cu_seqlens.data_ptr(), B, N, Hkv, D, ks, vs, nblk, bs, maxb,
+                                     _on(stream, dev)))
 
 
 def gqa_decode_attn_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale,
@@ -773,10 +781,10 @@ def gqa_decode_attn_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table
         out = _new(torch.empty, (B, Hq, D), torch.bfloat16, q, stream)
     else:
         _want(out, "out", torch.bfloat16, dev, (B, Hq, D))
-    _check(lib().gqa_decode_attn_paged_fp8(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
-                                           _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
-                                           _ptr(out), B, Hq, Hkv, D, nblk, bs, maxb, float(scale),
-                                           _stream_ptr(stream)))
+    _check(lib().gqa_decode_attn_paged_fp8(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                                           v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                                           out.data_ptr(), B, Hq, Hkv, D, nblk, bs, maxb, float(scale),
+                                           _on(stream, dev)))
     return out
 
 
