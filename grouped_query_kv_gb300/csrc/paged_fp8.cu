@@ -12,15 +12,17 @@
 //
 // A block of 128 threads writes (pool block, K/V head) pairs of K and of V one
 // after the other: it owns their scales, so nothing is shared between blocks
-// and no atomic decides an order.  Blocks of the grid are candidates: x < B is
-// request x's first touched pool block (the one that may hold earlier rows),
-// x >= B the pool blocks that start inside the bs packed rows from (x - B) bs;
-// y takes every gridDim.y-th head, K and V (few where there are many
-// candidates: a candidate's search for its request then serves all heads).
+// and no atomic decides an order.  `split` consecutive blocks of the grid share
+// a candidate: x < B is request x's first touched pool block (the one that may
+// hold earlier rows), x >= B the pool blocks that start inside the bs packed
+// rows from (x - B) bs; each takes a run of its heads, K and V (long runs where
+// there are many candidates: a search for the request then serves them all, and
+// blocks that run together read neighbouring heads of the same rows; with the
+// candidates consecutive instead 72.4 us for 71.1 in the case below).
 // What bounds it is the copy: 2 bytes read and 1 written per value.  Up to
 // kHeld 16-byte vectors a thread the new rows stay in registers between the
 // search for the largest and the rounding; longer blocks read them again.
-// 32 prompts, 67 k rows of 8 x 128 into blocks of 64: 73.4 us, 0.85 of the
+// 32 prompts, 67 k rows of 8 x 128 into blocks of 64: 70.6 us, 0.88 of the
 // measured copy rate; 64 single rows 4.9 us.
 #include <cuda_fp16.h>
 
@@ -44,6 +46,7 @@ struct Append8Params {
     const int32_t *table, *cached, *cu;
     unsigned int *err;
     int B, N, Hkv, lg, max_blocks, num_blocks;
+    int split;                   // blocks of the grid per candidate
 };
 
 // Exponent of the smallest power of two s (>= 2^-100) with a <= 448 s,
@@ -163,7 +166,7 @@ __device__ __forceinline__ void write_block(const Append8Params &p, int kv, int 
     if (held) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (row + i * RPP < m) *reinterpret_cast<uint2 *>(dst + i * RPP * D) = codes8(raw[i], inv);
+            if (row + i * RPP < m) __stcs(reinterpret_cast<uint2 *>(dst + i * RPP * D), codes8(raw[i], inv));
     } else {
         for (int r = 0; row + r < m; r += kHeld * RPP) {
 #pragma unroll
@@ -197,20 +200,22 @@ __global__ void __launch_bounds__(kThreads) append_paged8_kernel(const Append8Pa
     pdl_launch_dependents();
     pdl_wait_prior();
     const int bs = 1 << p.lg;
+    const int x = (int)(blockIdx.x / (unsigned)p.split), part = (int)(blockIdx.x - (unsigned)x * p.split);
+    const int hk0 = part * 2 * p.Hkv / p.split, hk1 = (part + 1) * 2 * p.Hkv / p.split;
     int first, n, c, turn = 0;
     bool bad;
-    if ((int)blockIdx.x < p.B) {
-        const int b = blockIdx.x;
+    if (x < p.B) {
+        const int b = x;
         const bool some = request(p, b, &first, &n, &c, &bad);
-        if (bad && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
+        if (bad && part == 0 && threadIdx.x == 0) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
         if (some)
-            for (int hk = blockIdx.y; hk < 2 * p.Hkv; hk += gridDim.y)
+            for (int hk = hk0; hk < hk1; ++hk)
                 write_block<D>(p, hk & 1, hk >> 1, b, c, first, min(n, bs - (c & (bs - 1))), red, turn);
         return;
     }
     // pool blocks that start at packed rows [t0, t1), the requests' first
     // touched ones aside: of bs consecutive rows of a request one starts a block
-    const int t0 = (int)(blockIdx.x - p.B) << p.lg, t1 = min(t0 + bs, p.N);
+    const int t0 = (x - p.B) << p.lg, t1 = min(t0 + bs, p.N);
     // the last request that starts at or before t0, 32 probes at a time
     int lo = 0, span = p.B;  // it is in [lo, lo + span)
     while (span > 1) {
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) append_paged8_kernel(const Append8Pa
     for (int i = 0; i < blocks; ++i) {
         const int b = s_b[i], t = s_t[i];
         request(p, b, &first, &n, &c, &bad);
-        for (int hk = blockIdx.y; hk < 2 * p.Hkv; hk += gridDim.y)
+        for (int hk = hk0; hk < hk1; ++hk)
             write_block<D>(p, hk & 1, hk >> 1, b, c + t - first, t, min(bs, first + n - t), red, turn);
     }
 }
@@ -301,11 +306,12 @@ extern "C" int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     cudaLaunchConfig_t cfg = {};
-    // candidates, and enough splits of the heads to give every SM 32 blocks (65 thousand
-    // rows of 8 heads of 128: 8 blocks 80 us, 16 76, 32 73.6, 64 73)
+    // candidates, and enough splits of the heads to give every SM 64 blocks (65 thousand
+    // rows of 8 heads of 128: 8 blocks 76.6 us, 16 73.1, 32 70.9, 64 70.6)
     const long long cand = (long long)B + ((long long)N + block_size - 1) / block_size;
-    const long long split = (32LL * ctas + cand - 1) / cand;
-    cfg.gridDim = dim3((unsigned)cand, (unsigned)(split < 2 * Hkv ? split : 2 * Hkv));
+    const long long split = (64LL * ctas + cand - 1) / cand;
+    p.split = (int)(split < 2 * Hkv ? split : 2 * Hkv);
+    cfg.gridDim = dim3((unsigned)(cand * p.split));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
