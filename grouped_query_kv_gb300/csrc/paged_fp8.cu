@@ -18,12 +18,12 @@
 // rows from (x - B) bs; each takes a run of its heads, K and V (long runs where
 // there are many candidates: a search for the request then serves them all, and
 // blocks that run together read neighbouring heads of the same rows; with the
-// candidates consecutive instead 72.4 us for 71.1 in the case below).
+// candidates consecutive instead some 2 % slower).
 // What bounds it is the copy: 2 bytes read and 1 written per value.  Up to
 // kHeld 16-byte vectors a thread the new rows stay in registers between the
 // search for the largest and the rounding; longer blocks read them again.
-// 32 prompts, 67 k rows of 8 x 128 into blocks of 64: 70.6 us, 0.88 of the
-// measured copy rate; 64 single rows 4.9 us.
+// 32 prompts, 67 k rows of 8 x 128 into blocks of 64: 65.0 us, 0.96 of the
+// measured copy rate; 64 single rows 4.3 us.
 #include <cuda_fp16.h>
 
 #include "../../include/kvattn.h"
@@ -192,8 +192,11 @@ __device__ __forceinline__ bool request(const Append8Params &p, int b, int *firs
     return !*bad && e > a;
 }
 
+// (p stays where the launch put it: indexed by K and V, a plain parameter is
+// copied to each thread's stack, 71 us for 66 below; ten blocks an SM, 48
+// registers: 65.0 us, eight 66.0, eleven 69.3)
 template <int D>
-__global__ void __launch_bounds__(kThreads) append_paged8_kernel(const Append8Params p) {
+__global__ void __launch_bounds__(kThreads, 10) append_paged8_kernel(const __grid_constant__ Append8Params p) {
     __shared__ float red[2][4];
     __shared__ int found;
     __shared__ int s_b[kMaxBlock], s_t[kMaxBlock];
@@ -307,7 +310,7 @@ extern "C" int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
     p.num_blocks = num_blocks;
     cudaLaunchConfig_t cfg = {};
     // candidates, and enough splits of the heads to give every SM 64 blocks (65 thousand
-    // rows of 8 heads of 128: 8 blocks 76.6 us, 16 73.1, 32 70.9, 64 70.6)
+    // rows of 8 heads of 128: 24 blocks 67.2 us, 64 65.1, 128 64.8)
     const long long cand = (long long)B + ((long long)N + block_size - 1) / block_size;
     const long long split = (64LL * ctas + cand - 1) / cand;
     p.split = (int)(split < 2 * Hkv ? split : 2 * Hkv);
