@@ -35,7 +35,7 @@
 // query tile's products and the next's; below a few hundred tokens the chain
 // of one unit (copy, Q K^T, softmax, P V, rows out: 8 us for four prompts of
 // up to 97 tokens).  Measured on the device, a call among others: 8192 tokens
-// of 64 heads over 8 of 128 718 us (1530 TFLOP/s, 0.80 of the cuBLAS bf16
+// of 64 heads over 8 of 128 720 us (1527 TFLOP/s, 0.80 of the cuBLAS bf16
 // rate), of 16 heads over 1 of 256 340 us (1620, 0.85); eight ragged prompts
 // of that layout 318 us (1405, 0.74); D = 64 some 905 TFLOP/s (P V with
 // N = 64 costs as much as with 128).
@@ -281,6 +281,14 @@ __device__ __forceinline__ Unit read_unit(const Unit &from) {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(Unit) / 4); ++i) dst[i] = __shfl_sync(0xffffffffu, src[i], 0);
     return u;
+}
+
+// First of the unit's key tiles that query tile s attends: its window may start
+// behind whole tiles that the first query tile needs (one of ten in a window of
+// 1024 with 128 tokens a tile: three prompts of 16 heads of 64, 78.3 us with them
+// computed, 74.1 without; full prompts lose 0.4 % to the test).
+__device__ __forceinline__ int first_tile(const PrefillParams &p, const Unit &u, int s) {
+    return max(0, u.t0 + s * p.tpt + 1 - p.window - u.kbeg) / kRows;
 }
 
 // Length of sequence b (0 where its bounds are not 0 <= cu[b] <= cu[b+1] <= N).
@@ -709,7 +717,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             int owed = 0;            // the step before: 1 its P V is due, 2 its V tile was not needed
             int owed_keys = 0;
             bool owed_first = false;
-            auto turn_of = [&](int n, int nmax, int j, int end) {  // j = nmax: the last P V alone
+            // (key tiles from j0 to n are the query tile's; j = nmax: the last P V alone)
+            auto turn_of = [&](int j0, int n, int nmax, int j, int end) {
                 // (one uniform wait after the other: what comes early is waited for
                 // while the other tile's MMAs are still running)
                 bool go = true;
@@ -717,7 +726,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 if (owed) go = slot_ready();
                 const auto rk = rc;
                 if (go && j < nmax) go = slot_ready();
-                if (go && j == 0 && n > 0) go = warp_wait(&q_full[s], units_q++ & 1, abort_flag);
+                if (go && j == j0 && j < n) go = warp_wait(&q_full[s], units_q++ & 1, abort_flag);
                 if (go && (s == 1 || !first_turn)) go = warp_wait(&turn[s], s == 0 ? it ^ 1 : it, abort_flag);
                 if (go && owed == 1) go = warp_wait(&p_full[s], g ^ 1, abort_flag, wlim);
                 if (!go) return false;
@@ -727,13 +736,13 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 else if (owed == 2 && lane == 0)
                     mbar_arrive(&slot_empty[rv.slot]);
                 owed = 0;
-                if (j < n) {
+                if (j0 <= j && j < n) {
                     const int keys = min(kRows, end - j * kRows);
                     qk(s, rk, keys, j == n - 1);
                     g ^= 1;
                     owed = 1;
                     owed_keys = keys;
-                    owed_first = j == 0;
+                    owed_first = j == j0;
                 } else if (j < nmax) {
                     if (lane == 0) mbar_arrive(&slot_empty[rk.slot]);
                     owed = 2;
@@ -747,13 +756,13 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 ok = next_unit(k, &u);
                 if (!ok) break;
                 if (u.n[0] == 0) {
-                    if (owed) ok = turn_of(0, 0, 0, 0);
+                    if (owed) ok = turn_of(0, 0, 0, 0, 0);
                     break;
                 }
-                const int n = u.n[s], nmax = max(u.n[0], u.n[1]);
+                const int n = u.n[s], nmax = max(u.n[0], u.n[1]), j0 = first_tile(p, u, s);
                 // keys of the unit's key tiles that the query tile attends at most
                 const int end = min(u.t0 + (s + 1) * p.tpt, u.len) - u.kbeg;
-                for (int j = 0; j < nmax && ok; ++j) ok = turn_of(n, nmax, j, end);
+                for (int j = 0; j < nmax && ok; ++j) ok = turn_of(j0, n, nmax, j, end);
             }
         } else {
             // One warp issues Q K^T, the other P V, so that each one's waits pass
@@ -842,7 +851,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         const int tq = min(tok, u.len - 1);
         float m = -INFINITY, l = 0.f;
 
-        for (int j = 0; j < n; ++j, ++g) {
+        const int j0 = first_tile(p, u, s);
+        for (int j = j0; j < n; ++j, ++g) {
             const int buf = NQ == 2 ? s : (int)(g & 1);
             const uint32_t par = (uint32_t)((NQ == 2 ? g : g >> 1) & 1);
             ok = warp_wait(&s_full[buf], par, abort_flag, wlim);
@@ -907,7 +917,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 const float alpha = (grow && m != -INFINITY) ? fast_exp2((m - mn) * p.sl) : 1.f;
                 if (grow) m = mn;
                 l *= alpha;
-                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     // O holds the tiles up to j - 1
                     const int pb = NQ == 2 ? s : buf ^ 1;
                     const uint32_t pp = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
