@@ -578,6 +578,8 @@ def _new(make, shape, dtype, like, stream):
     launches on, so that what fills it, or used its memory before, comes first."""
     if stream is None:
         return make(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):  # (anything with the handle will do)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
     with torch.cuda.stream(stream):
         return make(shape, dtype=dtype, device=like.device)
 

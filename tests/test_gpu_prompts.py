@@ -965,6 +965,18 @@ def test_calls_on_another_stream_than_the_current_one():
         assert (np.abs(step.double().cpu().numpy() - ref) <= bound).all()
 
 
+def test_a_stream_is_anything_with_its_handle():
+    class Handle:
+        cuda_stream = torch.cuda.Stream().cuda_stream
+
+    qkv = _normal((40, 3, 64), 1)
+    torch.cuda.synchronize()
+    out = g.gqa_prefill_attn(qkv[:, :1], qkv[:, 1:2], qkv[:, 2:], _i32([0, 40]), 0.1, stream=Handle())
+    torch.cuda.synchronize()
+    g.check_device_error()
+    check_prefill(out, *prefill_ref(qkv[:, :1], qkv[:, 1:2], qkv[:, 2:], [0, 40], 0.1))
+
+
 def test_the_path_captured_and_replayed():
     """One decode step of every call in a graph, replayed: lengths and the free
     list advance on the device."""
