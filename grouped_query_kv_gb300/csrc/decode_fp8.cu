@@ -40,16 +40,21 @@
 //     (the running max is refreshed once a score passes it by 2), w 2^cv
 //     stays <= 256, inside E4M3's range.  It is rounded to binary16 (11
 //     significant bits, as the f16 P of a widening design) and goes in as
-//     three E4M3 parts hi + mid + lo (each the rounded remainder of the
-//     previous, taken in binary16, where the remainders are exact), which
-//     carry its 11 bits whole (4 + 4 + 3; a remainder below E4M3's
-//     smallest step, 2^-9, is lost as before).  The
+//     three E4M3 parts, hi + 2^-5 mid + 2^-10 lo: each the rounded remainder
+//     of the previous, taken in binary16, where the remainders are exact, and
+//     in a unit of its own, since a remainder is at most 2^-5 of what it
+//     remains of (w <= 256 leaves mid and lo at 256 at most).  They carry its
+//     11 bits whole (4 + 4 + 3) down to w = 2^-9, and below that all but
+//     2^-20 of it: half of E4M3's smallest step, 2^-9, in lo's unit.  So a
+//     position counts until p v_scale is under 2^-25 of the largest v_scale.
+//     (With one unit for all three, positions under 2^-15 were lost: of 8192
+//     of them behind one 11 nats above, 22 to 58 % of the output.)  The
 //     parts sit side by side as the 3 NP columns of the B operand (P stored
 //     position-major, no swizzle), so 4 MMAs per tile accumulate three
-//     partial O^T blocks; the epilogue adds them and divides by 2^cv.  A
-//     tile whose v_scale would break the bound lowers cv first, rescaling
-//     the accumulator by the same power of two (with the running-max
-//     rescale, in the same step).
+//     partial O^T blocks; the epilogue adds them in their units and divides
+//     by 2^cv.  A tile whose v_scale would break the bound lowers cv first,
+//     rescaling the accumulators by the same power of two (with the
+//     running-max rescale, in the same step).
 // D = 128 or 256.  A 128-position tile of codes is D / 128 TMA boxes of 128
 // positions x 128 codes (the 128-byte swizzle's width), side by side in its
 // staging slot; the q parts have one 128-code slab per box; Q K^T runs
@@ -201,6 +206,18 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// a * 32 in f16x2 arithmetic (exact here: a is at most 8).
+__device__ __forceinline__ uint32_t f16x2_times32(uint32_t a) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x50005000u));
+    return r;
+}
+
+// The three partial outputs, each in its weights' unit.
+__device__ __forceinline__ float join_parts(float hi, float mid, float lo) {
+    return fmaf(lo, 0x1p-10f, fmaf(mid, 0x1p-5f, hi));
 }
 
 __device__ __forceinline__ float2 e4m3x2_value(uint16_t two) {
@@ -936,7 +953,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
 
             // probabilities p (summed into l); the weights p v_scale 2^cv in
             // binary16 as three E4M3 parts, each the rounded remainder of the
-            // previous
+            // previous in units of 2^-5 of its
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (u >= nu) continue;
@@ -960,9 +977,9 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                         // a binary16 value, so the subtractions are exact)
                         const uint32_t w = f16x2_of(p0 * vs2, p1 * vs2);
                         const uint16_t c1 = e4m3x2_of_f16x2(w);
-                        const uint32_t r1 = f16x2_sub(w, e4m3x2_to_f16x2(c1));
+                        const uint32_t r1 = f16x2_times32(f16x2_sub(w, e4m3x2_to_f16x2(c1)));
                         const uint16_t c2 = e4m3x2_of_f16x2(r1);
-                        const uint16_t c3 = e4m3x2_of_f16x2(f16x2_sub(r1, e4m3x2_to_f16x2(c2)));
+                        const uint16_t c3 = e4m3x2_of_f16x2(f16x2_times32(f16x2_sub(r1, e4m3x2_to_f16x2(c2))));
                         if (h == 0) {
                             ph[g4 / 4] = c1;
                             pm[g4 / 4] = c2;
@@ -1042,7 +1059,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (cg0 + c + k < gvalid) dst[(c + k) * D] = (v[k] + w[k] + x[k]) * vinv;
+                        if (cg0 + c + k < gvalid) dst[(c + k) * D] = join_parts(v[k], w[k], x[k]) * vinv;
                 }
             }
         } else
@@ -1051,14 +1068,14 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
             const uint32_t oa = lane_base + C::OA + sl * 3 * NP + cg0;
             float o[NPH];
 #pragma unroll
-            for (int c = 0; c + 16 <= NPH; c += 16) {  // O^T = (hi + mid + lo parts) 2^-cv
+            for (int c = 0; c + 16 <= NPH; c += 16) {  // O^T = (hi + 2^-5 mid + 2^-10 lo) 2^-cv
                 float v[16], w[16], x[16];
                 tmem_ld16(oa + c, v);
                 tmem_ld16(oa + NP + c, w);
                 tmem_ld16(oa + 2 * NP + c, x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[c + k] = (v[k] + w[k] + x[k]) * vinv;
+                for (int k = 0; k < 16; ++k) o[c + k] = join_parts(v[k], w[k], x[k]) * vinv;
             }
             if constexpr (NPH % 16 == 8) {
                 float v[8], w[8], x[8];
@@ -1067,7 +1084,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                 tmem_ld8(oa + 2 * NP + NPH - 8, x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[NPH - 8 + k] = (v[k] + w[k] + x[k]) * vinv;
+                for (int k = 0; k < 8; ++k) o[NPH - 8 + k] = join_parts(v[k], w[k], x[k]) * vinv;
             }
             const int d = sl * 128 + row;
             if (complete) {

@@ -375,7 +375,10 @@ KVATTN_API int kv_append_fp8(void *k_codes, void *v_codes, float *k_scale, float
  * per position and K/V head is 2 (D + 4) bytes instead of 4 D.  q bf16
  * [B, Hq, D] (any finite value: each head enters the 8-bit products as two
  * E4M3 parts under a power-of-two scale, exact for a bf16 value), out fp32
- * [B, Hq, D]; lengths, errors and ownership as gqa_decode_attn.
+ * [B, Hq, D]; lengths, errors and ownership as gqa_decode_attn.  A position's
+ * weight, exp(score - the largest score) times its value scale over the
+ * largest value scale, enters with 11 significant bits down to 2^-14 and to
+ * within 2^-25 below.
  * Needs D = 128 or 256: the kernel copies each position's codes in rows of
  * 128 (one 128-byte swizzled TMA box per 128 head dims); D = 64 is
  * KVATTN_ERR_UNSUPPORTED (not built: its 64-byte rows would need a layout
@@ -558,12 +561,13 @@ KVATTN_API int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
  *
  *   q   : bf16 [B, Hq, D]; seq_lens: int32 [B] (device), positions attended,
  *         0 <= seq_lens[b] <= max_blocks * block_size
- *   out : bf16 [B, Hq, D] (the 8-bit products carry the weights' 11
- *         significant bits, bf16 has 8)
+ *   out : bf16 [B, Hq, D]
  * Scales may be any finite values >= 0 (scale * q . K must stay finite in
- * fp32, and a value scale's weight counts down to 2^-15 of the largest one
- * its head's positions meet).  Pool rows at and past a length are
- * never read; table entries, lengths and device-side errors are those of
+ * fp32).  A position's weight, exp(score - the largest score) times its value
+ * scale over the largest value scale of its head's positions, enters the 8-bit
+ * products with 11 significant bits down to 2^-14 and to within 2^-25 below:
+ * n positions smaller than that are off by n 2^-25 together.  Pool rows at and
+ * past a length are never read; table entries, lengths and device-side errors are those of
  * gqa_decode_attn_paged.  Its workspace is the stream's, as for the other
  * attention calls, but a call that is being captured gets one of that
  * capture's own (allocated then, kept until kvattn_release): graphs captured
