@@ -94,11 +94,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeParams p,
     if (by_segment) {
         int c0, n, fs;
         segment_pieces(p, (int)blockIdx.x, num_ctas, &c0, &n, &fs);
+        // the partials come from the split-KV kernel just before.  Rows without any
+        // wait for it, too: what is launched next waits for this grid alone, and
+        // takes its end for the split-KV kernel's
+        pdl_wait_prior();
         if (n <= 1) return;  // not split: the split-KV kernel wrote this segment's rows
         const int segs_per_b = p.Hkv * p.head_groups;
         rec = make_int4((int)blockIdx.x / segs_per_b, (int)blockIdx.x % segs_per_b, fs, n);
         c = c0 + 1;
-        pdl_wait_prior();  // the partials come from the split-KV kernel just before
     } else {
         pdl_wait_prior();  // partials and records come from the split-KV kernel just before
         if (recs[c].x < 0) return;  // CTA c is not the first cut inside a segment

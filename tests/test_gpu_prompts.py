@@ -1014,3 +1014,60 @@ def test_the_path_captured_and_replayed():
             for b in range(B):
                 blk = int(th[b, step // bs])
                 assert torch.equal(vp[blk, :, step % bs], rows[step][b])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (128, 48, 1), (256, 16, 1)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_attention_before_an_append_that_rewrites_its_blocks(D, Hq, Hkv, captured):
+    # requests of one tile, so that no segment is split and the merge has nothing
+    # to do; the append behind it overwrites every row that the attention reads,
+    # and each attention call writes the output of the one before it
+    bs, lens, turns = 16, [100, 128, 33, 64], 40
+    table, nblk = make_table(lens, bs, D)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    slots = torch.as_tensor(np.concatenate([table[b, np.arange(n) // bs].astype(np.int64) * bs + np.arange(n) % bs
+                                            for b, n in enumerate(lens)]), device="cuda")
+    q = _normal((len(lens), Hq, D), 1)
+    rows = [(_normal((cu[-1], Hkv, D), 10 + i), _normal((cu[-1], Hkv, D), 20 + i)) for i in range(3)]
+    d_table, d_lens, d_cu, zero = _i32(table), _i32(lens), _i32(cu), _i32([0] * len(lens))
+
+    def run(settle):
+        codes = [torch.zeros((nblk, Hkv, bs, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros((nblk, Hkv), device="cuda") for _ in range(2)]
+        pools = [torch.zeros((nblk, Hkv, bs, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        outs8 = [torch.zeros((len(lens), Hq, D), dtype=torch.bfloat16, device="cuda") for _ in range(turns)]
+        outs16 = [torch.zeros((len(lens), Hq, D), device="cuda") for _ in range(turns)]
+
+        def steps():
+            for i in range(turns):
+                k, v = rows[i % 3]
+                g.kv_append_paged_fp8(*codes, *scales, k, v, d_table, zero, d_cu)
+                settle()
+                g.gqa_decode_attn_paged_fp8(q, *codes, *scales, d_table, d_lens, 0.1, out=outs8[i])
+                settle()
+            for i in range(turns):
+                g.kv_append_slots(*pools, *rows[i % 3], slots)
+                settle()
+                g.gqa_decode_attn_paged(q, *pools, d_table, d_lens, 0.1, out=outs16[i])
+                settle()
+
+        if captured and settle is not torch.cuda.synchronize:
+            g.gqa_decode_attn_paged(q, *pools, d_table, d_lens, 0.1)  # (its workspace is there before the capture)
+            gr, stream = torch.cuda.CUDAGraph(), torch.cuda.current_stream()
+            side = torch.cuda.Stream()
+            side.wait_stream(stream)
+            with torch.cuda.stream(side):
+                g.gqa_decode_attn_paged(q, *pools, d_table, d_lens, 0.1)
+            torch.cuda.synchronize()
+            with torch.cuda.graph(gr, stream=side):
+                steps()
+            gr.replay()
+        else:
+            torch.cuda.synchronize()
+            steps()
+        torch.cuda.synchronize()
+        g.check_device_error()
+        return outs8 + outs16
+
+    for a, b in zip(run(torch.cuda.synchronize), run(lambda: None)):
+        assert torch.equal(a, b)
