@@ -1,5 +1,6 @@
 // api.cu -- the C ABI declared in include/kvattn.h: argument checks, the
 // split plan, TMA descriptors, per-(device, stream) workspaces and launches.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -7,6 +8,7 @@
 #include <map>
 #include <vector>
 #include <mutex>
+#include <new>
 #include <utility>
 
 #include <cuda.h>
@@ -54,14 +56,34 @@ std::map<int, DeviceState> g_dev;
 struct Workspace {
     void *ptr = nullptr;
     size_t bytes = 0;
-    // buffers outgrown by this one: kept until kvattn_release, because work
-    // captured earlier (a CUDA graph) may still use them
-    std::vector<void *> retired;
+    // buffers outgrown by this one and their bytes: kept until kvattn_release
+    // (a capture's: as long as its graph), because work captured earlier (a
+    // CUDA graph) may still use them
+    std::vector<std::pair<void *, size_t>> retired;
 };
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
-// workspaces of captures, each its own (gqa_decode_attn_paged_fp8): by device,
-// stream and capture
-std::map<std::pair<std::pair<int, cudaStream_t>, unsigned long long>, Workspace> g_ws_captured;
+// Workspaces of captures, each its own (gqa_decode_attn_paged_fp8): by device,
+// stream and capture.  One belongs to its graph, which holds it as a user
+// object: CUDA calls capture_gone once the graph and everything instantiated
+// from it are destroyed and their launches have finished.  That call may come
+// from any thread and must not use CUDA, so it only puts the workspace on a
+// list; the next captured call takes the buffers over (g_idle).
+using CaptureKey = std::pair<std::pair<int, cudaStream_t>, unsigned long long>;
+struct CaptureWorkspace {
+    CaptureKey key;
+    Workspace ws;
+    CaptureWorkspace *next = nullptr;
+};
+std::map<CaptureKey, CaptureWorkspace *> g_ws_captured;
+std::atomic<CaptureWorkspace *> g_ws_gone{nullptr};
+std::multimap<std::pair<int, size_t>, void *> g_idle;  // by device and bytes
+
+void CUDART_CB capture_gone(void *arg) {
+    CaptureWorkspace *w = static_cast<CaptureWorkspace *>(arg);
+    w->next = g_ws_gone.load(std::memory_order_relaxed);
+    while (!g_ws_gone.compare_exchange_weak(w->next, w, std::memory_order_release, std::memory_order_relaxed)) {
+    }
+}
 
 // cuTensorMapEncodeTiled, fetched through the runtime so the library needs no
 // link-time dependency on the driver library.
@@ -292,18 +314,25 @@ int check_sizes(int B, int Hq, int Hkv, int D, int Lmax) {
     return KVATTN_OK;
 }
 
-int grow_workspace(Workspace &w, size_t bytes, void **ptr) {
+int alloc_workspace(size_t bytes, void **ptr) {
+    cudaError_t e = cudaMalloc(ptr, bytes);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(KVATTN_ERR_OOM, "workspace allocation of %zu bytes failed", bytes);
+    }
+    return KVATTN_OK;
+}
+
+int get_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
+    Workspace &w = g_ws[std::make_pair(dev, stream)];
     if (w.bytes < bytes) {
         // grow at least twofold; the old buffer is retired, not freed
         size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
         if (want < 2 * w.bytes) want = 2 * w.bytes;
         void *fresh = nullptr;
-        cudaError_t e = cudaMalloc(&fresh, want);
-        if (e != cudaSuccess) {
-            (void)cudaGetLastError();
-            return fail(KVATTN_ERR_OOM, "workspace allocation of %zu bytes failed", want);
-        }
-        if (w.ptr) w.retired.push_back(w.ptr);
+        int rc = alloc_workspace(want, &fresh);
+        if (rc) return rc;
+        if (w.ptr) w.retired.push_back({w.ptr, w.bytes});
         w.ptr = fresh;
         w.bytes = want;
     }
@@ -311,27 +340,84 @@ int grow_workspace(Workspace &w, size_t bytes, void **ptr) {
     return KVATTN_OK;
 }
 
-int get_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
-    return grow_workspace(g_ws[std::make_pair(dev, stream)], bytes, ptr);
+// The buffers of captures whose graphs are gone, for the next ones.
+void collect_gone() {
+    CaptureWorkspace *w = g_ws_gone.exchange(nullptr, std::memory_order_acquire);
+    while (w) {
+        const int dev = w->key.first.first;
+        if (w->ws.ptr) g_idle.insert({{dev, w->ws.bytes}, w->ws.ptr});
+        for (auto &old : w->ws.retired) g_idle.insert({{dev, old.second}, old.first});
+        auto at = g_ws_captured.find(w->key);
+        if (at != g_ws_captured.end() && at->second == w) g_ws_captured.erase(at);
+        CaptureWorkspace *next = w->next;
+        delete w;
+        w = next;
+    }
 }
 
-// The same, but a call that is being captured gets a workspace of its
-// capture's own, so that graphs captured on one stream may replay side by
-// side, and a first call may be a captured one: the thread's capture mode is
-// relaxed around the allocation, which is no part of the graph.
+// get_workspace, but a call that is being captured gets a workspace of its
+// capture's own, which lives as long as the graph, so that graphs captured on
+// one stream may replay side by side, and a first call may be a captured one:
+// the thread's capture mode is relaxed around the allocation, which is no part
+// of the graph.
 int get_call_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
-    cudaError_t e = cudaStreamGetCaptureInfo(stream, &st, &id);
+    cudaGraph_t graph = nullptr;
+    cudaError_t e = cudaStreamGetCaptureInfo(stream, &st, &id, &graph);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetCaptureInfo");
     if (st != cudaStreamCaptureStatusActive) return get_workspace(dev, stream, bytes, ptr);
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    e = cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
-    const int rc = grow_workspace(g_ws_captured[std::make_pair(std::make_pair(dev, stream), id)], bytes, ptr);
-    e = cudaThreadExchangeStreamCaptureMode(&mode);
-    if (rc == KVATTN_OK && e != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
-    return rc;
+    collect_gone();
+    const CaptureKey key(std::make_pair(dev, stream), id);
+    auto at = g_ws_captured.find(key);
+    if (at == g_ws_captured.end()) {
+        CaptureWorkspace *rec = new CaptureWorkspace;
+        rec->key = key;
+        cudaUserObject_t obj = nullptr;
+        e = cudaUserObjectCreate(&obj, rec, capture_gone, 1, cudaUserObjectNoDestructorSync);
+        if (e != cudaSuccess) {
+            delete rec;
+            return cuda_fail(e, "cudaUserObjectCreate");
+        }
+        // (from here on rec goes by way of the list)
+        e = cudaGraphRetainUserObject(graph, obj, 1, cudaGraphUserObjectMove);
+        if (e != cudaSuccess) {
+            cudaUserObjectRelease(obj, 1);
+            return cuda_fail(e, "cudaGraphRetainUserObject");
+        }
+        at = g_ws_captured.emplace(key, rec).first;
+    }
+    Workspace &w = at->second->ws;
+    if (w.bytes < bytes) {
+        // powers of two, at least 1 MB: an idle buffer of the size or the next
+        // one up, so that captures of many sizes leave few idle
+        size_t want = 1u << 20;
+        while (want < bytes) want *= 2;
+        if (w.ptr) w.retired.reserve(w.retired.size() + 1);
+        void *fresh = nullptr;
+        auto idle = g_idle.lower_bound({dev, want});
+        if (idle != g_idle.end() && idle->first.first == dev && idle->first.second <= 2 * want) {
+            fresh = idle->second;
+            want = idle->first.second;
+            g_idle.erase(idle);
+        } else {
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            e = cudaThreadExchangeStreamCaptureMode(&mode);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
+            const int rc = alloc_workspace(want, &fresh);
+            e = cudaThreadExchangeStreamCaptureMode(&mode);
+            if (rc) return rc;
+            if (e != cudaSuccess) {
+                g_idle.insert({{dev, want}, fresh});
+                return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
+            }
+        }
+        if (w.ptr) w.retired.push_back({w.ptr, w.bytes});
+        w.ptr = fresh;
+        w.bytes = want;
+    }
+    *ptr = w.ptr;
+    return KVATTN_OK;
 }
 
 }  // namespace
@@ -736,8 +822,12 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
         rc = make_plan(B, Hq, Hkv, D, Lmax, ds->num_sms, &pl);
         g_force_path = saved;
         if (rc) return rc;
-        rc = pg ? get_call_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws)
-                : get_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws);
+        try {
+            rc = pg ? get_call_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws)
+                    : get_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws);
+        } catch (const std::bad_alloc &) {
+            rc = fail(KVATTN_ERR_OOM, "%s: host memory for the workspace's record", who);
+        }
         if (rc) return rc;
     }
     const kvattn_plan &P = pl.pub;
@@ -992,18 +1082,23 @@ void kvattn_release(void) {
     std::lock_guard<std::mutex> lk(g_mu);
     int cur = 0;
     cudaGetDevice(&cur);
-    for (auto &kv : g_ws) {
-        cudaSetDevice(kv.first.first);
-        if (kv.second.ptr) cudaFree(kv.second.ptr);
-        for (void *old : kv.second.retired) cudaFree(old);
-    }
+    auto give_back = [](int dev, Workspace &w) {
+        cudaSetDevice(dev);
+        if (w.ptr) cudaFree(w.ptr);
+        for (auto &old : w.retired) cudaFree(old.first);
+        w = Workspace();
+    };
+    for (auto &kv : g_ws) give_back(kv.first.first, kv.second);
     g_ws.clear();
-    for (auto &kv : g_ws_captured) {
-        cudaSetDevice(kv.first.first.first);
-        if (kv.second.ptr) cudaFree(kv.second.ptr);
-        for (void *old : kv.second.retired) cudaFree(old);
-    }
+    // (a capture's record is deleted once its graph is gone)
+    collect_gone();
+    for (auto &kv : g_ws_captured) give_back(kv.first.first.first, kv.second->ws);
     g_ws_captured.clear();
+    for (auto &kv : g_idle) {
+        cudaSetDevice(kv.first.first);
+        cudaFree(kv.second);
+    }
+    g_idle.clear();
     cudaSetDevice(cur);
 }
 

@@ -570,9 +570,12 @@ KVATTN_API int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale,
  * past a length are never read; table entries, lengths and device-side errors are those of
  * gqa_decode_attn_paged.  Its workspace is the stream's, as for the other
  * attention calls, but a call that is being captured gets one of that
- * capture's own (allocated then, kept until kvattn_release): graphs captured
- * on one stream may replay side by side, and the first call on a stream may
- * be a captured one.  D = 128 or 256.
+ * capture's own: graphs captured on one stream may replay side by side (two
+ * instances of one graph may not), and the first call on a stream may be a
+ * captured one.  The graph keeps it; once the graph and all that was
+ * instantiated from it are destroyed, later captures take it over.
+ * kvattn_release frees it, so a graph of this call is not replayed after that.
+ * D = 128 or 256.
  */
 KVATTN_API int gqa_decode_attn_paged_fp8(const void *q, const void *k_codes, const void *v_codes,
                                          const float *k_scale, const float *v_scale,

@@ -1071,3 +1071,69 @@ def test_attention_before_an_append_that_rewrites_its_blocks(D, Hq, Hkv, capture
 
     for a, b in zip(run(torch.cuda.synchronize), run(lambda: None)):
         assert torch.equal(a, b)
+
+
+def _split_call(lens, seed, Hq=16, Hkv=1, D=128, bs=16):
+    """Arguments of a paged 8-bit call whose segments several CTAs share."""
+    table, nblk = make_table(lens, bs, seed)
+    kc, ks = new_pool8(nblk, Hkv, bs, D, seed)
+    vc, vs = new_pool8(nblk, Hkv, bs, D, seed + 10)
+    ks.fill_(2.0 ** -8)
+    vs.fill_(2.0 ** -8)
+    return _normal((len(lens), Hq, D), seed), kc, vc, ks, vs, _i32(table), _i32(lens), 0.1
+
+
+def test_attn8_workspaces_of_captures_go_with_their_graphs():
+    # graphs captured anew for ever, a few alive at a time: device memory does not
+    # grow, and the ones alive keep their workspaces to themselves
+    g.release()
+    calls = [_split_call(lens, seed) for seed, lens in ((1, [5000, 3000]), (2, [700] * 60), (3, [6000]))]
+    wants = [g.gqa_decode_attn_paged_fp8(*c).clone() for c in calls]
+    outs = [torch.zeros_like(w) for w in wants]
+    stream, alive = torch.cuda.Stream(), []
+
+    def turn(i):
+        which = [i % 3, (i + i // 3) % 3]  # (a second call may need a larger one)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=stream):
+            for j in which:
+                g.gqa_decode_attn_paged_fp8(*calls[j], out=outs[j])
+        alive.append((gr, which))
+        if len(alive) > 4:
+            alive.pop(0)
+        for gr, which in alive:
+            for o in outs:
+                o.fill_(7.0)
+            gr.replay()
+            torch.cuda.synchronize()
+            for j in which:
+                assert torch.equal(outs[j].view(torch.int16), wants[j].view(torch.int16))
+
+    for i in range(24):
+        turn(i)
+    free = torch.cuda.mem_get_info()[0]
+    for i in range(24, 120):
+        turn(i)
+    lost = free - torch.cuda.mem_get_info()[0]
+    g.check_device_error()
+    assert lost < 16 << 20, lost  # (96 captures with a workspace of 1 MB or more each)
+
+
+def test_attn8_release_between_captures():
+    call = _split_call([4000, 100], 4)
+    want = g.gqa_decode_attn_paged_fp8(*call).clone()
+    out = torch.zeros_like(want)
+    stream, old = torch.cuda.Stream(), []
+    for i in range(6):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=stream):
+            g.gqa_decode_attn_paged_fp8(*call, out=out)
+        out.zero_()
+        gr.replay()
+        torch.cuda.synchronize()
+        g.check_device_error()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        g.release()       # its workspace is gone: not replayed again,
+        old.append(gr)    # only destroyed, at once or after the next capture
+        if i % 2:
+            old.clear()
