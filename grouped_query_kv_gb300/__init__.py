@@ -14,7 +14,18 @@ import ctypes
 import os
 import threading
 
-import torch
+
+class _Torch:
+    """torch, imported at the first use (which puts the module in this one's
+    place): the library itself, its paths and its structures do without."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 
 __all__ = [
     "kv_append", "kv_append_multi", "kv_append_paged", "gqa_decode_attn", "gqa_decode_step",
@@ -150,18 +161,25 @@ def _check(status: int):
         raise KvAttnError(status, lib().kvattn_last_error().decode())
 
 
-# the current stream's handle without building a torch.cuda.Stream (several
-# microseconds of a decode step's host time)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-# the current device without torch.cuda's own call around it
-_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+def _raw_stream(dev):
+    # the current stream's handle without building a torch.cuda.Stream (several
+    # microseconds of a decode step's host time), where torch has it
+    global _raw_stream
+    _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    return _raw_stream(dev)
+
+
+def _device():
+    # the current device without torch.cuda's own call around it
+    global _device
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device()
 
 
 def _stream_ptr(stream):
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
-        stream = torch.cuda.current_stream()
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream  # a plain int: ctypes converts it for the c_void_p argument
 
 
@@ -557,7 +575,7 @@ def _home(t, name):
 
 def _on(stream, dev):
     """The handle of the stream to launch on, of device `dev` if None."""
-    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream_ptr(stream)
+    return _raw_stream(dev) if stream is None else _stream_ptr(stream)
 
 
 def _want(t, name, dtype, dev, shape=None):
