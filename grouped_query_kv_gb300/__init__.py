@@ -273,7 +273,7 @@ def gqa_decode_attn(q, k_cache, v_cache, seq_lens, scale, out=None, stream=None,
     else:
         _check(lib().gqa_decode_attn_window(_ptr(q), _ptr(k_cache), _ptr(v_cache),
                                             _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, Lmax,
-                                            float(scale), int(window), _stream_ptr(stream)))
+                                            float(scale), _window(window), _stream_ptr(stream)))
     return out
 
 
@@ -309,7 +309,7 @@ def gqa_decode_step(q, k_new, v_new, k_cache, v_cache, seq_lens, scale, out=None
     else:
         _check(lib().gqa_decode_step_window(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                             _ptr(v_cache), _ptr(seq_lens), _ptr(out), B, Hq,
-                                            Hkv, D, Lmax, float(scale), int(window),
+                                            Hkv, D, Lmax, float(scale), _window(window),
                                             _stream_ptr(stream)))
     return out
 
@@ -345,7 +345,7 @@ def gqa_decode_attn_multi(q, k_cache, v_cache, seq_lens, scale, out=None, stream
     else:
         _check(lib().gqa_decode_attn_multi_window(_ptr(q), _ptr(k_cache), _ptr(v_cache),
                                                   _ptr(seq_lens), _ptr(out), B, T, Hq, Hkv, D,
-                                                  Lmax, float(scale), int(window),
+                                                  Lmax, float(scale), _window(window),
                                                   _stream_ptr(stream)))
     return out
 
@@ -422,7 +422,7 @@ def gqa_decode_attn_paged(q, k_pool, v_pool, block_table, seq_lens, scale, out=N
         _check(lib().gqa_decode_attn_paged_window(_ptr(q), _ptr(k_pool), _ptr(v_pool),
                                                   _ptr(block_table), _ptr(seq_lens), _ptr(out),
                                                   B, T, Hq, Hkv, D, nblk, bs, maxb,
-                                                  float(scale), int(window),
+                                                  float(scale), _window(window),
                                                   _stream_ptr(stream)))
     return out
 
@@ -459,7 +459,7 @@ def gqa_decode_step_paged(q, k_new, v_new, k_pool, v_pool, block_table, seq_lens
         _check(lib().gqa_decode_step_paged_window(_ptr(q), _ptr(k_new), _ptr(v_new),
                                                   _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
                                                   _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D,
-                                                  nblk, bs, maxb, float(scale), int(window),
+                                                  nblk, bs, maxb, float(scale), _window(window),
                                                   _stream_ptr(stream)))
     return out
 
@@ -602,6 +602,12 @@ def _new(make, shape, dtype, like, stream):
         return make(shape, dtype=dtype, device=like.device)
 
 
+def _window(w):
+    """w as a C int: what is beyond it attends everything, or is refused, as the
+    nearest int that holds does (a window past every position, one below 1)."""
+    return max(-0x80000000, min(int(w), 0x7fffffff))
+
+
 def _int32(x, name):
     """x as an int that a C int holds."""
     x = int(x)
@@ -735,7 +741,7 @@ def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=N
         _want(out, "out", torch.bfloat16, dev, (N, Hq, D))
     _check(lib().gqa_prefill_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
                                   cu_seqlens.shape[0] - 1, N, Hq, Hkv, D, qs, ks, vs, float(scale),
-                                  0x7fffffff if window is None else min(int(window), 0x7fffffff),
+                                  0x7fffffff if window is None else _window(window),
                                   _on(stream, dev)))
     return out
 

@@ -1137,3 +1137,30 @@ def test_attn8_release_between_captures():
         old.append(gr)    # only destroyed, at once or after the next capture
         if i % 2:
             old.clear()
+
+
+def test_windows_beyond_32_bits():
+    # past every position: the full attention; below 1: refused; never the low bits
+    n, D = 300, 128
+    q, k, v = _normal((n, 8, D), 1), _normal((n, 2, D), 2), _normal((n, 2, D), 3)
+    kc, vc = (t.transpose(0, 1).contiguous()[None] for t in (k, v))
+    table = _i32([[0, 1, 2]])
+    kp, vp = (torch.zeros((3, 2, 128, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g.kv_append_slots(kp, vp, k, v, torch.arange(n, device="cuda"))
+    lens, before = _i32([n]), _i32([n - 1])
+    calls = [lambda w: g.gqa_prefill_attn(q, k, v, _i32([0, n]), 0.1, window=w),
+             lambda w: g.gqa_decode_attn(q[:1], kc, vc, lens, 0.1, window=w),
+             lambda w: g.gqa_decode_step(q[:1], k[-1:], v[-1:], kc, vc, before, 0.1, window=w),
+             lambda w: g.gqa_decode_attn_multi(q[None, :2], kc, vc, lens, 0.1, window=w),
+             lambda w: g.gqa_decode_attn_paged(q[:1], kp, vp, table, lens, 0.1, window=w),
+             lambda w: g.gqa_decode_step_paged(q[:1], k[-1:], v[-1:], kp, vp, table, before, 0.1, window=w)]
+    for call in calls:
+        full = call(n + 1)
+        assert not torch.equal(call(5), full)
+        for w in (2 ** 31, 2 ** 32 + 5, 2 ** 40):
+            assert torch.equal(call(w), full)
+        for w in (0, -5, -2 ** 31, -2 ** 32 + 5, -2 ** 40):
+            with pytest.raises(g.KvAttnError) as ei:
+                call(w)
+            assert ei.value.status == g.KVATTN_ERR_INVALID_ARG
+    g.check_device_error()
