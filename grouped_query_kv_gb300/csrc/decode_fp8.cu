@@ -19,15 +19,15 @@
 //
 //   * Q K^T.  The piece's q rows go in as two E4M3 parts under a per-head
 //     power-of-two scale 2^c (c puts the head's largest |q| in [128, 256)):
-//     hi = e4m3(q 2^c), lo = e4m3(q 2^c - hi).  A bf16 value has 8
+//     hi = e4m3(q 2^c), lo = e4m3((q 2^c - hi) 2^5).  A bf16 value has 8
 //     significant bits and E4M3 4, and the remainder after rounding to 4
 //     bits is a multiple of the bf16 ulp no larger than 8 of them, so
-//     hi + lo is q 2^c exactly for entries within 2^9 of the head's
-//     largest (smaller ones are off by at most 2^-17 of it: the remainder
+//     hi + 2^-5 lo is q 2^c exactly for entries within 2^14 of the head's
+//     largest (smaller ones are off by at most 2^-22 of it: the remainder
 //     falls below E4M3's smallest step).  The two parts sit side by side
 //     as the 2 NP columns of one B operand (at most 128, and 480 of the 512
 //     tensor-memory columns with the O accumulators at NP = 48, D = 256),
-//     so Q K^T takes 4 D / 128 MMAs per tile, and the softmax adds the two
+//     so Q K^T takes 4 D / 128 MMAs per tile, and the softmax joins the two
 //     partial scores 16 columns at a time.  (Running the lo part as 4 more
 //     MMAs into the same accumulator, as passes of more than 32 heads once
 //     did, took the PaLM-540B-shaped step from 58.0 to 59.4 us.)
@@ -592,8 +592,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                             const float a2 = x[16 * j + 4 * u + 2] * sc, a3 = x[16 * j + 4 * u + 3] * sc;
                             const uint16_t h01 = e4m3x2_of(a0, a1), h23 = e4m3x2_of(a2, a3);
                             const float2 v01 = e4m3x2_value(h01), v23 = e4m3x2_value(h23);
-                            const uint16_t l01 = e4m3x2_of(a0 - v01.x, a1 - v01.y);
-                            const uint16_t l23 = e4m3x2_of(a2 - v23.x, a3 - v23.y);
+                            const uint16_t l01 = e4m3x2_of((a0 - v01.x) * 32.f, (a1 - v01.y) * 32.f);
+                            const uint16_t l23 = e4m3x2_of((a2 - v23.x) * 32.f, (a3 - v23.y) * 32.f);
                             hw[u] = (uint32_t)h01 | ((uint32_t)h23 << 16);
                             lw[u] = (uint32_t)l01 | ((uint32_t)l23 << 16);
                         }
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                     vsc[u] = __ldcg(p.v_scale + zrow + pos[u]);
                 }
                 tc_fence_after();
-                // the group's scores: hi-part plus lo-part columns
+                // the group's scores: hi-part plus 2^-5 lo-part columns
                 tmem_ld_n<NPH>(lane_base + sb * C::SW + cg0, s[u]);
                 tmem_ld_wait();
 #pragma unroll
@@ -850,14 +850,14 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                     tmem_ld16(lane_base + sb * C::SW + NP + cg0 + c, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) s[u][c + k] += v[k];
+                    for (int k = 0; k < 16; ++k) s[u][c + k] = fmaf(v[k], 0x1p-5f, s[u][c + k]);
                 }
                 if constexpr (NPH % 16 == 8) {
                     float v[8];
                     tmem_ld8(lane_base + sb * C::SW + NP + cg0 + NPH - 8, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) s[u][NPH - 8 + k] += v[k];
+                    for (int k = 0; k < 8; ++k) s[u][NPH - 8 + k] = fmaf(v[k], 0x1p-5f, s[u][NPH - 8 + k]);
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -374,7 +374,8 @@ KVATTN_API int kv_append_fp8(void *k_codes, void *v_codes, float *k_scale, float
  * E4M3(k_codes[b,kvh,j,:]) * k_scale[b,kvh,j], V likewise.  The cache read
  * per position and K/V head is 2 (D + 4) bytes instead of 4 D.  q bf16
  * [B, Hq, D] (any finite value: each head enters the 8-bit products as two
- * E4M3 parts under a power-of-two scale, exact for a bf16 value), out fp32
+ * E4M3 parts under a power-of-two scale, exact for entries down to 2^-14 of
+ * the head's largest and within 2^-22 of it below), out fp32
  * [B, Hq, D]; lengths, errors and ownership as gqa_decode_attn.  A position's
  * weight, exp(score - the largest score) times its value scale over the
  * largest value scale, enters with 11 significant bits down to 2^-14 and to

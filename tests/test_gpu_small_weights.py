@@ -143,3 +143,52 @@ def test_contiguous_8_bit(D, Hq, Hkv, lens, gaps, sigma, ctas):
         s = [x[b, :, :n].double().T for x in (ks, vs)]
         kvs.append((c[0] * s[0][:, :, None], c[1] * s[1][:, :, None], c[1].abs(), s[1]))
     check(out, q, kvs, scale, 2.0 ** -20)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", HEADS)
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_query_entry_far_above_the_others(D, Hq, Hkv, paged):
+    """One entry of q stands 2^11 to 2^12 above the others, where K is zero: the
+    scores come from the others, which the parts hold exactly (2^14 below the
+    largest they still do).  So what moves a score is the sum in fp32 alone."""
+    lens, bs, scale = [1, 5, 40, 200, 1000], 64, 0.5
+    gen = torch.Generator(device="cuda").manual_seed(D + Hq)
+
+    def uniform(*shape):
+        return torch.rand(shape, generator=gen, device="cuda")
+
+    q = (0.5 + 0.5 * uniform(len(lens), Hq, D)) * (2 * (uniform(len(lens), Hq, D) < 0.5) - 1)
+    q[:, :, 3] = 2048.0
+    q = q.to(torch.bfloat16)
+    cache = [torch.randn((len(lens), Hkv, 1024, D), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    cache[0][:, :, :, 3] = 0
+    if paged:
+        table = _i32(np.arange(len(lens) * 16).reshape(len(lens), 16))
+        codes = [torch.zeros((len(lens) * 16, Hkv, bs, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros((len(lens) * 16, Hkv), device="cuda") for _ in range(2)]
+        rows = [c.transpose(1, 2).reshape(-1, Hkv, D).contiguous() for c in cache]
+        g.kv_append_paged_fp8(*codes, *scales, *rows, table, _i32([0] * len(lens)),
+                              _i32(np.arange(len(lens) + 1) * 1024))
+        out = g.gqa_decode_attn_paged_fp8(q, *codes, *scales, table, _i32(lens), scale)
+        codes = [c.view(len(lens), 16, Hkv, bs, D).transpose(2, 3).reshape(-1, 1024, Hkv, D) for c in codes]
+        scales = [x.view(len(lens), 16, Hkv).repeat_interleave(bs, 1) for x in scales]
+    else:
+        (kc, ks), (vc, vs) = (g.kv_quantize_fp8(c) for c in cache)
+        out = g.gqa_decode_attn_fp8(q, kc, vc, ks, vs, _i32(lens), scale)
+        codes = [c.transpose(1, 2) for c in (kc, vc)]
+        scales = [x.transpose(1, 2) for x in (ks, vs)]
+    g.check_device_error()
+    for b, n in enumerate(lens):
+        k, v = (c[b, :n].contiguous().view(torch.float8_e4m3fn).double() * x[b, :n, :, None].double()
+                for c, x in zip(codes, scales))
+        for h in range(Hkv):
+            heads = slice(h * (Hq // Hkv), (h + 1) * (Hq // Hkv))
+            qs = q[b, heads].double()
+            w = torch.softmax(qs @ k[:, h].T * scale, 1)
+            ref, mag = w @ v[:, h], w @ v[:, h].abs()
+            ds = scale * D * 2.0 ** -24 * (qs.abs() @ k[:, h].abs().T).amax(1, keepdim=True)
+            lost = 2.0 ** -25 * v[:, h].abs().max() * n
+            err = (2.0 ** -11 + 2 * ds + 2.0 ** -18) * mag + lost
+            o = out[b, heads].double()
+            over = (o - ref).abs() - err - (2.0 ** -8 if paged else 2.0 ** -20) * (ref.abs() + err)
+            assert float(over.max()) <= 0, (b, h, float(over.max()))
