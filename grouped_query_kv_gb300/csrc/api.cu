@@ -810,9 +810,11 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
     DeviceState *ds;
     Plan pl;
     void *ws = nullptr;
+    unsigned int wait_limit = 0;
     cudaEvent_t ev_before = nullptr, ev_after = nullptr;
     {
         std::lock_guard<std::mutex> lk(g_mu);
+        wait_limit = g_wait_limit;
         ev_before = g_ev_before;
         ev_after = g_ev_after;
         if ((rc = device_state(dev, &ds))) return rc;
@@ -874,6 +876,7 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
     p.max_blocks = pg ? pg->max_blocks : 0;
     p.num_blocks = pg ? pg->num_blocks : 0;
     p.out_bf16 = p.even_small = pg ? 1 : 0;
+    p.wait_limit = wait_limit;
     cudaError_t e;
     if (ev_before && (e = cudaEventRecord(ev_before, stream)) != cudaSuccess)
         return cuda_fail(e, "recording the event before the split-KV kernel");

@@ -711,7 +711,10 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                 continue;
             }
             ++idle;
-            if (((idle & 255u) == 0 && __any_sync(0xffffffffu, *abort_flag)) || idle >= kMmaIdleLimit) {
+            // (the failure tests shorten this wait alone: the other roles' waits
+            // see the flag, and their limits take no registers)
+            if (((idle & 255u) == 0 && __any_sync(0xffffffffu, *abort_flag)) ||
+                idle >= (p.wait_limit ? p.wait_limit : kMmaIdleLimit)) {
                 ok = false;
                 break;
             }

@@ -653,8 +653,8 @@ KVATTN_API int kvattn_set_tuning(int force_path, int num_ctas);
  * issued keep their default limit.  With a very small value (1) a call is
  * sure to give up, which is how the tests exercise this path.  It shortens
  * gqa_prefill_attn's waits for scores, probabilities and P.V products the
- * same way; the 8-bit kernels' waits keep their limit.  Always returns
- * KVATTN_OK.
+ * same way, and in the 8-bit kernels the MMA warp's polling (the other waits
+ * there end with it).  Always returns KVATTN_OK.
  */
 KVATTN_API int kvattn_set_wait_limit(unsigned int polls);
 
