@@ -692,7 +692,7 @@ def kv_block_tables(cached_lens, new_lens, block_table, free_blocks, free_count,
 def kv_append_slots(k_pool, v_pool, k_new, v_new, slots, stream=None):
     """Write packed K/V rows into a paged pool: row i goes to row
     slots[i] % block_size of block slots[i] // block_size; a negative slot
-    skips its row.
+    skips its row.  At least one row.
 
     k_pool, v_pool: bf16 [num_blocks, Hkv, block_size, D] (in place); k_new,
     v_new: bf16 [N, Hkv, D], rows contiguous or slices of wider rows; slots:
@@ -716,8 +716,10 @@ def kv_append_slots(k_pool, v_pool, k_new, v_new, slots, stream=None):
 
 def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=None):
     """Causal attention of whole prompts packed one after the other: token i
-    of sequence b (rows [cu_seqlens[b], cu_seqlens[b + 1])) attends the tokens
-    j <= i of its sequence (j > i - window on a local attention layer).
+    of sequence b (rows [cu_seqlens[b], cu_seqlens[b + 1])) attends the rows
+    j <= i of its sequence (j > i - window on a local attention layer).  Only
+    these rows: it is for prompts with nothing cached, not for tokens that
+    continue a cached prefix.
 
     q: bf16 [N, Hq, D]; k, v: bf16 [N, Hkv, D], rows contiguous or slices of
     wider rows; cu_seqlens: int32 [B + 1]; out: optional bf16 [N, Hq, D] (if
@@ -767,6 +769,7 @@ def kv_append_paged_fp8(k_codes, v_codes, k_scale, v_scale, k_new, v_new, block_
     scale per block and K/V head: token i of request b (packed row
     cu_seqlens[b] + i) goes to position cached_lens[b] + i of its table row.  A
     block's scale grows with its rows; earlier codes are rewritten for it.
+    gqa_decode_attn_paged_fp8 reads such pools where D is 128 or 256.
 
     k_codes, v_codes: uint8 [num_blocks, Hkv, block_size, D]; k_scale,
     v_scale: fp32 [num_blocks, Hkv] (all in place); k_new, v_new: bf16

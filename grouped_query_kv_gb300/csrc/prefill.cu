@@ -34,11 +34,14 @@
 // What bounds it: the tensor pipe, which idles some 300 cycles between one
 // query tile's products and the next's; below a few hundred tokens the chain
 // of one unit (copy, Q K^T, softmax, P V, rows out: 8 us for four prompts of
-// up to 97 tokens).  Measured on the device, a call among others: 8192 tokens
-// of 64 heads over 8 of 128 720 us (1527 TFLOP/s, 0.80 of the cuBLAS bf16
-// rate), of 16 heads over 1 of 256 340 us (1620, 0.85); eight ragged prompts
-// of that layout 318 us (1405, 0.74); D = 64 some 905 TFLOP/s (P V with
-// N = 64 costs as much as with 128).
+// up to 97 tokens).  Measured in a graph of calls: 8192 tokens of 64 heads
+// over 8 of 128 720 us (1527 TFLOP/s, 0.80 of the cuBLAS bf16 rate; called one
+// after the other, with other inputs each, 760 us, 1447), of 16 heads over 1 of
+// 256 340 us (1620, 0.85); eight ragged prompts of that layout 320 us (1396,
+// 0.73; 331 called).  D = 64 some 905 TFLOP/s: a key tile's MMAs take 678
+// cycles (64 an MMA at N = 128, 53 at N = 64) where D = 128 takes 1027 for
+// twice the operations, but its softmax takes as long, and the tensor pipe is
+// busy a third of the time.
 //
 // Work list.  A unit is (sequence, block of NQ x 128 / hpg tokens, K/V head,
 // head group); its cost grows with its block's index.  Every CTA of the

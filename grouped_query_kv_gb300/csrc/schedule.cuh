@@ -218,8 +218,9 @@ __device__ inline void sched_totals(LenView lens, int B, int Lmax, int tile, int
 // the grid: a piece is charged more than the work it would share): equal runs of
 // tiles instead, whatever a piece costs, as short as the grid allows -- the other
 // CTAs' SMs would be idle, and a second piece of a CTA is the longer wait -- but
-// no more than kPiecesEach pieces of a segment, which are merged in a chain of
-// batches.  A whole number of tiles each: 192 tiles on 152 CTAs are 96 pairs
+// no more CTAs than kPiecesEach to a segment of the call, since a segment's
+// pieces are merged in a chain of batches (beside many short segments a long one
+// may still be cut in more).  A whole number of tiles each: 192 tiles on 152 CTAs are 96 pairs
 // (one segment of 4096 in each of six requests at D = 256 13.5 us by cost, 16.9
 // cut 152 ways, 12.8 in pairs).  Paged 8-bit calls, by cost and by this rule:
 // five requests of up to 301 (40 segments, 64 tiles) 11.1 and 9.0 us; one of 2048

@@ -453,10 +453,12 @@ KVATTN_API int gqa_decode_step_fp8(const void *q, const void *k_new, const void 
  * blocks, its rows end within num_slots, and the blocks wanted by it and all
  * requests before it are no more than free_count[0].  One that is not takes
  * no block, its rows get slot -1, the table entries it lacks become -1 (those
- * of its first num_slots rows), and KVATTN_ERR_DEVICE_BOUNDS is set; a
+ * of packed rows below num_slots; with lengths that are negative or do not fit
+ * its table row stays as it is), and KVATTN_ERR_DEVICE_BOUNDS is set; a
  * negative n counts as 0 rows.  free_count[0] outside [0, num_free] sets it
  * too and counts as 0.  cu_seqlens is capped at 2^31 - 1.
- * Limits: B <= 65535, max_blocks * block_size <= 2^24, num_slots <= 2^28.
+ * Limits: 1 <= B <= 65535, max_blocks * block_size <= 2^24,
+ * 1 <= num_slots <= 2^28.
  */
 KVATTN_API int kv_block_tables(const int32_t *cached_lens, const int32_t *new_lens,
                                int32_t *block_table, const int32_t *free_blocks,
@@ -476,7 +478,7 @@ KVATTN_API int kv_block_tables(const int32_t *cached_lens, const int32_t *new_le
  * Bit-exact; rows no slot names stay as they are.  A slot at or past
  * num_blocks * block_size skips its row and sets KVATTN_ERR_DEVICE_BOUNDS.
  * Slots must differ: of two rows with one slot either may land, in pieces of
- * 16 bytes.  D in {64, 128, 256}; N <= 2^28.
+ * 16 bytes.  D in {64, 128, 256}; 1 <= N <= 2^28.
  */
 KVATTN_API int kv_append_slots(void *k_pool, void *v_pool, const void *k_new, const void *v_new,
                                const int64_t *slots, int N, int Hkv, int D, long long k_stride,
@@ -484,7 +486,11 @@ KVATTN_API int kv_append_slots(void *k_pool, void *v_pool, const void *k_new, co
                                kvattn_stream_t stream);
 
 /*
- * gqa_prefill_attn -- causal attention of whole prompts, packed.
+ * gqa_prefill_attn -- causal attention of whole prompts, packed.  Nothing of
+ * a cache is read: it is the attention of prompts that have no token cached.
+ * Rows that continue a cached prefix (cached_lens > 0 in kv_block_tables)
+ * would attend each other alone here; gqa_decode_attn_paged takes up to 64 new
+ * tokens a request, the same number for each, over a bf16 pool.
  *
  * For every sequence b, token i of its n_b = cu_seqlens[b+1] - cu_seqlens[b]
  * and query head h (kvh = h / (Hq / Hkv)):
@@ -506,7 +512,7 @@ KVATTN_API int kv_append_slots(void *k_pool, void *v_pool, const void *k_new, co
  * 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <= N is skipped and sets
  * KVATTN_ERR_DEVICE_BOUNDS; of sequences that overlap either may have
  * written the shared rows.  The single-token form is gqa_decode_attn
- * (gqa_decode_attn_paged).  D in {64, 128, 256}; N <= 2^28.
+ * (gqa_decode_attn_paged).  D in {64, 128, 256}; 1 <= N <= 2^28.
  */
 KVATTN_API int gqa_prefill_attn(const void *q, const void *k, const void *v,
                                 const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv,
@@ -547,8 +553,11 @@ KVATTN_API int gqa_prefill_attn(const void *q, const void *k, const void *v,
  * belong to one request each.  A request with negative lengths, rows outside
  * [0, N) or positions outside its table row is skipped, a table entry outside
  * [0, num_blocks) skips its block; both set KVATTN_ERR_DEVICE_BOUNDS.
+ * cu_seqlens must not decrease: a request that ends before it starts is
+ * skipped and reported, but then blocks of the others may stay unwritten, too.
  * Deterministic, codes and scales exact by the rule above.
- * D in {64, 128, 256}; N <= 2^28.
+ * D in {64, 128, 256} (gqa_decode_attn_paged_fp8 reads pools of 128 and 256);
+ * 1 <= N <= 2^28.
  */
 KVATTN_API int kv_append_paged_fp8(void *k_codes, void *v_codes, float *k_scale, float *v_scale,
                                    const void *k_new, const void *v_new,
