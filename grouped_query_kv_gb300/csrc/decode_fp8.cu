@@ -80,25 +80,6 @@ constexpr float kTauQ8 = 2.f;    // rescale once a score passes the running max 
 constexpr float kVHi = 64.f;     // v_scale[j] 2^cv stays <= 64
 constexpr int kCvNone = 1 << 20; // cv not chosen yet (piece start)
 
-// wait_bar by a whole warp, which leaves it together.
-__device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    for (uint32_t it = 0; it < KVATTN_SPIN_LIMIT; ++it) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
-    }
-    *abort_flag = 1;
-    return false;
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)::"memory");
-    return r != 0;
-}
-
 template <int D, int NP, bool PG>
 struct Q8Cfg {
     static constexpr int SL = D / 128;        // 128-code slabs per row
@@ -171,21 +152,6 @@ struct Q8Cfg {
     static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(128, 3 * NP, true, true);
 };
 
-// Two E4M3 codes (low byte first) -> f16x2 (low half first); exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
-    return r;
-}
-
-// Two binary32 values -> two E4M3 codes (nearest, ties to even,
-// saturating), a in the low byte.
-__device__ __forceinline__ uint16_t e4m3x2_of(float a, float b) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    return r;
-}
-
 // Two binary32 values -> f16x2 (a in the low half), nearest even.
 __device__ __forceinline__ uint32_t f16x2_of(float a, float b) {
     uint32_t r;
@@ -218,11 +184,6 @@ __device__ __forceinline__ uint32_t f16x2_times32(uint32_t a) {
 // The three partial outputs, each in its weights' unit.
 __device__ __forceinline__ float join_parts(float hi, float mid, float lo) {
     return fmaf(lo, 0x1p-10f, fmaf(mid, 0x1p-5f, hi));
-}
-
-__device__ __forceinline__ float2 e4m3x2_value(uint16_t two) {
-    const uint32_t h = e4m3x2_to_f16x2(two);
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
 // 2^e as a binary32 value, e in [-126, 127].
@@ -394,7 +355,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
         uint32_t par = 1;  // of the slot's release before its fill
         bool ok = true;
         for (; n < nt; ++n) {
-            if (n >= ns && !wait_bar_warp(&empty[slot], par, abort_flag)) {
+            if (n >= ns && !mbar_wait_warp(&empty[slot], par, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -452,7 +413,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
         auto issue = [&](const void *tm, const TileIter &it, uint8_t *base, uint64_t *full,
                          uint64_t *empty, int ns, long long &n) -> bool {
             const int slot = (int)(n % ns);
-            if (n >= ns && !wait_bar_warp(&empty[slot], (uint32_t)(((n / ns) - 1) & 1), abort_flag))
+            if (n >= ns && !mbar_wait_warp(&empty[slot], (uint32_t)(((n / ns) - 1) & 1), abort_flag))
                 return false;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&full[slot], kStage);
@@ -590,10 +551,10 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                         for (int u = 0; u < 4; ++u) {
                             const float a0 = x[16 * j + 4 * u] * sc, a1 = x[16 * j + 4 * u + 1] * sc;
                             const float a2 = x[16 * j + 4 * u + 2] * sc, a3 = x[16 * j + 4 * u + 3] * sc;
-                            const uint16_t h01 = e4m3x2_of(a0, a1), h23 = e4m3x2_of(a2, a3);
+                            const uint16_t h01 = e4m3x2_from_f32(a0, a1), h23 = e4m3x2_from_f32(a2, a3);
                             const float2 v01 = e4m3x2_value(h01), v23 = e4m3x2_value(h23);
-                            const uint16_t l01 = e4m3x2_of((a0 - v01.x) * 32.f, (a1 - v01.y) * 32.f);
-                            const uint16_t l23 = e4m3x2_of((a2 - v23.x) * 32.f, (a3 - v23.y) * 32.f);
+                            const uint16_t l01 = e4m3x2_from_f32((a0 - v01.x) * 32.f, (a1 - v01.y) * 32.f);
+                            const uint16_t l23 = e4m3x2_from_f32((a2 - v23.x) * 32.f, (a3 - v23.y) * 32.f);
                             hw[u] = (uint32_t)h01 | ((uint32_t)h23 << 16);
                             lw[u] = (uint32_t)l01 | ((uint32_t)l23 << 16);
                         }
@@ -727,7 +688,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
         if (elect_one()) umma_commit(drain);
         __syncwarp();
         volatile int never = 0;
-        wait_bar_warp(drain, 0, &never);
+        mbar_wait_warp(drain, 0, &never);
         __syncwarp();
         named_bar_sync(kBarEnd, C::END_THREADS);
         tc_fence_after();
@@ -780,7 +741,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
         for (int g = 0; g < NPH; ++g) l[g] = 0.f;
         if (row < NPH) mref_s[cg0 + row] = -INFINITY;
         // the piece's 2^-c (written by the q warps)
-        carry_fail = carry_fail || !wait_bar_warp(&q_full[qs], (uint32_t)((spiece >> 1) & 1), abort_flag);
+        carry_fail = carry_fail || !mbar_wait_warp(&q_full[qs], (uint32_t)((spiece >> 1) & 1), abort_flag);
         named_bar_sync(bar_grp, 128);
 
         while (true) {
@@ -833,7 +794,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                     continue;
                 }
                 const int iu = (int)i + u, sb = iu & 1;
-                fail = fail || !wait_bar_warp(&s_full[sb], (uint32_t)((iu >> 1) & 1), abort_flag);
+                fail = fail || !mbar_wait_warp(&s_full[sb], (uint32_t)((iu >> 1) & 1), abort_flag);
                 if (PG && valid[u]) {  // the copy warp's: row r of the tile came in box r / block size
                     const float *sc = sc_s + (iu & (C::SCR - 1)) * 16 + (p.block_lg >= 7 ? 0 : row >> p.block_lg);
                     ksc[u] = sc[0];
@@ -936,7 +897,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                 for (int g = 0; g < NPH; ++g) l[g] *= alpha_s[cg0 + g];
                 if (i > i0) {
                     const long long j = i - 1;
-                    if (!wait_bar_warp(&pv_done[j & 1], (uint32_t)((j >> 1) & 1), abort_flag))
+                    if (!mbar_wait_warp(&pv_done[j & 1], (uint32_t)((j >> 1) & 1), abort_flag))
                         fail = true;
                     tc_fence_after();
                     // the group's columns of every part of every O^T block
@@ -996,7 +957,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                 }
                 if (iu >= C::PST) {
                     const int jp = iu - C::PST;
-                    if (!wait_bar_warp(&pv_done[jp & 1], (uint32_t)((jp >> 1) & 1), abort_flag))
+                    if (!mbar_wait_warp(&pv_done[jp & 1], (uint32_t)((jp >> 1) & 1), abort_flag))
                         fail = true;
                 }
                 // P stage: column n's byte at 2048 (n / 16) + n mod 16 of its
@@ -1034,7 +995,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
 
         // ---- piece end
         const long long e = i - 1;
-        bool fail = carry_fail || !wait_bar_warp(&pv_done[e & 1], (uint32_t)((e >> 1) & 1), abort_flag);
+        bool fail = carry_fail || !mbar_wait_warp(&pv_done[e & 1], (uint32_t)((e >> 1) & 1), abort_flag);
         carry_fail = false;
         tc_fence_after();
         warp_cols_n<NPH>(l, redg + q4 * 64, lane, OpSum());

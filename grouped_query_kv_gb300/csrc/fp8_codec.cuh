@@ -1,6 +1,6 @@
-// fp8_codec.cuh -- the row quantizer of the 8-bit KV cache, shared by the
-// stand-alone writers (kv_fp8.cu) and the fused append of the 8-bit
-// attention kernel (decode_fp8.cu), so that both write the same bytes.
+// fp8_codec.cuh -- E4M3 conversions, and the row quantizer of the 8-bit KV
+// cache, shared by the stand-alone writers (kv_fp8.cu) and the fused append of
+// the 8-bit attention kernel (decode_fp8.cu), so that both write the same bytes.
 // A cached row (one position of one K/V head, D values) is stored as D E4M3
 // codes and one fp32 scale ("The Basics of Transformer Inference", item
 // "Quantization"; "Machine Learning Engineering and AI Systems at Scale",
@@ -11,15 +11,30 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_fp16.h>
 
 namespace kvattn {
 
-// Two binary32 values -> two E4M3 codes, a in the low byte.
+// Two binary32 values -> two E4M3 codes (nearest, ties to even, saturating), a
+// in the low byte.
 __device__ __forceinline__ uint16_t e4m3x2_from_f32(float a, float b) {
     uint16_t r;
     // the first source goes to the upper byte
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
+}
+
+// Two E4M3 codes (low byte first) -> f16x2 (low half first); exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+    return r;
+}
+
+// Their values in binary32.
+__device__ __forceinline__ float2 e4m3x2_value(uint16_t two) {
+    const uint32_t h = e4m3x2_to_f16x2(two);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
 // Quantize one row of D bf16 values held by a warp (D / 32 values per

@@ -24,8 +24,6 @@
 // search for the largest and the rounding; longer blocks read them again.
 // 32 prompts, 67 k rows of 8 x 128 into blocks of 64: 65.0 us, 0.96 of the
 // measured copy rate; 64 single rows 4.3 us.
-#include <cuda_fp16.h>
-
 #include "../../include/kvattn.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -70,9 +68,7 @@ __device__ __forceinline__ void unpack8(uint4 raw, float (&x)[8]) {
 
 // Two codes times a power of two <= 1, as codes.
 __device__ __forceinline__ uint32_t rescale2(uint32_t two, float f) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    const float2 v = e4m3x2_value((uint16_t)two);
     return e4m3x2_from_f32(v.x * f, v.y * f);
 }
 

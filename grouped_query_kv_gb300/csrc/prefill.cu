@@ -155,27 +155,13 @@ struct PfCfg {
 
 __device__ __forceinline__ void pf_error(unsigned int *err, unsigned int code) { atomicCAS(err, 0u, code); }
 
-// Bounded wait that also gives up once another role has.  A poll sleeps until
-// the phase ends or a hardware limit passes; under the shortened limit of the
-// failure tests it does not, so that few polls are sure to give up.
-__device__ __forceinline__ bool pf_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                        uint32_t limit = KVATTN_SPIN_LIMIT) {
-    for (uint32_t it = 0; it < limit; ++it) {
-        if (limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity)) return true;
+// A bounded wait by one lane.  (The copies' end, after a role gave up; mbar_wait
+// there has the compiler lay the whole kernel out otherwise: 8192 tokens of 64
+// heads over 8 of 128 724 us with this, 742 with that.)
+__device__ __forceinline__ bool pf_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    for (uint32_t it = 0; it < KVATTN_SPIN_LIMIT; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
         if ((it & 255u) == 255u && *abort_flag) return false;
-    }
-    *abort_flag = 1;
-    return false;
-}
-
-// The same by a whole warp, which leaves it together (a uniform branch: with
-// each lane leaving on its own the wait took some 90 cycles, so 36).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                          uint32_t limit = KVATTN_SPIN_LIMIT) {
-    for (uint32_t it = 0; it < limit; ++it) {
-        const bool done = limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity);
-        if (__all_sync(0xffffffffu, done)) return true;
-        if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
     }
     *abort_flag = 1;
     return false;
@@ -256,15 +242,6 @@ __device__ __forceinline__ void st_global_32b(uint16_t *dst, const uint32_t *w) 
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)::"memory");
-    return r != 0;
 }
 
 template <int N>
@@ -414,7 +391,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     const uint32_t wlim = p.wait_limit ? p.wait_limit : KVATTN_SPIN_LIMIT;
     // (by a whole warp) unit k of this CTA's list
     auto next_unit = [&](int k, Unit *u) {
-        if (!warp_wait(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag)) return false;
+        if (!mbar_wait_warp(&u_full[k % kDesc], (uint32_t)((k / kDesc) & 1), abort_flag)) return false;
         *u = read_unit(units[k % kDesc]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&u_empty[k % kDesc]);
@@ -424,7 +401,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     int fills = 0;  // slots filled by this warp
     auto issue = [&](const void *tm, int c, int head, int row, auto &r) -> bool {
         const int slot = r.slot;
-        if (fills >= r.N && !warp_wait(&slot_empty[slot], r.parity ^ 1, abort_flag)) return false;
+        if (fills >= r.N && !mbar_wait_warp(&slot_empty[slot], r.parity ^ 1, abort_flag)) return false;
         if (elect_one()) {
             mbar_arrive_expect_tx(&slot_full[slot], C::SLOT);
 #pragma unroll
@@ -536,7 +513,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             *done = false;
             if (k >= kDesc) {
                 if (!must && !__all_sync(0xffffffffu, mbar_test(place, parity))) return true;
-                if (!warp_wait(place, parity, abort_flag)) return false;
+                if (!mbar_wait_warp(place, parity, abort_flag)) return false;
             }
             if (lane == 0) {
                 units[k % kDesc] = u;
@@ -592,7 +569,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         auto load_q = [&](const Unit &u) -> bool {
             for (int s = 0; s < NQ; ++s) {
                 if (u.n[s] == 0) continue;
-                if (qn[s] && !warp_wait(&q_empty[s], (qn[s] - 1) & 1, abort_flag)) return false;
+                if (qn[s] && !mbar_wait_warp(&q_empty[s], (qn[s] - 1) & 1, abort_flag)) return false;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&q_full[s], C::QT);
 #pragma unroll
@@ -713,7 +690,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
             // wait for both, 1009 us; in turns 869 us.
             typename C::KRing rc;    // the next slot that this warp has not waited for
             auto slot_ready = [&]() {
-                const bool go = warp_wait(&slot_full[rc.slot], rc.parity, abort_flag);
+                const bool go = mbar_wait_warp(&slot_full[rc.slot], rc.parity, abort_flag);
                 rc.next();
                 return go;
             };
@@ -729,9 +706,9 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 if (owed) go = slot_ready();
                 const auto rk = rc;
                 if (go && j < nmax) go = slot_ready();
-                if (go && j == j0 && j < n) go = warp_wait(&q_full[s], units_q++ & 1, abort_flag);
-                if (go && (s == 1 || !first_turn)) go = warp_wait(&turn[s], s == 0 ? it ^ 1 : it, abort_flag);
-                if (go && owed == 1) go = warp_wait(&p_full[s], g ^ 1, abort_flag, wlim);
+                if (go && j == j0 && j < n) go = mbar_wait_warp(&q_full[s], units_q++ & 1, abort_flag);
+                if (go && (s == 1 || !first_turn)) go = mbar_wait_warp(&turn[s], s == 0 ? it ^ 1 : it, abort_flag);
+                if (go && owed == 1) go = mbar_wait_warp(&p_full[s], g ^ 1, abort_flag, wlim);
                 if (!go) return false;
                 tc_fence_after();
                 if (owed == 1)
@@ -779,12 +756,12 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                     const int buf = w.g & 1;
                     const uint32_t parity = (w.g >> 1) & 1;
                     const auto r = rc;
-                    if (warp == 1 && w.j == 0) ok = warp_wait(&q_full[0], units_q++ & 1, abort_flag);
+                    if (warp == 1 && w.j == 0) ok = mbar_wait_warp(&q_full[0], units_q++ & 1, abort_flag);
 #pragma unroll
                     for (int c = 0; c < CPT; ++c, rc.next())
-                        ok = ok && warp_wait(&slot_full[rc.slot], rc.parity, abort_flag);
-                    if (ok && warp == 1 && w.g >= 2) ok = warp_wait(&turn[buf], parity ^ 1, abort_flag);
-                    if (ok && warp == 2) ok = warp_wait(&p_full[buf], parity, abort_flag, wlim);
+                        ok = ok && mbar_wait_warp(&slot_full[rc.slot], rc.parity, abort_flag);
+                    if (ok && warp == 1 && w.g >= 2) ok = mbar_wait_warp(&turn[buf], parity ^ 1, abort_flag);
+                    if (ok && warp == 2) ok = mbar_wait_warp(&p_full[buf], parity, abort_flag, wlim);
                     if (!ok) break;
                     tc_fence_after();
                     const int keys = min(kRows, min(w.u.t0 + p.tpt, w.u.len) - w.u.kbeg - w.j * kRows);
@@ -819,7 +796,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         if (elect_one()) umma_commit(drain);
         __syncwarp();
         volatile int never = 0;
-        warp_wait(drain, 0, &never);
+        mbar_wait_warp(drain, 0, &never);
         __syncwarp();
         named_bar_sync(kBarEndPf, C::THREADS);
         if (warp == 1) {
@@ -858,7 +835,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         for (int j = j0; j < n; ++j, ++g) {
             const int buf = NQ == 2 ? s : (int)(g & 1);
             const uint32_t par = (uint32_t)((NQ == 2 ? g : g >> 1) & 1);
-            ok = warp_wait(&s_full[buf], par, abort_flag, wlim);
+            ok = mbar_wait_warp(&s_full[buf], par, abort_flag, wlim);
             if (!ok) break;
             tc_fence_after();
             const uint32_t s_t = lanes + buf * 128;
@@ -924,7 +901,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                     // O holds the tiles up to j - 1
                     const int pb = NQ == 2 ? s : buf ^ 1;
                     const uint32_t pp = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
-                    ok = warp_wait(&pv_done[pb], pp, abort_flag, wlim);
+                    ok = mbar_wait_warp(&pv_done[pb], pp, abort_flag, wlim);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -970,10 +947,10 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
                 const long long iv = NQ == 2 ? base + 2 * j + 1 : g * CPT;  // (of the ring that V is in)
                 // (one query tile: the scores may be two tiles ahead of P V, and
                 // the slot's parity says something once the V tile before is done with)
-                if (NQ == 1 && g > 0) ok = warp_wait(&pv_done[buf ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abort_flag);
+                if (NQ == 1 && g > 0) ok = mbar_wait_warp(&pv_done[buf ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abort_flag);
                 for (int c = 0; c < CPT && ok; ++c) {
                     const int slot = (NQ == 2 ? 0 : C::KN) + (int)((iv + c) % C::VN);
-                    ok = warp_wait(&slot_full[slot], (uint32_t)(((iv + c) / C::VN) & 1), abort_flag);
+                    ok = mbar_wait_warp(&slot_full[slot], (uint32_t)(((iv + c) / C::VN) & 1), abort_flag);
                     if (ok)
                         for (int i = row; i < (stop - past) * (C::KC / 64) * 8; i += 128) {
                             const int r = past + (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
@@ -993,7 +970,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
         if (n > 0) {
             const int buf = NQ == 2 ? s : (int)((g - 1) & 1);
             const uint32_t par = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
-            ok = warp_wait(&pv_done[buf], par, abort_flag, wlim);
+            ok = mbar_wait_warp(&pv_done[buf], par, abort_flag, wlim);
             if (!ok) break;
             tc_fence_after();
             const float inv = 1.f / l;  // (every row attends itself)

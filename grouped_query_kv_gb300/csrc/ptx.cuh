@@ -90,6 +90,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     return false;
 }
 
+// The same by a whole warp, which leaves it together (a uniform branch: with
+// each lane leaving on its own the wait took some 90 cycles, so 36), and which
+// also gives up once another role has (*abort_flag).  A poll sleeps until the
+// phase ends or a hardware limit passes; under a shortened limit (the failure
+// tests') it does not, so that few polls are sure to give up.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                               uint32_t limit = KVATTN_SPIN_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
+        const bool done = limit < KVATTN_SPIN_LIMIT ? mbar_test(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
+    return r != 0;
+}
+
 __device__ __forceinline__ void prefetch_tmap(const void *tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
