@@ -12,8 +12,8 @@
 // itself (B lengths from L2, no workspace, nothing to wait for), then takes
 // tiles of 4096 packed rows, a row's thread also writing the table entry of
 // the block that starts at it; up to one tile the call is one block.  On the
-// device 64 requests of one token take 4.4 us, 1024 requests of 1.0 M rows
-// 8.6 (their 8.4 MB of slots are 1.3).
+// device 64 requests of one token take 4.3 us, 1024 requests of 1.0 M rows
+// 8.6 to 9.8 (their 8.4 MB of slots are 1.3).
 //
 // Row write.  A copy of 16-byte vectors, four K and four V vectors of a
 // thread in flight; both sides are contiguous per (token, head), so it runs
