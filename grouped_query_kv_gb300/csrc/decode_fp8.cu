@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NP, PG>::THREADS, 1)
                         cv = cn;
                     }
                 } else if (cv == kCvNone) {
-                    cv = 0;
+                    cv = 125;  // no scale but 0 yet: the first other one lowers it to its own
                 }
                 vsf = pow2i(cv);
                 named_bar_sync(bar_grp, 128);

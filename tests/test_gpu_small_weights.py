@@ -192,3 +192,39 @@ def test_a_query_entry_far_above_the_others(D, Hq, Hkv, paged):
             o = out[b, heads].double()
             over = (o - ref).abs() - err - (2.0 ** -8 if paged else 2.0 ** -20) * (ref.abs() + err)
             assert float(over.max()) <= 0, (b, h, float(over.max()))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", HEADS)
+@pytest.mark.parametrize("small", [2.0 ** -9, 2.0 ** -30, 2.0 ** -110])
+@pytest.mark.parametrize("ctas", [0, 1])
+def test_value_scales_of_zero_before_others(D, Hq, Hkv, small, ctas):
+    """The first tiles' value scales are 0 (of whole blocks, paged, and of rows),
+    so they say nothing about the unit that the others need."""
+    lens, zeros, bs, L = [1000, 128, 300, 129], [300, 0, 256, 128], 32, 1024
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    q = torch.randn((len(lens), Hq, D), generator=gen, device="cuda").to(torch.bfloat16)
+    codes = [torch.randint(0, 120, (len(lens) * L // bs, Hkv, bs, D), generator=gen, device="cuda", dtype=torch.uint8)
+             for _ in range(2)]
+    nb, scale = L // bs, 1 / math.sqrt(D)
+    ks = torch.full((len(lens) * nb, Hkv), 2.0 ** -7, device="cuda")
+    vs = torch.full((len(lens) * nb, Hkv), small, device="cuda")
+    for b, z in enumerate(zeros):
+        vs[b * nb:b * nb + z // bs] = 0
+    table = _i32(np.arange(len(lens) * nb).reshape(len(lens), nb))
+    cont = [c.view(len(lens), nb, Hkv, bs, D).permute(0, 2, 1, 3, 4).reshape(len(lens), Hkv, L, D).contiguous()
+            for c in codes]
+    rows = [x.view(len(lens), nb, Hkv).permute(0, 2, 1).repeat_interleave(bs, 2).contiguous() for x in (ks, vs)]
+    g.set_tuning(0, ctas)
+    try:
+        out = g.gqa_decode_attn_paged_fp8(q, *codes, ks, vs, table, _i32(lens), scale)
+        out32 = g.gqa_decode_attn_fp8(q, *cont, *rows, _i32(lens), scale)
+        g.check_device_error()
+    finally:
+        g.set_tuning(0, 0)
+    kvs = []
+    for b, n in enumerate(lens):
+        c = [x[b, :, :n].contiguous().view(torch.float8_e4m3fn).double().transpose(0, 1) for x in cont]
+        s = [x[b, :, :n].double().T for x in rows]
+        kvs.append((c[0] * s[0][:, :, None], c[1] * s[1][:, :, None], c[1].abs(), s[1]))
+    check(out, q, kvs, scale, 2.0 ** -8)
+    check(out32, q, kvs, scale, 2.0 ** -20)
