@@ -378,8 +378,9 @@ KVATTN_API int kv_append_fp8(void *k_codes, void *v_codes, float *k_scale, float
  * the head's largest and within 2^-22 of it below), out fp32
  * [B, Hq, D]; lengths, errors and ownership as gqa_decode_attn.  A position's
  * weight, exp(score - the largest score) times its value scale over the
- * largest value scale, enters with 11 significant bits down to 2^-14 and to
- * within 2^-25 below.
+ * largest value scale of its head's positions (an all-zero row's scale is 1
+ * and counts among them), enters with 11 significant bits down to 2^-14 and
+ * to within 2^-25 below.
  * Needs D = 128 or 256: the kernel copies each position's codes in rows of
  * 128 (one 128-byte swizzled TMA box per 128 head dims); D = 64 is
  * KVATTN_ERR_UNSUPPORTED (not built: its 64-byte rows would need a layout
