@@ -33,6 +33,8 @@ __all__ = [
     "kv_quantize_fp8", "kv_append_fp8", "gqa_decode_attn_fp8", "gqa_decode_step_fp8",
     "kv_block_tables", "kv_append_slots", "gqa_prefill_attn",
     "kv_append_paged_fp8", "gqa_decode_attn_paged_fp8",
+    "qk_norm_rope", "kv_append_rope",
+    "kv_fork_blocks", "kv_free_blocks", "kv_compact_blocks", "kv_copy_blocks",
     "check_device_error", "get_plan",
     "set_tuning", "set_wait_limit", "set_kernel_events", "release", "KvAttnError", "library_path", "lib",
     "KVATTN_OK", "KVATTN_ERR_INVALID_ARG", "KVATTN_ERR_UNSUPPORTED",
@@ -112,6 +114,12 @@ _SIGS = {
                                  _LL, _LL, _I, _I, _I, _VP]),
     "gqa_decode_attn_paged_fp8": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I,
                                        _I, _I, _I, ctypes.c_float, _VP]),
+    "qk_norm_rope": (_I, [_VP] * 9 + [_I] * 6 + [_LL] * 4 + [ctypes.c_float, _I, _VP]),
+    "kv_append_rope": (_I, [_VP] * 12 + [_I] * 6 + [_LL] * 4 + [ctypes.c_float, _I, _I, _I, _VP]),
+    "kv_fork_blocks": (_I, [_VP] * 9 + [_I] * 6 + [_VP]),
+    "kv_free_blocks": (_I, [_VP] * 7 + [_I] * 6 + [_VP]),
+    "kv_compact_blocks": (_I, [_VP] * 11 + [_I] * 5 + [_VP]),
+    "kv_copy_blocks": (_I, [_VP, _VP, _VP, _I, _I, _LL, _VP]),
     "kvattn_status_string": (ctypes.c_char_p, [_I]),
     "kvattn_last_error": (ctypes.c_char_p, []),
     "kvattn_check_device_error": (_I, [_VP]),
@@ -815,6 +823,230 @@ def gqa_decode_attn_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table
                                            out.data_ptr(), B, Hq, Hkv, D, nblk, bs, maxb, float(scale),
                                            _on(stream, dev)))
     return out
+
+
+def _rotation(positions, cos, sin, q_weight, k_weight, N, D, dev):
+    """Checks a rotation's arguments; returns (max_pos, rope_dim)."""
+    _want(positions, "positions", torch.int32, dev, (N,))
+    _want(cos, "cos", torch.float32, dev)
+    if cos.dim() != 2:
+        raise ValueError("cos must be [max_pos, rope_dim / 2]")
+    _want(sin, "sin", torch.float32, dev, cos.shape)
+    if q_weight is not None:
+        _want(q_weight, "q_weight", torch.float32, dev, (D,))
+    if k_weight is not None:
+        _want(k_weight, "k_weight", torch.float32, dev, (D,))
+    return cos.shape[0], 2 * cos.shape[1]
+
+
+def qk_norm_rope(q, k, positions, cos, sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """Norm of each head of q and k (where its weights are given) and rotation
+    by position, in fp32 and rounded once: values j and j + rope_dim / 2 of a head
+    (interleaved: 2 j and 2 j + 1) turn by the angle whose cosine and sine are
+    cos[positions[i], j] and sin[positions[i], j]; values from rope_dim on do not.
+
+    q: bf16 [N, Hq, D]; k: bf16 [N, Hkv, D], rows contiguous or slices of wider
+    rows; positions: int32 [N], negative for padding rows, which become zeros;
+    cos, sin: fp32 [max_pos, rope_dim / 2]; q_weight, k_weight: None or fp32 [D];
+    q_out, k_out: optional, like q and k, and may be q and k.  Returns
+    (q_out, k_out).
+    """
+    dev = _home(q, "q")
+    qs = _packed_rows(q, "q", dev)
+    N, Hq, D = q.shape
+    ks = _packed_rows(k, "k", dev)
+    Hkv = k.shape[1]
+    if k.shape[0] != N or k.shape[2] != D:
+        raise ValueError("k must be [N, Hkv, D] matching q")
+    max_pos, rd = _rotation(positions, cos, sin, q_weight, k_weight, N, D, dev)
+    if q_out is None:
+        q_out, qos = _new(torch.empty, (N, Hq, D), torch.bfloat16, q, stream), Hq * D
+    else:
+        qos = _packed_rows(q_out, "q_out", dev, (N, Hq, D))
+    if k_out is None:
+        k_out, kos = _new(torch.empty, (N, Hkv, D), torch.bfloat16, q, stream), Hkv * D
+    else:
+        kos = _packed_rows(k_out, "k_out", dev, (N, Hkv, D))
+    _check(lib().qk_norm_rope(q.data_ptr(), k.data_ptr(), positions.data_ptr(), cos.data_ptr(), sin.data_ptr(),
+                              None if q_weight is None else q_weight.data_ptr(),
+                              None if k_weight is None else k_weight.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                              N, Hq, Hkv, D, rd, max_pos, qs, ks, qos, kos, float(eps), bool(interleaved),
+                              _on(stream, dev)))
+    return q_out, k_out
+
+
+def kv_append_rope(q, k, v, positions, cos, sin, slots, k_pool, v_pool, q_weight=None, k_weight=None, eps=1e-6,
+                   interleaved=False, q_out=None, stream=None):
+    """qk_norm_rope, with the rotated keys and the values written to their rows
+    of a paged pool as kv_append_slots writes them.
+
+    q, k, positions, cos, sin, weights, q_out as for qk_norm_rope; v: bf16
+    [N, Hkv, D]; slots: int64 [N], all different, negative for rows that write
+    nothing; k_pool, v_pool: bf16 [num_blocks, Hkv, block_size, D] (in place).
+    Returns q_out.
+    """
+    dev = _home(q, "q")
+    qs = _packed_rows(q, "q", dev)
+    N, Hq, D = q.shape
+    _want(k_pool, "k_pool", torch.bfloat16, dev)
+    if k_pool.dim() != 4 or k_pool.shape[3] != D:
+        raise ValueError("k_pool must be [num_blocks, Hkv, block_size, D] matching q")
+    nblk, Hkv, bs = k_pool.shape[:3]
+    _want(v_pool, "v_pool", torch.bfloat16, dev, (nblk, Hkv, bs, D))
+    ks = _packed_rows(k, "k", dev, (N, Hkv, D))
+    vs = _packed_rows(v, "v", dev, (N, Hkv, D))
+    _want(slots, "slots", torch.int64, dev, (N,))
+    max_pos, rd = _rotation(positions, cos, sin, q_weight, k_weight, N, D, dev)
+    if q_out is None:
+        q_out, qos = _new(torch.empty, (N, Hq, D), torch.bfloat16, q, stream), Hq * D
+    else:
+        qos = _packed_rows(q_out, "q_out", dev, (N, Hq, D))
+    _check(lib().kv_append_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), cos.data_ptr(),
+                                sin.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
+                                None if k_weight is None else k_weight.data_ptr(), slots.data_ptr(),
+                                q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), N, Hq, Hkv, D, rd, max_pos,
+                                qs, ks, vs, qos, float(eps), bool(interleaved), nblk, bs, _on(stream, dev)))
+    return q_out
+
+
+def _held(block_table, seq_lens, refs, free_blocks, free_count, dev):
+    """Checks the tables of a pool whose blocks have several holders; returns
+    (R, max_blocks, num_blocks, num_free)."""
+    i32 = torch.int32
+    _want(block_table, "block_table", i32, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R, max_blocks]")
+    R, maxb = block_table.shape
+    _want(seq_lens, "seq_lens", i32, dev, (R,))
+    _want(refs, "refs", i32, dev)
+    _want(free_blocks, "free_blocks", i32, dev)
+    if refs.dim() != 1 or free_blocks.dim() != 1:
+        raise ValueError("refs must be [num_blocks] and free_blocks [num_free]")
+    _want(free_count, "free_count", i32, dev, (1,))
+    return R, maxb, refs.shape[0], free_blocks.shape[0]
+
+
+def _or_new(t, name, shape, dev, like, stream):
+    if t is None:
+        return _new(torch.empty, shape, torch.int32, like, stream)
+    _want(t, name, torch.int32, dev, shape)
+    return t
+
+
+def _or_same(t, name, same, dev):
+    if t is None:
+        return same
+    _want(t, name, torch.int32, dev, same.shape)
+    return t
+
+
+def kv_fork_blocks(block_table, seq_lens, refs, free_blocks, free_count, parents, children, block_size,
+                   copies=None, free_count_out=None, stream=None):
+    """Table rows children become forks of rows parents: they share the whole
+    blocks (refs + 1 each) and take a block from the free stack for a last one
+    that is partly filled, whose rows kv_copy_blocks then copies by `copies`.
+
+    block_table: int32 [R, max_blocks]; seq_lens: int32 [R]; refs: int32
+    [num_blocks], holders beyond the first (all three in place; zeros for a
+    new pool); free_blocks: int32 [num_free]; free_count: int32 [1]; parents,
+    children: int32 [n], the children rows of length 0, all different and no
+    parents.  copies (int32 [n, 2]) is allocated if None; the count left goes to
+    free_count_out (None: back into free_count).  Returns
+    (copies, free_count_out).  Forks that cannot be served set the device error
+    word (see include/kvattn.h).
+    """
+    dev = _home(block_table, "block_table")
+    R, maxb, nblk, nfree = _held(block_table, seq_lens, refs, free_blocks, free_count, dev)
+    _want(parents, "parents", torch.int32, dev)
+    if parents.dim() != 1:
+        raise ValueError("parents must be [n]")
+    n = parents.shape[0]
+    _want(children, "children", torch.int32, dev, (n,))
+    copies = _or_new(copies, "copies", (n, 2), dev, parents, stream)
+    free_count_out = _or_same(free_count_out, "free_count_out", free_count, dev)
+    _check(lib().kv_fork_blocks(block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
+                                free_blocks.data_ptr(), free_count.data_ptr(), parents.data_ptr(),
+                                children.data_ptr(), copies.data_ptr(), free_count_out.data_ptr(), n, R, maxb,
+                                _int32(block_size, "block_size"), nblk, nfree, _on(stream, dev)))
+    return copies, free_count_out
+
+
+def kv_free_blocks(block_table, seq_lens, refs, free_blocks, free_count, requests, block_size,
+                   free_count_out=None, stream=None):
+    """The named requests (int32 [n], table rows) let go of their blocks: their
+    entries become -1, their lengths 0, refs - 1 per block; blocks without a
+    holder are pushed onto the free stack in ascending order.  Other arguments
+    as for kv_fork_blocks; free_blocks is written, too.  Returns
+    free_count_out."""
+    dev = _home(block_table, "block_table")
+    R, maxb, nblk, nfree = _held(block_table, seq_lens, refs, free_blocks, free_count, dev)
+    _want(requests, "requests", torch.int32, dev)
+    if requests.dim() != 1:
+        raise ValueError("requests must be [n]")
+    free_count_out = _or_same(free_count_out, "free_count_out", free_count, dev)
+    _check(lib().kv_free_blocks(block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
+                                free_blocks.data_ptr(), free_count.data_ptr(), requests.data_ptr(),
+                                free_count_out.data_ptr(), requests.shape[0], R, maxb,
+                                _int32(block_size, "block_size"), nblk, nfree, _on(stream, dev)))
+    return free_count_out
+
+
+def kv_compact_blocks(block_table, seq_lens, refs, free_blocks, free_count, block_size, moves=None, remap=None,
+                      block_table_out=None, refs_out=None, free_blocks_out=None, free_count_out=None, stream=None):
+    """The blocks that are not on the free stack move to the front of the pool:
+    the k-th of them at or past their number goes to the k-th free one below.
+    Tables, references, stack and count are rewritten (in place, or into the
+    *_out tensors); kv_copy_blocks moves the rows by `moves`.
+
+    Tensors as for kv_fork_blocks; moves (int32 [num_blocks // 2, 2], (-1, -1)
+    behind the last move) and remap (int32 [num_blocks], each held block's new
+    id, -1 for free ones) are allocated if None.  Returns (moves, remap).
+    """
+    dev = _home(block_table, "block_table")
+    R, maxb, nblk, nfree = _held(block_table, seq_lens, refs, free_blocks, free_count, dev)
+    moves = _or_new(moves, "moves", (nblk // 2, 2), dev, refs, stream)
+    remap = _or_new(remap, "remap", (nblk,), dev, refs, stream)
+    outs = (_or_same(block_table_out, "block_table_out", block_table, dev),
+            _or_same(refs_out, "refs_out", refs, dev),
+            _or_same(free_blocks_out, "free_blocks_out", free_blocks, dev),
+            _or_same(free_count_out, "free_count_out", free_count, dev))
+    _check(lib().kv_compact_blocks(block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
+                                   free_blocks.data_ptr(), free_count.data_ptr(), *(t.data_ptr() for t in outs),
+                                   moves.data_ptr() or remap.data_ptr(), remap.data_ptr(), R, maxb,
+                                   _int32(block_size, "block_size"), nblk, nfree, _on(stream, dev)))
+    return moves, remap
+
+
+def kv_copy_blocks(k_pool, v_pool, copies, k_scale=None, v_scale=None, stream=None):
+    """Block copies[i, 0] to block copies[i, 1] in the pools of one layer;
+    (-1, -1) copies nothing.
+
+    k_pool, v_pool: bf16, or uint8 codes of a paged 8-bit cache, [num_blocks,
+    Hkv, block_size, D] (in place); copies: int32 [n, 2], as kv_fork_blocks and
+    kv_compact_blocks give them; k_scale, v_scale: the 8-bit cache's fp32
+    [num_blocks, Hkv], copied too.
+    """
+    dev = _home(k_pool, "k_pool")
+    if k_pool.dtype is not torch.uint8:
+        _want(k_pool, "k_pool", torch.bfloat16, dev)
+    _want(k_pool, "k_pool", k_pool.dtype, dev)
+    if k_pool.dim() != 4:
+        raise ValueError("k_pool must be [num_blocks, Hkv, block_size, D]")
+    nblk, Hkv, bs, D = k_pool.shape
+    _want(v_pool, "v_pool", k_pool.dtype, dev, (nblk, Hkv, bs, D))
+    _want(copies, "copies", torch.int32, dev)
+    if copies.dim() != 2 or copies.shape[1] != 2:
+        raise ValueError("copies must be [n, 2]")
+    if (k_pool.dtype is torch.uint8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go with pools of 8-bit codes")
+    n, on = copies.shape[0], _on(stream, dev)
+    if k_scale is not None:
+        _want(k_scale, "k_scale", torch.float32, dev, (nblk, Hkv))
+        _want(v_scale, "v_scale", torch.float32, dev, (nblk, Hkv))
+        _check(lib().kv_copy_blocks(k_scale.data_ptr(), v_scale.data_ptr(), copies.data_ptr(), n, nblk, 4 * Hkv, on))
+    _check(lib().kv_copy_blocks(k_pool.data_ptr(), v_pool.data_ptr(), copies.data_ptr(), n, nblk,
+                                Hkv * bs * D * k_pool.element_size(), on))
 
 
 def check_device_error(stream=None):

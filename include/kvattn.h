@@ -596,6 +596,165 @@ KVATTN_API int gqa_decode_attn_paged_fp8(const void *q, const void *k_codes, con
                                          kvattn_stream_t stream);
 
 /*
+ * Serving running requests from a paged cache.  A step's tokens, packed as
+ * above, are normalised and rotated on their way into attention
+ * (qk_norm_rope, or kv_append_rope with the write of their K/V rows);
+ * requests that share a prefix share its blocks (kv_fork_blocks,
+ * kv_copy_blocks, kv_free_blocks), and a pool can be compacted
+ * (kv_compact_blocks).  None of these six keeps device memory.  The calls run
+ * on the current device; every pointer belongs to it.
+ */
+
+/*
+ * qk_norm_rope -- norm of each query and key head and rotation by position.
+ * The pages give no rule; this library's, for every row i and head of D
+ * values x (fp32, rounded once at the end):
+ *     y_d = x_d / sqrt(mean_d x_d^2 + eps) * weight_d
+ *     (a, b) -> (a c_j - b s_j, a s_j + b c_j),  0 <= j < rope_dim / 2
+ * with c_j, s_j = cos_table, sin_table[positions[i]][j] and (a, b) the values
+ * j and j + rope_dim / 2 of y, or, interleaved, 2 j and 2 j + 1.  Values from
+ * rope_dim on are not rotated.
+ *
+ *   q, k       : bf16, N rows [Hq, D] and [Hkv, D]
+ *   positions  : int32 [N]
+ *   cos_table, sin_table : fp32 [max_pos, rope_dim / 2], the caller's (any base
+ *                or scaling)
+ *   q_weight, k_weight : fp32 [D], or null: y = x for q, or for k
+ *   q_out, k_out : bf16, N rows like q and k, written in full.  They may be q
+ *                and k themselves, with the same strides
+ *   rope_dim   : a multiple of 16 in [16, D]; eps >= 0 and finite
+ * A row with a negative position (padding) becomes zeros; so does one whose
+ * position is max_pos or more, which sets KVATTN_ERR_DEVICE_BOUNDS.  Squares
+ * are summed in fp32, which values of 2^60 and more overflow.
+ * D in {64, 128, 256}; 1 <= N <= 2^28.
+ */
+KVATTN_API int qk_norm_rope(const void *q, const void *k, const int32_t *positions,
+                            const float *cos_table, const float *sin_table, const float *q_weight,
+                            const float *k_weight, void *q_out, void *k_out, int N, int Hq, int Hkv,
+                            int D, int rope_dim, int max_pos, long long q_stride,
+                            long long k_stride, long long q_out_stride, long long k_out_stride,
+                            float eps, int interleaved, kvattn_stream_t stream);
+
+/*
+ * kv_append_rope -- qk_norm_rope and kv_append_slots in one pass: the rotated
+ * keys and the values (copied bit for bit) go to the pool rows that slots
+ * names, as kv_append_slots writes them; q_out gets the rotated queries.
+ *
+ *   v          : bf16, N rows [Hkv, D]; slots: int64 [N], all different
+ *   k_pool, v_pool : bf16 [num_blocks, Hkv, block_size, D], in place
+ * A negative slot writes no K/V row; one at or past num_blocks * block_size
+ * neither, and sets KVATTN_ERR_DEVICE_BOUNDS; a row without a valid position
+ * writes none whatever its slot.  The rest as qk_norm_rope.
+ */
+KVATTN_API int kv_append_rope(const void *q, const void *k, const void *v,
+                              const int32_t *positions, const float *cos_table,
+                              const float *sin_table, const float *q_weight,
+                              const float *k_weight, const int64_t *slots, void *q_out,
+                              void *k_pool, void *v_pool, int N, int Hq, int Hkv, int D,
+                              int rope_dim, int max_pos, long long q_stride, long long k_stride,
+                              long long v_stride, long long q_out_stride, float eps,
+                              int interleaved, int num_blocks, int block_size,
+                              kvattn_stream_t stream);
+
+/*
+ * Blocks with several holders.  refs, int32 [num_blocks], counts the holders
+ * of each block beyond the first: 0 for a free block and for one that a single
+ * request holds, so that kv_block_tables needs none of it.  The table rows'
+ * entries [0, ceil(seq_lens[r] / block_size)) are the holders.  The free stack
+ * is that of kv_block_tables: free_count[0] ids in free_blocks, taken from and
+ * pushed onto its top.  A row is written at its request's end only, so whole
+ * blocks can be shared and a partly filled one cannot: kv_fork_blocks gives a
+ * fork its own.  refs must be 16-byte aligned, copies and moves 8, other int32
+ * arrays 4.  Limits: R <= 65535 table rows, n <= 65535 named, num_blocks and
+ * num_free <= 2^28, max_blocks * block_size <= 2^24, block_size a power of two
+ * in [16, 2^20].
+ */
+
+/*
+ * kv_fork_blocks -- table row children[i] becomes a fork of row parents[i].
+ *
+ *   block_table : int32 [R, max_blocks], in place: the child's row gets the
+ *                 parent's whole blocks (refs + 1 each) and, if its last block is
+ *                 partly filled, a block from the free stack for it
+ *   seq_lens    : int32 [R], in place: the child's becomes the parent's
+ *   copies      : int32 [n, 2], written: (parent's last block, child's), whose
+ *                 rows kv_copy_blocks is to copy in each layer's pools, or
+ *                 (-1, -1) where there is nothing to copy
+ *   free_count, free_count_out : int32 [1]; may be the same word
+ * Blocks are taken in the order of i.  A fork is served if both rows are within
+ * [0, R), the child's length is 0, no earlier fork of the call has the same
+ * child, its parent's row is not a fork's of the call either, the parent's
+ * length is within its row, and the blocks wanted by it and all forks before it
+ * are no more than free_count[0].  One that is not changes nothing, has copies
+ * (-1, -1) and sets KVATTN_ERR_DEVICE_BOUNDS, and so does a block id outside
+ * [0, num_blocks): a table entry is copied as it is, without a count.
+ */
+KVATTN_API int kv_fork_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *refs,
+                              const int32_t *free_blocks, const int32_t *free_count,
+                              const int32_t *parents, const int32_t *children, int32_t *copies,
+                              int32_t *free_count_out, int n, int R, int max_blocks,
+                              int block_size, int num_blocks, int num_free,
+                              kvattn_stream_t stream);
+
+/*
+ * kv_free_blocks -- the named requests let go of their blocks: their table
+ * entries become -1, their lengths 0, refs - 1 per block; a block that has no
+ * holder left is pushed onto the free stack, in ascending order of the ids.
+ *
+ *   requests    : int32 [n], table rows; one named twice is freed once
+ *   free_blocks : int32 [num_free], written from free_count[0] on
+ * A request outside [0, R), or whose length is not within its row, is left as
+ * it is; an entry outside [0, num_blocks) is only cleared; a block freed more
+ * often than it is held is pushed once; blocks that the stack has no room for
+ * are dropped.  All of these set KVATTN_ERR_DEVICE_BOUNDS.  With free_count[0]
+ * outside [0, num_free] nothing is freed.
+ */
+KVATTN_API int kv_free_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *refs,
+                              int32_t *free_blocks, const int32_t *free_count,
+                              const int32_t *requests, int32_t *free_count_out, int n, int R,
+                              int max_blocks, int block_size, int num_blocks, int num_free,
+                              kvattn_stream_t stream);
+
+/*
+ * kv_compact_blocks -- the held blocks of a pool moved to its front.  A block
+ * is free if the stack has it and held if not; with `used` held ones, the k-th
+ * held block at or past `used` moves to the k-th free one below it.
+ *
+ *   moves  : int32 [num_blocks / 2, 2], written in full: (from, to), for
+ *            kv_copy_blocks in each layer's pools, (-1, -1) behind the last
+ *   remap  : int32 [num_blocks] (16-byte aligned), written: each held block's
+ *            new id, -1 for free blocks (to rewrite other tables by)
+ *   *_out  : the tables, references, stack and count after the moves; each may
+ *            be its input.  Entries of a row past its length, and stack places
+ *            past the count, are as before; the stack has the lowest id on top
+ * A length that is not within its row leaves the row as it is; an entry that
+ * names no held block becomes -1 if it was within [0, num_blocks); an id on the
+ * stack that is outside or there twice counts once or not at all.  All of these
+ * set KVATTN_ERR_DEVICE_BOUNDS; with free_count[0] outside [0, num_free] nothing
+ * moves.
+ */
+KVATTN_API int kv_compact_blocks(const int32_t *block_table, const int32_t *seq_lens,
+                                 const int32_t *refs, const int32_t *free_blocks,
+                                 const int32_t *free_count, int32_t *block_table_out,
+                                 int32_t *refs_out, int32_t *free_blocks_out,
+                                 int32_t *free_count_out, int32_t *moves, int32_t *remap, int R,
+                                 int max_blocks, int block_size, int num_blocks, int num_free,
+                                 kvattn_stream_t stream);
+
+/*
+ * kv_copy_blocks -- block copies[i][0] to block copies[i][1], in two pools.
+ *
+ *   k_pool, v_pool : num_blocks blocks of block_bytes each (a multiple of 4; of
+ *            16 for 16-byte vectors): a bf16 pool, 8-bit codes, or their scales
+ *   copies : int32 [n, 2] (8-byte aligned); (-1, -1) copies nothing, any other
+ *            id outside [0, num_blocks) neither, and sets KVATTN_ERR_DEVICE_BOUNDS
+ * The blocks copied to must differ from each other and from those copied from.
+ * n <= 2^28, block_bytes <= 2^32.
+ */
+KVATTN_API int kv_copy_blocks(void *k_pool, void *v_pool, const int32_t *copies, int n,
+                              int num_blocks, long long block_bytes, kvattn_stream_t stream);
+
+/*
  * gqa_decode_attn_noalloc -- the same computation as gqa_decode_attn, for
  * callers that must not have the library allocate device memory (for
  * example a server that gives all free GPU memory to its own pool at
