@@ -33,7 +33,7 @@ __all__ = [
     "kv_quantize_fp8", "kv_append_fp8", "gqa_decode_attn_fp8", "gqa_decode_step_fp8",
     "kv_block_tables", "kv_append_slots", "gqa_prefill_attn",
     "kv_append_paged_fp8", "gqa_decode_attn_paged_fp8",
-    "qk_norm_rope", "kv_append_rope",
+    "qk_norm_rope", "kv_append_rope", "gqa_extend_attn", "gqa_cross_attn",
     "kv_fork_blocks", "kv_free_blocks", "kv_compact_blocks", "kv_copy_blocks",
     "check_device_error", "get_plan",
     "set_tuning", "set_wait_limit", "set_kernel_events", "release", "KvAttnError", "library_path", "lib",
@@ -116,6 +116,8 @@ _SIGS = {
                                        _I, _I, _I, ctypes.c_float, _VP]),
     "qk_norm_rope": (_I, [_VP] * 9 + [_I] * 6 + [_LL] * 4 + [ctypes.c_float, _I, _VP]),
     "kv_append_rope": (_I, [_VP] * 12 + [_I] * 6 + [_LL] * 4 + [ctypes.c_float, _I, _I, _I, _VP]),
+    "gqa_extend_attn": (_I, [_VP] * 7 + [_I] * 5 + [_LL, _I, _I, _I, ctypes.c_float, _I, _VP]),
+    "gqa_cross_attn": (_I, [_VP] * 7 + [_I] * 5 + [_LL, _I, _I, _I, ctypes.c_float, _VP]),
     "kv_fork_blocks": (_I, [_VP] * 9 + [_I] * 6 + [_VP]),
     "kv_free_blocks": (_I, [_VP] * 7 + [_I] * 6 + [_VP]),
     "kv_compact_blocks": (_I, [_VP] * 11 + [_I] * 5 + [_VP]),
@@ -726,8 +728,8 @@ def gqa_prefill_attn(q, k, v, cu_seqlens, scale, out=None, stream=None, window=N
     """Causal attention of whole prompts packed one after the other: token i
     of sequence b (rows [cu_seqlens[b], cu_seqlens[b + 1])) attends the rows
     j <= i of its sequence (j > i - window on a local attention layer).  Only
-    these rows: it is for prompts with nothing cached, not for tokens that
-    continue a cached prefix.
+    these rows: it is for prompts with nothing cached; tokens that continue a
+    cached prefix are gqa_extend_attn's.
 
     q: bf16 [N, Hq, D]; k, v: bf16 [N, Hkv, D], rows contiguous or slices of
     wider rows; cu_seqlens: int32 [B + 1]; out: optional bf16 [N, Hq, D] (if
@@ -908,6 +910,62 @@ def kv_append_rope(q, k, v, positions, cos, sin, slots, k_pool, v_pool, q_weight
                                 q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), N, Hq, Hkv, D, rd, max_pos,
                                 qs, ks, vs, qos, float(eps), bool(interleaved), nblk, bs, _on(stream, dev)))
     return q_out
+
+
+def _extend_args(q, k_pool, v_pool, block_table, lens, name, cu_seqlens, out, stream):
+    """Checks what gqa_extend_attn and gqa_cross_attn share; returns out and the
+    C call's arguments up to the scale."""
+    dev = _home(q, "q")
+    qs = _packed_rows(q, "q", dev)
+    N, Hq, D = q.shape
+    _want(k_pool, "k_pool", torch.bfloat16, dev)
+    if k_pool.dim() != 4 or k_pool.shape[3] != D:
+        raise ValueError("k_pool must be [num_blocks, Hkv, block_size, D] matching q")
+    nblk, Hkv, bs, _ = k_pool.shape
+    _want(v_pool, "v_pool", torch.bfloat16, dev, k_pool.shape)
+    _want(block_table, "block_table", torch.int32, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B, maxb = block_table.shape
+    _want(lens, name, torch.int32, dev, (B,))
+    _want(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    if out is None:
+        out = _new(torch.zeros, (N, Hq, D), torch.bfloat16, q, stream)
+    else:
+        _want(out, "out", torch.bfloat16, dev, (N, Hq, D))
+    return out, dev, (q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+                      cu_seqlens.data_ptr(), out.data_ptr(), B, N, Hq, Hkv, D, qs, nblk, bs, maxb)
+
+
+def gqa_extend_attn(q, k_pool, v_pool, block_table, seq_lens, cu_seqlens, scale, out=None, stream=None,
+                    window=None):
+    """Causal attention of packed tokens over a paged cache that holds them and
+    what came before: token i of sequence b's n rows [cu_seqlens[b],
+    cu_seqlens[b + 1]) is at position seq_lens[b] - n + i of block table row b and
+    attends the positions up to its own (the last `window` of them on a local
+    attention layer).  Any mixture of prompts, parts of prompts and single tokens.
+
+    q: bf16 [N, Hq, D], rows contiguous or slices of wider rows; k_pool, v_pool:
+    bf16 [num_blocks, Hkv, block_size, D] with the new tokens' rows written;
+    block_table: int32 [B, max_blocks]; seq_lens: int32 [B], tokens cached with
+    the new ones; cu_seqlens: int32 [B + 1]; out: optional bf16 [N, Hq, D] (if
+    None allocated as zeros, since rows of no sequence are not written); window:
+    None (all positions) or an int >= 1.  Returns out.
+    """
+    out, dev, args = _extend_args(q, k_pool, v_pool, block_table, seq_lens, "seq_lens", cu_seqlens, out, stream)
+    _check(lib().gqa_extend_attn(*args, float(scale), 0x7fffffff if window is None else _window(window),
+                                 _on(stream, dev)))
+    return out
+
+
+def gqa_cross_attn(q, k_pool, v_pool, block_table, kv_lens, cu_seqlens, scale, out=None, stream=None):
+    """Attention of packed tokens over another sequence's rows in a paged pool,
+    such as an encoder's states: every token of sequence b attends positions
+    [0, kv_lens[b]) of block table row b.  kv_lens: int32 [B]; the rest as for
+    gqa_extend_attn.  Returns out."""
+    out, dev, args = _extend_args(q, k_pool, v_pool, block_table, kv_lens, "kv_lens", cu_seqlens, out, stream)
+    _check(lib().gqa_cross_attn(*args, float(scale), _on(stream, dev)))
+    return out
 
 
 def _held(block_table, seq_lens, refs, free_blocks, free_count, dev):

@@ -505,6 +505,13 @@ int api_device(int *ctas, unsigned int **err, unsigned int *wait_limit) {
     return KVATTN_OK;
 }
 
+int api_call_workspace(cudaStream_t stream, size_t bytes, void **ptr) {
+    int dev, rc;
+    if ((rc = current_device(&dev))) return rc;
+    std::lock_guard<std::mutex> lk(g_mu);
+    return get_call_workspace(dev, stream, bytes, ptr);
+}
+
 int api_encode_bf16_3d(CUtensorMap *m, const void *base, const cuuint64_t *dims,
                        const cuuint64_t *strides, const cuuint32_t *box) {
     {

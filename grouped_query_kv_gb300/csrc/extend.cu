@@ -1,0 +1,241 @@
+// extend.cu -- gqa_extend_attn and gqa_cross_attn: packed tokens of ragged counts
+// over K/V rows in a paged pool, causal behind what their request has cached, or
+// over all rows of another sequence, such as an encoder's states.
+//
+// The kernel is that of prefill.cuh; what differs over a pool:
+//  * K/V tiles come through the block table, a box of min(block size, 128) rows
+//    a lane of the copy warp, whose ids are looked up a tile ahead; a tile is the
+//    positions from a multiple of 128 on, so that boxes are whole blocks;
+//  * token t attends [max(0, e - window), e) with e = cached + t + 1 (extend) or all
+//    positions (cross); rows that attend nothing are zeroed beside the schedule;
+//  * a step's requests bring one token each as often as thousands: the key tiles
+//    of all units in a row are cut into equal ranges, a CTA each (units.cuh), so
+//    that a single long request fills the chip as 64 ragged ones do.  A unit that
+//    a range ends in leaves unnormalised rows O with their maximum and sum (m, l)
+//    in the workspace, two pieces a CTA at most, which merge_kernel joins:
+//        out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max m_i.
+#include <cfloat>
+#include <cmath>
+
+#include "../../include/kvattn.h"
+#include "prefill.cuh"
+
+namespace kvattn {
+
+namespace {
+
+struct MergeParams {
+    const float *ws_o, *ws_ml;
+    const int4 *split;  // per CTA: (packed row, tokens, first head, pieces) of the unit it leaves unfinished
+    uint16_t *out;
+    int Hq, hpg, tpt;
+    int slot_rows;      // rows of a workspace slot
+};
+
+constexpr int kMergeThreads = 256;
+
+// Block (c, y): rows of the unit that CTA c leaves unfinished, a warp each.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
+    constexpr int V = D / 32;  // values of a lane
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int4 u = __ldcg(p.split + c);
+    const int rows = u.w > 0 ? u.y * p.hpg : 0;
+    for (int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < rows;
+         r += gridDim.y * (kMergeThreads / 32)) {
+        const int t = r / p.hpg, h = r - t * p.hpg;
+        const int row = t / p.tpt * kRows + t % p.tpt * p.hpg + h;
+        auto at = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.slot_rows + row; };
+        float m = -INFINITY;
+        for (int i = lane; i < u.w; i += 32) m = fmaxf(m, __ldcg(p.ws_ml + at(i) * 2));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float o[V], l = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = 0.f;
+        for (int i0 = 0; i0 < u.w; i0 += 32) {
+            float w = 0.f;
+            if (i0 + lane < u.w) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + at(i0 + lane));
+                if (ml.y > 0.f) w = fast_exp2(ml.x - m);
+                l += w * ml.y;
+            }
+            const int n = min(32, u.w - i0);
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                if (wi == 0.f) continue;  // (a piece that held none of the row's keys may hold anything)
+                const float *src = p.ws_o + at(i0 + i) * D + lane * V;
+                float x[V];
+                if constexpr (V == 2) {
+                    *reinterpret_cast<float2 *>(x) = __ldcg(reinterpret_cast<const float2 *>(src));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; k += 4)
+                        *reinterpret_cast<float4 *>(x + k) = __ldcg(reinterpret_cast<const float4 *>(src + k));
+                }
+#pragma unroll
+                for (int k = 0; k < V; ++k) o[k] = fmaf(wi, x[k], o[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+        const float inv = 1.f / l;  // (every row attends something)
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) w[k] = bf16x2_of(o[2 * k] * inv, o[2 * k + 1] * inv);
+        uint16_t *dst = p.out + ((size_t)(u.x + t) * p.Hq + u.z + h) * D + lane * V;
+        if constexpr (V == 2)
+            *reinterpret_cast<uint32_t *>(dst) = w[0];
+        else if constexpr (V == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int D>
+cudaError_t launch_merge(const MergeParams &p, int ctas, int parts, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, parts);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+}
+
+// 3-D map over a pool [num_blocks, Hkv, block_size, D]: dims (D, block_size,
+// num_blocks * Hkv), box (64, min(block_size, 128), 1).
+int encode_pool(CUtensorMap *m, const void *base, int D, int block_size, long long heads, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)block_size, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * (cuuint64_t)block_size};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    return api_encode_bf16_3d(m, base, dims, strides, box);
+}
+
+int run_extend(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+               const int32_t *kv_lens, const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv, int D,
+               long long q_stride, int num_blocks, int block_size, int max_blocks, float scale, int causal,
+               int window, kvattn_stream_t stream_, const char *who) {
+    api_begin();
+    if (!q || !k_pool || !v_pool || !block_table || !kv_lens || !cu_seqlens || !out)
+        return api_failf(KVATTN_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pool) |
+          reinterpret_cast<uintptr_t>(v_pool)) & 15u) ||
+        (reinterpret_cast<uintptr_t>(out) & 31u) ||
+        ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(kv_lens)) & 3u))
+        return api_failf(KVATTN_ERR_INVALID_ARG, "%s: q and pools must be 16-byte, out 32-byte aligned", who);
+    if (!std::isfinite(scale)) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: scale must be finite", who);
+    if (window < 1) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: window must be >= 1 (got %d)", who, window);
+    PagedPrefillParams p = {};
+    int rc, lmax;
+    if ((rc = api_check_sizes(B, Hq, Hkv, D, 1))) return rc;
+    if ((rc = api_check_paged(block_table, Hkv, block_size, max_blocks, num_blocks, who, &p.lg, &lmax))) return rc;
+    if (N < 1) return api_failf(KVATTN_ERR_INVALID_ARG, "%s: N must be positive (got %d)", who, N);
+    if (N > (1 << 28)) return api_failf(KVATTN_ERR_UNSUPPORTED, "%s: N = %d rows beyond 2^28", who, N);
+    if ((rc = api_check_row_stride(q_stride, Hq, D, who))) return rc;
+    int ctas;
+    if ((rc = api_device(&ctas, &p.err, &p.wait_limit))) return rc;
+
+    p.cu = cu_seqlens;
+    p.out = static_cast<uint16_t *>(out);
+    p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.hpg = 1;
+    while (p.hpg < kRows && p.G % (2 * p.hpg) == 0) p.hpg *= 2;
+    p.tpt = kRows / p.hpg;
+    // Few tokens a request: all heads of a group in one tile, by as many tokens as
+    // are left a power of two, so that a request's keys are read once for the group
+    // whatever its size; else every row of the tile counts.
+    if (p.G <= kRows && p.hpg < p.G) {
+        int tpt = 1;
+        while (2 * tpt * p.G <= kRows) tpt *= 2;
+        if ((long long)N <= (long long)B * tpt) {
+            p.hpg = p.G;
+            p.tpt = tpt;
+        }
+    }
+    p.passes = p.G / p.hpg;
+    p.rows = p.hpg * p.tpt;
+    p.q_bytes = p.rows * D * 2;
+    p.window = window < lmax ? window : lmax;
+    const float sl = (float)(std::fabs((double)scale) * 1.4426950408889634);
+    p.sl = std::isfinite(sl) ? std::fmax(sl, FLT_MIN) : FLT_MAX;  // (masked scores stay -inf at scale 0)
+    p.neg = scale < 0.f;
+    p.table = block_table;
+    p.kv_lens = kv_lens;
+    p.max_blocks = max_blocks;
+    p.num_blocks = num_blocks;
+    p.box = block_size < 128 ? block_size : 128;
+    p.causal = causal;
+    p.cost_piece = 1;
+    p.min_tiles = 2;
+
+    CUtensorMap tmq, tmk, tmv;
+    const long long heads = (long long)num_blocks * Hkv;
+    if ((rc = encode_rows_map(&tmq, q, D, Hq, N, q_stride, p.hpg, p.tpt)) ||
+        (rc = encode_pool(&tmk, k_pool, D, block_size, heads, p.box)) ||
+        (rc = encode_pool(&tmv, v_pool, D, block_size, heads, p.box)))
+        return rc;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const int slot_rows = (D == 256 ? 1 : 2) * kRows;
+    const size_t rows = (size_t)2 * ctas * slot_rows;
+    void *ws = nullptr;
+    if ((rc = api_call_workspace(stream, rows * (D + 2) * sizeof(float) + (size_t)ctas * sizeof(int4), &ws)))
+        return rc;
+    p.ws_o = static_cast<float *>(ws);
+    p.ws_ml = p.ws_o + rows * D;
+    p.split = reinterpret_cast<int4 *>(p.ws_ml + rows * 2);
+
+    MergeParams m = {p.ws_o, p.ws_ml, p.split, p.out, Hq, p.hpg, p.tpt, slot_rows};
+    const long long unit_rows = (long long)N * p.hpg < slot_rows ? (long long)N * p.hpg : slot_rows;
+    const int parts = (int)((unit_rows + 15) / 16);
+    cudaError_t e;
+    switch (D) {
+        case 64:
+            e = launch_pf<64, true>(tmq, tmk, tmv, p, ctas, stream);
+            if (e == cudaSuccess) e = launch_merge<64>(m, ctas, parts, stream);
+            break;
+        case 128:
+            e = launch_pf<128, true>(tmq, tmk, tmv, p, ctas, stream);
+            if (e == cudaSuccess) e = launch_merge<128>(m, ctas, parts, stream);
+            break;
+        default:
+            e = launch_pf<256, true>(tmq, tmk, tmv, p, ctas, stream);
+            if (e == cudaSuccess) e = launch_merge<256>(m, ctas, parts, stream);
+            break;
+    }
+    if (e != cudaSuccess) return api_cuda_fail(e, "paged prompt attention launch");
+    return KVATTN_OK;
+}
+
+}  // namespace
+
+}  // namespace kvattn
+
+using namespace kvattn;
+
+extern "C" {
+
+int gqa_extend_attn(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                    const int32_t *seq_lens, const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv,
+                    int D, long long q_stride, int num_blocks, int block_size, int max_blocks, float scale,
+                    int window, kvattn_stream_t stream) {
+    return run_extend(q, k_pool, v_pool, block_table, seq_lens, cu_seqlens, out, B, N, Hq, Hkv, D, q_stride,
+                      num_blocks, block_size, max_blocks, scale, 1, window, stream, "gqa_extend_attn");
+}
+
+int gqa_cross_attn(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                   const int32_t *kv_lens, const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv,
+                   int D, long long q_stride, int num_blocks, int block_size, int max_blocks, float scale,
+                   kvattn_stream_t stream) {
+    return run_extend(q, k_pool, v_pool, block_table, kv_lens, cu_seqlens, out, B, N, Hq, Hkv, D, q_stride,
+                      num_blocks, block_size, max_blocks, scale, 0, 0x7fffffff, stream, "gqa_cross_attn");
+}
+
+}  // extern "C"

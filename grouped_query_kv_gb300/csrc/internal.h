@@ -159,6 +159,9 @@ int api_check_paged(const int32_t *table, int Hkv, int block_size, int max_block
 // The current device: its grid size for a persistent kernel (the SM count
 // unless the tuning knob forces another), error word and the wait-limit knob.
 int api_device(int *ctas, unsigned int **err, unsigned int *wait_limit);
+// A workspace of the current device and this stream, or, while it is captured, of
+// the capture's own (see get_call_workspace).
+int api_call_workspace(cudaStream_t stream, size_t bytes, void **ptr);
 // 3-D map of bf16 values, 128-byte swizzle, out-of-range reads as zeros.
 int api_encode_bf16_3d(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
                        const cuuint32_t *box);

@@ -490,8 +490,8 @@ KVATTN_API int kv_append_slots(void *k_pool, void *v_pool, const void *k_new, co
  * gqa_prefill_attn -- causal attention of whole prompts, packed.  Nothing of
  * a cache is read: it is the attention of prompts that have no token cached.
  * Rows that continue a cached prefix (cached_lens > 0 in kv_block_tables)
- * would attend each other alone here; gqa_decode_attn_paged takes up to 64 new
- * tokens a request, the same number for each, over a bf16 pool.
+ * would attend each other alone here; gqa_extend_attn takes them, over a bf16
+ * pool.
  *
  * For every sequence b, token i of its n_b = cu_seqlens[b+1] - cu_seqlens[b]
  * and query head h (kvh = h / (Hq / Hkv)):
@@ -598,11 +598,13 @@ KVATTN_API int gqa_decode_attn_paged_fp8(const void *q, const void *k_codes, con
 /*
  * Serving running requests from a paged cache.  A step's tokens, packed as
  * above, are normalised and rotated on their way into attention
- * (qk_norm_rope, or kv_append_rope with the write of their K/V rows);
- * requests that share a prefix share its blocks (kv_fork_blocks,
- * kv_copy_blocks, kv_free_blocks), and a pool can be compacted
- * (kv_compact_blocks).  None of these six keeps device memory.  The calls run
- * on the current device; every pointer belongs to it.
+ * (qk_norm_rope, or kv_append_rope with the write of their K/V rows) and
+ * attend what their requests have cached (gqa_extend_attn) or an encoder's
+ * states (gqa_cross_attn); requests that share a prefix share its blocks
+ * (kv_fork_blocks, kv_copy_blocks, kv_free_blocks), and a pool can be compacted
+ * (kv_compact_blocks).  All but the two attention calls keep no device memory.
+ * The calls run on the current device; every pointer belongs to it.  Outputs
+ * must not overlap inputs, but where that is said.
  */
 
 /*
@@ -655,6 +657,65 @@ KVATTN_API int kv_append_rope(const void *q, const void *k, const void *v,
                               long long v_stride, long long q_out_stride, float eps,
                               int interleaved, int num_blocks, int block_size,
                               kvattn_stream_t stream);
+
+/*
+ * gqa_extend_attn -- causal attention of packed tokens that continue what their
+ * requests have cached, over the paged pool that holds both: a prompt taken in
+ * parts, a prompt behind a shared prefix, drafted tokens, or one token of each
+ * request, in any mixture.
+ *
+ * For every sequence b with n_b = cu_seqlens[b+1] - cu_seqlens[b] rows, token i
+ * of it is at position p = seq_lens[b] - n_b + i of its block table row, and for
+ * query head h (kvh = h / (Hq / Hkv))
+ *     out[i,h,:] = softmax_j(scale * q[i,h,:] . K[j,kvh]) . V[j,kvh]
+ * over max(0, p - window + 1) <= j <= p.
+ *
+ *   q          : bf16, N rows [Hq, D] (q_stride as above)
+ *   k_pool, v_pool : bf16 [num_blocks, Hkv, block_size, D], the new tokens' rows
+ *                written (kv_append_rope, kv_append_slots)
+ *   block_table: int32 [B, max_blocks]; seq_lens: int32 [B], tokens in the cache
+ *                with the new ones
+ *   cu_seqlens : int32 [B + 1], non-decreasing, within [0, N]
+ *   out        : bf16 [N, Hq, D], contiguous, 32-byte aligned; rows of no
+ *                sequence stay as they are
+ *   scale      : finite; window >= 1 (past every position: all)
+ *
+ * Tokens that attend nothing (n_b > seq_lens[b], the first n_b - seq_lens[b] of
+ * them) get zeros.  A sequence whose bounds are not 0 <= cu_seqlens[b] <=
+ * cu_seqlens[b+1] <= N is skipped, one whose length is outside [0, max_blocks *
+ * block_size] gets zeros, a table entry outside [0, num_blocks) that holds
+ * attended positions reads as a block of zeros; all three set
+ * KVATTN_ERR_DEVICE_BOUNDS.  Entries and pool rows at and past a length, and
+ * those before every window, may hold anything; of sequences whose rows overlap
+ * either may have written them.
+ *
+ * Scores, maxima and sums are held in fp32 (scale * q . K must stay finite
+ * there), the weights enter the second product as bf16, unnormalised, and the
+ * result is rounded once more.  The same inputs give the same bits.  The
+ * workspace (41 MB on a GPU of 152 SMs at D = 128 and 256, 21 MB at D = 64) is the
+ * stream's, or of a captured call's own, as for gqa_decode_attn_paged_fp8.
+ * D in {64, 128, 256}; block_size a power of two in [16, 2^20]; 1 <= N <= 2^28.
+ */
+KVATTN_API int gqa_extend_attn(const void *q, const void *k_pool, const void *v_pool,
+                               const int32_t *block_table, const int32_t *seq_lens,
+                               const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv,
+                               int D, long long q_stride, int num_blocks, int block_size,
+                               int max_blocks, float scale, int window, kvattn_stream_t stream);
+
+/*
+ * gqa_cross_attn -- attention of packed tokens over all rows of another
+ * sequence, such as an encoder's states: gqa_extend_attn without the causal
+ * limit.  Every token of sequence b attends the positions 0 <= j < kv_lens[b] of
+ * block table row b, whatever the number of its tokens; kv_lens[b] = 0 gives
+ * zeros.  The states' K/V rows are written to their blocks once (kv_append_slots)
+ * and may be shared (kv_fork_blocks, or the same ids in several rows).  The rest
+ * as gqa_extend_attn.
+ */
+KVATTN_API int gqa_cross_attn(const void *q, const void *k_pool, const void *v_pool,
+                              const int32_t *block_table, const int32_t *kv_lens,
+                              const int32_t *cu_seqlens, void *out, int B, int N, int Hq, int Hkv,
+                              int D, long long q_stride, int num_blocks, int block_size,
+                              int max_blocks, float scale, kvattn_stream_t stream);
 
 /*
  * Blocks with several holders.  refs, int32 [num_blocks], counts the holders
@@ -804,7 +865,8 @@ KVATTN_API void kvattn_release(void);
  *   force_path : 0 auto, 1 CUDA-core FMA kernel, 2 tensor-core kernel
  *   num_ctas   : 0 auto, else the persistent grid size of the attention
  *                kernel (a small value forces long multi-CTA splits); also that
- *                of gqa_prefill_attn, kv_block_tables and the split of
+ *                of gqa_prefill_attn, gqa_extend_attn, gqa_cross_attn,
+ *                kv_block_tables and the split of
  *                kv_append_paged_fp8
  * Returns KVATTN_ERR_INVALID_ARG for values out of range.
  */
@@ -821,8 +883,8 @@ KVATTN_API int kvattn_set_tuning(int force_path, int num_ctas);
  * and returns; the output of that call is undefined.  Waits for work already
  * issued keep their default limit.  With a very small value (1) a call is
  * sure to give up, which is how the tests exercise this path.  It shortens
- * gqa_prefill_attn's waits for scores, probabilities and P.V products the
- * same way, and in the 8-bit kernels the MMA warp's polling (the other waits
+ * gqa_prefill_attn's, gqa_extend_attn's and gqa_cross_attn's waits for scores,
+ * probabilities and P.V products the same way, and in the 8-bit kernels the MMA warp's polling (the other waits
  * there end with it).  Always returns KVATTN_OK.
  */
 KVATTN_API int kvattn_set_wait_limit(unsigned int polls);
@@ -832,7 +894,8 @@ KVATTN_API int kvattn_set_wait_limit(unsigned int polls);
  * handles, owned by the caller), every later attention call records
  * `before` on its stream just before its split-KV kernel and `after` just
  * after it, so that cudaEventElapsedTime(before, after) is that kernel's
- * duration alone (gqa_prefill_attn has no such kernel and records nothing).
+ * duration alone (gqa_prefill_attn, gqa_extend_attn and gqa_cross_attn record
+ * nothing).
  * The records sit between the kernel and its neighbours on
  * the stream, so they also end the programmatic overlap with them: use it to
  * time, not in production.  Pass (NULL, NULL) to stop; one NULL alone is

@@ -16,6 +16,9 @@ ROPE = dict(q=P, k=P, positions=P, cos_table=P, sin_table=P, q_weight=P, k_weigh
 APPEND = dict(q=P, k=P, v=P, positions=P, cos_table=P, sin_table=P, q_weight=P, k_weight=P, slots=P, q_out=P,
               k_pool=P, v_pool=P, N=10, Hq=4, Hkv=2, D=128, rope_dim=64, max_pos=100, q_stride=512, k_stride=256,
               v_stride=256, q_out_stride=512, eps=1e-6, interleaved=1, num_blocks=4, block_size=16)
+EXTEND = dict(q=P, k_pool=P, v_pool=P, block_table=P, seq_lens=P, cu_seqlens=P, out=P, B=2, N=10, Hq=4, Hkv=2, D=128,
+              q_stride=512, num_blocks=4, block_size=16, max_blocks=3, scale=0.1, window=10)
+CROSS = {("kv_lens" if k == "seq_lens" else k): v for k, v in EXTEND.items() if k != "window"}
 FORK = dict(block_table=P, seq_lens=P, refs=P, free_blocks=P, free_count=P, parents=P, children=P, copies=P,
             free_count_out=P, n=3, R=5, max_blocks=8, block_size=16, num_blocks=20, num_free=20)
 FREE = dict(block_table=P, seq_lens=P, refs=P, free_blocks=P, free_count=P, requests=P, free_count_out=P, n=3, R=5,
@@ -27,8 +30,8 @@ COPY = dict(k_pool=P, v_pool=P, copies=P, n=3, num_blocks=20, block_bytes=4096)
 
 
 def _cases():
-    calls = dict(qk_norm_rope=ROPE, kv_append_rope=APPEND, kv_fork_blocks=FORK, kv_free_blocks=FREE,
-                 kv_compact_blocks=COMPACT, kv_copy_blocks=COPY)
+    calls = dict(qk_norm_rope=ROPE, kv_append_rope=APPEND, gqa_extend_attn=EXTEND, gqa_cross_attn=CROSS,
+                 kv_fork_blocks=FORK, kv_free_blocks=FREE, kv_compact_blocks=COMPACT, kv_copy_blocks=COPY)
     for call, args in calls.items():
         for name, v in args.items():
             if v == P:
@@ -37,11 +40,14 @@ def _cases():
                 yield call, args, {name: P + 2}, INV
         for bs in (0, 8, 24, 1 << 21):
             yield call, args, dict(block_size=bs), UNS
-        for name in ("N", "n", "R", "max_blocks", "num_blocks", "num_free", "max_pos", "Hkv"):
+        for name in ("N", "n", "R", "max_blocks", "num_blocks", "num_free", "max_pos", "Hkv", "B", "window"):
             for bad in (0, -1):
                 yield call, args, {name: bad}, INV
         yield call, args, dict(N=(1 << 28) + 1), UNS
         yield call, args, dict(R=65536), UNS
+        yield call, args, dict(B=65536), UNS
+        for scale in (float("nan"), float("inf")):
+            yield call, args, dict(scale=scale), INV
         yield call, args, dict(n=(1 << 28) + 1), UNS
         if "R" in args:
             yield call, args, dict(n=65536), UNS
@@ -72,6 +78,9 @@ def _cases():
     yield "kv_copy_blocks", COPY, dict(k_pool=P + 4), INV
     yield "kv_append_rope", APPEND, dict(slots=P + 4), INV
     yield "kv_append_rope", APPEND, dict(num_blocks=1 << 30), UNS
+    for call, args in (("gqa_extend_attn", EXTEND), ("gqa_cross_attn", CROSS)):
+        yield call, args, dict(num_blocks=1 << 30), UNS
+        yield call, args, dict(out=P + 16), INV
 
 
 @pytest.fixture(scope="module")
@@ -110,5 +119,9 @@ def test_the_binding_refuses_host_tensors():
         g.kv_compact_blocks(i[None], i, i, i, i[:1], 16)
     with pytest.raises(ValueError, match="CUDA"):
         g.kv_copy_blocks(q[None], q[None], i[None])
+    with pytest.raises(ValueError, match="CUDA"):
+        g.gqa_extend_attn(q, q[None], q[None], i[None], i, i, 1.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        g.gqa_cross_attn(q, q[None], q[None], i[None], i, i, 1.0)
     with pytest.raises(TypeError):
         g.qk_norm_rope([1], q, i, f, f)
