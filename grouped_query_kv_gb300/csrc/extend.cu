@@ -34,64 +34,97 @@ struct MergeParams {
 
 constexpr int kMergeThreads = 256;
 
+// (by a warp) one row from its n partial results, the i-th at row at(i) of the
+// workspace: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, M = max m_i.
+// The first AHEAD of them are loaded with their (m, l), before it is known what
+// they weigh.
+template <int D, int AHEAD, class At>
+__device__ __forceinline__ void join_row(const float *ws_o, const float *ws_ml, At at, int n, uint16_t *out) {
+    constexpr int V = D / 32;  // values of a lane
+    const int lane = threadIdx.x & 31;
+    auto load = [&](int i, float *x) {
+        const float *src = ws_o + at(i) * D + lane * V;
+        if constexpr (V == 2) {
+            const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
+            x[0] = f.x;
+            x[1] = f.y;
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; k += 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4 *>(src + k));
+                x[k] = f.x;
+                x[k + 1] = f.y;
+                x[k + 2] = f.z;
+                x[k + 3] = f.w;
+            }
+        }
+    };
+    auto ml_of = [&](int i) {
+        return i < n ? __ldcg(reinterpret_cast<const float2 *>(ws_ml) + at(i)) : make_float2(-INFINITY, 0.f);
+    };
+    float2 ml = ml_of(lane);
+    float x[AHEAD][V];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < n) load(i, x[i]);
+    float m = ml.x;
+    for (int i = 32 + lane; i < n; i += 32) m = fmaxf(m, ml_of(i).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float o[V], l = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        if (i0 > 0) ml = ml_of(i0 + lane);
+        const float w = ml.y > 0.f ? fast_exp2(ml.x - m) : 0.f;
+        l += w * ml.y;
+        // (a piece that held none of the row's keys weighs nothing, and may hold anything)
+        if (i0 == 0) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                if (i < n && wi != 0.f) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) o[k] = fmaf(wi, x[i][k], o[k]);
+                }
+            }
+        }
+        const int e = min(32, n - i0);
+        for (int i = i0 == 0 ? AHEAD : 0; i < e; i += 4) {
+            float y[4][V];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i + q < e) load(i0 + i + q, y[q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float wi = __shfl_sync(0xffffffffu, w, min(i + q, 31));
+                if (i + q < e && wi != 0.f) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) o[k] = fmaf(wi, y[q][k], o[k]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    store_row<V>(out + lane * V, o, 1.f / l);  // (every row attends something)
+}
+
 // Block (c, y): rows of the unit that CTA c leaves unfinished, a warp each.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
-    constexpr int V = D / 32;  // values of a lane
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
     const int4 u = __ldcg(p.split + c);
     const int rows = u.w > 0 ? u.y * p.hpg : 0;
     for (int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < rows;
          r += gridDim.y * (kMergeThreads / 32)) {
         const int t = r / p.hpg, h = r - t * p.hpg;
         const int row = t / p.tpt * kRows + t % p.tpt * p.hpg + h;
-        auto at = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.slot_rows + row; };
-        float m = -INFINITY;
-        for (int i = lane; i < u.w; i += 32) m = fmaxf(m, __ldcg(p.ws_ml + at(i) * 2));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float o[V], l = 0.f;
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = 0.f;
-        for (int i0 = 0; i0 < u.w; i0 += 32) {
-            float w = 0.f;
-            if (i0 + lane < u.w) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + at(i0 + lane));
-                if (ml.y > 0.f) w = fast_exp2(ml.x - m);
-                l += w * ml.y;
-            }
-            const int n = min(32, u.w - i0);
-            for (int i = 0; i < n; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                if (wi == 0.f) continue;  // (a piece that held none of the row's keys may hold anything)
-                const float *src = p.ws_o + at(i0 + i) * D + lane * V;
-                float x[V];
-                if constexpr (V == 2) {
-                    *reinterpret_cast<float2 *>(x) = __ldcg(reinterpret_cast<const float2 *>(src));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < V; k += 4)
-                        *reinterpret_cast<float4 *>(x + k) = __ldcg(reinterpret_cast<const float4 *>(src + k));
-                }
-#pragma unroll
-                for (int k = 0; k < V; ++k) o[k] = fmaf(wi, x[k], o[k]);
-            }
-        }
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-        const float inv = 1.f / l;  // (every row attends something)
-        uint32_t w[V / 2];
-#pragma unroll
-        for (int k = 0; k < V / 2; ++k) w[k] = bf16x2_of(o[2 * k] * inv, o[2 * k + 1] * inv);
-        uint16_t *dst = p.out + ((size_t)(u.x + t) * p.Hq + u.z + h) * D + lane * V;
-        if constexpr (V == 2)
-            *reinterpret_cast<uint32_t *>(dst) = w[0];
-        else if constexpr (V == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        join_row<D, 3>(p.ws_o, p.ws_ml,
+                       [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.slot_rows + row; }, u.w,
+                       p.out + ((size_t)(u.x + t) * p.Hq + u.z + h) * D);
     }
 }
 
@@ -163,6 +196,13 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     p.passes = p.G / p.hpg;
     p.rows = p.hpg * p.tpt;
     p.q_bytes = p.rows * D * 2;
+    p.tpu_lg = 0;
+    while (1 << p.tpu_lg < (D == 256 ? 1 : 2) * p.tpt) ++p.tpu_lg;
+    int few = 0;  // tokens whose rows fit a quarter of the tile, where a request has no more on average
+    if (p.hpg <= 32 && (long long)N * p.hpg <= 32LL * B)
+        for (few = 1; 2 * few * p.hpg <= 32;) few *= 2;
+    p.few_tok = few;
+    p.few_bytes = few * p.hpg * D * 2;
     p.window = window < lmax ? window : lmax;
     const float sl = (float)(std::fabs((double)scale) * 1.4426950408889634);
     p.sl = std::isfinite(sl) ? std::fmax(sl, FLT_MIN) : FLT_MAX;  // (masked scores stay -inf at scale 0)
@@ -171,20 +211,26 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     p.kv_lens = kv_lens;
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
-    p.box = block_size < 128 ? block_size : 128;
+    p.box_lg = p.lg < 7 ? p.lg : 7;
+    p.box = 1 << p.box_lg;
     p.causal = causal;
-    p.cost_piece = 1;
-    p.min_tiles = 2;
+    // A unit's start and end (its copies' latency, the output's read-out, a join) in
+    // key tiles, as measured: 64 requests of 16 heads of 64 over up to 2048 states 91
+    // us with 2, 75 with 5, 78 with 10; 8192 tokens of 64 heads over 8 of 128 794 with
+    // 2, 837 with 1, of 16 over 1 of 256 432 with 3, 536 with 1.
+    p.cost_piece = p.few_tok ? (D == 64 ? 5 : 2) : D == 256 ? 3 : 2;
+    p.min_tiles = 1 + p.cost_piece;
 
-    CUtensorMap tmq, tmk, tmv;
+    CUtensorMap tmq, tmq4, tmk, tmv;
     const long long heads = (long long)num_blocks * Hkv;
     if ((rc = encode_rows_map(&tmq, q, D, Hq, N, q_stride, p.hpg, p.tpt)) ||
+        (rc = encode_rows_map(&tmq4, q, D, Hq, N, q_stride, few ? p.hpg : 1, few ? few : 1)) ||
         (rc = encode_pool(&tmk, k_pool, D, block_size, heads, p.box)) ||
         (rc = encode_pool(&tmv, v_pool, D, block_size, heads, p.box)))
         return rc;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int slot_rows = (D == 256 ? 1 : 2) * kRows;
-    const size_t rows = (size_t)2 * ctas * slot_rows;
+    const size_t rows = (size_t)2 * ctas * slot_rows;  // two pieces a CTA
     void *ws = nullptr;
     if ((rc = api_call_workspace(stream, rows * (D + 2) * sizeof(float) + (size_t)ctas * sizeof(int4), &ws)))
         return rc;
@@ -198,15 +244,18 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     cudaError_t e;
     switch (D) {
         case 64:
-            e = launch_pf<64, true>(tmq, tmk, tmv, p, ctas, stream);
+            e = p.few_tok ? launch_extend_few(D, tmq, tmk, tmv, &p, ctas, stream, tmq4)
+                          : launch_pf<64, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
             if (e == cudaSuccess) e = launch_merge<64>(m, ctas, parts, stream);
             break;
         case 128:
-            e = launch_pf<128, true>(tmq, tmk, tmv, p, ctas, stream);
+            e = p.few_tok ? launch_extend_few(D, tmq, tmk, tmv, &p, ctas, stream, tmq4)
+                          : launch_pf<128, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
             if (e == cudaSuccess) e = launch_merge<128>(m, ctas, parts, stream);
             break;
         default:
-            e = launch_pf<256, true>(tmq, tmk, tmv, p, ctas, stream);
+            e = p.few_tok ? launch_extend_few(D, tmq, tmk, tmv, &p, ctas, stream, tmq4)
+                          : launch_pf<256, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
             if (e == cudaSuccess) e = launch_merge<256>(m, ctas, parts, stream);
             break;
     }

@@ -133,6 +133,11 @@ cudaError_t launch_kv_append_fp8(void *k_codes, void *v_codes, float *k_scale, f
                                  int B, int Hkv, int D, int Lmax, unsigned int *err,
                                  cudaStream_t stream);
 
+// The paged prompt attention with units of few rows (extend_few.cu); params: its
+// PagedPrefillParams.
+cudaError_t launch_extend_few(int D, const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                              const void *params, int num_ctas, cudaStream_t stream, const CUtensorMap &tmq4);
+
 // Shared with the allocation-free entry point (defined in api.cu).
 int api_fail(int status, const char *msg);
 int api_check_args(const void *q, const void *k_cache, const void *v_cache,

@@ -54,9 +54,9 @@ extern "C" int gqa_prefill_attn(const void *q, const void *k, const void *v,
     const int ctas = (int)(most < num_sms ? most : num_sms);
     cudaError_t e;
     switch (D) {
-        case 64: e = launch_pf<64, false>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
-        case 128: e = launch_pf<128, false>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
-        default: e = launch_pf<256, false>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
+        case 64: e = launch_pf<64, false, false>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
+        case 128: e = launch_pf<128, false, false>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
+        default: e = launch_pf<256, false, false>(tmq, tmk, tmv, p, ctas, reinterpret_cast<cudaStream_t>(stream)); break;
     }
     if (e != cudaSuccess) return api_cuda_fail(e, "prefill kernel launch");
     return KVATTN_OK;

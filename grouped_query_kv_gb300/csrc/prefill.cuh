@@ -96,9 +96,14 @@ struct PagedPrefillParams : PrefillParams {
     float *ws_ml;            // [2 * CTAs, rows of a unit, 2] partial (m in log2 units, l)
     int4 *split;             // [CTAs] split units, see MergeParams
     int lg, max_blocks, num_blocks;
-    int box;                 // rows of a copy: min(block size, 128)
+    int box, box_lg;         // rows of a copy, min(block size, 128), and their log2
     int rows;                // query rows of a tile, hpg * tpt
     int q_bytes;             // bytes of a query tile's copy
+    // A unit of at most few_tok tokens (32 query rows) has them four times in
+    // its tile, 32 lanes each, and every warp of the softmax takes a quarter of a
+    // key tile's columns for its copy: four partial results that are joined.
+    int few_tok, few_bytes;  // (0: hpg > 32)
+    int tpu_lg;              // log2 of a unit's tokens
     int causal;              // token t sees up to itself; else the whole pool rows
     int cost_piece;          // key tiles that starting and ending a unit costs
     int min_tiles;           // cost of a CTA's range at least
@@ -120,9 +125,13 @@ struct PagedUnit : Unit {
     int shift;   // cached positions before token 0 (causal), or all of them
     int kend;    // end of the piece's keys
     int slot;    // workspace slot of its partial result; -1: it is a whole unit
+    int few;     // its rows are in the tile four times
 };
 template <bool PG>
 using ParamsOf = std::conditional_t<PG, PagedPrefillParams, PrefillParams>;
+struct NoMap {};
+template <bool PG>
+using QuarterMap = std::conditional_t<PG, CUtensorMap, NoMap>;  // of q, a few_tok box
 template <bool PG>
 using UnitOf = std::conditional_t<PG, PagedUnit, Unit>;
 
@@ -137,6 +146,23 @@ struct Ring {
     __device__ __forceinline__ void next() {
         if (++slot == OFF + N) {
             slot = OFF;
+            parity ^= 1;
+        }
+    }
+};
+
+// The places of one of two copy warps that fill a ring of N slots from slot OFF
+// in turns (STEP 2), or of one that fills it alone.
+template <int N_, int OFF_, int STEP_>
+struct CopyRing {
+    static constexpr int N = N_, OFF = OFF_, STEP = STEP_;
+    int slot, pos;  // pos: place counted on
+    uint32_t parity = 0;
+    __device__ __forceinline__ explicit CopyRing(int start) : slot(OFF_ + start), pos(start) {}
+    __device__ __forceinline__ void next() {
+        pos += STEP;
+        if ((slot += STEP) >= OFF + N) {
+            slot -= N;
             parity ^= 1;
         }
     }
@@ -161,7 +187,7 @@ struct PfCfg {
     static constexpr int off_q = 0;
     static constexpr int off_ring = NQ * QT;
     static constexpr int off_bar = off_ring + NS * SLOT;
-    static constexpr int nbar = 2 * NS + 2 * 2 + 3 * 2 + 2 * kDesc + 1 + 2;
+    static constexpr int nbar = 2 * NS + 2 * 2 + 3 * 2 + 2 * kDesc + 1 + 2 + (PG ? 2 : 0);
     static constexpr int off_misc = off_bar + nbar * 8;          // tmem base, abort flag
     static constexpr int off_unit = (off_misc + 32 + 15) / 16 * 16;
     static constexpr int off_cnt = off_unit + kDesc * (int)sizeof(UnitOf<PG>);
@@ -176,6 +202,10 @@ struct PfCfg {
     static constexpr int KN = NQ == 2 ? NS : NS - CPT, VN = NQ == 2 ? NS : CPT;
     using KRing = Ring<KN, 0>;
     using VRing = Ring<VN, NQ == 2 ? 0 : KN>;
+    // Over a pool, where a slot's boxes are a lane's each (a copy warp each for K and
+    // V at D = 64 and 128: 8192 tokens of 64 heads over 8 of 128 950 us for 800).
+    using KCopies = CopyRing<KN, 0, 1>;
+    using VCopies = CopyRing<VN, NQ == 2 ? 0 : KN, 1>;
     static_assert(NS > 2 * CPT && NS >= 4, "the ring holds more than one K and one V tile");
     static_assert(alloc <= kSmemMax, "shared memory");
     // TMEM: S0, S1 (128 columns each; P over the first 64), then O per tile
@@ -267,6 +297,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ float max_of(const float (&x)[32]) {
+    float mx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx[i] = max3(x[i], x[4 + i], x[8 + i]);
+#pragma unroll
+    for (int c = 12; c < 28; c += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], x[c + i], x[c + 4 + i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[28 + i]);
+    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
 // 32 bytes, a whole sector, from one thread (dst 32-byte aligned).
 __device__ __forceinline__ void st_global_32b(void *dst, const uint32_t *w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
@@ -283,6 +327,20 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// (by a warp) a row of 32 V values times f, V consecutive ones of each lane from dst on.
+template <int V>
+__device__ __forceinline__ void store_row(uint16_t *dst, const float *o, float f) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) w[k] = bf16x2_of(o[2 * k] * f, o[2 * k + 1] * f);
+    if constexpr (V == 2)
+        *reinterpret_cast<uint32_t *>(dst) = w[0];
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A published unit, the same in every lane.
 template <class U>
 __device__ __forceinline__ U read_unit(const U &from) {
@@ -296,6 +354,8 @@ __device__ __forceinline__ U read_unit(const U &from) {
 
 __device__ __forceinline__ bool ends_list(const Unit &u) { return u.n[0] == 0; }
 __device__ __forceinline__ bool ends_list(const PagedUnit &u) { return u.n[0] < 0; }
+__device__ __forceinline__ bool few_of(const Unit &) { return false; }
+__device__ __forceinline__ bool few_of(const PagedUnit &u) { return u.few; }
 
 // First of the unit's key tiles that query tile s attends: its window may start
 // behind whole tiles that the first query tile needs (one of ten in a window of
@@ -372,28 +432,29 @@ __device__ __forceinline__ bool load_seq(const PagedPrefillParams &p, int b, Uni
 }
 
 // Rows that attend nothing, dealt out by sequence.
-__device__ __forceinline__ void zero_rows(const PagedPrefillParams &p, int D, int threads) {
+__device__ __forceinline__ void zero_rows(const PagedPrefillParams &p, int D, int thread, int threads) {
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         UnitSeq s;
         int row0, none;
         load_seq(p, b, &s, &row0, &none);
         uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)(row0 - none) * p.Hq * D);
         const size_t n = none > 0 ? (size_t)none * p.Hq * D / 8 : 0;
-        for (size_t i = threadIdx.x; i < n; i += threads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (size_t i = thread; i < n; i += threads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
 // (by all threads) this CTA's range: prefix sums of the sequences' costs, as many
-// consecutive ones to a thread as it takes, then a walk of the thread that has it.
-__device__ __forceinline__ PagedRange find_range(const PagedPrefillParams &p, int tpu, int heads, long long *sm,
-                                                 int threads) {
+// consecutive ones to a thread as it takes; the thread that has the range's start
+// leaves its sequence in shared memory.
+__device__ __forceinline__ PagedRange find_range(const PagedPrefillParams &p, int heads, long long *sm, int threads) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *found = reinterpret_cast<int *>(sm + 33);
     const int per = (p.B + threads - 1) / threads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     PagedRange r = {};
     r.seq.causal = p.causal;
     r.seq.window = p.window;
-    r.seq.tpu = tpu;
+    r.seq.tpu_lg = p.tpu_lg;
     r.seq.piece = p.cost_piece;
     auto cost_of = [&](int b) {
         int none;
@@ -415,32 +476,37 @@ __device__ __forceinline__ PagedRange find_range(const PagedPrefillParams &p, in
         if (w < warp) before += sm[w];
         r.total += sm[w];
     }
-    const long long most = r.total / p.min_tiles;
+    const long long most = r.total < 1LL << 31 ? (long long)((unsigned)r.total / (unsigned)p.min_tiles)
+                                               : r.total / p.min_tiles;
     r.ranges = most < 1 ? 1 : most < gridDim.x ? (int)most : (int)gridDim.x;
     if ((int)blockIdx.x < r.ranges && r.total > 0) {
         r.x0 = range_start(r.total, r.ranges, blockIdx.x);
         r.x1 = range_start(r.total, r.ranges, blockIdx.x + 1);
         if (before <= r.x0 && r.x0 < before + mine) {
-            for (int b = b0; b < b1; ++b) {
-                const long long c = cost_of(b);
-                if (r.x0 < before + c) {
-                    sm[32] = b;
-                    sm[33] = before;
-                    break;
+            int b = b0;
+            if (per > 1)
+                for (;; ++b) {
+                    const long long c = cost_of(b);
+                    if (r.x0 < before + c) break;
+                    before += c;
                 }
-                before += c;
-            }
+            sm[32] = before;
+            found[0] = b;
+            found[1] = r.row0;
+            found[2] = r.seq.len;
+            found[3] = r.seq.shift;
         }
     }
     __syncthreads();
     if (r.x0 < r.x1 && warp == 3) {
-        int none;
-        r.b = (int)sm[32];
-        load_seq(p, r.b, &r.seq, &r.row0, &none);
-        const long long off = r.x0 - sm[33], each = blocks_cost(r.seq, seq_blocks(r.seq));
-        r.hh = (int)(off / each);
+        r.b = found[0];
+        r.row0 = found[1];
+        r.seq.len = found[2];
+        r.seq.shift = found[3];
+        const long long off = r.x0 - sm[32], each = blocks_cost(r.seq, seq_blocks(r.seq));
+        r.hh = off < 1LL << 31 && each < 1LL << 31 ? (int)((unsigned)off / (unsigned)each) : (int)(off / each);
         r.blk = block_at_cost(r.seq, off - r.hh * each);
-        r.u0 = sm[33] + r.hh * each + blocks_cost(r.seq, r.blk);
+        r.u0 = sm[32] + r.hh * each + blocks_cost(r.seq, r.blk);
     }
     return r;
 }
@@ -489,6 +555,7 @@ __device__ __forceinline__ void next_piece(const PagedPrefillParams &p, PagedRan
             u->b = r.b;
             u->shift = r.seq.shift;
             const int stop = min(u->t0 + tpu, u->len);
+            u->few = stop - u->t0 <= p.few_tok;  // (both query tiles have the same rows then)
             u->kend = min((first + tb) * kRows, key_end(p, u->shift, stop - 1));
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -498,6 +565,7 @@ __device__ __forceinline__ void next_piece(const PagedPrefillParams &p, PagedRan
                     if (first_tile(p, *u, s) < n) u->n[s] = n;
                 }
             }
+            if (u->few && p.tpt < tpu) u->n[1] = u->n[0];
             u->slot = -1;
             if (ta > 0) {
                 u->slot = 2 * blockIdx.x;
@@ -513,10 +581,14 @@ __device__ __forceinline__ void next_piece(const PagedPrefillParams &p, PagedRan
     }
 }
 
-template <int D, bool PG>
+// PG: over a paged pool; FEW: with units of few rows (by their own loop over key
+// tiles, beside which the other spills registers: 8192 tokens of 64 heads over 8 of
+// 128 812 us without it, 894 with).
+template <int D, bool PG, bool FEW>
 __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                   const __grid_constant__ CUtensorMap tmv, const ParamsOf<PG> p) {
+                   const __grid_constant__ CUtensorMap tmv, const ParamsOf<PG> p,
+                   const __grid_constant__ QuarterMap<PG> tmq4) {
     using C = PfCfg<D, PG>;
     using Unit = UnitOf<PG>;
     constexpr int NQ = C::NQ, NS = C::NS, CPT = C::CPT;
@@ -533,6 +605,8 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2;
     uint64_t *u_full = pv_done + 2, *u_empty = u_full + kDesc, *drain = u_empty + kDesc;
     uint64_t *turn = drain + 1;  // the MMA warps' turns
+    // (few rows) the softmax warps' steps of a join, and its end
+    [[maybe_unused]] uint64_t *join = turn + 2, *joined = join + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::off_misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::off_misc + 16);
     Unit *units = reinterpret_cast<Unit *>(smem + C::off_unit);
@@ -563,6 +637,10 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             mbar_init(&u_empty[s], (NQ == 2 ? 3 : 4) + 4 * NQ);
         }
         mbar_init(drain, 2);  // warps 1 and 2
+        if (PG) {
+            mbar_init(join, 4 * NQ);
+            mbar_init(joined, 1);
+        }
         *abort_flag = 0;
         *sum_pairs = 0;
         *max_nb = 0;
@@ -587,8 +665,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     int width = 0, nbk = 0;
     PagedRange range;  // (paged: this CTA's range of the call's cost, and where it starts)
     if constexpr (PG) {
-        range = find_range(p, tpu, heads, reinterpret_cast<long long *>(cnt), C::THREADS);
-        zero_rows(p, D, C::THREADS);
+        range = find_range(p, heads, reinterpret_cast<long long *>(cnt), C::THREADS);
     } else {
     {
         unsigned long long s = 0;
@@ -659,15 +736,20 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         return true;
     };
     // (paged) the same: the boxes of the blocks that hold the unit's rows of the
-    // tile at position kb, a lane each; z: the lane's block and K/V head in the pool
-    [[maybe_unused]] auto issue_paged = [&](const void *tm, int c, int z, const Unit &u, int kb, auto &r) -> bool {
+    // tile at position kb, a lane each, whose block is blk (one that is none reads
+    // as zeros: a place past the pool)
+    [[maybe_unused]] auto issue_paged = [&](const void *tm, int c, int blk, const Unit &u, int kb, auto &r) -> bool {
         if constexpr (PG) {
             const int slot = r.slot;
-            const int b0 = max(0, first_key(p, u) - kb) / p.box, b1 = (min(kRows, u.kend - kb) + p.box - 1) / p.box;
-            if (fills >= r.N && !mbar_wait_warp(&slot_empty[slot], r.parity ^ 1, abort_flag)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], (b1 - b0) * p.box * 2 * C::KC);
+            const int b0 = max(0, first_key(p, u) - kb) >> p.box_lg;
+            const int b1 = (min(kRows, u.kend - kb) + p.box - 1) >> p.box_lg;
+            if (r.pos >= r.N && !mbar_wait_warp(&slot_empty[slot], r.parity ^ 1, abort_flag)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], ((b1 - b0) << p.box_lg) * 2 * C::KC);
             __syncwarp();
             if (lane >= b0 && lane < b1) {
+                const bool bad = blk < 0 || blk >= p.num_blocks;
+                if (bad) pf_error(p.err, DEV_ERR_BOUNDS);
+                const int z = bad ? p.num_blocks * p.Hkv : blk * p.Hkv + u.kvh;
 #pragma unroll
                 for (int sl = 0; sl < C::KC / 64; ++sl)
                     tma_load_3d_plain(ring + slot * C::SLOT + sl * kSlab + lane * p.box * 128, tm, &slot_full[slot],
@@ -679,20 +761,38 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         }
         return true;
     };
-    // (paged) the lane's block of the tile at position kb of a unit, times the K/V
-    // heads; past the pool (which reads as zeros) where the table names none
-    [[maybe_unused]] auto block_at = [&](const Unit &u, int kb) -> int {
-        int z = 0;
+    // (paged) The blocks of a unit's tiles, 32 table entries at a time and 32 ahead,
+    // so that a copy warp does not wait for memory at each tile.
+    struct Blocks {
+        int now, then;  // entry first + lane of the unit's row, and first + 32 + lane
+        int first;
+    };
+    [[maybe_unused]] auto entry = [&](const Unit &u, int e) -> int {
+        if constexpr (PG) return e <= (u.kend - 1) >> p.lg ? p.table[(size_t)u.b * p.max_blocks + e] : 0;
+        return 0;
+    };
+    [[maybe_unused]] auto blocks_of = [&](const Unit &u) -> Blocks {
+        Blocks x = {};
         if constexpr (PG) {
-            const int at = kb + lane * p.box;
-            if (at < u.kend && at + p.box > first_key(p, u) && lane < kRows / p.box) {
-                const int blk = p.table[(size_t)u.b * p.max_blocks + (at >> p.lg)];
-                const bool bad = blk < 0 || blk >= p.num_blocks;
-                if (bad) pf_error(p.err, DEV_ERR_BOUNDS);
-                z = bad ? p.num_blocks * p.Hkv : blk * p.Hkv + u.kvh;
-            }
+            x.first = u.kbeg >> p.lg;
+            x.now = entry(u, x.first + lane);
+            x.then = entry(u, x.first + 32 + lane);
         }
-        return z;
+        return x;
+    };
+    // the lane's block of the tile at position kb (a tile's are in one group of 32)
+    [[maybe_unused]] auto block_at = [&](const Unit &u, Blocks &x, int kb) -> int {
+        if constexpr (PG) {
+            int e = (kb >> p.lg) - x.first;
+            if (e >= 32) {
+                x.first += 32;
+                e -= 32;
+                x.now = x.then;
+                x.then = entry(u, x.first + 32 + lane);
+            }
+            return __shfl_sync(0xffffffffu, x.now, (e + lane) & 31);
+        }
+        return 0;
     };
     // (by one lane) the last fills of a ring of n slots from slot `off` have landed
     auto landed = [&](int n, int off) {
@@ -700,7 +800,13 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         for (int i = fills > n ? fills - n : 0; i < fills; ++i)
             pf_wait(&slot_full[off + i % n], (uint32_t)((i / n) & 1), &never);
     };
-    // A walk over the key tiles of all units (one query tile).
+    // (paged, by one lane) the last fills of r's warp have landed
+    [[maybe_unused]] auto landed_paged = [&](const auto &r) {
+        volatile int never = 0;
+        for (int pos = r.pos - r.STEP, i = 0; pos >= 0 && i < (r.N + r.STEP - 1) / r.STEP; pos -= r.STEP, ++i)
+            pf_wait(&slot_full[r.OFF + pos % r.N], (uint32_t)((pos / r.N) & 1), &never);
+    };
+    // A walk over the key tiles of all units (where a copy warp has K or V alone).
     struct Walk {
         Unit u;
         int k = -1, g = -1;  // unit, key tile of the CTA
@@ -709,7 +815,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     };
     auto step = [&](Walk &w) -> bool {
         ++w.g;
-        if (w.k >= 0 && ++w.j < w.u.n[0]) return true;
+        if (w.k >= 0 && ++w.j < (PG && NQ == 2 ? max(w.u.n[0], w.u.n[1]) : w.u.n[0])) return true;
         w.j = 0;
         if (!next_unit(++w.k, &w.u)) return false;
         w.done = ends_list(w.u);
@@ -807,6 +913,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             *done = true;
             return true;
         };
+        [[maybe_unused]] typename C::VCopies vcopies(0);
         Unit u = {};
         int k = 0;
         bool more = true, done;  // the last unit published does not end the list
@@ -823,20 +930,27 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         };
         if (NQ == 2) {
             while (ok && more) ok = pump(true);
-        } else {
+        } else if constexpr (PG) {
             // this warp copies V, too, and publishes units as their places come free
+            Walk w;
+            ok = pump(true) && pump(true) && pump(true) && step(w);
+            Blocks x = {};
+            while (ok && !w.done) {
+                if (w.j == 0) x = blocks_of(w.u);
+                const int kb = w.u.kbeg + w.j * kRows, blk = block_at(w.u, x, kb);
+                const bool last = w.j + 1 == max(w.u.n[0], w.u.n[1]);
+                for (int c = 0; c < CPT && ok; ++c) ok = issue_paged(&tmv, c, blk, w.u, kb, vcopies);
+                if (ok) ok = pump(last && w.k + 1 >= k);
+                if (ok) ok = step(w);
+            }
+        } else {
+            // (the same over packed rows)
             typename C::VRing rc;
             Walk w;
             ok = pump(true) && pump(true) && pump(true) && step(w);
             while (ok && !w.done) {
-                if constexpr (PG) {
-                    const int kb = w.u.kbeg + w.j * kRows, z = block_at(w.u, kb);
-                    for (int c = 0; c < CPT && ok; ++c)
-                        ok = issue_paged(&tmv, c, z, w.u, kb, rc);
-                } else {
-                    for (int c = 0; c < CPT && ok; ++c)
-                        ok = issue(&tmv, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows, rc);
-                }
+                for (int c = 0; c < CPT && ok; ++c)
+                    ok = issue(&tmv, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows, rc);
                 if (ok) ok = pump(w.j + 1 == w.u.n[0] && w.k + 1 >= k);
                 if (ok) ok = step(w);
             }
@@ -850,7 +964,11 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         }
         __syncwarp();
         named_bar_sync(kBarEndPf, C::THREADS);
-        if (NQ == 1 && *abort_flag && lane == 0) landed(C::VN, C::KN);
+        if constexpr (PG) {
+            if (NQ == 1 && *abort_flag && lane == 0) landed_paged(vcopies);
+        } else {
+            if (NQ == 1 && *abort_flag && lane == 0) landed(C::VN, C::KN);
+        }
         return;
     }
 
@@ -859,62 +977,82 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         bool ok = true;
         uint32_t qn[2] = {0, 0};     // query tiles issued
         typename C::KRing rc;
+        [[maybe_unused]] uint32_t joins = 0, seen = 0;  // units of few rows so far, joins waited for
+        [[maybe_unused]] auto joins_seen = [&](uint32_t n) -> bool {
+            for (; seen < n; ++seen)
+                if (!mbar_wait_warp(joined, seen & 1, abort_flag)) return false;
+            return true;
+        };
         auto load_q = [&](const Unit &u) -> bool {
+            if constexpr (FEW && NQ == 2) {
+                // Units of few rows are joined in query tile 1's place: the last one's
+                // join is over before another's rows go there (and seen to be, one
+                // behind, so that every phase of the barrier is waited for in turn).
+                if (joins > (u.few ? 1 : 0) && !joins_seen(u.few ? joins - 1 : joins)) return false;
+                if (u.few) ++joins;
+            }
+#pragma unroll(PG ? 2 : 1)
             for (int s = 0; s < NQ; ++s) {
-                if (u.n[s] == 0) continue;
+                if (u.n[s] == 0 || (FEW && s > 0 && few_of(u))) continue;  // (few rows: one tile for both)
                 if (qn[s] && !mbar_wait_warp(&q_empty[s], (qn[s] - 1) & 1, abort_flag)) return false;
                 if (elect_one()) {
-                    if constexpr (PG)
-                        mbar_arrive_expect_tx(&q_full[s], p.q_bytes);
-                    else
-                        mbar_arrive_expect_tx(&q_full[s], C::QT);
+                    bool few = false;
+                    if constexpr (PG) {
+                        few = FEW && u.few;
+                        mbar_arrive_expect_tx(&q_full[s], few ? 4 * p.few_bytes : p.q_bytes);
+                        if (few)
 #pragma unroll
-                    for (int sl = 0; sl < C::SLABS; ++sl)
-                        tma_load_3d_plain(qbuf + s * C::QT + sl * kSlab, &tmq, &q_full[s], sl * 64, u.h0,
-                                          u.row0 + u.t0 + s * p.tpt);
+                            for (int sl = 0; sl < C::SLABS; ++sl)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    tma_load_3d_plain(qbuf + s * C::QT + sl * kSlab + c * (32 * 128), &tmq4,
+                                                      &q_full[s], sl * 64, u.h0, u.row0 + u.t0);
+                    } else {
+                        mbar_arrive_expect_tx(&q_full[s], C::QT);
+                    }
+                    if (!few)
+#pragma unroll
+                        for (int sl = 0; sl < C::SLABS; ++sl)
+                            tma_load_3d_plain(qbuf + s * C::QT + sl * kSlab, &tmq, &q_full[s], sl * 64, u.h0,
+                                              u.row0 + u.t0 + s * p.tpt);
                 }
                 __syncwarp();
                 ++qn[s];
             }
             return true;
         };
-        if (NQ == 2) {
+        [[maybe_unused]] typename C::KCopies kcopies(0);
+        if constexpr (PG) {
+            Walk w;
+            ok = step(w);
+            Blocks x = {};
+            while (ok && !w.done) {
+                if (w.j == 0) x = blocks_of(w.u);
+                const int kb = w.u.kbeg + w.j * kRows, blk = block_at(w.u, x, kb);
+                for (int c = 0; c < CPT && ok; ++c) ok = issue_paged(&tmk, c, blk, w.u, kb, kcopies);
+                if (ok && w.j == 0) ok = load_q(w.u);
+                if (NQ == 2 && ok) ok = issue_paged(&tmv, 0, blk, w.u, kb, kcopies);
+                if (ok) ok = step(w);
+            }
+        } else if (NQ == 2) {
             Unit u;
             for (int k = 0; ok; ++k) {
                 ok = next_unit(k, &u);
                 if (!ok || ends_list(u)) break;
                 const int n = max(u.n[0], u.n[1]);
-                if constexpr (PG) {
-                    // (a tile's blocks are looked up while the tile before waits for its slots)
-                    int next = block_at(u, u.kbeg);
-                    for (int j = 0; j < n && ok; ++j) {
-                        const int kb = u.kbeg + j * kRows, z = next;
-                        if (j + 1 < n) next = block_at(u, kb + kRows);
-                        ok = issue_paged(&tmk, 0, z, u, kb, rc);
-                        if (ok && j == 0) ok = load_q(u);
-                        if (ok) ok = issue_paged(&tmv, 0, z, u, kb, rc);
-                    }
-                } else {
-                    const int kv0 = u.row0 + u.kbeg;
-                    for (int j = 0; j < n && ok; ++j) {
-                        ok = issue(&tmk, 0, u.kvh, kv0 + j * kRows, rc);
-                        if (ok && j == 0) ok = load_q(u);
-                        if (ok) ok = issue(&tmv, 0, u.kvh, kv0 + j * kRows, rc);
-                    }
+                const int kv0 = u.row0 + u.kbeg;
+                for (int j = 0; j < n && ok; ++j) {
+                    ok = issue(&tmk, 0, u.kvh, kv0 + j * kRows, rc);
+                    if (ok && j == 0) ok = load_q(u);
+                    if (ok) ok = issue(&tmv, 0, u.kvh, kv0 + j * kRows, rc);
                 }
             }
         } else {
             Walk w;
             ok = step(w);
             while (ok && !w.done) {
-                if constexpr (PG) {
-                    const int kb = w.u.kbeg + w.j * kRows, z = block_at(w.u, kb);
-                    for (int c = 0; c < CPT && ok; ++c)
-                        ok = issue_paged(&tmk, c, z, w.u, kb, rc);
-                } else {
-                    for (int c = 0; c < CPT && ok; ++c)
-                        ok = issue(&tmk, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows, rc);
-                }
+                for (int c = 0; c < CPT && ok; ++c)
+                    ok = issue(&tmk, c, w.u.kvh, w.u.row0 + w.u.kbeg + w.j * kRows, rc);
                 if (ok && w.j == 0) ok = load_q(w.u);
                 if (ok) ok = step(w);
             }
@@ -928,7 +1066,10 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         named_bar_sync(kBarEndPf, C::THREADS);
         if (*abort_flag && lane == 0) {
             // a role gave up: let the copies in flight land before the CTA exits
-            landed(C::KN, 0);
+            if constexpr (PG)
+                landed_paged(kcopies);
+            else
+                landed(C::KN, 0);
             volatile int never = 0;
             for (int s = 0; s < NQ; ++s)
                 if (qn[s]) pf_wait(&q_full[s], (qn[s] - 1) & 1, &never);
@@ -974,8 +1115,8 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             __syncwarp();
         };
         // O_s (+)= P[buf] V_j from the slots at r
-        auto pv = [&](int buf, typename C::VRing r, int keys, bool first) {
-            const uint32_t a = tmem + buf * 128, d = tmem + C::O0 + s * D;
+        auto pv = [&](int buf, typename C::VRing r, int keys, bool first, int acc = -1) {
+            const uint32_t a = tmem + buf * 128, d = tmem + C::O0 + (acc < 0 ? s : acc) * D;
             if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < CPT; ++c, r.next()) {
@@ -1046,14 +1187,103 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 first_turn = false;
                 return true;
             };
-            for (int k = 0; ok; ++k) {
+            // With units of few rows.  The even key tiles of one go through S and O of
+            // query tile 0 and its softmax warps, the odd ones through those of query
+            // tile 1; warp 1 issues Q K^T of all, warp 2 P V of all, as at D = 256, so
+            // that the chains of copy, Q K^T, softmax, P V of several key tiles overlap
+            // (one chain alone leaves memory idle: 64 requests of 16 heads of 64 over up
+            // to 2048 states 96 us).  Each gives its slots back for both.
+            uint32_t tiles[2] = {0, 0};  // through S buffer 0 and 1 so far
+            bool after_few = false;
+            [[maybe_unused]] auto turn_few = [&](bool visit, bool own, bool first, bool last, int keys) {
+                bool go = true;
+                const auto rv = rc;
+                if (owed) go = slot_ready();
+                const auto rk = rc;
+                if (go && visit) go = slot_ready();
+                if (go && own && first) go = mbar_wait_warp(&q_full[s], units_q++ & 1, abort_flag);
+                if (go && own && after_few && tiles[s] > 0) {
+                    go = mbar_wait_warp(&pv_done[s], (tiles[s] - 1) & 1, abort_flag);
+                    after_few = false;
+                }
+                if (go && (s == 1 || !first_turn)) go = mbar_wait_warp(&turn[s], s == 0 ? it ^ 1 : it, abort_flag);
+                if (go && owed == 1) go = mbar_wait_warp(&p_full[s], (tiles[s] - 1) & 1, abort_flag, wlim);
+                if (!go) return false;
+                tc_fence_after();
+                if (owed == 1)
+                    pv(s, rv, owed_keys, owed_first);
+                else if (owed == 2 && lane == 0)
+                    mbar_arrive(&slot_empty[rv.slot]);
+                owed = 0;
+                if (own) {
+                    qk(s, rk, keys, last);
+                    ++tiles[s];
+                    owed = 1;
+                    owed_keys = keys;
+                    owed_first = first;
+                } else if (visit) {
+                    if (lane == 0) mbar_arrive(&slot_empty[rk.slot]);
+                    owed = 2;
+                }
+                if (lane == 0) mbar_arrive(&turn[s ^ 1]);
+                it ^= 1;
+                first_turn = false;
+                return true;
+            };
+            for (int k = 0; FEW && ok; ++k) {
+                ok = next_unit(k, &u);
+                if (!ok) break;
+                if (owed && (ends_list(u) || few_of(u))) ok = turn_few(false, false, false, false, 0);
+                if (!ok || ends_list(u)) break;
+                const int end = last_key(p, u, few_of(u) ? 0 : s);
+                if (few_of(u)) {
+                    const int n = u.n[0];
+                    if (s == 0) ok = mbar_wait_warp(&q_full[0], units_q++ & 1, abort_flag);
+                    for (int j = 0; j < n && ok; ++j) {
+                        // (what is waited for first has every fill of the slot before its
+                        // present one behind it: its parity means this one)
+                        const int buf = j & 1, keys = min(kRows, end - j * kRows);
+                        const bool before = tiles[buf] > 0;
+                        const uint32_t par = tiles[buf] & 1;
+                        if (s == 1) rc.next();
+                        const auto r = rc;
+                        if (s == 0 && before) ok = mbar_wait_warp(&pv_done[buf], par ^ 1, abort_flag);
+                        if (s == 1) ok = mbar_wait_warp(&p_full[buf], par, abort_flag, wlim);
+                        ok = ok && mbar_wait_warp(&slot_full[r.slot], r.parity, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (s == 0)
+                            qk(buf, r, keys, j == n - 1);
+                        else
+                            pv(buf, r, keys, j < 2, buf);
+                        if (elect_one()) umma_commit(&slot_empty[r.slot]);  // (the other warp's)
+                        __syncwarp();
+                        rc.next();
+                        if (s == 0) rc.next();
+                        ++tiles[buf];
+                    }
+                    after_few = true;
+                } else {
+                    const int n = s == 0 ? u.n[0] : u.n[1], nmax = max(u.n[0], u.n[1]), j0 = first_tile(p, u, s);
+                    for (int j = 0; j < nmax && ok; ++j)
+                        ok = turn_few(true, j0 <= j && j < n, j == j0, j == n - 1, min(kRows, end - j * kRows));
+                    const int other = s == 0 ? u.n[1] : u.n[0];
+                    if (other > 0) tiles[s ^ 1] += other - first_tile(p, u, s ^ 1);
+                }
+            }
+            for (int k = 0; !FEW && ok; ++k) {
                 ok = next_unit(k, &u);
                 if (!ok) break;
                 if (ends_list(u)) {
                     if (owed) ok = turn_of(0, 0, 0, 0, 0);
                     break;
                 }
-                const int n = u.n[s], nmax = max(u.n[0], u.n[1]), j0 = first_tile(p, u, s);
+                const int nmax = max(u.n[0], u.n[1]), j0 = first_tile(p, u, s);
+                int n;
+                if constexpr (PG)
+                    n = s == 0 ? u.n[0] : u.n[1];
+                else
+                    n = u.n[s];
                 const int end = last_key(p, u, s);
                 for (int j = 0; j < nmax && ok; ++j) ok = turn_of(j0, n, nmax, j, end);
             }
@@ -1079,7 +1309,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                     tc_fence_after();
                     const int keys = min(kRows, last_key(p, w.u, 0) - w.j * kRows);
                     if constexpr (std::is_same_v<std::remove_const_t<decltype(r)>, typename C::KRing>) {
-                        qk(buf, r, keys, w.j == w.u.n[0] - 1);
+                        qk(buf, r, keys, w.j == w.u.n[0] - 1 && !(FEW && few_of(w.u)));
                     } else {
                         pv(buf, r, keys, w.j == 0);
                         if (elect_one()) {  // (the lane that issued)
@@ -1129,9 +1359,13 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t o_t = lanes + C::O0 + s * D;
     int r_tok, r_head;
+    constexpr int kNobody = 1 << 20;
+    [[maybe_unused]] int few_tok_of = 0;  // (paged) the token of the lane's row in a copy of few rows
     if constexpr (PG) {  // (any number of heads; rows past the tile's are nobody's)
-        r_tok = row < p.rows ? row / p.hpg : 1 << 20;
+        zero_rows(p, D, tid - 32 * C::SOFT0, 128 * NQ);
+        r_tok = row < p.rows ? row / p.hpg : kNobody;
         r_head = row % p.hpg;
+        if (FEW) few_tok_of = lane < p.few_tok * p.hpg ? lane / p.hpg : kNobody;
     } else {
         r_tok = row >> p.hpg_lg;
         r_head = row & (p.hpg - 1);
@@ -1139,22 +1373,160 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     long long g = 0;      // key tiles so far
     long long base = 0;   // ring slots of the units before this one
     bool ok = true;
+    [[maybe_unused]] uint32_t joins = 0;  // (few rows) steps of joins so far
 
     Unit u;
     for (int k = 0;; ++k) {
         ok = next_unit(k, &u);
         if (!ok || (PG ? u.n[0] < 0 : u.n[0] == 0)) break;  // (ends_list, which takes u's address, spills here)
-        const int n = u.n[s], nmax = max(u.n[0], u.n[1]);
-        const int first_tok = u.t0 + s * p.tpt;
+        const int nmax = max(u.n[0], u.n[1]);
+        int n;
+        if constexpr (PG)
+            n = NQ == 2 && s == 1 ? u.n[1] : u.n[0];  // (an index known when it is compiled keeps u in registers)
+        else
+            n = u.n[s];
+        int first_tok = u.t0 + s * p.tpt;
+        if constexpr (FEW)
+            if (u.few) first_tok = u.t0;  // (both tiles)
         const int end_tok = min(first_tok + p.tpt, u.len);
-        const int tok = first_tok + r_tok;
+        int tok = first_tok + r_tok;
+        if constexpr (PG)
+            if (FEW && u.few) tok = first_tok + few_tok_of;
         const int tq = min(tok, u.len - 1);
         float m = -INFINITY, l = 0.f;
         bool alive = true;  // (paged) some row of the warp is a token's
-        if constexpr (PG) alive = q4 * 32 < (end_tok - first_tok) * p.hpg;
+        [[maybe_unused]] int e_row, e_first, e_last;  // (paged) where the row's keys end, the tile's first and last
+        if constexpr (PG) {
+            alive = (FEW && u.few) || q4 * 32 < (end_tok - first_tok) * p.hpg;
+            e_row = key_end(p, u.shift, tq);
+            e_first = key_end(p, u.shift, first_tok);
+            e_last = key_end(p, u.shift, end_tok - 1);
+        }
 
         const int j0 = first_tile(p, u, s);
-        for (int j = j0; j < n; ++j, ++g) {
+        // the running maximum follows mn where it is far behind; O and l with it
+        auto move_max = [&](float mn, bool more, int buf) -> bool {
+            const bool grow = (mn - m) * p.sl > kTauPf;  // (both -inf: no)
+            if (__any_sync(0xffffffffu, grow)) {
+                const float alpha = (grow && m != -INFINITY) ? fast_exp2((m - mn) * p.sl) : 1.f;
+                if (grow) m = mn;
+                l *= alpha;
+                if (more && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // O holds the tiles up to j - 1
+                    const int pb = NQ == 2 ? s : buf ^ 1;
+                    const uint32_t pp = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
+                    ok = mbar_wait_warp(&pv_done[pb], pp, abort_flag, wlim);
+                    if (!ok) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        tmem_ld16(o_t + c * 16, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                        tmem_st16(o_t + c * 16, o);
+                    }
+                }
+            }
+            return true;
+        };
+        // (few rows) the weights of 32 scores to column `to` of P, and into l
+        [[maybe_unused]] auto weigh = [&](const float (&x)[32], uint32_t to) {
+            const float neg_m = m == -INFINITY ? 0.f : -m * p.sl;
+            const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(neg_m, neg_m);
+            float2 ls[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 y = fma2(make_float2(x[2 * i], x[2 * i + 1]), sl2, nm2);
+                const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                ls[i & 1] = add2(ls[i & 1], e);
+                pk[i] = bf16x2_of(e.x, e.y);
+            }
+            tmem_st16u(to, pk);
+            ls[0] = add2(ls[0], ls[1]);
+            l = ls[0].x + ls[0].y;
+        };
+        auto hide_rows = [&](int j, int buf, int kb, int keys) -> bool {
+            // rows past the sequence's end that the last 16 keys of P V would
+            // read belong to another sequence (or to none) and may hold
+            // anything, which a weight of zero does not hide: they are zeroed
+            const int stop = (keys + 15) / 16 * 16, past = seq_keys(p, u) - kb;
+            // (paged: so are those before the first that a token of the unit attends)
+            int before = 0;
+            if constexpr (PG) before = first_key(p, u) - kb;
+            if (past < stop || (PG && before > 0)) {
+                const long long iv = NQ == 2 ? base + 2 * j + 1 : g * CPT;  // (of the ring that V is in)
+                // (one query tile: the scores may be two tiles ahead of P V, and
+                // the slot's parity says something once the V tile before is done with)
+                if (NQ == 1 && g > 0) ok = mbar_wait_warp(&pv_done[buf ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abort_flag);
+                for (int c = 0; c < CPT && ok; ++c) {
+                    const int slot = (NQ == 2 ? 0 : C::KN) + (int)((iv + c) % C::VN);
+                    ok = mbar_wait_warp(&slot_full[slot], (uint32_t)(((iv + c) / C::VN) & 1), abort_flag);
+                    if constexpr (PG) {
+                        if (ok)
+                            for (int i = row; i < before * (C::KC / 64) * 8; i += 128) {
+                                const int r = (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
+                                *reinterpret_cast<uint4 *>(ring + slot * C::SLOT + sl * kSlab + r * 128 +
+                                                           (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                    }
+                    if (ok)
+                        for (int i = row; i < (stop - past) * (C::KC / 64) * 8; i += 128) {
+                            const int r = past + (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
+                            *reinterpret_cast<uint4 *>(ring + slot * C::SLOT + sl * kSlab + r * 128 +
+                                                       (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                }
+                if (!ok) return false;
+                fence_proxy_async_smem();
+            }
+            return true;
+        };
+        if constexpr (FEW) {
+            for (int j = s; u.few && j < n; j += NQ, ++g) {
+            const int buf = NQ == 2 ? s : (int)(g & 1);
+            const uint32_t par = (uint32_t)((NQ == 2 ? g : g >> 1) & 1);
+            ok = mbar_wait_warp(&s_full[buf], par, abort_flag, wlim);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t s_t = lanes + buf * 128;
+            const int kb = u.kbeg + j * kRows, keys = min(kRows, min(u.kend, e_last) - kb);
+            const int hi = e_row - kb, lo = hi - p.window, sure_hi = e_first - kb, sure_lo = e_last - p.window - kb;
+            // this warp's quarter of the columns, for its copy of the rows; the
+            // other columns of P are zero
+            float x[32];
+            const int c0 = q4 * 32;
+            float mn = m;
+            if (c0 < keys) {
+                tmem_ld32(s_t + c0, x);
+                tmem_ld_wait();
+                if (c0 + 32 > sure_hi || c0 < sure_lo) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = (c0 + i < hi && c0 + i >= lo) ? x[i] : -INFINITY;
+                }
+                mn = fmaxf(mn, max_of(x));
+            }
+            if (!move_max(mn, j > s, buf)) break;
+            {
+                uint32_t none[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) none[i] = 0u;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c != q4 && c * 32 < keys) tmem_st16u(s_t + c * 16, none);
+            }
+            if (c0 < keys) weigh(x, s_t + c0 / 2);
+            if (!hide_rows(j, buf, kb, keys)) break;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[buf]);
+            }
+            if (!ok) break;
+        }
+        for (int j = j0; j < n && !(FEW && few_of(u)); ++j, ++g) {
             const int buf = NQ == 2 ? s : (int)(g & 1);
             const uint32_t par = (uint32_t)((NQ == 2 ? g : g >> 1) & 1);
             ok = mbar_wait_warp(&s_full[buf], par, abort_flag, wlim);
@@ -1165,21 +1537,49 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             // any row attends are left out (the MMAs stop there too), and only
             // parts at the diagonal or the window's edge hide some keys from
             // some rows: a row's are [lo, hi).
-            float v[128];
+            [[maybe_unused]] float v[FEW ? 1 : 128];
             const int kb = u.kbeg + j * kRows;
             int keys, hi, lo, sure_hi, sure_lo;
             if constexpr (PG) {
-                const int e_last = key_end(p, u.shift, end_tok - 1);
                 keys = min(kRows, min(u.kend, e_last) - kb);
-                hi = key_end(p, u.shift, tq) - kb;
+                hi = e_row - kb;
                 lo = hi - p.window;
-                sure_hi = key_end(p, u.shift, first_tok) - kb;
+                sure_hi = e_first - kb;
                 sure_lo = e_last - p.window - kb;
             } else {
                 keys = min(kRows, end_tok - kb);
                 hi = tq + 1 - kb, lo = tq + 1 - p.window - kb;
                 sure_hi = first_tok + 1 - kb, sure_lo = end_tok - p.window - kb;
             }
+            if constexpr (FEW) {
+                // 32 columns at a time, twice: beside the join 128 scores in registers
+                // would spill, and with 227 KB of shared memory what spills goes to L2
+                if (alive) {
+                    auto scores = [&](int c, float (&x)[32]) {
+                        tmem_ld32(s_t + c * 32, x);
+                        tmem_ld_wait();
+                        if (c * 32 + 32 > sure_hi || c * 32 < sure_lo) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                x[i] = (c * 32 + i < hi && c * 32 + i >= lo) ? x[i] : -INFINITY;
+                        }
+                    };
+                    float mn = m;
+#pragma unroll 1
+                    for (int c = 0; c * 32 < keys; ++c) {
+                        float x[32];
+                        scores(c, x);
+                        mn = fmaxf(mn, max_of(x));
+                    }
+                    if (!move_max(mn, j > j0, buf)) break;
+#pragma unroll 1
+                    for (int c = 0; c * 32 < keys; ++c) {  // (P of a part lies over scores of the parts before)
+                        float x[32];
+                        scores(c, x);
+                        weigh(x, s_t + c * 16);
+                    }
+                }
+            } else {
             if (!PG || alive) {
             // (a whole tile that hides nothing takes the straight path)
             const bool whole = keys == kRows && kRows <= sure_hi && sure_lo <= 0;
@@ -1225,29 +1625,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                     }
                 }
             }
-            const bool grow = (mn - m) * p.sl > kTauPf;  // (both -inf: no)
-            if (__any_sync(0xffffffffu, grow)) {
-                const float alpha = (grow && m != -INFINITY) ? fast_exp2((m - mn) * p.sl) : 1.f;
-                if (grow) m = mn;
-                l *= alpha;
-                if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // O holds the tiles up to j - 1
-                    const int pb = NQ == 2 ? s : buf ^ 1;
-                    const uint32_t pp = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
-                    ok = mbar_wait_warp(&pv_done[pb], pp, abort_flag, wlim);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        float o[16];
-                        tmem_ld16(o_t + c * 16, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                        tmem_st16(o_t + c * 16, o);
-                    }
-                }
-            }
+            if (!move_max(mn, j > j0, buf)) break;
             const float neg_m = m == -INFINITY ? 0.f : -m * p.sl;
             const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(neg_m, neg_m);
             float2 ls[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
@@ -1273,45 +1651,148 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             ls[0] = add2(ls[0], ls[1]);
             l = ls[0].x + ls[0].y;
             }
-            // rows past the sequence's end that the last 16 keys of P V would
-            // read belong to another sequence (or to none) and may hold
-            // anything, which a weight of zero does not hide: they are zeroed
-            const int stop = (keys + 15) / 16 * 16, past = seq_keys(p, u) - kb;
-            // (paged: so are those before the first that a token of the unit attends)
-            int before = 0;
-            if constexpr (PG) before = first_key(p, u) - kb;
-            if (past < stop || (PG && before > 0)) {
-                const long long iv = NQ == 2 ? base + 2 * j + 1 : g * CPT;  // (of the ring that V is in)
-                // (one query tile: the scores may be two tiles ahead of P V, and
-                // the slot's parity says something once the V tile before is done with)
-                if (NQ == 1 && g > 0) ok = mbar_wait_warp(&pv_done[buf ^ 1], (uint32_t)(((g - 1) >> 1) & 1), abort_flag);
-                for (int c = 0; c < CPT && ok; ++c) {
-                    const int slot = (NQ == 2 ? 0 : C::KN) + (int)((iv + c) % C::VN);
-                    ok = mbar_wait_warp(&slot_full[slot], (uint32_t)(((iv + c) / C::VN) & 1), abort_flag);
-                    if constexpr (PG) {
-                        if (ok)
-                            for (int i = row; i < before * (C::KC / 64) * 8; i += 128) {
-                                const int r = (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
-                                *reinterpret_cast<uint4 *>(ring + slot * C::SLOT + sl * kSlab + r * 128 +
-                                                           (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                    }
-                    if (ok)
-                        for (int i = row; i < (stop - past) * (C::KC / 64) * 8; i += 128) {
-                            const int r = past + (i >> 3) / (C::KC / 64), sl = (i >> 3) % (C::KC / 64);
-                            *reinterpret_cast<uint4 *>(ring + slot * C::SLOT + sl * kSlab + r * 128 +
-                                                       (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                }
-                if (!ok) break;
-                fence_proxy_async_smem();
             }
+            if (!hide_rows(j, buf, kb, keys)) break;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[buf]);
         }
         if (!ok) break;
+        // (paged) the rows as they are, and what they stand for
+        [[maybe_unused]] auto store_partial = [&](int slot) {
+            if constexpr (PG) {
+                const size_t at = (size_t)slot * (NQ * kRows) + s * kRows + row;
+                float *dst = p.ws_o + at * D;
+                if (tok < end_tok)
+                    *reinterpret_cast<float2 *>(p.ws_ml + at * 2) =
+                        make_float2(m == -INFINITY ? -INFINITY : m * p.sl, l);
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {  // (unrolled, it spills at D = 256)
+                    float o[16];
+                    tmem_ld16(o_t + c * 16, o);
+                    tmem_ld_wait();
+                    if (tok < end_tok) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i]);
+                        st_global_32b(dst + c * 16, w);
+                        st_global_32b(dst + c * 16 + 8, w + 8);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+            }
+        };
+        [[maybe_unused]] auto store_nothing = [&](int slot) {
+            if constexpr (PG)
+                if (tok < end_tok)
+                    *reinterpret_cast<float2 *>(p.ws_ml + ((size_t)slot * (NQ * kRows) + s * kRows + row) * 2) =
+                        make_float2(-INFINITY, 0.f);
+        };
+        if constexpr (FEW) {
+            if (u.few) {
+                // The copies of a row, each with the keys of its columns, are joined in
+                // shared memory (through the workspace it took some 6 us a unit under
+                // load): maxima, then sums and the rows scaled to the joint maximum, a
+                // group of rows at a time, which all warps add up, one row each.
+                constexpr int COPIES = 4 * NQ, GROUP = C::QT / (COPIES * D * 4), V = D / 32;
+                const int copy = s * 4 + q4, rows = (end_tok - first_tok) * p.hpg;
+                float *exch = reinterpret_cast<float *>(cnt);                     // [COPIES][32]
+                float *part = reinterpret_cast<float *>(qbuf + (NQ - 1) * C::QT);  // [COPIES][GROUP][D]
+                auto all_here = [&]() -> bool {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(join);
+                    return mbar_wait_warp(join, joins++ & 1, abort_flag);
+                };
+                const bool own = n > s;
+                if (own) {
+                    const int buf = NQ == 2 ? s : (int)((g - 1) & 1);
+                    ok = mbar_wait_warp(&pv_done[buf], (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1), abort_flag, wlim);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                exch[copy * 32 + lane] = m;
+                if (!(ok = all_here())) break;
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) top = fmaxf(top, exch[c * 32 + lane]);
+                const float w = m == -INFINITY ? 0.f : fast_exp2((m - top) * p.sl);
+                if (!(ok = all_here())) break;
+                exch[copy * 32 + lane] = l * w;
+                for (int r0 = 0; r0 < rows; r0 += GROUP) {
+                    // (16-byte pieces of a row change places by its number: the lanes'
+                    // stores, a row apart, meet different banks)
+                    float *mine = part + (copy * GROUP + lane - r0) * D;
+                    const bool here = lane >= r0 && lane < min(rows, r0 + GROUP);
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        if (own) {
+                            tmem_ld16(o_t + c * 16, o);
+                            tmem_ld_wait();
+                        }
+                        if (here) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int at = ((c * 4 + i) ^ (lane & 7)) * 4;
+                                *reinterpret_cast<float4 *>(mine + at) =
+                                    own ? make_float4(o[4 * i] * w, o[4 * i + 1] * w, o[4 * i + 2] * w, o[4 * i + 3] * w)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                            }
+                        }
+                    }
+                    if (!(ok = all_here())) break;
+                    for (int r = r0 + copy; r < min(rows, r0 + GROUP); r += COPIES) {
+                        float o[V], sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) o[i] = 0.f;
+#pragma unroll
+                        for (int c = 0; c < COPIES; ++c) {
+                            const float *from = part + (c * GROUP + r - r0) * D;
+                            sum += exch[c * 32 + r];
+                            if constexpr (V == 2) {
+                                const float2 x = *reinterpret_cast<const float2 *>(from + ((lane >> 1) ^ (r & 7)) * 4 + (lane & 1) * 2);
+                                o[0] += x.x;
+                                o[1] += x.y;
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < V; i += 4) {
+                                    const float4 x = *reinterpret_cast<const float4 *>(from + ((lane * (V / 4) + i / 4) ^ (r & 7)) * 4);
+                                    o[i] += x.x;
+                                    o[i + 1] += x.y;
+                                    o[i + 2] += x.z;
+                                    o[i + 3] += x.w;
+                                }
+                            }
+                        }
+                        const float of_row = __shfl_sync(0xffffffffu, top, r);
+                        if (u.slot >= 0) {
+                            const size_t at = (size_t)u.slot * (NQ * kRows) + r;
+                            float *dst = p.ws_o + at * D + lane * V;
+                            if constexpr (V == 2)
+                                *reinterpret_cast<float2 *>(dst) = make_float2(o[0], o[1]);
+                            else
+#pragma unroll
+                                for (int i = 0; i < V; i += 4)
+                                    *reinterpret_cast<float4 *>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            if (lane == 0)
+                                *reinterpret_cast<float2 *>(p.ws_ml + at * 2) =
+                                    make_float2(of_row == -INFINITY ? -INFINITY : of_row * p.sl, sum);
+                        } else {
+                            const int t = r / p.hpg;
+                            store_row<V>(p.out + ((size_t)(u.row0 + u.t0 + t) * p.Hq + u.h0 + r - t * p.hpg) * D + lane * V,
+                                         o, 1.f / sum);
+                        }
+                    }
+                    if (!(ok = all_here())) break;
+                }
+                if (!ok) break;
+                if (copy == 0 && lane == 0) mbar_arrive(NQ == 2 ? joined : &q_empty[0]);
+                base += 2 * nmax;
+                continue;
+            }
+        }
         if (n > 0) {
             const int buf = NQ == 2 ? s : (int)((g - 1) & 1);
             const uint32_t par = (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1);
@@ -1319,25 +1800,8 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             if constexpr (PG) {
-                if (u.slot >= 0) {  // a piece: the rows as they are, and what they stand for
-                    const size_t at = (size_t)u.slot * (NQ * kRows) + s * kRows + row;
-                    float *dst = p.ws_o + at * D;
-                    if (tok < end_tok)
-                        *reinterpret_cast<float2 *>(p.ws_ml + at * 2) =
-                            make_float2(m == -INFINITY ? -INFINITY : m * p.sl, l);
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tmem_ld32(o_t + c * 32, o);
-                        tmem_ld_wait();
-                        if (tok < end_tok) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                st_global_32b(dst + c * 32 + i, reinterpret_cast<const uint32_t *>(o + i));
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
+                if (u.slot >= 0) {  // a piece
+                    store_partial(u.slot);
                     base += 2 * nmax;
                     continue;
                 }
@@ -1361,9 +1825,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             __syncwarp();
         } else if constexpr (PG) {
             // (a piece behind this query tile's last key)
-            if (tok < end_tok)
-                *reinterpret_cast<float2 *>(p.ws_ml + ((size_t)u.slot * (NQ * kRows) + s * kRows + row) * 2) =
-                    make_float2(-INFINITY, 0.f);
+            store_nothing(u.slot);
         }
         base += 2 * nmax;
     }
@@ -1375,15 +1837,15 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     named_bar_sync(kBarEndPf, C::THREADS);
 }
 
-template <int D, bool PG>
+template <int D, bool PG, bool FEW>
 cudaError_t launch_pf(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                      const ParamsOf<PG> &p, int num_ctas, cudaStream_t stream) {
+                      const ParamsOf<PG> &p, int num_ctas, cudaStream_t stream, const QuarterMap<PG> &tmq4 = {}) {
     static int done_for_device[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!(dev >= 0 && dev < 64 && done_for_device[dev])) {
-        e = cudaFuncSetAttribute(prefill_kernel<D, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(prefill_kernel<D, PG, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  PfCfg<D, PG>::alloc);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done_for_device[dev] = 1;
@@ -1398,7 +1860,7 @@ cudaError_t launch_pf(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUte
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefill_kernel<D, PG>, tmq, tmk, tmv, p);
+    return cudaLaunchKernelEx(&cfg, prefill_kernel<D, PG, FEW>, tmq, tmk, tmv, p, tmq4);
 }
 
 // 3-D map over packed rows [N, H, D] with `stride` elements from token to

@@ -17,38 +17,38 @@
 
 namespace kvattn {
 
-constexpr int kUnitKeys = 128;  // keys of a tile
+constexpr int kUnitKeys = 128, kUnitLg = 7;  // keys of a tile
 
 // One sequence of a call: token t (of `len`) attends the positions
 // [max(0, e - window), e), e = shift + (causal ? t + 1 : 0).
 struct UnitSeq {
     int len, shift, causal, window;
-    int tpu;    // tokens of a unit, a power of two up to 256
+    int tpu_lg;  // log2 of the tokens of a unit, up to 8
     int piece;  // cost_piece
 };
 
-KVATTN_HD int seq_blocks(const UnitSeq &s) { return (s.len + s.tpu - 1) / s.tpu; }
+KVATTN_HD int seq_blocks(const UnitSeq &s) { return (s.len + (1 << s.tpu_lg) - 1) >> s.tpu_lg; }
 KVATTN_HD int seq_end(const UnitSeq &s, int t) { return s.shift + (s.causal ? t + 1 : 0); }
 
 // First key tile of a block of tokens, and how many there are.
 KVATTN_HD int unit_first(const UnitSeq &s, int blk) {
-    const int lo = seq_end(s, blk * s.tpu) - s.window;
-    return lo > 0 ? lo / kUnitKeys : 0;
+    const int lo = seq_end(s, blk << s.tpu_lg) - s.window;
+    return lo > 0 ? lo >> kUnitLg : 0;
 }
 KVATTN_HD int unit_tiles(const UnitSeq &s, int blk) {
-    const long long past = (long long)(blk + 1) * s.tpu;
+    const long long past = (long long)(blk + 1) << s.tpu_lg;
     const int last = (int)(past < s.len ? past : s.len) - 1;
-    return (seq_end(s, last) + kUnitKeys - 1) / kUnitKeys - unit_first(s, blk);
+    return ((seq_end(s, last) + kUnitKeys - 1) >> kUnitLg) - unit_first(s, blk);
 }
 
-// sum of ceil(y / k), 1 <= y <= x, and of floor(y / k), 0 <= y <= x (x >= -1)
-KVATTN_HD long long sum_ceil(long long x, int k) {
-    const long long q = x / k, r = x % k;
-    return k * (q * (q + 1) / 2) + r * (q + 1);
+// sum of ceil(y / 2^lg), 1 <= y <= x, and of floor(y / 2^lg), 0 <= y <= x (x >= -1)
+KVATTN_HD long long sum_ceil(long long x, int lg) {
+    const long long q = x >> lg, r = x & ((1 << lg) - 1);
+    return ((q * (q + 1) / 2) << lg) + r * (q + 1);
 }
-KVATTN_HD long long sum_floor(long long x, int k) {
-    const long long q = (x + 1) / k, r = (x + 1) % k;
-    return k * (q * (q - 1) / 2) + r * q;
+KVATTN_HD long long sum_floor(long long x, int lg) {
+    const long long q = (x + 1) >> lg, r = (x + 1) & ((1 << lg) - 1);
+    return ((q * (q - 1) / 2) << lg) + r * q;
 }
 
 // Cost of a sequence's first m blocks (of one head group).
@@ -58,20 +58,21 @@ KVATTN_HD long long blocks_cost(const UnitSeq &s, int m) {
     const int f = m < nb ? m : nb - 1;  // full blocks; the last may end early
     long long c = (long long)m * s.piece;
     if (m == nb) c += unit_tiles(s, nb - 1);
-    if (!s.causal) return c + (long long)f * ((s.shift + kUnitKeys - 1) / kUnitKeys - unit_first(s, 0));
+    if (f == 0) return c;
+    if (!s.causal) return c + (long long)f * unit_tiles(s, 0);
     const long long lo = (long long)s.shift + 1 - s.window;  // where block 0's window starts
-    if (s.tpu > kUnitKeys) {                                 // two key tiles a block
-        c += (long long)f * ((s.shift + kUnitKeys - 1) / kUnitKeys) + (long long)f * (f + 1);
-        const long long a = lo >= 0 ? lo / kUnitKeys : -((-lo + kUnitKeys - 1) / kUnitKeys);  // floor
+    if (s.tpu_lg > kUnitLg) {                                // two key tiles a block
+        c += (long long)f * ((s.shift + kUnitKeys - 1) >> kUnitLg) + (long long)f * (f + 1);
+        const long long a = lo >> kUnitLg;                   // (rounded down, below 0 too)
         const long long i0 = a >= 0 ? 0 : (-a + 1) / 2;      // blocks whose window starts at 0
         if (f > i0) c -= (f - i0) * a + (f - i0) * (f + i0 - 1);
-    } else {  // k blocks a key tile
-        const int k = kUnitKeys / s.tpu;
-        const long long up = ((long long)s.shift + s.tpu - 1) / s.tpu;
-        c += sum_ceil(up + f, k) - sum_ceil(up, k);
-        const long long a = lo >= 0 ? lo / s.tpu : -((-lo + s.tpu - 1) / s.tpu);
+    } else {  // 2^lg blocks a key tile
+        const int lg = kUnitLg - s.tpu_lg;
+        const long long up = ((long long)s.shift + (1 << s.tpu_lg) - 1) >> s.tpu_lg;
+        c += sum_ceil(up + f, lg) - sum_ceil(up, lg);
+        const long long a = lo >> s.tpu_lg;
         const long long i0 = a >= 0 ? 0 : -a;
-        if (f > i0) c -= sum_floor(a + f - 1, k) - sum_floor(a + i0 - 1, k);
+        if (f > i0) c -= sum_floor(a + f - 1, lg) - sum_floor(a + i0 - 1, lg);
     }
     return c;
 }
@@ -87,14 +88,25 @@ KVATTN_HD int block_at_cost(const UnitSeq &s, long long r) {
     return lo;
 }
 
-// Range c of C equal ones of a call's cost starts here (no product passes 64 bits).
+// Range c of C equal ones of a call's cost starts here (no product passes 64
+// bits; in 32 where they do, which the device divides in several times faster).
 KVATTN_HD long long range_start(long long total, int C, int c) {
+    if (total < 1LL << 31 && C < 1 << 15) {
+        const unsigned t = (unsigned)total, n = (unsigned)C, i = (unsigned)c;
+        const unsigned q = t / n;
+        return (long long)q * i + (t - q * n) * i / n;
+    }
     return total / C * c + total % C * c / C;
 }
 // The last range that starts at or before e.
 KVATTN_HD int range_of(long long total, int C, long long e) {
-    const long long q = total / C;
-    long long c = q > 0 ? e / q : C - 1;
+    long long c;
+    if (total < 1LL << 31) {
+        const unsigned q = (unsigned)total / (unsigned)C;
+        c = q > 0 ? (unsigned)e / q : C - 1;
+    } else {
+        c = e / (total / C);
+    }
     if (c > C - 1) c = C - 1;
     while (range_start(total, C, (int)c) > e) --c;
     return (int)c;
