@@ -9,13 +9,15 @@
 // rounding to bf16, at the end: norm and rotation in bf16 one after the other
 // would round three times.
 //
-// Layout.  A head's row is D / 8 lanes of 16 bytes; a warp takes 4 x 32 / (D /
-// 8) heads of one token, four loads a lane in flight, so that a lane's cosines,
-// sines and weights (the same for all heads) are loaded once for four rows.
-// Partners of a rotation D / 16 lanes apart meet by a shuffle.  The heads are
-// the token's queries, then its keys, then its values, which are copied.
+// Layout.  A head's row is D / 8 lanes, four values of each half of its rotated
+// dims (or 16 bytes of neighbours) a lane, so that a lane has both partners of its
+// rotations.  A warp takes up to 8 x 32 / (D / 8) heads of one token, with all their
+// loads in flight; a lane's cosines and sines, times the weights, serve all of
+// them.  The heads are the token's queries, then its keys, then its values, which
+// are copied.
 //
-// What bounds it: HBM, every value read once and written once.
+// What bounds it: HBM, every value read once and written once; for a step's tokens
+// the chain of position, table and rows.
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -28,173 +30,185 @@ namespace kvattn {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 4;  // head rows per lane
+constexpr int kRopeRows = 8;  // head rows per lane at most
 
 struct RopeParams {
-    const uint4 *q, *k, *v;
+    const uint2 *q, *k, *v;
     const int32_t *pos;
     const float *cos, *sin;
     const float *qw, *kw;      // [D], or null: no norm
     const long long *slots;    // null: no pool
-    uint4 *q_out, *k_out;      // k_out null: the pool takes the keys
-    uint4 *k_pool, *v_pool;
+    uint2 *q_out, *k_out;      // k_out null: the pool takes the keys
+    uint2 *k_pool, *v_pool;
     unsigned int *err;
-    long long q_stride, k_stride, v_stride, qo_stride, ko_stride;  // vectors from row to row
+    long long q_stride, k_stride, v_stride, qo_stride, ko_stride;  // of four values, from row to row
     long long num_slots;
-    int N, Hq, Hkv, heads;     // heads: of q, k and (with a pool) v together
-    int chunks;                // warps per token
+    int N, Hq, Hkv;
+    int chunks, q_chunks, k_chunks;  // warps per token: of all, of q, of k (and of v)
+    int q_per, k_per;                // head rows of their lanes
     int half;                  // rope_dim / 2
     int max_pos;
     int lg;                    // log2(block_size)
     float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float *x) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint4 pack8(const float *x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ void load4(const float *src, float *x) {
+// Four values in two pairs.
+struct Four {
+    float2 x, y;
+};
+__device__ __forceinline__ Four load4(const float *src) {
     const float4 f = __ldg(reinterpret_cast<const float4 *>(src));
-    x[0] = f.x;
-    x[1] = f.y;
-    x[2] = f.z;
-    x[3] = f.w;
+    return {make_float2(f.x, f.y), make_float2(f.z, f.w)};
+}
+__device__ __forceinline__ Four times(Four a, Four b) { return {mul2(a.x, b.x), mul2(a.y, b.y)}; }
+__device__ __forceinline__ Four times(Four a, float f) {
+    return {mul2(a.x, make_float2(f, f)), mul2(a.y, make_float2(f, f))};
 }
 
 // D head dims; NEXT: neighbours rotate together, else values rope_dim / 2 apart.
 template <int D, bool NEXT>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-    constexpr int LP = D / 8;        // lanes of a head's row
-    constexpr int VPW = 32 / LP;     // head rows of a warp at once
-    constexpr int NC = NEXT ? 4 : 8;  // cosines of a lane
+    constexpr int LP = D / 8;      // lanes of a head's row
+    constexpr int VPW = 32 / LP;   // head rows of a warp at once
+    constexpr int HV = D / 4;      // vectors of four values of a head
     pdl_launch_dependents();
     pdl_wait_prior();
     const int lane = threadIdx.x & 31, l = lane % LP;
-    const unsigned long long w = (unsigned long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-    const long long row = (long long)(w / (unsigned)p.chunks);
+    // a block has one chunk of eight tokens' heads, the next block the next chunk
+    const unsigned group = blockIdx.x / (unsigned)p.chunks;
+    const int chunk = (int)(blockIdx.x - group * (unsigned)p.chunks);
+    const long long row = (long long)group * (kRopeThreads / 32) + (threadIdx.x >> 5);
     if (row >= p.N) return;
-    const int h0 = (int)(w - (unsigned long long)row * (unsigned)p.chunks) * (VPW * kRopeRows) + lane / LP;
-
     const int pos = p.pos[row];
-    uint4 raw[kRopeRows];
+
+    // what the chunk's heads are (the same in the whole block), and which the lane's
+    const int kind = chunk < p.q_chunks ? 0 : chunk < p.q_chunks + p.k_chunks ? 1 : 2;
+    const int nth = chunk - (kind == 0 ? 0 : kind == 1 ? p.q_chunks : p.q_chunks + p.k_chunks);
+    const int per = (kind == 0 ? p.q_per : p.k_per) * VPW;
+    const int h0 = nth * per + lane / LP, h1 = min(nth * per + per, kind == 0 ? p.Hq : p.Hkv);
+    const uint2 *src = (kind == 0 ? p.q + row * p.q_stride : kind == 1 ? p.k + row * p.k_stride : p.v + row * p.v_stride) +
+                       h0 * HV;
+    // the lane's vectors of a head: of the first and the second partners, or of two
+    // that pass through
+    const bool turns = l < p.half / 4;
+    const int va = NEXT ? 2 * l : turns ? l : p.half / 2 + 2 * (l - p.half / 4);
+    const int vb = NEXT || !turns ? va + 1 : l + p.half / 4;
+    uint2 a[kRopeRows], b[kRopeRows];
 #pragma unroll
     for (int u = 0; u < kRopeRows; ++u) {
-        const int h = h0 + u * VPW;
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < p.Hq)
-            raw[u] = __ldcs(p.q + row * p.q_stride + (long long)h * LP + l);
-        else if (h < p.Hq + p.Hkv)
-            raw[u] = __ldcs(p.k + row * p.k_stride + (long long)(h - p.Hq) * LP + l);
-        else if (h < p.heads)
-            raw[u] = __ldcs(p.v + row * p.v_stride + (long long)(h - p.Hq - p.Hkv) * LP + l);
+        a[u] = b[u] = make_uint2(0u, 0u);
+        if (h0 + u * VPW < h1) {
+            if constexpr (NEXT) {
+                const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(src + u * (VPW * HV)) + l);
+                a[u] = make_uint2(x.x, x.y);
+                b[u] = make_uint2(x.z, x.w);
+            } else {
+                a[u] = __ldcs(src + u * (VPW * HV) + va);
+                b[u] = __ldcs(src + u * (VPW * HV) + vb);
+            }
+        }
     }
     const bool there = pos >= 0 && pos < p.max_pos;
-    if (pos >= p.max_pos && h0 == 0 && l == 0) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
-    // where the row's keys and values go in the pool
-    long long to = -1;  // vectors to row 0's head
-    if (p.slots && there) {
-        const long long slot = p.slots[row];
-        if (slot >= p.num_slots) {
-            if (h0 == 0 && l == 0) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
-        } else if (slot >= 0) {
-            to = ((((slot >> p.lg) * p.Hkv) << p.lg) + (slot & ((1 << p.lg) - 1))) * LP;
+    if (pos >= p.max_pos && chunk == 0 && lane == 0) atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
+    // where the rows go: a head's, and the elements from one of the lane's to the next
+    uint2 *dst;
+    long long step = VPW * HV;
+    bool keep = true;
+    if (kind == 0) {
+        dst = p.q_out + row * p.qo_stride + h0 * HV;
+    } else if (!p.slots) {
+        dst = p.k_out + row * p.ko_stride + h0 * HV;
+    } else {
+        const long long slot = there ? p.slots[row] : -1;
+        keep = slot >= 0 && slot < p.num_slots;
+        if (slot >= p.num_slots && kind == 1 && nth == 0 && lane == 0)
+            atomicCAS(p.err, 0u, (unsigned int)DEV_ERR_BOUNDS);
+        dst = (kind == 1 ? p.k_pool : p.v_pool) +
+              ((((keep ? slot >> p.lg : 0) * p.Hkv + h0) << p.lg) + (slot & ((1 << p.lg) - 1))) * HV;
+        step <<= p.lg;
+    }
+    auto put = [&](int u, uint2 f, uint2 g) {
+        if (!keep || h0 + u * VPW >= h1) return;
+        uint2 *to = dst + u * step;
+        if constexpr (NEXT) {
+            *reinterpret_cast<uint4 *>(to + va) = make_uint4(f.x, f.y, g.x, g.y);
+        } else {
+            to[va] = f;
+            to[vb] = g;
         }
+    };
+    if (kind == 2) {
+#pragma unroll
+        for (int u = 0; u < kRopeRows; ++u) put(u, a[u], b[u]);
+        return;
     }
-
-    // the lane's rotation: none, of the first of its pairs, or of the second
-    const int d0 = 8 * l;
-    const bool turns = d0 < 2 * p.half;
-    const bool second = !NEXT && d0 >= p.half;
-    float c[NC], s[NC];
+    if (!there) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) c[i] = 1.f, s[i] = 0.f;
-    if (there && turns) {
-        const int j0 = NEXT ? d0 / 2 : second ? d0 - p.half : d0;
-        const long long at = (long long)pos * p.half + j0;
-#pragma unroll
-        for (int i = 0; i < NC; i += 4) {
-            load4(p.cos + at + i, c + i);
-            load4(p.sin + at + i, s + i);
+        for (int u = 0; u < kRopeRows; ++u) put(u, make_uint2(0u, 0u), make_uint2(0u, 0u));
+        return;
+    }
+    Four c = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, s = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    if (turns) {
+        const long long at = (long long)pos * p.half + 4 * l;
+        c = load4(p.cos + at);
+        s = load4(p.sin + at);
+    }
+    // with weights wa, wb of the two vectors: a' = a wa c - b wb s, b' = a wa s + b wb c
+    Four ac = c, as = s, bc = c, bs = times(s, -1.f);
+    const float *wp = kind == 0 ? p.qw : p.kw;
+    if (wp) {
+        Four wa, wb;
+        if constexpr (NEXT) {
+            const Four e = load4(wp + 8 * l), f = load4(wp + 8 * l + 4);
+            wa = {make_float2(e.x.x, e.y.x), make_float2(f.x.x, f.y.x)};
+            wb = {make_float2(e.x.y, e.y.y), make_float2(f.x.y, f.y.y)};
+        } else {
+            wa = load4(wp + 4 * va);
+            wb = load4(wp + 4 * vb);
         }
+        ac = times(ac, wa);
+        as = times(as, wa);
+        bc = times(bc, wb);
+        bs = times(bs, wb);
     }
-    if (!NEXT && !second) {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) s[i] = -s[i];  // a c - b s; b c + a s
-    }
-    // the lane that holds the partners
-    const int mate = !turns ? lane : second ? lane - p.half / 8 : lane + p.half / 8;
-
-    const float *w_of = nullptr;
-    float wt[8];
 #pragma unroll
     for (int u = 0; u < kRopeRows; ++u) {
-        const int h = h0 + u * VPW;
-        const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;  // q, k, v (or none)
-        float x[8];
-        unpack8(raw[u], x);
-        const float *wp = kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr;
-        if (p.qw || p.kw) {  // (the same in every lane)
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        if (u * VPW >= per) break;  // (the same in every lane)
+        Four x, y;
+        if constexpr (NEXT) {
+            x = {make_float2(bf_lo(a[u].x), bf_lo(a[u].y)), make_float2(bf_lo(b[u].x), bf_lo(b[u].y))};
+            y = {make_float2(bf_hi(a[u].x), bf_hi(a[u].y)), make_float2(bf_hi(b[u].x), bf_hi(b[u].y))};
+        } else {
+            x = {make_float2(bf_lo(a[u].x), bf_hi(a[u].x)), make_float2(bf_lo(a[u].y), bf_hi(a[u].y))};
+            y = {make_float2(bf_lo(b[u].x), bf_hi(b[u].x)), make_float2(bf_lo(b[u].y), bf_hi(b[u].y))};
+        }
+        Four xt = times(x, ac), yt = times(y, bc);
+        if (turns) {  // (elsewhere 0 times an infinity is none of its business)
+            xt = {fma2(y.x, bs.x, xt.x), fma2(y.y, bs.y, xt.y)};
+            yt = {fma2(x.x, as.x, yt.x), fma2(x.y, as.y, yt.y)};
+        }
+        if (wp) {
+            const float2 q = fma2(x.x, x.x, fma2(x.y, x.y, fma2(y.x, y.x, mul2(y.y, y.y))));
+            float ss = q.x + q.y;
 #pragma unroll
             for (int o = LP / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (wp) {
-                const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                if (wp != w_of) {
-                    w_of = wp;
-                    load4(wp + d0, wt);
-                    load4(wp + d0 + 4, wt + 4);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= r * wt[i];
-            }
+            const float r = rsqrtf(ss * (1.f / D) + p.eps);
+            xt = times(xt, r);
+            yt = times(yt, r);
         }
-        float y[8];
-        if constexpr (NEXT) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-                y[2 * i + 1] = x[2 * i] * s[i] + x[2 * i + 1] * c[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float b = __shfl_sync(0xffffffffu, x[i], mate);
-                y[i] = x[i] * c[i] + b * s[i];
-            }
-        }
-        if (!turns) {  // (0 times an infinity is none of its business)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i];
-        }
-        uint4 out = pack8(y);
-        if (!there) out = make_uint4(0u, 0u, 0u, 0u);
-        if (kind == 0) {
-            p.q_out[row * p.qo_stride + (long long)h * LP + l] = out;
-        } else if (kind == 1) {
-            const int kh = h - p.Hq;
-            if (p.k_out) p.k_out[row * p.ko_stride + (long long)kh * LP + l] = out;
-            if (to >= 0) p.k_pool[to + (((long long)kh << p.lg) * LP) + l] = out;
-        } else if (h < p.heads && to >= 0) {
-            const int vh = h - p.Hq - p.Hkv;
-            p.v_pool[to + (((long long)vh << p.lg) * LP) + l] = raw[u];
-        }
+        if constexpr (NEXT)
+            put(u, make_uint2(bf_pair(xt.x.x, yt.x.x), bf_pair(xt.x.y, yt.x.y)),
+                make_uint2(bf_pair(xt.y.x, yt.y.x), bf_pair(xt.y.y, yt.y.y)));
+        else
+            put(u, make_uint2(bf_pair(xt.x.x, xt.x.y), bf_pair(xt.y.x, xt.y.y)),
+                make_uint2(bf_pair(yt.x.x, yt.x.y), bf_pair(yt.y.x, yt.y.y)));
     }
 }
 
@@ -239,17 +253,20 @@ int run_rope(RopeParams p, int D, int rope_dim, long long q_stride, long long k_
     int ctas;
     unsigned int wait_limit;
     if ((rc = api_device(&ctas, &p.err, &wait_limit))) return rc;
-    p.q_stride = q_stride / 8;
-    p.k_stride = k_stride / 8;
-    p.v_stride = v_stride / 8;
-    p.qo_stride = qo_stride / 8;
-    p.ko_stride = ko_stride / 8;
+    p.q_stride = q_stride / 4;
+    p.k_stride = k_stride / 4;
+    p.v_stride = v_stride / 4;
+    p.qo_stride = qo_stride / 4;
+    p.ko_stride = ko_stride / 4;
     p.half = rope_dim / 2;
-    p.heads = p.Hq + (p.slots ? 2 : 1) * p.Hkv;
-    const int per_warp = kRopeRows * 32 / (D / 8);
-    p.chunks = (p.heads + per_warp - 1) / per_warp;
-    const unsigned long long warps = (unsigned long long)p.N * p.chunks;
-    const unsigned long long grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    const int at_once = 32 / (D / 8);  // head rows of a warp
+    p.q_chunks = (p.Hq + kRopeRows * at_once - 1) / (kRopeRows * at_once);
+    p.k_chunks = (p.Hkv + kRopeRows * at_once - 1) / (kRopeRows * at_once);
+    p.q_per = (p.Hq + p.q_chunks * at_once - 1) / (p.q_chunks * at_once);
+    p.k_per = (p.Hkv + p.k_chunks * at_once - 1) / (p.k_chunks * at_once);
+    p.chunks = p.q_chunks + (p.slots ? 2 : 1) * p.k_chunks;
+    const unsigned long long groups = ((unsigned long long)p.N + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    const unsigned long long grid = groups * p.chunks;
     if (grid > 0x7fffffffULL) return api_failf(KVATTN_ERR_UNSUPPORTED, "%s: too many rows for one launch", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -280,15 +297,15 @@ int qk_norm_rope(const void *q, const void *k, const int32_t *positions, const f
     if (!q || !k || !positions || !cos_table || !sin_table || !q_out || !k_out)
         return api_failf(KVATTN_ERR_INVALID_ARG, "%s: null pointer", who);
     RopeParams p = {};
-    p.q = static_cast<const uint4 *>(q);
-    p.k = static_cast<const uint4 *>(k);
+    p.q = static_cast<const uint2 *>(q);
+    p.k = static_cast<const uint2 *>(k);
     p.pos = positions;
     p.cos = cos_table;
     p.sin = sin_table;
     p.qw = q_weight;
     p.kw = k_weight;
-    p.q_out = static_cast<uint4 *>(q_out);
-    p.k_out = static_cast<uint4 *>(k_out);
+    p.q_out = static_cast<uint2 *>(q_out);
+    p.k_out = static_cast<uint2 *>(k_out);
     p.N = N; p.Hq = Hq; p.Hkv = Hkv;
     p.max_pos = max_pos;
     p.eps = eps;
@@ -311,18 +328,18 @@ int kv_append_rope(const void *q, const void *k, const void *v, const int32_t *p
     static const int32_t no_table = 0;  // (the sizes' check wants a table)
     if ((rc = api_check_sizes(1, Hq, Hkv, D, 1))) return rc;
     if ((rc = api_check_paged(&no_table, Hkv, block_size, 1, num_blocks, who, &p.lg, &lmax))) return rc;
-    p.q = static_cast<const uint4 *>(q);
-    p.k = static_cast<const uint4 *>(k);
-    p.v = static_cast<const uint4 *>(v);
+    p.q = static_cast<const uint2 *>(q);
+    p.k = static_cast<const uint2 *>(k);
+    p.v = static_cast<const uint2 *>(v);
     p.pos = positions;
     p.cos = cos_table;
     p.sin = sin_table;
     p.qw = q_weight;
     p.kw = k_weight;
     p.slots = reinterpret_cast<const long long *>(slots);
-    p.q_out = static_cast<uint4 *>(q_out);
-    p.k_pool = static_cast<uint4 *>(k_pool);
-    p.v_pool = static_cast<uint4 *>(v_pool);
+    p.q_out = static_cast<uint2 *>(q_out);
+    p.k_pool = static_cast<uint2 *>(k_pool);
+    p.v_pool = static_cast<uint2 *>(v_pool);
     p.num_slots = (long long)num_blocks << p.lg;
     p.N = N; p.Hq = Hq; p.Hkv = Hkv;
     p.max_pos = max_pos;
