@@ -37,8 +37,8 @@ constexpr int kMergeThreads = 256;
 // (by a warp) one row from its n partial results, the i-th at row at(i) of the
 // workspace: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, M = max m_i.
 // The first AHEAD of them are loaded with their (m, l), before it is known what
-// they weigh.
-template <int D, int AHEAD, class At>
+// they weigh, the others MORE at a time.
+template <int D, int AHEAD, int MORE, class At>
 __device__ __forceinline__ void join_row(const float *ws_o, const float *ws_ml, At at, int n, uint16_t *out) {
     constexpr int V = D / 32;  // values of a lane
     const int lane = threadIdx.x & 31;
@@ -90,13 +90,13 @@ __device__ __forceinline__ void join_row(const float *ws_o, const float *ws_ml, 
             }
         }
         const int e = min(32, n - i0);
-        for (int i = i0 == 0 ? AHEAD : 0; i < e; i += 4) {
-            float y[4][V];
+        for (int i = i0 == 0 ? AHEAD : 0; i < e; i += MORE) {
+            float y[MORE][V];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < MORE; ++q)
                 if (i + q < e) load(i0 + i + q, y[q]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < MORE; ++q) {
                 const float wi = __shfl_sync(0xffffffffu, w, min(i + q, 31));
                 if (i + q < e && wi != 0.f) {
 #pragma unroll
@@ -110,8 +110,11 @@ __device__ __forceinline__ void join_row(const float *ws_o, const float *ws_ml, 
     store_row<V>(out + lane * V, o, 1.f / l);  // (every row attends something)
 }
 
-// Block (c, y): rows of the unit that CTA c leaves unfinished, a warp each.
-template <int D>
+// Block (c, y): rows of the unit that CTA c leaves unfinished, a warp each.  What
+// bounds it is latency: of the record, then of (m, l) and the rows; with few tokens a
+// request, whose keys may be in many pieces, more of a row is in flight, else more
+// rows are (fewer registers a warp).
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
     pdl_launch_dependents();
     pdl_wait_prior();
@@ -122,14 +125,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
          r += gridDim.y * (kMergeThreads / 32)) {
         const int t = r / p.hpg, h = r - t * p.hpg;
         const int row = t / p.tpt * kRows + t % p.tpt * p.hpg + h;
-        join_row<D, 3>(p.ws_o, p.ws_ml,
+        join_row<D, FEW ? 8 : 2, FEW ? 4 : 1>(p.ws_o, p.ws_ml,
                        [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.slot_rows + row; }, u.w,
                        p.out + ((size_t)(u.x + t) * p.Hq + u.z + h) * D);
     }
 }
 
 template <int D>
-cudaError_t launch_merge(const MergeParams &p, int ctas, int parts, cudaStream_t stream) {
+cudaError_t launch_merge(const MergeParams &p, bool few, int ctas, int parts, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, parts);
     cfg.blockDim = dim3(kMergeThreads);
@@ -139,7 +142,7 @@ cudaError_t launch_merge(const MergeParams &p, int ctas, int parts, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+    return few ? cudaLaunchKernelEx(&cfg, merge_kernel<D, true>, p) : cudaLaunchKernelEx(&cfg, merge_kernel<D, false>, p);
 }
 
 // 3-D map over a pool [num_blocks, Hkv, block_size, D]: dims (D, block_size,
@@ -214,12 +217,16 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     p.box_lg = p.lg < 7 ? p.lg : 7;
     p.box = 1 << p.box_lg;
     p.causal = causal;
-    // A unit's start and end (its copies' latency, the output's read-out, a join) in
-    // key tiles, as measured: 64 requests of 16 heads of 64 over up to 2048 states 91
-    // us with 2, 75 with 5, 78 with 10; 8192 tokens of 64 heads over 8 of 128 794 with
-    // 2, 837 with 1, of 16 over 1 of 256 432 with 3, 536 with 1.
-    p.cost_piece = p.few_tok ? (D == 64 ? 5 : 2) : D == 256 ? 3 : 2;
-    p.min_tiles = 1 + p.cost_piece;
+    // Costs as measured, in fifths of a key tile of two query tiles (1.7 us at D =
+    // 128; of one 1.35, of few rows the same for all).  A unit's start and end (its
+    // copies' latency, the output's read-out, a join) is 2 tiles' work, at D = 64
+    // with few rows 5: 64 requests of 16 heads of 64 over up to 2048 states 91 us
+    // with 2, 75 with 5, 78 with 10; 8192 tokens of 64 heads over 8 of 128 793 with 2,
+    // 824 with 1, of 16 over 1 of 256 447 with 2.6, 522 with 1.
+    p.w2 = 5;
+    p.w1 = p.few_tok || D == 256 ? 5 : 4;
+    p.cost_piece = p.few_tok ? (D == 64 ? 25 : 10) : D == 256 ? 13 : 10;
+    p.min_range = p.w2 + p.cost_piece;
 
     CUtensorMap tmq, tmq4, tmk, tmv;
     const long long heads = (long long)num_blocks * Hkv;
@@ -246,17 +253,17 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
         case 64:
             e = p.few_tok ? launch_extend_few(D, tmq, tmk, tmv, &p, ctas, stream, tmq4)
                           : launch_pf<64, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
-            if (e == cudaSuccess) e = launch_merge<64>(m, ctas, parts, stream);
+            if (e == cudaSuccess) e = launch_merge<64>(m, p.few_tok > 0, ctas, parts, stream);
             break;
         case 128:
             e = p.few_tok ? launch_extend_few(D, tmq, tmk, tmv, &p, ctas, stream, tmq4)
                           : launch_pf<128, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
-            if (e == cudaSuccess) e = launch_merge<128>(m, ctas, parts, stream);
+            if (e == cudaSuccess) e = launch_merge<128>(m, p.few_tok > 0, ctas, parts, stream);
             break;
         default:
             e = p.few_tok ? launch_extend_few(D, tmq, tmk, tmv, &p, ctas, stream, tmq4)
                           : launch_pf<256, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
-            if (e == cudaSuccess) e = launch_merge<256>(m, ctas, parts, stream);
+            if (e == cudaSuccess) e = launch_merge<256>(m, p.few_tok > 0, ctas, parts, stream);
             break;
     }
     if (e != cudaSuccess) return api_cuda_fail(e, "paged prompt attention launch");

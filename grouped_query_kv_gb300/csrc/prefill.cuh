@@ -105,8 +105,8 @@ struct PagedPrefillParams : PrefillParams {
     int few_tok, few_bytes;  // (0: hpg > 32)
     int tpu_lg;              // log2 of a unit's tokens
     int causal;              // token t sees up to itself; else the whole pool rows
-    int cost_piece;          // key tiles that starting and ending a unit costs
-    int min_tiles;           // cost of a CTA's range at least
+    int w1, w2, cost_piece;  // costs, see UnitSeq
+    int min_range;           // cost of a CTA's range at least
 };
 
 // One unit of work as its readers see it.
@@ -436,6 +436,9 @@ __device__ __forceinline__ PagedRange find_range(const PagedPrefillParams &p, in
     r.seq.causal = p.causal;
     r.seq.window = p.window;
     r.seq.tpu_lg = p.tpu_lg;
+    r.seq.tpt = p.tpt;
+    r.seq.w1 = p.w1;
+    r.seq.w2 = p.w2;
     r.seq.piece = p.cost_piece;
     auto cost_of = [&](int b) {
         int none;
@@ -457,8 +460,8 @@ __device__ __forceinline__ PagedRange find_range(const PagedPrefillParams &p, in
         if (w < warp) before += sm[w];
         r.total += sm[w];
     }
-    const long long most = r.total < 1LL << 31 ? (long long)((unsigned)r.total / (unsigned)p.min_tiles)
-                                               : r.total / p.min_tiles;
+    const long long most = r.total < 1LL << 31 ? (long long)((unsigned)r.total / (unsigned)p.min_range)
+                                               : r.total / p.min_range;
     r.ranges = most < 1 ? 1 : most < gridDim.x ? (int)most : (int)gridDim.x;
     if ((int)blockIdx.x < r.ranges && r.total > 0) {
         r.x0 = range_start(r.total, r.ranges, blockIdx.x);
@@ -523,8 +526,9 @@ __device__ __forceinline__ void next_piece(const PagedPrefillParams &p, PagedRan
                 }
             }
         }
-        const int nt = unit_tiles(r.seq, r.blk);
-        const int ta = tiles_before(r.u0, nt, p.cost_piece, r.x0), tb = tiles_before(r.u0, nt, p.cost_piece, r.x1);
+        const int nt = unit_tiles(r.seq, r.blk), w = unit_weight(r.seq, r.blk);
+        const int ta = tiles_before(r.u0, nt, w, p.cost_piece, r.x0);
+        const int tb = tiles_before(r.u0, nt, w, p.cost_piece, r.x1);
         if (ta < tb) {
             const int first = unit_first(r.seq, r.blk);
             u->row0 = r.row0;
@@ -552,11 +556,11 @@ __device__ __forceinline__ void next_piece(const PagedPrefillParams &p, PagedRan
                 u->slot = 2 * blockIdx.x;
             } else if (tb < nt) {
                 u->slot = 2 * blockIdx.x + 1;
-                const int last = range_of(r.total, r.ranges, r.u0 + p.cost_piece + nt - 1);
+                const int last = range_of(r.total, r.ranges, r.u0 + p.cost_piece + (long long)w * (nt - 1));
                 r.record = make_int4(u->row0 + u->t0, stop - u->t0, u->h0, last - (int)blockIdx.x + 1);
             }
         }
-        r.u0 += p.cost_piece + nt;
+        r.u0 += p.cost_piece + (long long)w * nt;
         ++r.blk;
         if (ta < tb) return;
     }
