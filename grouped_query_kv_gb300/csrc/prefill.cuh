@@ -720,25 +720,23 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         r.next();
         return true;
     };
-    // (paged) the same: the boxes of the blocks that hold the unit's rows of the
-    // tile at position kb, a lane each, whose block is blk (one that is none reads
-    // as zeros: a place past the pool)
-    [[maybe_unused]] auto issue_paged = [&](const void *tm, int c, int blk, const Unit &u, int kb, auto &r) -> bool {
+    // (paged) the same from the boxes of a tile's blocks, a lane each
+    struct Boxes {
+        int z, row;   // the lane's block and K/V head in the pool, its first row there
+        bool mine;    // the lane has one
+        int bytes;    // of all, per 64 head dims
+    };
+    [[maybe_unused]] auto issue_paged = [&](const void *tm, int c, const Boxes &t, auto &r) -> bool {
         if constexpr (PG) {
             const int slot = r.slot;
-            const int b0 = max(0, first_key(p, u) - kb) >> p.box_lg;
-            const int b1 = (min(kRows, u.kend - kb) + p.box - 1) >> p.box_lg;
             if (r.pos >= r.N && !mbar_wait_warp(&slot_empty[slot], r.parity ^ 1, abort_flag)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], ((b1 - b0) << p.box_lg) * 2 * C::KC);
+            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], t.bytes * (C::KC / 64));
             __syncwarp();
-            if (lane >= b0 && lane < b1) {
-                const bool bad = blk < 0 || blk >= p.num_blocks;
-                if (bad) pf_error(p.err, DEV_ERR_BOUNDS);
-                const int z = bad ? p.num_blocks * p.Hkv : blk * p.Hkv + u.kvh;
+            if (t.mine) {
 #pragma unroll
                 for (int sl = 0; sl < C::KC / 64; ++sl)
                     tma_load_3d_plain(ring + slot * C::SLOT + sl * kSlab + lane * p.box * 128, tm, &slot_full[slot],
-                                      c * C::KC + sl * 64, kb & ((1 << p.lg) - 1), z);
+                                      c * C::KC + sl * 64, t.row, t.z);
             }
             __syncwarp();
             ++fills;
@@ -765,8 +763,10 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         }
         return x;
     };
-    // the lane's block of the tile at position kb (a tile's are in one group of 32)
-    [[maybe_unused]] auto block_at = [&](const Unit &u, Blocks &x, int kb) -> int {
+    // the boxes of the unit's rows of the tile at position kb (whose blocks are in one
+    // group of 32); a block that is none reads as zeros, from past the pool
+    [[maybe_unused]] auto boxes_at = [&](const Unit &u, Blocks &x, int kb) -> Boxes {
+        Boxes t = {};
         if constexpr (PG) {
             int e = (kb >> p.lg) - x.first;
             if (e >= 32) {
@@ -775,9 +775,17 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 x.now = x.then;
                 x.then = entry(u, x.first + 32 + lane);
             }
-            return __shfl_sync(0xffffffffu, x.now, (e + lane) & 31);
+            const int blk = __shfl_sync(0xffffffffu, x.now, (e + lane) & 31);
+            const int b0 = max(0, first_key(p, u) - kb) >> p.box_lg;
+            const int b1 = (min(kRows, u.kend - kb) + p.box - 1) >> p.box_lg;
+            t.mine = lane >= b0 && lane < b1;
+            t.bytes = (b1 - b0) << p.box_lg << 7;
+            t.row = kb & ((1 << p.lg) - 1);
+            const bool bad = blk < 0 || blk >= p.num_blocks;
+            if (t.mine && bad) pf_error(p.err, DEV_ERR_BOUNDS);
+            t.z = bad ? p.num_blocks * p.Hkv : blk * p.Hkv + u.kvh;
         }
-        return 0;
+        return t;
     };
     // (by one lane) the last fills of a ring of n slots from slot `off` have landed
     auto landed = [&](int n, int off) {
@@ -922,9 +930,9 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             Blocks x = {};
             while (ok && !w.done) {
                 if (w.j == 0) x = blocks_of(w.u);
-                const int kb = w.u.kbeg + w.j * kRows, blk = block_at(w.u, x, kb);
+                const Boxes t = boxes_at(w.u, x, w.u.kbeg + w.j * kRows);
                 const bool last = w.j + 1 == max(w.u.n[0], w.u.n[1]);
-                for (int c = 0; c < CPT && ok; ++c) ok = issue_paged(&tmv, c, blk, w.u, kb, vcopies);
+                for (int c = 0; c < CPT && ok; ++c) ok = issue_paged(&tmv, c, t, vcopies);
                 if (ok) ok = pump(last && w.k + 1 >= k);
                 if (ok) ok = step(w);
             }
@@ -1013,10 +1021,10 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             Blocks x = {};
             while (ok && !w.done) {
                 if (w.j == 0) x = blocks_of(w.u);
-                const int kb = w.u.kbeg + w.j * kRows, blk = block_at(w.u, x, kb);
-                for (int c = 0; c < CPT && ok; ++c) ok = issue_paged(&tmk, c, blk, w.u, kb, kcopies);
+                const Boxes t = boxes_at(w.u, x, w.u.kbeg + w.j * kRows);
+                for (int c = 0; c < CPT && ok; ++c) ok = issue_paged(&tmk, c, t, kcopies);
                 if (ok && w.j == 0) ok = load_q(w.u);
-                if (NQ == 2 && ok) ok = issue_paged(&tmv, 0, blk, w.u, kb, kcopies);
+                if (NQ == 2 && ok) ok = issue_paged(&tmv, 0, t, kcopies);
                 if (ok) ok = step(w);
             }
         } else if (NQ == 2) {
