@@ -13,12 +13,13 @@
 // either).  Compaction: with `used` blocks held, the k-th held block at or past
 // `used` moves to the k-th free one below it.
 //
-// Layout.  Some hundred kilobytes of integers and three to eight steps that each
-// need all of the one before: one cluster of eight CTAs of 1024 threads does
-// all steps of a call, with a cluster barrier between them and the counts of the
-// CTAs exchanged through distributed shared memory, where a kernel per step
-// would cost a launch each.  No workspace.  What bounds a call: the chain of
-// barriers and dependent loads.
+// Layout.  Some kilobytes of integers, or some hundred, and four to six steps that
+// each need all of the one before: one CTA of 1024 threads does all steps of a
+// small call (barriers of a CTA are a tenth of a cluster's: 64 forks of up to 128
+// blocks XXX us for 8.7, dropping them XXX for 9.9), one cluster of eight those of a
+// large one, the counts of the CTAs exchanged through distributed shared memory; a
+// kernel per step would cost a launch each.  No workspace.  What bounds a call: the
+// chain of barriers and dependent loads.
 //
 // kv_copy_blocks is a copy of 16-byte vectors of K and V, four of each in flight
 // per thread, and bound by HBM.
@@ -35,19 +36,55 @@ namespace kvattn {
 
 namespace {
 
-constexpr int kCtas = 8;                       // of the cluster
+constexpr int kCtas = 8;                       // of a large call's cluster
 constexpr int kThr = 1024;
-constexpr int kAll = kCtas * kThr;             // threads
-constexpr int kWarps = kAll / 32;
-constexpr int kPer = 8;                        // requests per thread at most (65535 / kAll)
+constexpr int kPer = 8;                        // requests per thread at most (65535 / (kCtas kThr))
 constexpr int kTile = 4 * kThr;                // blocks of a CTA's step, four to a thread
+constexpr int kSmallNames = 256, kSmallBlocks = 1 << 15;  // a call up to these is one CTA's
 
 // ------------------------------------------------------------------- scans
 
 struct Scan {
     int warp[32];
     int total;
-    int cta;  // this CTA's sum, read by the others
+    long long cta[3];  // this CTA's sums, read by the others (each place once)
+};
+
+// The CTAs of a call, NC of them: one or a cluster.
+template <int NC>
+struct Team {
+    static constexpr int kAll = NC * kThr, kWarps = kAll / 32;
+    int rank = 0;
+    __device__ __forceinline__ Team() {
+        if constexpr (NC > 1) rank = (int)cg::this_cluster().block_rank();
+    }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (NC > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+    }
+    // (a barrier) the sums of the CTAs before this one, given its own, and of all
+    __device__ __forceinline__ long long scan(long long mine, Scan &s, int place, long long *all) const {
+        if constexpr (NC > 1) {
+            cg::cluster_group cl = cg::this_cluster();
+            if (threadIdx.x == 0) s.cta[place] = mine;
+            cl.sync();
+            long long before = 0, sum = 0;
+#pragma unroll
+            for (int r = 0; r < NC; ++r) {
+                const long long x = *cl.map_shared_rank(&s.cta[place], r);
+                if (r < rank) before += x;
+                sum += x;
+            }
+            *all = sum;
+            return before;
+        } else {
+            __syncthreads();
+            *all = mine;
+            return 0;
+        }
+    }
 };
 
 // Exclusive prefix sum over a CTA's threads, and their sum.  (Its barriers also
@@ -79,22 +116,6 @@ __device__ __forceinline__ int cta_scan(int v, Scan &s, int *total) {
     return s.warp[warp] + incl - v;
 }
 
-// The sums of the CTAs before this one, given its own, and of all.
-__device__ __forceinline__ int cluster_scan(cg::cluster_group &cl, int mine, Scan &s, int *total) {
-    cl.sync();  // (nobody reads the last sums any more)
-    if (threadIdx.x == 0) s.cta = mine;
-    cl.sync();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int r = 0; r < kCtas; ++r) {
-        const int x = *cl.map_shared_rank(&s.cta, r);
-        if (r < (int)cl.block_rank()) before += x;
-        all += x;
-    }
-    *total = all;
-    return before;
-}
-
 __device__ __forceinline__ void blk_error(unsigned int *err) { atomicCAS(err, 0u, (unsigned int)DEV_ERR_BOUNDS); }
 
 // Four consecutive counts of blocks from b on (b a multiple of 4), `pad` past the end.
@@ -121,16 +142,19 @@ struct ForkParams {
     int n, R, max_blocks, lg, num_blocks, num_free;
 };
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) fork_kernel(const ForkParams p) {
+template <int NC>
+__global__ void __launch_bounds__(kThr) fork_kernel(const ForkParams p) {
+    using T = Team<NC>;
     __shared__ Scan s;
-    cg::cluster_group cl = cg::this_cluster();
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int t = (int)cl.block_rank() * kThr + threadIdx.x;
-    const int per = (p.n + kAll - 1) / kAll;  // consecutive forks of a thread
+    const T team;
+    const int t = team.rank * kThr + threadIdx.x;
+    const int per = (p.n + T::kAll - 1) / T::kAll;  // consecutive forks of a thread
     const int i0 = min(t * per, p.n), i1 = min(i0 + per, p.n);
     int count = __ldcg(p.free_count);
     bool bad = count < 0 || count > p.num_free;
+    const int said = count;
     if (bad) count = 0;
 
     // whose row is free (its length 0) and within the table
@@ -139,12 +163,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) fork_kerne
         const int a = p.parents[i], c = p.children[i];
         if (a >= 0 && a < p.R && c >= 0 && c < p.R && __ldcg(p.lens + c) == 0) able |= 1u << (i - i0);
     }
-    cl.sync();
+    team.sync();
     // of forks into one row the first has it: it leaves the smallest mark in the
     // row's length.  A parent that is marked is some fork's child.
     for (int i = i0; i < i1; ++i)
         if (able >> (i - i0) & 1) atomicMin(p.lens + p.children[i], INT_MIN + i);
-    cl.sync();
+    team.sync();
     int need = 0;
     unsigned parts = 0;
     const int cap = p.max_blocks << p.lg, rest = (1 << p.lg) - 1;
@@ -157,13 +181,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) fork_kerne
             parts |= 1u << (i - i0);
             ++need;
         }
+        p.copies[2 * i] = len;  // (a fork's length and block wait in its place of the copies)
     }
-    int cta, all;
+    int cta;
+    long long all;
     const int in_cta = cta_scan(need, s, &cta);
-    int before = cluster_scan(cl, cta, s, &all) + in_cta;
-    // (that was a barrier: every length and mark has been read; what follows
-    // until the next one reads none of them.)  A fork's length and block wait in
-    // its place of the copies.
+    int before = (int)team.scan(cta, s, 0, &all) + in_cta;
+    // (a barrier: every length and mark has been read)
     for (int i = i0; i < i1; ++i) {
         const bool own = able >> (i - i0) & 1, part = parts >> (i - i0) & 1;
         bool ok = own;
@@ -174,15 +198,16 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) fork_kerne
             ok = ok && fresh >= 0 && fresh < p.num_blocks;
             ++before;
         }
-        if (!ok) bad = true;
-        p.copies[2 * i] = ok ? __ldcg(p.lens + p.parents[i]) : -1;
+        if (!ok) {
+            bad = true;
+            p.copies[2 * i] = -1;
+        }
         p.copies[2 * i + 1] = ok ? fresh : -1;
     }
-    if (t == 0) p.count_out[0] = bad && count == 0 ? __ldcg(p.free_count) : count - min(all, count);
-    cl.sync();
-    // (the marks go: a parent's length is no longer asked for)
+    if (t == 0) p.count_out[0] = said == count ? count - (int)min(all, (long long)count) : said;
+    team.sync();
     const int gw = t >> 5, lane = t & 31;
-    for (int i = gw; i < p.n; i += kWarps) {  // a warp per fork
+    for (int i = gw; i < p.n; i += T::kWarps) {  // a warp per fork
         const int len = __ldcg(p.copies + 2 * i), fresh = __ldcg(p.copies + 2 * i + 1);
         const int a = p.parents[i], c = p.children[i];
         int src = -1, dst = -1;
@@ -190,16 +215,22 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) fork_kerne
             const int32_t *from = p.table + (size_t)a * p.max_blocks;
             int32_t *to = p.table + (size_t)c * p.max_blocks;
             const int whole = len >> p.lg;
-            for (int e = lane; e < whole; e += 32) {
-                const int b = from[e];
-                to[e] = b;
-                if (b >= 0 && b < p.num_blocks)
-                    atomicAdd(p.refs + b, 1);
-                else
-                    bad = true;
+            if (len & rest) src = from[whole];
+            for (int e0 = lane; e0 < whole; e0 += 128) {
+                int b[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b[q] = e0 + 32 * q < whole ? from[e0 + 32 * q] : -1;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (e0 + 32 * q < whole) {
+                        to[e0 + 32 * q] = b[q];
+                        if (b[q] >= 0 && b[q] < p.num_blocks)
+                            atomicAdd(p.refs + b[q], 1);
+                        else
+                            bad = true;
+                    }
             }
             if (len & rest) {
-                src = from[whole];
                 dst = fresh;
                 if (lane == 0) to[whole] = fresh;
                 if (src < 0 || src >= p.num_blocks) {  // nothing to copy
@@ -231,29 +262,33 @@ struct FreeParams {
 };
 
 // A CTA's share of the blocks: whole tiles, the same order as the CTAs'.
+template <int NC>
 __device__ __forceinline__ void share_of(int num_blocks, int rank, int *b0, int *b1) {
     const int tiles = (int)(((long long)num_blocks + kTile - 1) / kTile);
-    const int each = (tiles + kCtas - 1) / kCtas;
+    const int each = (tiles + NC - 1) / NC;
     *b0 = (int)min((long long)num_blocks, (long long)rank * each * kTile);
     *b1 = (int)min((long long)num_blocks, (long long)*b0 + (long long)each * kTile);
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) free_kernel(const FreeParams p) {
+template <int NC>
+__global__ void __launch_bounds__(kThr) free_kernel(const FreeParams p) {
+    using T = Team<NC>;
     __shared__ Scan s;
-    cg::cluster_group cl = cg::this_cluster();
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int t = (int)cl.block_rank() * kThr + threadIdx.x, gw = t >> 5, lane = t & 31;
+    const T team;
+    const int t = team.rank * kThr + threadIdx.x, gw = t >> 5, lane = t & 31;
     const int count = __ldcg(p.free_count);
     const bool refuse = count < 0 || count > p.num_free;  // nothing is done
     bool bad = refuse;
     const int cap = p.max_blocks << p.lg, rest = (1 << p.lg) - 1;
 
     // request gw + kWarps (lane + 32 u) is this lane's u-th, and its warp's to free
-    int len[kPer], req[kPer];
+    constexpr int PER = NC == 1 ? 1 : kPer;  // (one CTA has up to kSmallNames)
+    int len[PER], req[PER];
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-        const int i = gw + kWarps * (lane + 32 * u);
+    for (int u = 0; u < PER; ++u) {
+        const int i = gw + T::kWarps * (lane + 32 * u);
         len[u] = 0;
         req[u] = -1;
         if (i < p.n && !refuse) {
@@ -270,15 +305,15 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) free_kerne
             }
         }
     }
-    cl.sync();
+    team.sync();
     // a request named twice is freed once: the first name leaves the smallest mark
 #pragma unroll
-    for (int u = 0; u < kPer; ++u)
-        if (len[u] > 0) atomicMin(p.lens + req[u], INT_MIN + gw + kWarps * (lane + 32 * u));
-    cl.sync();
+    for (int u = 0; u < PER; ++u)
+        if (len[u] > 0) atomicMin(p.lens + req[u], INT_MIN + gw + T::kWarps * (lane + 32 * u));
+    team.sync();
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-        const int i = gw + kWarps * (lane + 32 * u);
+    for (int u = 0; u < PER; ++u) {
+        const int i = gw + T::kWarps * (lane + 32 * u);
         const bool mine = len[u] > 0 && __ldcg(p.lens + req[u]) == INT_MIN + i;
         unsigned todo = __ballot_sync(0xffffffffu, mine);
         while (todo) {
@@ -287,25 +322,31 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) free_kerne
             const int r = __shfl_sync(0xffffffffu, req[u], src);
             const int nb = (__shfl_sync(0xffffffffu, len[u], src) + rest) >> p.lg;
             int32_t *row = p.table + (size_t)r * p.max_blocks;
-            for (int e = lane; e < nb; e += 32) {
-                const int b = row[e];
-                row[e] = -1;
-                if (b >= 0 && b < p.num_blocks)
-                    atomicSub(p.refs + b, 1);
-                else
-                    bad = true;
+            for (int e0 = lane; e0 < nb; e0 += 128) {
+                int b[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b[q] = e0 + 32 * q < nb ? row[e0 + 32 * q] : 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (e0 + 32 * q < nb) {
+                        row[e0 + 32 * q] = -1;
+                        if (b[q] >= 0 && b[q] < p.num_blocks)
+                            atomicSub(p.refs + b[q], 1);
+                        else
+                            bad = true;
+                    }
             }
         }
     }
-    cl.sync();
+    team.sync();
     // (every mark has been compared)
 #pragma unroll
-    for (int u = 0; u < kPer; ++u)
+    for (int u = 0; u < PER; ++u)
         if (len[u] > 0) p.lens[req[u]] = 0;
 
     // the blocks without a holder, in the order of their ids
     int b0, b1;
-    share_of(p.num_blocks, (int)cl.block_rank(), &b0, &b1);
+    share_of<NC>(p.num_blocks, team.rank, &b0, &b1);
     int mine = 0;
     for (int b = b0 + 4 * (int)threadIdx.x; b < b1; b += kTile) {
         int v[4];
@@ -313,9 +354,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) free_kerne
 #pragma unroll
         for (int i = 0; i < 4; ++i) mine += v[i] < 0;
     }
-    int cta, all;
+    int cta;
+    long long all;
     cta_scan(mine, s, &cta);
-    long long at = count + (long long)cluster_scan(cl, cta, s, &all);
+    long long at = count + team.scan(cta, s, 0, &all);
     if (cta > 0 && !refuse) {
         for (int b = b0; b < b1; b += kTile) {
             const int mb = b + 4 * (int)threadIdx.x;
@@ -324,6 +366,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) free_kerne
             int k = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) k += v[i] < 0;
+            if (!__syncthreads_or(k)) continue;
             int tile;
             const int rank = cta_scan(k, s, &tile);
             long long to = at + rank;
@@ -341,9 +384,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) free_kerne
             at += tile;
         }
     }
-    if (t == 0) p.count_out[0] = refuse ? count : (int)min((long long)count + all, (long long)p.num_free);
+    if (t == 0) p.count_out[0] = refuse ? count : (int)min(count + all, (long long)p.num_free);
     if (bad) blk_error(p.err);
-    cl.sync();  // (the others may still read this CTA's sum)
+    if (NC > 1) team.sync();  // (the others may still read this CTA's sum)
 }
 
 // -------------------------------------------------------------- compaction
@@ -355,31 +398,45 @@ struct CompactParams {
     int R, max_blocks, lg, num_blocks, num_free;
 };
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) compact_kernel(const CompactParams p) {
+template <int NC>
+__global__ void __launch_bounds__(kThr) compact_kernel(const CompactParams p) {
+    using T = Team<NC>;
     __shared__ Scan s;
-    cg::cluster_group cl = cg::this_cluster();
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int t = (int)cl.block_rank() * kThr + threadIdx.x, gw = t >> 5, lane = t & 31;
+    const T team;
+    const int t = team.rank * kThr + threadIdx.x, gw = t >> 5, lane = t & 31;
     const int n = p.num_blocks;
     const int said = __ldcg(p.free_count);
     bool bad = said < 0 || said > p.num_free;
     const int count = bad ? 0 : said;
 
     // remap: -1 for the blocks on the stack, each other block itself
-    for (int b = t; b < n; b += kAll) p.remap[b] = b;
-    for (int k = t; k < n / 2 * 2; k += kAll) p.moves[k] = -1;
-    cl.sync();
-    for (int k = t; k < count; k += kAll) {
-        const int b = p.free_ids[k];
-        if (b >= 0 && b < n)
-            p.remap[b] = -1;
+    int b0, b1, cta;
+    long long all;
+    share_of<NC>(n, team.rank, &b0, &b1);
+    for (int b = b0 + 4 * (int)threadIdx.x; b < b1; b += kTile) {
+        if (b + 4 <= b1)
+            *reinterpret_cast<int4 *>(p.remap + b) = make_int4(b, b + 1, b + 2, b + 3);
         else
-            bad = true;
+            for (int i = b; i < b1; ++i) p.remap[i] = i;
     }
-    cl.sync();
-    int b0, b1, cta, all;
-    share_of(n, (int)cl.block_rank(), &b0, &b1);
+    team.sync();
+    // (here and below four loads of a thread are in flight: a step is some loads long)
+    for (int k0 = t; k0 < count; k0 += 4 * T::kAll) {
+        int b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) b[q] = k0 + q * T::kAll < count ? p.free_ids[k0 + q * T::kAll] : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (k0 + q * T::kAll < count) {
+                if (b[q] >= 0 && b[q] < n)
+                    p.remap[b[q]] = -1;
+                else
+                    bad = true;
+            }
+    }
+    team.sync();
     int mine = 0;
     for (int b = b0 + 4 * (int)threadIdx.x; b < b1; b += kTile) {
         int v[4];
@@ -388,94 +445,131 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThr) compact_ke
         for (int i = 0; i < 4; ++i) mine += v[i] < 0;
     }
     cta_scan(mine, s, &cta);
-    cluster_scan(cl, cta, s, &all);
-    const int used = n - all;
-    if (all != count) bad = true;  // an id twice
+    team.scan(cta, s, 0, &all);
+    const int used = n - (int)all;
+    if ((int)all != count) bad = true;  // an id twice
 
     // holes: free blocks below `used`; movers: held ones from there on
     auto kind = [&](int b, int v) { return v < 0 ? (b < used ? 1 : 0) : (b >= used && b < n ? 1 << 16 : 0); };
-    int holes = 0, movers = 0;
+    int holes = b1 <= used ? cta : 0, movers = b0 >= used ? b1 - b0 - cta : 0;
+    if (b0 < used && used < b1) {  // (one CTA's share has the border)
+        int h = 0, m = 0;
+        for (int b = b0 + 4 * (int)threadIdx.x; b < b1; b += kTile) {
+            int v[4];
+            load_blocks(p.remap, b, b1, 0, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = b + i < b1 ? kind(b + i, v[i]) : 0;
+                h += k & 1;
+                m += k >> 16;
+            }
+        }
+        cta_scan(h, s, &holes);
+        cta_scan(m, s, &movers);
+    }
+    const long long first = team.scan((long long)holes << 32 | (unsigned)movers, s, 1, &all);
+    int hole = (int)(first >> 32), mover = (int)first;
+    const int moved = (int)(all >> 32);
+    if (holes + movers > 0)
+        for (int b = b0; b < b1; b += kTile) {
+            const int mb = b + 4 * (int)threadIdx.x;
+            int v[4], k[4] = {0, 0, 0, 0}, sum = 0;
+            if (mb < b1) {
+                load_blocks(p.remap, mb, b1, 0, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) k[i] = mb + i < b1 ? kind(mb + i, v[i]) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += k[i];
+            int tile;
+            const int rank = cta_scan(sum, s, &tile);  // (4096 of a kind at most: 16 bits each)
+            int h = hole + (rank & 0xffff), m = mover + (rank >> 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (k[i] == 1) p.moves[2 * h++ + 1] = mb + i;
+                if (k[i] > 1) p.moves[2 * m++] = mb + i;
+            }
+            hole += tile & 0xffff;
+            mover += tile >> 16;
+        }
+    for (int k = 2 * moved + t; k < n / 2 * 2; k += T::kAll) p.moves[k] = -1;
+    team.sync();
+    // references: a hole's are its mover's, and nobody holds what lies from `used` on.
+    // (Holes and movers are left to the second loop; a mover's place of the map says
+    // that it is held before and after it.)
     for (int b = b0 + 4 * (int)threadIdx.x; b < b1; b += kTile) {
-        int v[4];
+        int v[4], r[4] = {0, 0, 0, 0};
         load_blocks(p.remap, b, b1, 0, v);
+        if (b < used && p.refs_out != p.refs) load_blocks(p.refs, b, b1, 0, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = b + i < b1 ? kind(b + i, v[i]) : 0;
-            holes += k & 1;
-            movers += k >> 16;
-        }
+        for (int i = 0; i < 4; ++i)
+            if (b + i < b1) {
+                if (b + i >= used ? v[i] < 0 : v[i] >= 0 && p.refs_out != p.refs)
+                    p.refs_out[b + i] = b + i >= used ? 0 : r[i];
+            }
     }
-    cta_scan(holes, s, &cta);
-    int hole = cluster_scan(cl, cta, s, &all);
-    const int moved = all;
-    cta_scan(movers, s, &cta);
-    int mover = cluster_scan(cl, cta, s, &all);
-    for (int b = b0; b < b1; b += kTile) {
-        const int mb = b + 4 * (int)threadIdx.x;
-        int v[4], k[4] = {0, 0, 0, 0}, sum = 0;
-        if (mb < b1) {
-            load_blocks(p.remap, mb, b1, 0, v);
+    for (int k0 = t; k0 < moved; k0 += 4 * T::kAll) {
+        int2 m[4];  // (from, to)
+        int r[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) k[i] = mb + i < b1 ? kind(mb + i, v[i]) : 0;
-        }
+        for (int q = 0; q < 4; ++q)
+            if (k0 + q * T::kAll < moved) m[q] = __ldcg(reinterpret_cast<const int2 *>(p.moves) + k0 + q * T::kAll);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += k[i];
-        int tile;
-        const int rank = cta_scan(sum, s, &tile);  // (4096 of a kind at most: 16 bits each)
-        int h = hole + (rank & 0xffff), m = mover + (rank >> 16);
+        for (int q = 0; q < 4; ++q)
+            if (k0 + q * T::kAll < moved) r[q] = p.refs[m[q].x];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (k[i] == 1) p.moves[2 * h++ + 1] = mb + i;
-            if (k[i] > 1) p.moves[2 * m++] = mb + i;
-        }
-        hole += tile & 0xffff;
-        mover += tile >> 16;
-    }
-    cl.sync();
-    // references: a hole's are its mover's, and nobody holds what lies from `used` on
-    for (int b = t; b < n; b += kAll) {
-        const int v = __ldcg(p.remap + b);
-        if (b < used) {
-            if (v >= 0 && p.refs_out != p.refs) p.refs_out[b] = p.refs[b];
-        } else if (v < 0) {
-            p.refs_out[b] = 0;
-        }
-    }
-    cl.sync();
-    for (int k = t; k < moved; k += kAll) {
-        const int src = __ldcg(p.moves + 2 * k), dst = __ldcg(p.moves + 2 * k + 1);
-        const int r = p.refs[src];
-        p.refs_out[dst] = r;
-        p.refs_out[src] = 0;
-        p.remap[src] = dst;
+        for (int q = 0; q < 4; ++q)
+            if (k0 + q * T::kAll < moved) {
+                p.refs_out[m[q].y] = r[q];
+                p.refs_out[m[q].x] = 0;
+                p.remap[m[q].x] = m[q].y;
+            }
     }
     const int left = n - used;
-    for (int k = t; k < p.num_free; k += kAll) {
-        if (k < left)
-            p.free_out[k] = n - 1 - k;  // the lowest id on top
-        else if (p.free_out != p.free_ids)
-            p.free_out[k] = p.free_ids[k];
-    }
-    if (t == 0) p.count_out[0] = said < 0 || said > p.num_free ? said : left;
-    cl.sync();
+    for (int k = t; k < min(left, p.num_free); k += T::kAll) p.free_out[k] = n - 1 - k;  // the lowest id on top
+    if (p.free_out != p.free_ids)
+        for (int k0 = left + t; k0 < p.num_free; k0 += 4 * T::kAll) {
+            int b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) b[q] = k0 + q * T::kAll < p.num_free ? p.free_ids[k0 + q * T::kAll] : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (k0 + q * T::kAll < p.num_free) p.free_out[k0 + q * T::kAll] = b[q];
+        }
+    if (t == 0) p.count_out[0] = said == count ? left : said;
+    team.sync();
     const int cap = p.max_blocks << p.lg, rest = (1 << p.lg) - 1;
-    for (int r = gw; r < p.R; r += kWarps) {  // a warp per request
-        int len = p.lens[r];
+    const bool in_place = p.table_out == p.table;
+    for (int r0 = 4 * gw; r0 < p.R; r0 += 4 * T::kWarps) {  // four requests a warp
+        int len = lane < 4 && r0 + lane < p.R ? p.lens[r0 + lane] : 0;
         if (len < 0 || len > cap) {
             bad = true;
             len = 0;
         }
-        const int nb = (len + rest) >> p.lg;
-        const int32_t *row = p.table + (size_t)r * p.max_blocks;
-        int32_t *to = p.table_out + (size_t)r * p.max_blocks;
-        const int last = p.table_out == p.table ? nb : p.max_blocks;
+        int nb[4], last = in_place ? 0 : p.max_blocks;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            nb[q] = (__shfl_sync(0xffffffffu, len, q) + rest) >> p.lg;
+            if (in_place) last = max(last, nb[q]);
+        }
         for (int e = lane; e < last; e += 32) {
-            int b = row[e];
-            if (e < nb) {
-                if (b >= 0 && b < n) b = __ldcg(p.remap + b);
-                if (b < 0 || b >= n) bad = true;  // no block, or a free one
+            int b[4], to[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool here = r0 + q < p.R && (!in_place || e < nb[q]);
+                b[q] = here ? p.table[(size_t)(r0 + q) * p.max_blocks + e] : -1;
             }
-            to[e] = b;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                to[q] = b[q];
+                if (e < nb[q] && b[q] >= 0 && b[q] < n) to[q] = __ldcg(p.remap + b[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (r0 + q < p.R && (!in_place || e < nb[q])) {
+                    if (e < nb[q] && (to[q] < 0 || to[q] >= n)) bad = true;  // no block, or a free one
+                    p.table_out[(size_t)(r0 + q) * p.max_blocks + e] = to[q];
+                }
         }
     }
     if (bad) blk_error(p.err);
@@ -541,6 +635,25 @@ cudaError_t launch_pdl(Kernel kernel, unsigned grid, unsigned block, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// One CTA, or a cluster of kCtas.
+template <class Kernel, class Params>
+cudaError_t launch_team(Kernel one, Kernel many, bool small, cudaStream_t stream, const Params &p) {
+    if (small) return launch_pdl(one, 1, kThr, stream, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCtas);
+    cfg.blockDim = dim3(kThr);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, many, p);
 }
 
 template <class T>
@@ -620,7 +733,8 @@ int kv_fork_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *refs, const
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     p.num_free = num_free;
-    cudaError_t e = launch_pdl(fork_kernel, kCtas, kThr, reinterpret_cast<cudaStream_t>(stream), p);
+    cudaError_t e = launch_team(fork_kernel<1>, fork_kernel<kCtas>, n <= kSmallNames,
+                                reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) return api_cuda_fail(e, "fork launch");
     return KVATTN_OK;
 }
@@ -653,7 +767,8 @@ int kv_free_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *refs, int32
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     p.num_free = num_free;
-    cudaError_t e = launch_pdl(free_kernel, kCtas, kThr, reinterpret_cast<cudaStream_t>(stream), p);
+    cudaError_t e = launch_team(free_kernel<1>, free_kernel<kCtas>, n <= kSmallNames && num_blocks <= kSmallBlocks,
+                                reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) return api_cuda_fail(e, "free launch");
     return KVATTN_OK;
 }
@@ -693,7 +808,8 @@ int kv_compact_blocks(const int32_t *block_table, const int32_t *seq_lens, const
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     p.num_free = num_free;
-    cudaError_t e = launch_pdl(compact_kernel, kCtas, kThr, reinterpret_cast<cudaStream_t>(stream), p);
+    cudaError_t e = launch_team(compact_kernel<1>, compact_kernel<kCtas>, R <= kSmallNames && num_blocks <= kSmallBlocks,
+                                reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) return api_cuda_fail(e, "compaction launch");
     return KVATTN_OK;
 }
