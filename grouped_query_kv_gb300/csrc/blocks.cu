@@ -181,17 +181,18 @@ __global__ void __launch_bounds__(kThr) fork_kernel(const ForkParams p) {
             parts |= 1u << (i - i0);
             ++need;
         }
-        p.copies[2 * i] = len;  // (a fork's length and block wait in its place of the copies)
     }
     int cta;
     long long all;
     const int in_cta = cta_scan(need, s, &cta);
     int before = (int)team.scan(cta, s, 0, &all) + in_cta;
     // (a barrier: every length and mark has been read)
+    __shared__ int served[NC == 1 ? kSmallNames : 1];  // (one CTA) a fork's length, or -1
     for (int i = i0; i < i1; ++i) {
         const bool own = able >> (i - i0) & 1, part = parts >> (i - i0) & 1;
+        const int a = p.parents[i], c = p.children[i];
         bool ok = own;
-        int fresh = -1;
+        int len = own ? __ldcg(p.lens + a) : -1, fresh = -1;
         if (part) {
             ok = before < count;
             if (ok) fresh = p.free_ids[count - 1 - before];
@@ -200,23 +201,43 @@ __global__ void __launch_bounds__(kThr) fork_kernel(const ForkParams p) {
         }
         if (!ok) {
             bad = true;
-            p.copies[2 * i] = -1;
+            len = -1;
+            fresh = -1;
         }
-        p.copies[2 * i + 1] = ok ? fresh : -1;
+        if constexpr (NC == 1)
+            served[i] = len;
+        else  // (what the fork's warp is to know waits in its place of the copies)
+            p.copies[2 * i] = len, p.copies[2 * i + 1] = fresh;
+        if constexpr (NC == 1) {
+            int src = -1;
+            if (fresh >= 0) {
+                src = p.table[(size_t)a * p.max_blocks + (len >> p.lg)];
+                p.table[(size_t)c * p.max_blocks + (len >> p.lg)] = fresh;
+                if (src < 0 || src >= p.num_blocks) {  // nothing to copy
+                    src = -1;
+                    bad = true;
+                }
+            }
+            p.copies[2 * i] = src;
+            p.copies[2 * i + 1] = src < 0 ? -1 : fresh;
+        }
     }
     if (t == 0) p.count_out[0] = said == count ? count - (int)min(all, (long long)count) : said;
     team.sync();
+    // (nobody reads the marks and the parents' lengths any more, but a refused fork
+    // its own mark)
     const int gw = t >> 5, lane = t & 31;
-    for (int i = gw; i < p.n; i += T::kWarps) {  // a warp per fork
-        const int len = __ldcg(p.copies + 2 * i), fresh = __ldcg(p.copies + 2 * i + 1);
+    // a warp per fork, or several for its entries where there are few forks
+    const int ways = max(1, T::kWarps / p.n);
+    for (int i = gw / ways; i < p.n; i += T::kWarps / ways) {
+        const int way = gw % ways;
+        const int len = NC == 1 ? served[i] : __ldcg(p.copies + 2 * i);
         const int a = p.parents[i], c = p.children[i];
-        int src = -1, dst = -1;
         if (len >= 0) {
             const int32_t *from = p.table + (size_t)a * p.max_blocks;
             int32_t *to = p.table + (size_t)c * p.max_blocks;
             const int whole = len >> p.lg;
-            if (len & rest) src = from[whole];
-            for (int e0 = lane; e0 < whole; e0 += 128) {
+            for (int e0 = lane + 128 * way; e0 < whole; e0 += 128 * ways) {
                 int b[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) b[q] = e0 + 32 * q < whole ? from[e0 + 32 * q] : -1;
@@ -230,22 +251,26 @@ __global__ void __launch_bounds__(kThr) fork_kernel(const ForkParams p) {
                             bad = true;
                     }
             }
-            if (len & rest) {
-                dst = fresh;
-                if (lane == 0) to[whole] = fresh;
+            if (way == 0 && lane == 0) p.lens[c] = len;
+        } else if (way == 0 && lane == 0 && c >= 0 && c < p.R && __ldcg(p.lens + c) == INT_MIN + i) {
+            p.lens[c] = 0;  // the row that this fork had marked
+        }
+        if constexpr (NC > 1) {  // (one warp a fork)
+            int src = -1, dst = -1;
+            if (len >= 0 && (len & rest)) {
+                dst = __ldcg(p.copies + 2 * i + 1);
+                src = p.table[(size_t)a * p.max_blocks + (len >> p.lg)];
+                if (lane == 0) p.table[(size_t)c * p.max_blocks + (len >> p.lg)] = dst;
                 if (src < 0 || src >= p.num_blocks) {  // nothing to copy
                     src = dst = -1;
                     bad = true;
                 }
             }
-            if (lane == 0) p.lens[c] = len;
-        } else if (lane == 0 && c >= 0 && c < p.R && __ldcg(p.lens + c) == INT_MIN + i) {
-            p.lens[c] = 0;  // the row that this fork had marked
-        }
-        __syncwarp();
-        if (lane == 0) {
-            p.copies[2 * i] = src;
-            p.copies[2 * i + 1] = dst;
+            __syncwarp();
+            if (lane == 0) {
+                p.copies[2 * i] = src;
+                p.copies[2 * i + 1] = dst;
+            }
         }
     }
     if (bad) blk_error(p.err);
@@ -283,66 +308,89 @@ __global__ void __launch_bounds__(kThr) free_kernel(const FreeParams p) {
     bool bad = refuse;
     const int cap = p.max_blocks << p.lg, rest = (1 << p.lg) - 1;
 
-    // request gw + kWarps (lane + 32 u) is this lane's u-th, and its warp's to free
-    constexpr int PER = NC == 1 ? 1 : kPer;  // (one CTA has up to kSmallNames)
-    int len[PER], req[PER];
+    // lets go of the entries of row r from e0 on, 128 of every `every`
+    auto let_go = [&](int r, int nb, int e0, int every) {
+        int32_t *row = p.table + (size_t)r * p.max_blocks;
+        for (e0 += lane; e0 < nb; e0 += every) {
+            int b[4];
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int i = gw + T::kWarps * (lane + 32 * u);
-        len[u] = 0;
-        req[u] = -1;
+            for (int q = 0; q < 4; ++q) b[q] = e0 + 32 * q < nb ? row[e0 + 32 * q] : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (e0 + 32 * q < nb) {
+                    row[e0 + 32 * q] = -1;
+                    if (b[q] >= 0 && b[q] < p.num_blocks)
+                        atomicSub(p.refs + b[q], 1);
+                    else
+                        bad = true;
+                }
+        }
+    };
+    // the length of the i-th request, 0 if there is nothing to free, and its row
+    auto length_of = [&](int i, int *r) {
+        int len = 0;
+        *r = -1;
         if (i < p.n && !refuse) {
-            const int r = p.requests[i];
-            if (r >= 0 && r < p.R) {
-                req[u] = r;
-                len[u] = __ldcg(p.lens + r);
-                if (len[u] < 0 || len[u] > cap) {
-                    len[u] = 0;
+            *r = p.requests[i];
+            if (*r >= 0 && *r < p.R) {
+                len = __ldcg(p.lens + *r);
+                if (len < 0 || len > cap) {
+                    len = 0;
                     bad = true;
                 }
             } else {
                 bad = true;
             }
         }
-    }
-    team.sync();
-    // a request named twice is freed once: the first name leaves the smallest mark
+        return len;
+    };
+    // A request named twice is freed once: the first name leaves the smallest mark in
+    // its length.
+    if (p.n <= kSmallNames) {
+        // every CTA has the whole list, and all warps share the entries
+        __shared__ int rows[kSmallNames], lens[kSmallNames];
+        int r;
+        const int i = threadIdx.x, len = length_of(i, &r);
+        team.sync();
+        if (team.rank == 0 && len > 0) atomicMin(p.lens + r, INT_MIN + i);
+        team.sync();
+        if (i < kSmallNames) {
+            rows[i] = r;
+            lens[i] = len > 0 && __ldcg(p.lens + r) == INT_MIN + i ? len : 0;
+        }
+        __syncthreads();
+        const int ways = max(1, T::kWarps / p.n);
+        for (int k = gw / ways; k < p.n; k += T::kWarps / ways)
+            let_go(rows[k], (lens[k] + rest) >> p.lg, 128 * (gw % ways), 128 * ways);
+        team.sync();
+        if (team.rank == 0 && len > 0) p.lens[r] = 0;  // (every mark has been compared)
+    } else {
+        // request gw + kWarps (lane + 32 u) is this lane's u-th, and its warp's to free
+        int len[kPer], req[kPer];
 #pragma unroll
-    for (int u = 0; u < PER; ++u)
-        if (len[u] > 0) atomicMin(p.lens + req[u], INT_MIN + gw + T::kWarps * (lane + 32 * u));
-    team.sync();
+        for (int u = 0; u < kPer; ++u) len[u] = length_of(gw + T::kWarps * (lane + 32 * u), &req[u]);
+        team.sync();
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int i = gw + T::kWarps * (lane + 32 * u);
-        const bool mine = len[u] > 0 && __ldcg(p.lens + req[u]) == INT_MIN + i;
-        unsigned todo = __ballot_sync(0xffffffffu, mine);
-        while (todo) {
-            const int src = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int r = __shfl_sync(0xffffffffu, req[u], src);
-            const int nb = (__shfl_sync(0xffffffffu, len[u], src) + rest) >> p.lg;
-            int32_t *row = p.table + (size_t)r * p.max_blocks;
-            for (int e0 = lane; e0 < nb; e0 += 128) {
-                int b[4];
+        for (int u = 0; u < kPer; ++u)
+            if (len[u] > 0) atomicMin(p.lens + req[u], INT_MIN + gw + T::kWarps * (lane + 32 * u));
+        team.sync();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) b[q] = e0 + 32 * q < nb ? row[e0 + 32 * q] : 0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (e0 + 32 * q < nb) {
-                        row[e0 + 32 * q] = -1;
-                        if (b[q] >= 0 && b[q] < p.num_blocks)
-                            atomicSub(p.refs + b[q], 1);
-                        else
-                            bad = true;
-                    }
+        for (int u = 0; u < kPer; ++u) {
+            const int i = gw + T::kWarps * (lane + 32 * u);
+            const bool mine = len[u] > 0 && __ldcg(p.lens + req[u]) == INT_MIN + i;
+            unsigned todo = __ballot_sync(0xffffffffu, mine);
+            while (todo) {
+                const int src = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int r = __shfl_sync(0xffffffffu, req[u], src);
+                let_go(r, (__shfl_sync(0xffffffffu, len[u], src) + rest) >> p.lg, 0, 128);
             }
         }
-    }
-    team.sync();
-    // (every mark has been compared)
+        team.sync();
 #pragma unroll
-    for (int u = 0; u < PER; ++u)
-        if (len[u] > 0) p.lens[req[u]] = 0;
+        for (int u = 0; u < kPer; ++u)
+            if (len[u] > 0) p.lens[req[u]] = 0;
+    }
 
     // the blocks without a holder, in the order of their ids
     int b0, b1;
@@ -540,7 +588,9 @@ __global__ void __launch_bounds__(kThr) compact_kernel(const CompactParams p) {
     team.sync();
     const int cap = p.max_blocks << p.lg, rest = (1 << p.lg) - 1;
     const bool in_place = p.table_out == p.table;
-    for (int r0 = 4 * gw; r0 < p.R; r0 += 4 * T::kWarps) {  // four requests a warp
+    // four requests a warp, or several warps for their entries where there are few
+    const int fours = (p.R + 3) / 4, ways = max(1, T::kWarps / fours);
+    for (int r0 = gw / ways * 4; r0 < p.R; r0 += T::kWarps / ways * 4) {
         int len = lane < 4 && r0 + lane < p.R ? p.lens[r0 + lane] : 0;
         if (len < 0 || len > cap) {
             bad = true;
@@ -552,7 +602,7 @@ __global__ void __launch_bounds__(kThr) compact_kernel(const CompactParams p) {
             nb[q] = (__shfl_sync(0xffffffffu, len, q) + rest) >> p.lg;
             if (in_place) last = max(last, nb[q]);
         }
-        for (int e = lane; e < last; e += 32) {
+        for (int e = lane + 32 * (gw % ways); e < last; e += 32 * ways) {
             int b[4], to[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
