@@ -509,7 +509,11 @@ int api_call_workspace(cudaStream_t stream, size_t bytes, void **ptr) {
     int dev, rc;
     if ((rc = current_device(&dev))) return rc;
     std::lock_guard<std::mutex> lk(g_mu);
-    return get_call_workspace(dev, stream, bytes, ptr);
+    try {
+        return get_call_workspace(dev, stream, bytes, ptr);
+    } catch (const std::bad_alloc &) {
+        return fail(KVATTN_ERR_OOM, "no host memory for a workspace's record");
+    }
 }
 
 int api_encode_bf16_3d(CUtensorMap *m, const void *base, const cuuint64_t *dims,

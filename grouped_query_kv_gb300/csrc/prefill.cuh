@@ -1195,9 +1195,9 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 const auto rk = rc;
                 if (go && visit) go = slot_ready();
                 if (go && own && first) go = mbar_wait_warp(&q_full[s], units_q++ & 1, abort_flag);
-                if (go && own && after_few && tiles[s] > 0) {
-                    go = mbar_wait_warp(&pv_done[s], (tiles[s] - 1) & 1, abort_flag);
+                if (go && own && after_few) {  // (P V of the last few rows was the other warp's)
                     after_few = false;
+                    if (tiles[s] > 0) go = mbar_wait_warp(&pv_done[s], (tiles[s] - 1) & 1, abort_flag);
                 }
                 if (go && (s == 1 || !first_turn)) go = mbar_wait_warp(&turn[s], s == 0 ? it ^ 1 : it, abort_flag);
                 if (go && owed == 1) go = mbar_wait_warp(&p_full[s], (tiles[s] - 1) & 1, abort_flag, wlim);
@@ -1661,16 +1661,16 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                     *reinterpret_cast<float2 *>(p.ws_ml + at * 2) =
                         make_float2(m == -INFINITY ? -INFINITY : m * p.sl, l);
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {  // (unrolled, it spills at D = 256)
-                    float o[16];
-                    tmem_ld16(o_t + c * 16, o);
+                for (int c = 0; c < D / 32; ++c) {  // (unrolled, it spills at D = 256)
+                    float o[32];
+                    tmem_ld32(o_t + c * 32, o);
                     tmem_ld_wait();
                     if (tok < end_tok) {
-                        uint32_t w[16];
+                        uint32_t w[32];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i]);
-                        st_global_32b(dst + c * 16, w);
-                        st_global_32b(dst + c * 16 + 8, w + 8);
+                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i]);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) st_global_32b(dst + c * 32 + i, w + i);
                     }
                 }
                 tc_fence_before();

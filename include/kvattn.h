@@ -685,15 +685,18 @@ KVATTN_API int kv_append_rope(const void *q, const void *k, const void *v,
  * cu_seqlens[b+1] <= N is skipped, one whose length is outside [0, max_blocks *
  * block_size] gets zeros, a table entry outside [0, num_blocks) that holds
  * attended positions reads as a block of zeros; all three set
- * KVATTN_ERR_DEVICE_BOUNDS.  Entries and pool rows at and past a length, and
- * those before every window, may hold anything; of sequences whose rows overlap
- * either may have written them.
+ * KVATTN_ERR_DEVICE_BOUNDS.  A sequence's q rows and the pool rows that some
+ * token of it attends must hold finite values; entries and pool rows at and past
+ * its length, and those before its tokens' windows, may hold anything.  Of
+ * sequences whose rows overlap either may have written them.
  *
  * Scores, maxima and sums are held in fp32 (scale * q . K must stay finite
  * there), the weights enter the second product as bf16, unnormalised, and the
- * result is rounded once more.  The same inputs give the same bits.  The
- * workspace (41 MB on a GPU of 152 SMs at D = 128 and 256, 21 MB at D = 64) is the
- * stream's, or of a captured call's own, as for gqa_decode_attn_paged_fp8.
+ * result is rounded once more.  The same call gives the same bits; how a
+ * request's keys are divided, and with it the rounding, depends on the others'
+ * lengths.  The workspace (41 MB on a GPU of 152 SMs at D = 128 and 256, 21 MB at
+ * D = 64) is the stream's, or of a captured call's own, as for
+ * gqa_decode_attn_paged_fp8.
  * D in {64, 128, 256}; block_size a power of two in [16, 2^20]; 1 <= N <= 2^28.
  */
 KVATTN_API int gqa_extend_attn(const void *q, const void *k_pool, const void *v_pool,

@@ -235,6 +235,45 @@ def test_scores_that_grow_along_the_keys_move_the_maximum():
     c.check()
 
 
+@pytest.mark.parametrize("bs", [16, 64, 256])
+@pytest.mark.parametrize("causal,window", [(True, None), (True, 1), (True, 100), (True, 700), (False, None)])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 4), (64, 8, 1), (128, 64, 8), (128, 3, 1), (256, 16, 1), (256, 2, 2)])
+def test_few_tokens_on_average_and_some_of_many(D, Hq, Hkv, causal, window, bs):
+    # (units of few rows and of many in one call, in every order)
+    new = [1, 300, 1, 2, 0, 1, 70, 1, 1, 3, 129, 1, 4, 31, 1, 33, 8, 1] + [0] * 300
+    old = [2000, 100, 127, 128, 5, 0, 600, 129, 383, 1, 0, 1300, 255, 7, 1, 0, 77, 640] + [0, 17] * 150
+    kv = [n + o for n, o in zip(new, old)] if causal else old
+    c = Case(new, kv, Hq, Hkv, D, bs, seed=bs + D, causal=causal, window=window)
+    ref = c.ref()
+    for ctas in (0, 1, 3, 40):
+        g.set_tuning(0, ctas)
+        try:
+            before = torch.full((c.q.shape[0], Hq, D), 7.25, dtype=torch.bfloat16, device="cuda")
+            out = c.run(out=before.clone())
+            g.check_device_error()
+            c.check(out, before, ref)
+        finally:
+            g.set_tuning(0, 0)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 16, 16), (128, 64, 8), (128, 20, 1), (256, 16, 1), (256, 32, 1)])
+def test_steps_back_to_back(D, Hq, Hkv):
+    cases = [Case([1] * 40, [(37 * i + 11 * s) % 900 + 1 for i in range(40)], Hq, Hkv, D, 16, seed=s) for s in range(3)]
+    outs = [c.run() for _ in range(10) for c in cases]
+    g.check_device_error()
+    for i, c in enumerate(cases):
+        ref = c.ref()
+        for o in outs[i::3]:
+            c.check(o, ref=ref)
+            assert torch.equal(o[:40], outs[i][:40])
+
+
+def test_heads_that_fill_no_power_of_two():
+    for Hq, Hkv, D in ((96, 1, 128), (130, 1, 64), (24, 2, 128), (200, 2, 256), (33, 1, 128), (18, 6, 64)):
+        Case([1, 1, 2, 0], [300, 129, 77, 5], Hq, Hkv, D, 16, seed=Hq).check()
+        Case([40, 1, 150], [300, 129, 200], Hq, Hkv, D, 64, seed=Hq, causal=False).check()
+
+
 def test_many_sequences_most_of_them_empty():
     rng = np.random.RandomState(1)
     new = [0] * 3000
@@ -319,14 +358,14 @@ def test_bad_bounds_lengths_and_entries_are_reported_and_the_others_served():
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_a_wait_that_runs_out_reports_and_the_next_call_is_clean(D):
-    c = Case([200, 1], [700, 900], 8, 2, D, 64, seed=11)
-    g.set_wait_limit(1)
-    try:
-        c.run()
-        _raises(g.KVATTN_ERR_TIMEOUT)
-    finally:
-        g.set_wait_limit(0)
-    c.check()
+    for c in (Case([200, 1], [700, 900], 8, 2, D, 64, seed=11), Case([1] * 9, [700, 900, 5] * 3, 8, 2, D, 64, seed=12)):
+        g.set_wait_limit(1)
+        try:
+            c.run()
+            _raises(g.KVATTN_ERR_TIMEOUT)
+        finally:
+            g.set_wait_limit(0)
+        c.check()
 
 
 def test_graphs_side_by_side_other_streams_and_release():

@@ -500,3 +500,150 @@ def test_copy_blocks_past_32_bits():
     for i in range(2):
         assert torch.equal(pools[i][nblk - 1], a[i]) and torch.equal(pools[i][1], a[i])
         assert not bool(pools[i][2:nblk - 2].any())
+
+
+def test_few_rows_of_many_blocks_and_many_rows_of_few():
+    for R, maxb, nblk, bs in ((4, 9000, 30000, 16), (1500, 3, 50000, 16), (300, 40, 33000, 32)):
+        pool = Pool(R, maxb, nblk, bs)
+        random.Random(R).shuffle(pool.free)
+        for r in range(0, R, 2):
+            pool.grow(r, maxb * bs - r % 5)
+        dev = Device(pool)
+        parents, children = list(range(0, R, 2))[:R // 2], list(range(1, R, 2))
+        copies, _ = g.kv_fork_blocks(*dev.args(), _i32(parents), _i32(children), bs)
+        g.check_device_error()
+        assert np.array_equal(copies.cpu().numpy(), pool.fork(parents, children))
+        dev.same(pool)
+        rows = parents[::2] + children[1::2]
+        g.kv_free_blocks(*dev.args(), _i32(rows), bs)
+        g.check_device_error()
+        pool.drop(rows)
+        dev.same(pool)
+        moves, remap = g.kv_compact_blocks(*dev.args(), bs)
+        g.check_device_error()
+        want_moves, want_remap = pool.compact()
+        assert np.array_equal(moves.cpu().numpy(), want_moves) and np.array_equal(remap.cpu().numpy(), want_remap)
+        dev.same(pool)
+
+
+def test_a_request_s_life_forked_copied_compacted_and_dropped():
+    # blocks, rows, attention; a fork that goes its own way; compaction; the drop
+    Hq, Hkv, D, bs, R, nblk = 8, 2, 128, 16, 4, 24
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, lens = torch.full((R, 8), -1, **i32), torch.zeros(R, **i32)
+    refs, free = torch.zeros(nblk, **i32), torch.arange(nblk - 1, -1, -1, **i32)
+    free[[3, 20]] = free[[20, 3]]
+    count = torch.tensor([nblk], **i32)
+    pools = [torch.full((nblk, Hkv, bs, D), NAN, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cos, sin = rope_tables(200, D)
+    hist = {r: [torch.zeros((0, Hkv, D), dtype=torch.float64, device="cuda")] * 2 for r in range(R)}
+
+    def step(new, seed):
+        n = sum(new)
+        cu, slots, _ = g.kv_block_tables(lens, _i32(new), table, free, count, bs, n)
+        qkv = _normal((n, Hq + 2 * Hkv, D), seed)
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        pos = torch.cat([torch.arange(m, **i32) + lens[r] for r, m in enumerate(new)])
+        qo = g.kv_append_rope(q, k, v, pos, cos, sin, slots, *pools)
+        _, ko = g.qk_norm_rope(q, k, pos, cos, sin)
+        lens.add_(_i32(new))
+        out = g.gqa_extend_attn(qo, *pools, table, lens, cu, 0.1)
+        g.check_device_error()
+        at = 0
+        for r, m in enumerate(new):
+            if not m:
+                continue
+            hist[r] = [torch.cat([h, x[at:at + m].double()]) for h, x in zip(hist[r], (ko, v))]
+            K, V = (h.repeat_interleave(Hq // Hkv, 1) for h in hist[r])
+            e = K.shape[0]
+            s = torch.einsum("ihd,jhd->hij", qo[at:at + m].double(), K) * 0.1
+            s = s.masked_fill(torch.arange(e, device="cuda")[None, :] > torch.arange(e - m, e, device="cuda")[:, None],
+                              -math.inf)
+            w = torch.softmax(s, 2)
+            ref, mag = torch.einsum("hij,jhd->ihd", w, V), torch.einsum("hij,jhd->ihd", w, V.abs())
+            o = out[at:at + m].double()
+            assert float(((o - ref).abs() - (2.0 ** -8 + 2.0 ** -10) * mag - 2.0 ** -8 * o.abs()).max()) <= 0
+            at += m
+
+    step([37, 20, 0, 0], 1)
+    copies, _ = g.kv_fork_blocks(table, lens, refs, free, count, _i32([0, 1]), _i32([2, 3]), bs)
+    g.kv_copy_blocks(*pools, copies)
+    for a, b in ((0, 2), (1, 3)):
+        hist[b] = list(hist[a])
+    step([1, 13, 30, 1], 2)
+    step([1, 1, 1, 1], 3)
+    g.kv_free_blocks(table, lens, refs, free, count, _i32([0]), bs)  # its fork keeps the shared blocks
+    hist[0] = [h[:0] for h in hist[0]]
+    moves, _ = g.kv_compact_blocks(table, lens, refs, free, count, bs)
+    g.kv_copy_blocks(*pools, moves)
+    used = nblk - int(count)
+    assert int(table.max()) < used
+    for p in pools:  # nothing is read from behind the used blocks
+        p[used:] = NAN
+    step([0, 1, 20, 2], 4)
+    step([5, 1, 1, 1], 5)
+    g.kv_free_blocks(table, lens, refs, free, count, _i32([0, 1, 2, 3]), bs)
+    g.check_device_error()
+    assert int(count) == nblk and not bool(refs.any()) and sorted(free.tolist()) == list(range(nblk))
+
+
+def test_on_another_stream_and_captured():
+    Hq, Hkv, D, bs = 8, 2, 128, 16
+    q, k, v, pos, cos, sin, qw, kw = rope_inputs(64, Hq, Hkv, D, D, 500, seed=3)
+    slots = torch.randperm(128, generator=_gen(1), device="cuda")[:64]
+    pool = Pool(40, 6, 200, bs)
+    for r in range(20):
+        pool.grow(r, 5 + 4 * r)
+    dev = Device(pool)
+    start = [t.clone() for t in dev.args()]
+    parents, children = _i32(range(20)), _i32(range(20, 40))
+    pools = [_normal((200, Hkv, bs, D), 9 + i) for i in range(2)]
+    first = [p.clone() for p in pools]
+    copies = torch.zeros((20, 2), dtype=torch.int32, device="cuda")
+    qo, moves, remap = torch.zeros_like(q, memory_format=torch.contiguous_format), None, None
+    moves, remap = torch.zeros((100, 2), dtype=torch.int32, device="cuda"), torch.zeros(200, dtype=torch.int32, device="cuda")
+
+    def path(**more):
+        g.kv_append_rope(q, k, v, pos, cos, sin, slots, *pools, q_weight=qw, k_weight=kw, q_out=qo, **more)
+        g.kv_fork_blocks(*dev.args(), parents, children, bs, copies=copies, **more)
+        g.kv_copy_blocks(*pools, copies, **more)
+        g.kv_free_blocks(*dev.args(), parents, bs, **more)
+        g.kv_compact_blocks(*dev.args(), bs, moves=moves, remap=remap, **more)
+        g.kv_copy_blocks(*pools, moves, **more)
+
+    def reset():
+        for t, s in zip(dev.args(), start):
+            t.copy_(s)
+        for p, f in zip(pools, first):
+            p.copy_(f)
+        qo.zero_()
+
+    def state():
+        torch.cuda.synchronize()
+        g.check_device_error()
+        return [t.clone() for t in (*dev.args(), *pools, qo, copies, moves, remap)]
+
+    path()
+    want = state()
+    pool.fork(range(20), range(20, 40))
+    pool.drop(range(20))
+    pool.compact()
+    dev.same(pool)
+    side = torch.cuda.Stream()
+    reset()
+    torch.cuda.synchronize()
+    busy = torch.cuda._sleep  # the current stream is busy meanwhile
+    busy(20_000_000)
+    path(stream=side)
+    for a, b in zip(state(), want):
+        assert torch.equal(a, b)
+    reset()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=side):
+        path()
+    for _ in range(3):
+        reset()
+        gr.replay()
+        for a, b in zip(state(), want):
+            assert torch.equal(a, b)
