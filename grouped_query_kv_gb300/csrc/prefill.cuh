@@ -187,7 +187,7 @@ struct PfCfg {
     static constexpr int off_q = 0;
     static constexpr int off_ring = NQ * QT;
     static constexpr int off_bar = off_ring + NS * SLOT;
-    static constexpr int nbar = 2 * NS + 2 * 2 + 3 * 2 + 2 * kDesc + 1 + 2 + (PG ? 2 : 0);
+    static constexpr int nbar = 2 * NS + 2 * 2 + 3 * 2 + 2 * kDesc + 1 + 2 + (PG ? 1 : 0);
     static constexpr int off_misc = off_bar + nbar * 8;          // tmem base, abort flag
     static constexpr int off_unit = (off_misc + 32 + 15) / 16 * 16;
     static constexpr int off_cnt = off_unit + kDesc * (int)sizeof(UnitOf<PG>);
@@ -590,10 +590,10 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2;
     uint64_t *u_full = pv_done + 2, *u_empty = u_full + kDesc, *drain = u_empty + kDesc;
     uint64_t *turn = drain + 1;  // the MMA warps' turns
-    // (few rows) the softmax warps' steps of a join, and its end
-    [[maybe_unused]] uint64_t *join = turn + 2, *joined = join + 1;
+    [[maybe_unused]] uint64_t *join = turn + 2;  // (few rows) the softmax warps' steps of a join
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::off_misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::off_misc + 16);
+    [[maybe_unused]] volatile int *joined = abort_flag + 1;  // (few rows) units joined so far
     Unit *units = reinterpret_cast<Unit *>(smem + C::off_unit);
     int *cnt = reinterpret_cast<int *>(smem + C::off_cnt);  // [kBuckets] full, [kBuckets] rest
     unsigned long long *sum_pairs = reinterpret_cast<unsigned long long *>(smem + C::off_sum);
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         mbar_init(drain, 2);  // warps 1 and 2
         if (PG) {
             mbar_init(join, 4 * NQ);
-            mbar_init(joined, 1);
+            *joined = 0;
         }
         *abort_flag = 0;
         *sum_pairs = 0;
@@ -970,19 +970,27 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         bool ok = true;
         uint32_t qn[2] = {0, 0};     // query tiles issued
         typename C::KRing rc;
-        [[maybe_unused]] uint32_t joins = 0, seen = 0;  // units of few rows so far, joins waited for
-        [[maybe_unused]] auto joins_seen = [&](uint32_t n) -> bool {
-            for (; seen < n; ++seen)
-                if (!mbar_wait_warp(joined, seen & 1, abort_flag)) return false;
-            return true;
+        [[maybe_unused]] int joins = 0;  // units of few rows so far
+        // (a count, not a barrier's phase, which says nothing to who comes late)
+        [[maybe_unused]] auto joins_over = [&]() -> bool {
+            for (uint32_t it = 0; it < KVATTN_SPIN_LIMIT; ++it) {
+                if (__all_sync(0xffffffffu, *joined >= joins)) {
+                    __threadfence_block();
+                    return true;
+                }
+                if ((it & 255u) == 255u && __any_sync(0xffffffffu, *abort_flag)) return false;
+                __nanosleep(32);
+            }
+            *abort_flag = 1;
+            return false;
         };
         auto load_q = [&](const Unit &u) -> bool {
             if constexpr (FEW && NQ == 2) {
-                // Units of few rows are joined in query tile 1's place: the last one's
-                // join is over before another's rows go there (and seen to be, one
-                // behind, so that every phase of the barrier is waited for in turn).
-                if (joins > (u.few ? 1 : 0) && !joins_seen(u.few ? joins - 1 : joins)) return false;
-                if (u.few) ++joins;
+                // units of few rows are joined in query tile 1's place
+                if (u.few)
+                    ++joins;
+                else if (u.n[1] > 0 && joins > 0 && !joins_over())
+                    return false;
             }
 #pragma unroll(PG ? 2 : 1)
             for (int s = 0; s < NQ; ++s) {
@@ -1778,10 +1786,18 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                                          o, 1.f / sum);
                         }
                     }
+                    // (the next to write here is a copy of query rows)
+                    fence_proxy_async_smem();
                     if (!(ok = all_here())) break;
                 }
                 if (!ok) break;
-                if (copy == 0 && lane == 0) mbar_arrive(NQ == 2 ? joined : &q_empty[0]);
+                if (copy == 0 && lane == 0) {
+                    __threadfence_block();
+                    if constexpr (NQ == 2)
+                        *joined = *joined + 1;
+                    else
+                        mbar_arrive(&q_empty[0]);
+                }
                 base += 2 * nmax;
                 continue;
             }
