@@ -185,13 +185,16 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     p.hpg = 1;
     while (p.hpg < kRows && p.G % (2 * p.hpg) == 0) p.hpg *= 2;
     p.tpt = kRows / p.hpg;
-    // Few tokens a request: all heads of a group in one tile, by as many tokens as
-    // are left a power of two, so that a request's keys are read once for the group
-    // whatever its size; else every row of the tile counts.
+    // Groups of no power of two: with up to two units' tokens a request on average,
+    // all heads of a group in one tile, by a power of two of tokens, so that a
+    // request's keys are read once for the group; beyond, every row of the tile counts.
+    // 16 requests of 4096 positions, one pass / as many as it takes: 20 heads over 4
+    // of 128 with 1 token 37 / 81 us, 64 tokens 72 / 125, 128 126 / 133; 24 over 2 of
+    // 128 with 32 tokens 48 / 54, 64 75 / 67; 48 over 1 of 256 with 4 38 / 38, 8 50 / 46.
     if (p.G <= kRows && p.hpg < p.G) {
         int tpt = 1;
         while (2 * tpt * p.G <= kRows) tpt *= 2;
-        if ((long long)N <= (long long)B * tpt) {
+        if ((long long)N <= 2LL * B * tpt * (D == 256 ? 1 : 2)) {
             p.hpg = p.G;
             p.tpt = tpt;
         }
@@ -201,9 +204,13 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     p.q_bytes = p.rows * D * 2;
     p.tpu_lg = 0;
     while (1 << p.tpu_lg < (D == 256 ? 1 : 2) * p.tpt) ++p.tpu_lg;
-    int few = 0;  // tokens whose rows fit a quarter of the tile, where a request has no more on average
-    if (p.hpg <= 32 && (long long)N * p.hpg <= 32LL * B)
-        for (few = 1; 2 * few * p.hpg <= 32;) few *= 2;
+    // Units of few rows in a form of their own where a request has few on average
+    // (with it / without, 16 requests of 4096 positions: 16 heads of 64 56 / 91 us, 32
+    // over 2 of 64 21 / 22, with 2 tokens 25 / 22; 64 over 8 of 128 56 / 59, with 2 60 /
+    // 60, 32 over 2 of 128 30 / 26; at D = 256 it loses).
+    int few = 0;
+    if (D < 256 && p.hpg <= 32 && (long long)N * p.hpg <= (D == 64 ? 16LL : 8LL) * B)
+        for (few = 1; 2 * few * p.hpg <= 32;) few *= 2;  // tokens whose rows fit a quarter of the tile
     p.few_tok = few;
     p.few_bytes = few * p.hpg * D * 2;
     p.window = window < lmax ? window : lmax;
@@ -261,8 +268,7 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
             if (e == cudaSuccess) e = launch_merge<128>(m, p.few_tok > 0, ctas, parts, stream);
             break;
         default:
-            e = p.few_tok ? launch_extend_few(D, tmq, tmk, tmv, &p, ctas, stream, tmq4)
-                          : launch_pf<256, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
+            e = launch_pf<256, true, false>(tmq, tmk, tmv, p, ctas, stream, tmq4);
             if (e == cudaSuccess) e = launch_merge<256>(m, p.few_tok > 0, ctas, parts, stream);
             break;
     }

@@ -8,11 +8,8 @@ namespace kvattn {
 cudaError_t launch_extend_few(int D, const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                               const void *params, int num_ctas, cudaStream_t stream, const CUtensorMap &tmq4) {
     const PagedPrefillParams &p = *static_cast<const PagedPrefillParams *>(params);
-    switch (D) {
-        case 64: return launch_pf<64, true, true>(tmq, tmk, tmv, p, num_ctas, stream, tmq4);
-        case 128: return launch_pf<128, true, true>(tmq, tmk, tmv, p, num_ctas, stream, tmq4);
-        default: return launch_pf<256, true, true>(tmq, tmk, tmv, p, num_ctas, stream, tmq4);
-    }
+    return D == 64 ? launch_pf<64, true, true>(tmq, tmk, tmv, p, num_ctas, stream, tmq4)
+                   : launch_pf<128, true, true>(tmq, tmk, tmv, p, num_ctas, stream, tmq4);
 }
 
 }  // namespace kvattn

@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                    const __grid_constant__ QuarterMap<PG> tmq4) {
     using C = PfCfg<D, PG>;
     using Unit = UnitOf<PG>;
+    static_assert(!FEW || (PG && C::NQ == 2), "few rows: two query tiles over a pool");
     constexpr int NQ = C::NQ, NS = C::NS, CPT = C::CPT;
 
     extern __shared__ uint8_t smem_raw[];
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             mbar_init(&u_empty[s], (NQ == 2 ? 3 : 4) + 4 * NQ);
         }
         mbar_init(drain, 2);  // warps 1 and 2
-        if (PG) {
+        if (FEW) {
             mbar_init(join, 4 * NQ);
             *joined = 0;
         }
@@ -985,7 +986,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             return false;
         };
         auto load_q = [&](const Unit &u) -> bool {
-            if constexpr (FEW && NQ == 2) {
+            if constexpr (FEW) {
                 // units of few rows are joined in query tile 1's place
                 if (u.few)
                     ++joins;
@@ -1310,7 +1311,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                     tc_fence_after();
                     const int keys = min(kRows, last_key(p, w.u, 0) - w.j * kRows);
                     if constexpr (std::is_same_v<std::remove_const_t<decltype(r)>, typename C::KRing>) {
-                        qk(buf, r, keys, w.j == w.u.n[0] - 1 && !(FEW && few_of(w.u)));
+                        qk(buf, r, keys, w.j == w.u.n[0] - 1);
                     } else {
                         pv(buf, r, keys, w.j == 0);
                         if (elect_one()) {  // (the lane that issued)
@@ -1486,9 +1487,9 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             return true;
         };
         if constexpr (FEW) {
-            for (int j = s; u.few && j < n; j += NQ, ++g) {
-            const int buf = NQ == 2 ? s : (int)(g & 1);
-            const uint32_t par = (uint32_t)((NQ == 2 ? g : g >> 1) & 1);
+            for (int j = s; u.few && j < n; j += 2, ++g) {
+            const int buf = s;
+            const uint32_t par = (uint32_t)(g & 1);
             ok = mbar_wait_warp(&s_full[buf], par, abort_flag, wlim);
             if (!ok) break;
             tc_fence_after();
@@ -1700,7 +1701,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 constexpr int COPIES = 4 * NQ, GROUP = C::QT / (COPIES * D * 4), V = D / 32;
                 const int copy = s * 4 + q4, rows = (end_tok - first_tok) * p.hpg;
                 float *exch = reinterpret_cast<float *>(cnt);                     // [COPIES][32]
-                float *part = reinterpret_cast<float *>(qbuf + (NQ - 1) * C::QT);  // [COPIES][GROUP][D]
+                float *part = reinterpret_cast<float *>(qbuf + C::QT);  // [COPIES][GROUP][D]: query tile 1's place
                 auto all_here = [&]() -> bool {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(join);
@@ -1708,8 +1709,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 };
                 const bool own = n > s;
                 if (own) {
-                    const int buf = NQ == 2 ? s : (int)((g - 1) & 1);
-                    ok = mbar_wait_warp(&pv_done[buf], (uint32_t)((NQ == 2 ? g - 1 : (g - 1) >> 1) & 1), abort_flag, wlim);
+                    ok = mbar_wait_warp(&pv_done[s], (uint32_t)((g - 1) & 1), abort_flag, wlim);
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -1793,10 +1793,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 if (!ok) break;
                 if (copy == 0 && lane == 0) {
                     __threadfence_block();
-                    if constexpr (NQ == 2)
-                        *joined = *joined + 1;
-                    else
-                        mbar_arrive(&q_empty[0]);
+                    *joined = *joined + 1;
                 }
                 base += 2 * nmax;
                 continue;
