@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThr) free_kernel(const FreeParams p) {
     };
     // A request named twice is freed once: the first name leaves the smallest mark in
     // its length.
-    if (p.n <= kSmallNames) {
+    if (NC == 1 || p.n <= kSmallNames) {
         // every CTA has the whole list, and all warps share the entries
         __shared__ int rows[kSmallNames], lens[kSmallNames];
         int r;
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const CopyPar
         const unsigned long long pair = first + more;
         dst[i] = -1;
         if (pair < (unsigned long long)p.n) {
-            const int2 m = __ldg(reinterpret_cast<const int2 *>(p.copies) + pair);
+            const int2 m = reinterpret_cast<const int2 *>(p.copies)[pair];
             if (m.x >= 0 && m.y >= 0 && m.x < p.num_blocks && m.y < p.num_blocks) {
                 dst[i] = (long long)m.y * p.vecs + c;
                 k[i] = __ldcs(p.k + (long long)m.x * p.vecs + c);

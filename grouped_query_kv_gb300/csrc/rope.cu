@@ -66,8 +66,10 @@ __device__ __forceinline__ uint32_t bf_pair(float lo, float hi) {
 struct Four {
     float2 x, y;
 };
+// (Plain loads: a kernel that starts before the one in front of it ends may not take
+// what that one writes, or the one before it wrote, through the read-only path.)
 __device__ __forceinline__ Four load4(const float *src) {
-    const float4 f = __ldg(reinterpret_cast<const float4 *>(src));
+    const float4 f = *reinterpret_cast<const float4 *>(src);
     return {make_float2(f.x, f.y), make_float2(f.z, f.w)};
 }
 __device__ __forceinline__ Four times(Four a, Four b) { return {mul2(a.x, b.x), mul2(a.y, b.y)}; }

@@ -627,7 +627,8 @@ KVATTN_API int gqa_decode_attn_paged_fp8(const void *q, const void *k_codes, con
  *   rope_dim   : a multiple of 16 in [16, D]; eps >= 0 and finite
  * A row with a negative position (padding) becomes zeros; so does one whose
  * position is max_pos or more, which sets KVATTN_ERR_DEVICE_BOUNDS.  Squares
- * are summed in fp32, which values of 2^60 and more overflow.
+ * are summed in fp32, which values of 2^60 and more overflow (and below 2^-63
+ * vanish: with eps = 0 a head of such values alone has no norm).
  * D in {64, 128, 256}; 1 <= N <= 2^28.
  */
 KVATTN_API int qk_norm_rope(const void *q, const void *k, const int32_t *positions,
@@ -745,13 +746,14 @@ KVATTN_API int gqa_cross_attn(const void *q, const void *k_pool, const void *v_p
  *                 rows kv_copy_blocks is to copy in each layer's pools, or
  *                 (-1, -1) where there is nothing to copy
  *   free_count, free_count_out : int32 [1]; may be the same word
- * Blocks are taken in the order of i.  A fork is served if both rows are within
- * [0, R), the child's length is 0, no earlier fork of the call has the same
- * child, its parent's row is not a fork's of the call either, the parent's
- * length is within its row, and the blocks wanted by it and all forks before it
- * are no more than free_count[0].  One that is not changes nothing, has copies
- * (-1, -1) and sets KVATTN_ERR_DEVICE_BOUNDS, and so does a block id outside
- * [0, num_blocks): a table entry is copied as it is, without a count.
+ * Blocks are taken in the order of i.  Of the forks whose rows are within [0, R)
+ * and whose child's length is 0, one is served if none of them before it has the
+ * same child, none of them has its parent for a child, the parent's length is
+ * within its row, and there is a block for it, if it wants one, beside those that
+ * forks before it want.  One that is not changes nothing, has copies (-1, -1) and
+ * sets KVATTN_ERR_DEVICE_BOUNDS, and so does a block id outside [0, num_blocks): a
+ * table entry is copied as it is, without a count.  A free_count[0] outside [0,
+ * num_free] is left as it is and counts as 0.
  */
 KVATTN_API int kv_fork_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *refs,
                               const int32_t *free_blocks, const int32_t *free_count,
