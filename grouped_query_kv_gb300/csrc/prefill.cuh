@@ -1557,9 +1557,12 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 hi = tq + 1 - kb, lo = tq + 1 - p.window - kb;
                 sure_hi = first_tok + 1 - kb, sure_lo = end_tok - p.window - kb;
             }
-            if constexpr (FEW) {
-                // 32 columns at a time, twice: beside the join 128 scores in registers
-                // would spill, and with 227 KB of shared memory what spills goes to L2
+            // (a whole tile that hides nothing takes the straight path)
+            const bool whole = !FEW && keys == kRows && kRows <= sure_hi && sure_lo <= 0;
+            if (PG && !whole) {
+                // 32 columns at a time, twice: code of a few hundred instructions (unrolled
+                // over the tile its first turn, and each after the straight path's, waits for
+                // instructions)
                 if (alive) {
                     auto scores = [&](int c, float (&x)[32]) {
                         tmem_ld32(s_t + c * 32, x);
@@ -1585,12 +1588,10 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                         weigh(x, s_t + c * 16);
                     }
                 }
-            } else {
+            } else if constexpr (!FEW) {
             if (!PG || alive) {
-            // (a whole tile that hides nothing takes the straight path)
-            const bool whole = keys == kRows && kRows <= sure_hi && sure_lo <= 0;
             float mn;
-            if (whole) {
+            if (PG || whole) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, v + c * 32);
                 tmem_ld_wait();
@@ -1646,7 +1647,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 }
                 tmem_st16u(s_t + c * 16, pk);
             };
-            if (whole) {
+            if (PG || whole) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) weights(c);
             } else {
