@@ -44,38 +44,36 @@ struct MergeParams {
     const int4 *split;  // per CTA: (packed row, tokens, first head, pieces) of the unit it leaves unfinished
     uint16_t *out;
     int Hq, hpg, tpt;
-    int slot_rows;      // rows of a workspace slot
 };
 
 constexpr int kMergeThreads = 256;
 
-// (by a warp) one row from its n partial results, the i-th at row at(i) of the
-// workspace: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, M = max m_i.
-// The first AHEAD of them are loaded with their (m, l), before it is known what
-// they weigh, the others MORE at a time.
-template <int D, int AHEAD, int MORE, class At>
-__device__ __forceinline__ void join_row(const float *ws_o, const float *ws_ml, At at, int n, uint16_t *out) {
+// (by a warp) row `row` of a unit from its n partial results, the i-th in workspace
+// slot at(i), where units have few rows.  The first AHEAD of them are loaded with
+// their (m, l), before it is known what they weigh, the others MORE at a time.
+template <int D, class At>
+__device__ __forceinline__ void join_row(const float *ws_o, const float *ws_ml, int row, At at, int n,
+                                         uint16_t *out) {
+    constexpr int AHEAD = 8, MORE = 4;
     constexpr int V = D / 32;  // values of a lane
     const int lane = threadIdx.x & 31;
     auto load = [&](int i, float *x) {
-        const float *src = ws_o + at(i) * D + lane * V;
+        const float *src = ws_o + Partial<D, true>::row(at(i), row) + lane * V;
         if constexpr (V == 2) {
             const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
             x[0] = f.x;
             x[1] = f.y;
         } else {
-#pragma unroll
-            for (int k = 0; k < V; k += 4) {
-                const float4 f = __ldcg(reinterpret_cast<const float4 *>(src + k));
-                x[k] = f.x;
-                x[k + 1] = f.y;
-                x[k + 2] = f.z;
-                x[k + 3] = f.w;
-            }
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
+            x[0] = f.x;
+            x[1] = f.y;
+            x[2] = f.z;
+            x[3] = f.w;
         }
     };
     auto ml_of = [&](int i) {
-        return i < n ? __ldcg(reinterpret_cast<const float2 *>(ws_ml) + at(i)) : make_float2(-INFINITY, 0.f);
+        return i < n ? __ldcg(reinterpret_cast<const float2 *>(ws_ml + Partial<D, true>::ml(at(i), row)))
+                     : make_float2(-INFINITY, 0.f);
     };
     float2 ml = ml_of(lane);
     float x[AHEAD][V];
@@ -125,24 +123,73 @@ __device__ __forceinline__ void join_row(const float *ws_o, const float *ws_ml, 
     store_row<V>(out + lane * V, o, 1.f / l);  // (every row attends something)
 }
 
-// Block (c, y): rows of the unit that CTA c leaves unfinished, a warp each.  What
-// bounds it is latency: of the record, then of (m, l) and the rows; with few tokens a
-// request, whose keys may be in many pieces, more of a row is in flight, else more
-// rows are (fewer registers a warp).
+// The same of units of many rows: up to 128 values from d0 on of four rows a warp, 8 of
+// every 64 a lane, since the rows' pieces of eight values are side by side.
+template <int D, class At>
+__device__ __forceinline__ void join_rows(const float *ws_o, const float *ws_ml, int row, At at, int n,
+                                          int d0, uint16_t *out, bool write) {
+    using P = Partial<D, false>;
+    constexpr int C = D > 64 ? 2 : 1;
+    const int d = d0 + (threadIdx.x & 31) / 4 * 8;
+    auto load = [&](int i, float (&x)[C][8]) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) ld_global_32b(ws_o + P::row(at(i), row) + (d / 8 + c * 8) * P::STEP, x[c]);
+    };
+    auto ml_of = [&](int i) { return __ldcg(reinterpret_cast<const float2 *>(ws_ml + P::ml(at(i), row))); };
+    float x[2][C][8];  // (two pieces at least; most have no more)
+    load(0, x[0]);
+    load(1, x[1]);
+    const float2 ml0 = ml_of(0), ml1 = ml_of(1);
+    float m = fmaxf(ml0.x, ml1.x);
+#pragma unroll 4
+    for (int i = 2; i < n; ++i) m = fmaxf(m, ml_of(i).x);
+    float o[C][8] = {}, l = 0.f;
+    auto add = [&](float2 ml, const float (&y)[C][8]) {
+        const float w = ml.y > 0.f ? fast_exp2(ml.x - m) : 0.f;
+        if (w == 0.f) return;  // (it held none of the row's keys, and may hold anything)
+        l += w * ml.y;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[c][k] = fmaf(w, y[c][k], o[c][k]);
+    };
+    add(ml0, x[0]);
+    add(ml1, x[1]);
+#pragma unroll 1
+    for (int i = 2; i < n; ++i) {
+        load(i, x[0]);
+        add(ml_of(i), x[0]);
+    }
+    const float inv = 1.f / l;  // (every row attends something)
+    if (write) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) store_row<8>(out + d + c * 64, o[c], inv);
+    }
+}
+
+// Block (c, y): rows of the unit that CTA c leaves unfinished.  What bounds it is
+// latency: of the record, then of (m, l) and the rows; with few tokens a request,
+// whose keys may be in many pieces, a warp takes a row, else four.
 template <int D, bool FEW>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
+    constexpr int AT_ONCE = FEW ? 1 : 4, COLS = FEW || D < 128 ? D : 128;
     pdl_launch_dependents();
     pdl_wait_prior();
     const int c = blockIdx.x;
     const int4 u = __ldcg(p.split + c);
     const int rows = u.w > 0 ? u.y * p.hpg : 0;
-    for (int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += gridDim.y * (kMergeThreads / 32)) {
+    auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+    const int warp = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    for (int r0 = warp / (D / COLS) * AT_ONCE; r0 < rows; r0 += gridDim.y * (kMergeThreads / 32) / (D / COLS) * AT_ONCE) {
+        const int r = FEW ? r0 : min(r0 + (int)(threadIdx.x & 3), rows - 1);
         const int t = r / p.hpg, h = r - t * p.hpg;
         const int row = t / p.tpt * kRows + t % p.tpt * p.hpg + h;
-        join_row<D, FEW ? 8 : 2, FEW ? 4 : 1>(p.ws_o, p.ws_ml,
-                       [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.slot_rows + row; }, u.w,
-                       p.out + ((size_t)(u.x + t) * p.Hq + u.z + h) * D);
+        uint16_t *out = p.out + ((size_t)(u.x + t) * p.Hq + u.z + h) * D;
+        if constexpr (FEW)
+            join_row<D>(p.ws_o, p.ws_ml, row, slot, u.w, out);
+        else
+            join_rows<D>(p.ws_o, p.ws_ml, row, slot, u.w, warp % (D / COLS) * COLS, out,
+                         r0 + (int)(threadIdx.x & 3) < rows);
     }
 }
 
@@ -157,7 +204,9 @@ cudaError_t launch_merge(const MergeParams &p, bool few, int ctas, int parts, cu
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, merge_kernel<D, true>, p) : cudaLaunchKernelEx(&cfg, merge_kernel<D, false>, p);
+    if constexpr (D < 256)
+        if (few) return cudaLaunchKernelEx(&cfg, merge_kernel<D, true>, p);
+    return cudaLaunchKernelEx(&cfg, merge_kernel<D, false>, p);
 }
 
 // 3-D map over a pool [num_blocks, Hkv, block_size, D]: dims (D, block_size,
@@ -267,9 +316,10 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     p.ws_ml = p.ws_o + rows * D;
     p.split = reinterpret_cast<int4 *>(p.ws_ml + rows * 2);
 
-    MergeParams m = {p.ws_o, p.ws_ml, p.split, p.out, Hq, p.hpg, p.tpt, slot_rows};
+    MergeParams m = {p.ws_o, p.ws_ml, p.split, p.out, Hq, p.hpg, p.tpt};
     const long long unit_rows = (long long)N * p.hpg < slot_rows ? (long long)N * p.hpg : slot_rows;
-    const int parts = (int)((unit_rows + 15) / 16);
+    const int share = few || D == 256 ? 16 : 32;  // rows of a block
+    const int parts = (int)((unit_rows + share - 1) / share);
     cudaError_t e;
     switch (D) {
         case 64:

@@ -96,7 +96,7 @@ struct PrefillParams {
 struct PagedPrefillParams : PrefillParams {
     const int32_t *table;    // [B, max_blocks]
     const int32_t *kv_lens;  // [B] positions of the pool that a sequence attends
-    float *ws_o;             // [2 * CTAs, rows of a unit, D] partial O (unnormalised)
+    float *ws_o;             // [2 * CTAs] partial O (unnormalised), see Partial
     float *ws_ml;            // [2 * CTAs, rows of a unit, 2] partial (m in log2 units, l)
     int4 *split;             // [CTAs] split units, see MergeParams
     int lg, max_blocks, num_blocks;
@@ -303,6 +303,13 @@ __device__ __forceinline__ void st_global_32b(void *dst, const uint32_t *w) {
                  : "memory");
 }
 
+__device__ __forceinline__ void ld_global_32b(const float *src, float (&v)[8]) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(src)
+                 : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -325,6 +332,22 @@ __device__ __forceinline__ void store_row(uint16_t *dst, const float *o, float f
     else
         *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// Where a row of a workspace slot begins, and how far from eight values of it to the
+// next eight: a thread stores its own row, and with eight values of one row beside
+// those of the next a warp's stores are whole lines (at D = 64, 128: 21 single tokens
+// and 3 x 256 of 32 heads over 8 of 128 68 us for 74; at D = 256, where the compiler
+// then lays the softmax out worse, 8192 tokens of 16 heads over 1 443 for 415).  With
+// few rows a warp stores and loads a row.
+template <int D, bool FEW>
+struct Partial {
+    static constexpr bool WHOLE = FEW || D == 256;  // rows in one piece
+    static constexpr int ROWS = (D == 256 ? 1 : 2) * kRows, STEP = WHOLE ? 8 : ROWS * 8;
+    static __device__ __forceinline__ size_t row(int slot, int r) {
+        return WHOLE ? ((size_t)slot * ROWS + r) * D : (size_t)slot * ROWS * D + (size_t)r * 8;
+    }
+    static __device__ __forceinline__ size_t ml(int slot, int r) { return ((size_t)slot * ROWS + r) * 2; }
+};
 
 // A published unit, the same in every lane.
 template <class U>
@@ -1671,6 +1694,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             if constexpr (PG) {
                 const size_t at = (size_t)slot * (NQ * kRows) + s * kRows + row;
                 float *dst = p.ws_o + at * D;
+                if constexpr (!Partial<D, FEW>::WHOLE) dst = p.ws_o + Partial<D, FEW>::row(slot, s * kRows + row);
                 if (tok < end_tok)
                     *reinterpret_cast<float2 *>(p.ws_ml + at * 2) =
                         make_float2(m == -INFINITY ? -INFINITY : m * p.sl, l);
@@ -1684,7 +1708,8 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i]);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) st_global_32b(dst + c * 32 + i, w + i);
+                        for (int i = 0; i < 32; i += 8)
+                            st_global_32b(dst + (c * 32 + i) / 8 * Partial<D, FEW>::STEP, w + i);
                     }
                 }
                 tc_fence_before();
