@@ -349,6 +349,32 @@ struct Partial {
     static __device__ __forceinline__ size_t ml(int slot, int r) { return ((size_t)slot * ROWS + r) * 2; }
 };
 
+// (by a warp) 128 bytes of each lane's row, w, to off[r] (lane 4 i + r's) from dst on:
+// four lanes exchange their rows' pieces of 32 bytes, so that they store whole lines
+// together.  off < 0: nobody's row.
+__device__ __forceinline__ void store_lines(void *dst, const long long (&off)[4], uint32_t (&w)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o <= 2; o *= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c & o) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t &a = w[c * 8 + i], &b = w[(c + o) * 8 + i];
+                const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? a : b, o);
+                if (up) a = x;
+                else b = x;
+            }
+        }
+    }
+    char *mine = static_cast<char *>(dst) + (lane & 3) * 32;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (off[r] >= 0) st_global_32b(mine + off[r], w + r * 8);
+}
+
 // A published unit, the same in every lane.
 template <class U>
 __device__ __forceinline__ U read_unit(const U &from) {
@@ -1698,12 +1724,23 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 if (tok < end_tok)
                     *reinterpret_cast<float2 *>(p.ws_ml + at * 2) =
                         make_float2(m == -INFINITY ? -INFINITY : m * p.sl, l);
+                [[maybe_unused]] long long off[4];
+                if constexpr (D == 256) {
+                    const long long mine = tok < end_tok ? (long long)at * (D * 4) : -1;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) off[r] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + r);
+                }
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {  // (unrolled, it spills at D = 256)
                     float o[32];
                     tmem_ld32(o_t + c * 32, o);
                     tmem_ld_wait();
-                    if (tok < end_tok) {
+                    if constexpr (D == 256) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i]);
+                        store_lines(p.ws_o + c * 32, off, w);
+                    } else if (tok < end_tok) {
                         uint32_t w[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i]);
@@ -1843,6 +1880,28 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                 }
             }
             const float inv = 1.f / l;  // (every row attends itself)
+            // (whole lines: 16 heads over 1 of 256 in a window of 1024 68.0 -> 65.6 us with
+            // the partial rows' below, 32 single tokens of 64 over 8 of 128 96.7 -> 95.8; at
+            // D = 64, a line a row, prompts over states lose 33.1 -> 34.0)
+            if constexpr (PG && D > 64) {
+                const long long at = tok < end_tok ? (((long long)(u.row0 + tok) * p.Hq + u.h0 + r_head) * D) * 2 : -1;
+                long long off[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) off[r] = __shfl_sync(0xffffffffu, at, (lane & ~3) + r);
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float o[32];
+                        tmem_ld32(o_t + c * 64 + h * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[h * 16 + i] = bf16x2_of(o[2 * i] * inv, o[2 * i + 1] * inv);
+                    }
+                    store_lines(p.out + c * 64, off, w);
+                }
+            } else {
             uint16_t *dst = p.out + ((size_t)(u.row0 + tok) * p.Hq + u.h0 + r_head) * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -1856,6 +1915,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                     st_global_32b(dst + c * 32, w);
                     st_global_32b(dst + c * 32 + 16, w + 8);
                 }
+            }
             }
             tc_fence_before();
             __syncwarp();
