@@ -22,8 +22,11 @@
 //
 // What bounds it.  Many tokens: what bounds prompt attention, the tensor pipe
 // between its turns (four prompts of 2048 tokens behind 6144, 64 heads over 8 of 128:
-// 1410 us, 1365 TFLOP/s, 0.72 of the cuBLAS rate), and the merge (10 to 25 us where
-// all CTAs leave units of 128 or 256 rows).  Single tokens: memory, 5.5 TB/s (0.81 of
+// 1380 us, 1395 TFLOP/s, 0.74 of the cuBLAS rate), and the merge (7 to 10 us where
+// all CTAs leave units of 128 or 256 rows).  Short units: their starts and ends, some
+// 4 us each (eight requests of up to 511 tokens in a window of 1024, 16 heads over 1
+// of 256: 66 us, of which a CTA's first piece takes 13: instructions and the first
+// rows are far away).  Single tokens: memory, 5.5 TB/s (0.81 of
 // copy bandwidth) for 32 of up to 8192 positions, 64 heads over 8 of 128, in blocks of
 // 16, 5.7 in larger ones; 3.9 for 64 of up to 2048 states, 16 heads of 64, whose units
 // are 1 to 16 key tiles long and take 2.5 us to begin and end.  A kernel's local
@@ -292,8 +295,9 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     // 128; of one 1.35, of few rows the same for all).  A unit's start and end (its
     // copies' latency, the output's read-out, a join) is 2 tiles' work, at D = 64
     // with few rows 5: 64 requests of 16 heads of 64 over up to 2048 states 91 us
-    // with 2, 75 with 5, 78 with 10; 8192 tokens of 64 heads over 8 of 128 793 with 2,
-    // 824 with 1, of 16 over 1 of 256 447 with 2.6, 522 with 1.
+    // with 2, 75 with 5, 78 with 10; 8192 tokens of 64 heads over 8 of 128 770 with 2,
+    // 755 with 1.6 (and the mixed calls the same), of 16 over 1 of 256 408 with 2.6, 412
+    // with 2, 429 with 1.6.
     p.w2 = 5;
     p.w1 = p.few_tok || D == 256 ? 5 : 4;
     p.cost_piece = p.few_tok ? (D == 64 ? 25 : 10) : D == 256 ? 13 : 10;
