@@ -12,14 +12,14 @@
 // Layout.  A head's row is D / 8 lanes, four values of each half of its rotated
 // dims (or 16 bytes of neighbours) a lane, so that a lane has both partners of its
 // rotations.  A warp takes up to 8 x 32 / (D / 8) heads of one token, with all their
-// loads in flight; a lane's cosines and sines, times the weights, serve all of
+// loads in flight (fewer where tokens are few); a lane's cosines and sines, times the weights, serve all of
 // them.  The heads are the token's queries, then its keys, then its values, which
 // are copied.
 //
 // What bounds it: HBM, every value read once and written once: 16 384 tokens of 64
 // heads over 8 of 128 with norms 115 us (5.9 TB/s, 0.87 of the measured copy rate;
 // 107 without norms; 197 with 16 bytes of a row a lane, partners met by shuffles and
-// rows of any kind in a warp: instructions).  64 such tokens 3.2 us: a launch and the
+// rows of any kind in a warp: instructions).  64 such tokens 2.4 us: a launch and the
 // chain of position, table and rows.
 #include <cmath>
 #include <cuda_bf16.h>
@@ -265,12 +265,18 @@ int run_rope(RopeParams p, int D, int rope_dim, long long q_stride, long long k_
     p.ko_stride = ko_stride / 4;
     p.half = rope_dim / 2;
     const int at_once = 32 / (D / 8);  // head rows of a warp
-    p.q_chunks = (p.Hq + kRopeRows * at_once - 1) / (kRopeRows * at_once);
-    p.k_chunks = (p.Hkv + kRopeRows * at_once - 1) / (kRopeRows * at_once);
-    p.q_per = (p.Hq + p.q_chunks * at_once - 1) / (p.q_chunks * at_once);
-    p.k_per = (p.Hkv + p.k_chunks * at_once - 1) / (p.k_chunks * at_once);
-    p.chunks = p.q_chunks + (p.slots ? 2 : 1) * p.k_chunks;
     const unsigned long long groups = ((unsigned long long)p.N + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    // head rows a lane: as many as leave two blocks an SM, else one at least (64 heads over
+    // 8 of 128: a token 2.1 us for 2.6, 64 2.4 for 3.2, 256 3.3 for 4.1 with eight; with
+    // three blocks an SM 256 take 4.1, too, and 512 5.3 for 4.7)
+    for (int rows = kRopeRows;; rows /= 2) {
+        p.q_chunks = (p.Hq + rows * at_once - 1) / (rows * at_once);
+        p.k_chunks = (p.Hkv + rows * at_once - 1) / (rows * at_once);
+        p.q_per = (p.Hq + p.q_chunks * at_once - 1) / (p.q_chunks * at_once);
+        p.k_per = (p.Hkv + p.k_chunks * at_once - 1) / (p.k_chunks * at_once);
+        p.chunks = p.q_chunks + (p.slots ? 2 : 1) * p.k_chunks;
+        if (rows == 1 || groups * p.chunks >= 2ULL * ctas) break;
+    }
     const unsigned long long grid = groups * p.chunks;
     if (grid > 0x7fffffffULL) return api_failf(KVATTN_ERR_UNSUPPORTED, "%s: too many rows for one launch", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
