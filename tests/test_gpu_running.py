@@ -155,6 +155,27 @@ def test_rope_in_place_and_into_wider_rows():
     g.check_device_error()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 40, 4), (128, 64, 8), (256, 16, 1), (128, 1, 1)])
+def test_rope_of_a_row_is_the_same_beside_any_others(D, Hq, Hkv):
+    # (a call's heads are divided by the number of its tokens)
+    q, k, v, pos, cos, sin, qw, kw = rope_inputs(2100, Hq, Hkv, D, D, 500, seed=D + 1)
+    qa, ka = g.qk_norm_rope(q, k, pos, cos, sin, qw, kw)
+    for N in (1, 9, 64, 257, 600, 1100):
+        qo, ko = g.qk_norm_rope(q[:N], k[:N], pos[:N], cos, sin, qw, kw)
+        g.check_device_error()
+        assert torch.equal(qo.view(torch.int16), qa[:N].view(torch.int16))
+        assert torch.equal(ko.view(torch.int16), ka[:N].view(torch.int16))
+        pools = [torch.zeros((N // 16 + 1, Hkv, 16, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        mine = q[:N].clone(memory_format=torch.contiguous_format)
+        back = g.kv_append_rope(mine, k[:N], v[:N], pos[:N], cos, sin, torch.arange(N, device="cuda"), *pools,
+                                q_weight=qw, k_weight=kw, q_out=mine)
+        g.check_device_error()
+        assert back is mine and torch.equal(mine.view(torch.int16), qo.view(torch.int16))
+        for p, x in zip(pools, (ka, v)):
+            got = p.permute(0, 2, 1, 3).reshape(-1, Hkv, D)
+            assert torch.equal(got[:N].view(torch.int16), x[:N].view(torch.int16)) and not bool(got[N:].any())
+
+
 def test_rope_bad_positions_and_slots_are_reported():
     q, k, v, pos, cos, sin, qw, kw = rope_inputs(20, 4, 2, 64, 64, 30, seed=2)
     clean, _ = g.qk_norm_rope(q, k, pos, cos, sin, qw, kw)
