@@ -61,14 +61,26 @@ struct Workspace {
     // CUDA graph) may still use them
     std::vector<std::pair<void *, size_t>> retired;
 };
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+using StreamKey = std::pair<int, cudaStream_t>;
+std::map<StreamKey, Workspace> g_ws;
+// Whose turn it is on a stream.  A call that leaves partial results in the stream's
+// workspace for a second kernel holds it from taking the workspace to that kernel's
+// launch: another host thread's call on the stream would put its own kernel between
+// them.  Taken before g_mu, never removed; new ones come in front of the list.
+struct Turn {
+    std::mutex mu;
+    Turn *next = nullptr;
+};
+std::map<StreamKey, Turn> g_turn;
+Turn *g_turns = nullptr;
+std::mutex g_release_mu;  // one kvattn_release at a time (taken before any turn)
 // Workspaces of captures, each its own (gqa_decode_attn_paged_fp8): by device,
 // stream and capture.  One belongs to its graph, which holds it as a user
 // object: CUDA calls capture_gone once the graph and everything instantiated
 // from it are destroyed and their launches have finished.  That call may come
 // from any thread and must not use CUDA, so it only puts the workspace on a
 // list; the next captured call takes the buffers over (g_idle).
-using CaptureKey = std::pair<std::pair<int, cudaStream_t>, unsigned long long>;
+using CaptureKey = std::pair<StreamKey, unsigned long long>;
 struct CaptureWorkspace {
     CaptureKey key;
     Workspace ws;
@@ -323,8 +335,28 @@ int alloc_workspace(size_t bytes, void **ptr) {
     return KVATTN_OK;
 }
 
+StreamKey stream_key(int dev, cudaStream_t stream) { return StreamKey(dev, stream); }
+
+// The stream's turn, held until *turn is destroyed (g_mu is not held here).
+int take_turn(int dev, cudaStream_t stream, std::unique_lock<std::mutex> *turn) {
+    Turn *t;
+    try {
+        std::lock_guard<std::mutex> lk(g_mu);
+        auto at = g_turn.try_emplace(stream_key(dev, stream));
+        t = &at.first->second;
+        if (at.second) {
+            t->next = g_turns;
+            g_turns = t;
+        }
+    } catch (const std::bad_alloc &) {
+        return fail(KVATTN_ERR_OOM, "no host memory for a stream's record");
+    }
+    *turn = std::unique_lock<std::mutex>(t->mu);
+    return KVATTN_OK;
+}
+
 int get_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
-    Workspace &w = g_ws[std::make_pair(dev, stream)];
+    Workspace &w = g_ws[stream_key(dev, stream)];
     if (w.bytes < bytes) {
         // grow at least twofold; the old buffer is retired, not freed
         size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
@@ -368,7 +400,7 @@ int get_call_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetCaptureInfo");
     if (st != cudaStreamCaptureStatusActive) return get_workspace(dev, stream, bytes, ptr);
     collect_gone();
-    const CaptureKey key(std::make_pair(dev, stream), id);
+    const CaptureKey key(stream_key(dev, stream), id);
     auto at = g_ws_captured.find(key);
     if (at == g_ws_captured.end()) {
         CaptureWorkspace *rec = new CaptureWorkspace;
@@ -505,12 +537,12 @@ int api_device(int *ctas, unsigned int **err, unsigned int *wait_limit) {
     return KVATTN_OK;
 }
 
-int api_call_workspace(cudaStream_t stream, size_t bytes, void **ptr) {
+int api_call_workspace(cudaStream_t stream, size_t bytes, WorkspaceLease *ws) {
     int dev, rc;
-    if ((rc = current_device(&dev))) return rc;
+    if ((rc = current_device(&dev)) || (rc = take_turn(dev, stream, &ws->turn))) return rc;
     std::lock_guard<std::mutex> lk(g_mu);
     try {
-        return get_call_workspace(dev, stream, bytes, ptr);
+        return get_call_workspace(dev, stream, bytes, &ws->ptr);
     } catch (const std::bad_alloc &) {
         return fail(KVATTN_ERR_OOM, "no host memory for a workspace's record");
     }
@@ -696,6 +728,8 @@ int run_decode(const void *q, const void *k_cache, const void *v_cache, const vo
     void *ws = nullptr;
     unsigned int wait_limit = 0;
     cudaEvent_t ev_before = nullptr, ev_after = nullptr;
+    std::unique_lock<std::mutex> turn;  // (to the end of this function)
+    if ((rc = take_turn(dev, stream, &turn))) return rc;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         wait_limit = g_wait_limit;
@@ -706,7 +740,12 @@ int run_decode(const void *q, const void *k_cache, const void *v_cache, const vo
         if ((rc = make_plan(B, Hq, Hkv, D, Lmax, ds->num_sms, &pl, T))) return rc;
         if (pg && pl.pub.path != 2)
             return fail(KVATTN_ERR_UNSUPPORTED, "%s: a paged cache needs the tensor-core path", who);
-        if ((rc = get_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws))) return rc;
+        try {
+            rc = get_workspace(dev, stream, (size_t)pl.pub.workspace_bytes, &ws);
+        } catch (const std::bad_alloc &) {
+            rc = fail(KVATTN_ERR_OOM, "%s: host memory for the workspace's record", who);
+        }
+        if (rc) return rc;
     }
     const kvattn_plan &P = pl.pub;
 
@@ -823,6 +862,8 @@ int run_decode_fp8(const void *q, const void *k_codes, const void *v_codes, cons
     void *ws = nullptr;
     unsigned int wait_limit = 0;
     cudaEvent_t ev_before = nullptr, ev_after = nullptr;
+    std::unique_lock<std::mutex> turn;  // (to the end of this function)
+    if ((rc = take_turn(dev, stream, &turn))) return rc;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         wait_limit = g_wait_limit;
@@ -1093,7 +1134,17 @@ int kvattn_check_device_error(kvattn_stream_t stream) {
 }
 
 void kvattn_release(void) {
-    std::lock_guard<std::mutex> lk(g_mu);
+    std::lock_guard<std::mutex> alone(g_release_mu);
+    // every stream's turn: no call is between taking its workspace and its last launch
+    std::unique_lock<std::mutex> lk(g_mu);
+    Turn *held = nullptr;
+    while (g_turns != held) {
+        Turn *all = g_turns;
+        lk.unlock();
+        for (Turn *t = all; t != held; t = t->next) t->mu.lock();
+        held = all;
+        lk.lock();
+    }
     int cur = 0;
     cudaGetDevice(&cur);
     auto give_back = [](int dev, Workspace &w) {
@@ -1114,6 +1165,7 @@ void kvattn_release(void) {
     }
     g_idle.clear();
     cudaSetDevice(cur);
+    for (Turn *t = held; t; t = t->next) t->mu.unlock();
 }
 
 }  // extern "C"

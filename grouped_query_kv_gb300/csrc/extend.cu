@@ -313,10 +313,10 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int slot_rows = (D == 256 ? 1 : 2) * kRows;
     const size_t rows = (size_t)2 * ctas * slot_rows;  // two pieces a CTA
-    void *ws = nullptr;
+    WorkspaceLease ws;  // (held until the merge is launched)
     if ((rc = api_call_workspace(stream, rows * (D + 2) * sizeof(float) + (size_t)ctas * sizeof(int4), &ws)))
         return rc;
-    p.ws_o = static_cast<float *>(ws);
+    p.ws_o = static_cast<float *>(ws.ptr);
     p.ws_ml = p.ws_o + rows * D;
     p.split = reinterpret_cast<int4 *>(p.ws_ml + rows * 2);
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -165,8 +166,13 @@ int api_check_paged(const int32_t *table, int Hkv, int block_size, int max_block
 // unless the tuning knob forces another), error word and the wait-limit knob.
 int api_device(int *ctas, unsigned int **err, unsigned int *wait_limit);
 // A workspace of the current device and this stream, or, while it is captured, of
-// the capture's own (see get_call_workspace).
-int api_call_workspace(cudaStream_t stream, size_t bytes, void **ptr);
+// the capture's own (see get_call_workspace), and the stream's turn, which a call
+// keeps until its last launch: calls of other host threads on the stream wait.
+struct WorkspaceLease {
+    void *ptr = nullptr;
+    std::unique_lock<std::mutex> turn;
+};
+int api_call_workspace(cudaStream_t stream, size_t bytes, WorkspaceLease *ws);
 // 3-D map of bf16 values, 128-byte swizzle, out-of-range reads as zeros.
 int api_encode_bf16_3d(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
                        const cuuint32_t *box);

@@ -41,6 +41,7 @@ struct NoallocDevice {
     int num_sms;
     void *scratch;      // device address of g_noalloc_scratch on this device
     unsigned int *err;  // device address of the sticky error word
+    std::mutex turn;    // held by a call over both of its launches
 };
 
 std::mutex g_noalloc_mu;
@@ -142,6 +143,8 @@ extern "C" int gqa_decode_attn_noalloc(const void *q, const void *k_cache,
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
 
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    // (another host thread's call on the stream comes before both launches or behind them)
+    std::lock_guard<std::mutex> turn(nd->turn);
     cudaError_t e = fma_prepare(D, hps, smem);
     if (e != cudaSuccess) return api_cuda_fail(e, "cudaFuncSetAttribute");
     e = launch_decode_fma(tmk, tmv, p, num_ctas, smem, stream);

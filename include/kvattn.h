@@ -42,8 +42,9 @@
  *    the offending sequence is skipped and a sticky per-device error word is
  *    set, read and cleared by kvattn_check_device_error().
  *  - Thread-safe: internal caches are guarded by a mutex.  Calls on the same
- *    stream run in order; calls on different streams use separate
- *    workspaces.
+ *    stream run in order, whichever host threads make them (a call's kernels are
+ *    launched together: another thread's call on the stream waits for them to be);
+ *    calls on different streams use separate workspaces.
  */
 #ifndef KVATTN_H
 #define KVATTN_H
@@ -861,7 +862,8 @@ KVATTN_API int kvattn_check_device_error(kvattn_stream_t stream);
 
 /*
  * Frees every workspace the library holds on every device (after a device
- * synchronisation).  Later calls allocate again on demand.
+ * synchronisation), when the calls that other host threads are making have
+ * launched their kernels.  Later calls allocate again on demand.
  */
 KVATTN_API void kvattn_release(void);
 
