@@ -22,11 +22,12 @@ unsigned long long next_address = 1ull << 32, capture = 0;
 int capture_objects = 0;
 unsigned int word;
 thread_local int me = -1;
+thread_local bool bound = false;  // this host thread has a context: some runtime calls give it one
 
 CUresult encode(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill) {
-    return CUDA_SUCCESS;
+    return bound ? CUDA_SUCCESS : CUDA_ERROR_INVALID_CONTEXT;
 }
 
 void note(const std::string &line) {
@@ -80,11 +81,13 @@ cudaError_t __cudaLaunchKernel(void *, dim3, dim3, void **, size_t, cudaStream_t
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *cfg, const void *host, void **) {
     const std::string name = names.count(host) ? names[host] : "?";
     note("launch " + std::to_string(me) + " " + std::to_string((unsigned long long)(uintptr_t)cfg->stream) + " " + name);
+    bound = true;
     if (!joins(name)) std::this_thread::sleep_for(std::chrono::milliseconds(3));
     return cudaSuccess;
 }
 cudaError_t cudaMalloc(void **p, size_t bytes) {
     std::lock_guard<std::mutex> lk(mu);
+    bound = true;
     *p = reinterpret_cast<void *>(next_address);
     next_address += (bytes + 4095) / 4096 * 4096;
     text += "malloc " + std::to_string(me) + " " + std::to_string(bytes) + "\n";
@@ -98,7 +101,10 @@ cudaError_t cudaGetDevice(int *d) {
     *d = 0;
     return cudaSuccess;
 }
-cudaError_t cudaSetDevice(int) { return cudaSuccess; }
+cudaError_t cudaSetDevice(int) {
+    bound = true;
+    return cudaSuccess;
+}
 cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr, int) {
     *v = 152;
     return cudaSuccess;

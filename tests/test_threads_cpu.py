@@ -151,3 +151,21 @@ def test_release_waits_for_the_calls_under_way(lib):
         elif x[0] == "free":
             assert not open_calls, (x, open_calls)
     assert any(x[0] == "free" for x in lines)
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_the_first_call_of_a_host_thread(lib, name):
+    # a thread has no context until a runtime call that needs one; the maps' encoding, a
+    # driver call, is refused without
+    _call(lib, name, 4, 0x500)  # (so that the thread's call has nothing to allocate)
+    _together(lib, [lambda: _call(lib, name, 4, 0x500)])
+
+
+def test_the_first_call_of_a_host_thread_that_needs_no_workspace(lib):
+    _together(lib, [lambda: _prefill(lib)])
+
+
+def _prefill(lib):
+    # (through internal maps too)
+    rc = lib.gqa_prefill_attn(P, P, P, P, P, 2, 100, 32, 4, 128, 4096, 512, 512, 0.1, 1000, 0x500)
+    assert rc == g.KVATTN_OK, lib.kvattn_last_error()
