@@ -9,6 +9,7 @@
 #include <vector>
 #include <mutex>
 #include <new>
+#include <tuple>
 #include <utility>
 
 #include <cuda.h>
@@ -61,7 +62,9 @@ struct Workspace {
     // CUDA graph) may still use them
     std::vector<std::pair<void *, size_t>> retired;
 };
-using StreamKey = std::pair<int, cudaStream_t>;
+// A stream: its device, its handle, and the host thread where the handle is
+// cudaStreamPerThread, which is another stream in each of them (else 0).
+using StreamKey = std::tuple<int, cudaStream_t, unsigned long long>;
 std::map<StreamKey, Workspace> g_ws;
 // Whose turn it is on a stream.  A call that leaves partial results in the stream's
 // workspace for a second kernel holds it from taking the workspace to that kernel's
@@ -336,7 +339,14 @@ int alloc_workspace(size_t bytes, void **ptr) {
     return KVATTN_OK;
 }
 
-StreamKey stream_key(int dev, cudaStream_t stream) { return StreamKey(dev, stream); }
+// (Threads are counted, since an ended one's id may come again while its work runs.)
+StreamKey stream_key(int dev, cudaStream_t stream) {
+    static std::atomic<unsigned long long> threads{0};
+    thread_local unsigned long long mine = 0;
+    if (stream != cudaStreamPerThread) return StreamKey(dev, stream, 0);
+    if (mine == 0) mine = ++threads;
+    return StreamKey(dev, stream, mine);
+}
 
 // The stream's turn, held until *turn is destroyed (g_mu is not held here).
 int take_turn(int dev, cudaStream_t stream, std::unique_lock<std::mutex> *turn) {
@@ -377,7 +387,7 @@ int get_workspace(int dev, cudaStream_t stream, size_t bytes, void **ptr) {
 void collect_gone() {
     CaptureWorkspace *w = g_ws_gone.exchange(nullptr, std::memory_order_acquire);
     while (w) {
-        const int dev = w->key.first.first;
+        const int dev = std::get<0>(w->key.first);
         if (w->ws.ptr) g_idle.insert({{dev, w->ws.bytes}, w->ws.ptr});
         for (auto &old : w->ws.retired) g_idle.insert({{dev, old.second}, old.first});
         auto at = g_ws_captured.find(w->key);
@@ -1150,11 +1160,11 @@ void kvattn_release(void) {
         for (auto &old : w.retired) cudaFree(old.first);
         w = Workspace();
     };
-    for (auto &kv : g_ws) give_back(kv.first.first, kv.second);
+    for (auto &kv : g_ws) give_back(std::get<0>(kv.first), kv.second);
     g_ws.clear();
     // (a capture's record is deleted once its graph is gone)
     collect_gone();
-    for (auto &kv : g_ws_captured) give_back(kv.first.first.first, kv.second->ws);
+    for (auto &kv : g_ws_captured) give_back(std::get<0>(kv.first.first), kv.second->ws);
     g_ws_captured.clear();
     for (auto &kv : g_idle) {
         cudaSetDevice(kv.first.first);

@@ -44,7 +44,9 @@
  *  - Thread-safe: internal caches are guarded by a mutex.  Calls on the same
  *    stream run in order, whichever host threads make them (a call's kernels are
  *    launched together: another thread's call on the stream waits for them to be);
- *    calls on different streams use separate workspaces.
+ *    calls on different streams use separate workspaces.  cudaStreamPerThread is a
+ *    stream, with a workspace, of each host thread that calls with it; the
+ *    workspace of a thread that has ended is kept, too, until kvattn_release().
  */
 #ifndef KVATTN_H
 #define KVATTN_H

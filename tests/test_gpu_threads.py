@@ -69,3 +69,31 @@ def test_host_threads_on_one_stream():
         assert len(outs) == 60
         for o in outs:
             assert torch.equal(o, w)
+
+
+class _PerThread:
+    """The stream of whichever host thread calls (cudaStreamPerThread)."""
+    cuda_stream = 2
+
+
+def test_the_streams_of_host_threads_side_by_side():
+    cases = [Case([1] * 8, [3000 + 7 * i for i in range(8)], 64, 8, 128, 64, seed=1, pad=0, wide=False),
+             Case([200, 1, 90], [2500, 1300, 90], 8, 2, 128, 16, seed=2, pad=0, wide=False),
+             Case([700], [5000], 16, 1, 256, 64, seed=3, pad=0, wide=False),
+             Case([9] * 30, [1000 + i for i in range(30)], 4, 4, 64, 32, seed=4, pad=0, wide=False, causal=False)]
+    want = [c.run() for c in cases]
+    outs = [[torch.zeros_like(w) for _ in range(40)] for w in want]
+    torch.cuda.synchronize()
+
+    def job(i):
+        for o in outs[i]:
+            cases[i].run(out=o, stream=_PerThread)
+
+    for _ in range(2):  # (the second time in other threads)
+        _together([lambda i=i: job(i) for i in range(len(cases))])
+        g.check_device_error()
+        for w, got in zip(want, outs):
+            for o in got:
+                assert torch.equal(o, w)
+                o.zero_()
+        torch.cuda.synchronize()

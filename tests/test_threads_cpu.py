@@ -169,3 +169,18 @@ def _prefill(lib):
     # (through internal maps too)
     rc = lib.gqa_prefill_attn(P, P, P, P, P, 2, 100, 32, 4, 128, 4096, 512, 512, 0.1, 1000, 0x500)
     assert rc == g.KVATTN_OK, lib.kvattn_last_error()
+
+
+@pytest.mark.parametrize("captured", [0, 7])
+@pytest.mark.parametrize("name", sorted(set(CALLS) - {"gqa_decode_attn_noalloc"}))
+def test_the_stream_of_each_host_thread_has_a_workspace_of_its_own(lib, name, captured):
+    # (one handle, a stream in each host thread: their calls run side by side)
+    per_thread = 2
+    lib.fake_capture(captured)
+    _together(lib, [lambda: [_call(lib, name, 4, per_thread) for _ in range(3)] for _ in range(3)])
+    assert sorted(x[1] for x in _log(lib, "malloc")) == ["0", "1", "2"]
+    launches = _log(lib, "launch")
+    for t in "012":
+        _joined_in_pairs([x for x in launches if x[1] == t])
+    # and they do not wait for each other
+    assert any(a[1] != b[1] for a, b in zip(launches[::2], launches[1::2])), launches
