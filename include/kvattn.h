@@ -47,8 +47,9 @@
  *    calls on different streams use separate workspaces.  cudaStreamPerThread is a
  *    stream, with a workspace, of each host thread that calls with it; the
  *    workspace of a thread that has ended is kept, too, until kvattn_release().
- *  - A stream is destroyed only once the work of the calls on it has finished
- *    (synchronise it first): its handle may come again, for a stream that would
+ *  - A stream is destroyed, and a thread that called with cudaStreamPerThread ends,
+ *    only once the work of those calls has finished (synchronise the stream
+ *    first): a destroyed stream's handle may come again, for a stream that would
  *    take the workspace over while the old one's kernels still use it.
  */
 #ifndef KVATTN_H

@@ -88,6 +88,7 @@ def test_the_streams_of_host_threads_side_by_side():
     def job(i):
         for o in outs[i]:
             cases[i].run(out=o, stream=_PerThread)
+        g.check_device_error(_PerThread)  # (a thread ends when its stream's work has)
 
     for _ in range(2):  # (the second time in other threads)
         _together([lambda i=i: job(i) for i in range(len(cases))])
