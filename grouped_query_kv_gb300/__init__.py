@@ -999,6 +999,19 @@ def _or_same(t, name, same, dev):
     return t
 
 
+def _pass_on(src, dst, stream):
+    """A call on an empty list: the count stays what it was (on the call's stream)."""
+    if dst is not src:
+        if stream is None:
+            dst.copy_(src)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(stream.cuda_stream)
+            with torch.cuda.stream(stream):
+                dst.copy_(src)
+    return dst
+
+
 def kv_fork_blocks(block_table, seq_lens, refs, free_blocks, free_count, parents, children, block_size,
                    copies=None, free_count_out=None, stream=None):
     """Table rows children become forks of rows parents: they share the whole
@@ -1011,8 +1024,8 @@ def kv_fork_blocks(block_table, seq_lens, refs, free_blocks, free_count, parents
     children: int32 [n], the children rows of length 0, all different and no
     parents.  copies (int32 [n, 2]) is allocated if None; the count left goes to
     free_count_out (None: back into free_count).  Returns
-    (copies, free_count_out).  Forks that cannot be served set the device error
-    word (see include/kvattn.h).
+    (copies, free_count_out).  Without names (n = 0) nothing is done.  Forks that
+    cannot be served set the device error word (see include/kvattn.h).
     """
     dev = _home(block_table, "block_table")
     R, maxb, nblk, nfree = _held(block_table, seq_lens, refs, free_blocks, free_count, dev)
@@ -1023,6 +1036,8 @@ def kv_fork_blocks(block_table, seq_lens, refs, free_blocks, free_count, parents
     _want(children, "children", torch.int32, dev, (n,))
     copies = _or_new(copies, "copies", (n, 2), dev, parents, stream)
     free_count_out = _or_same(free_count_out, "free_count_out", free_count, dev)
+    if n == 0:
+        return copies, _pass_on(free_count, free_count_out, stream)
     _check(lib().kv_fork_blocks(block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
                                 free_blocks.data_ptr(), free_count.data_ptr(), parents.data_ptr(),
                                 children.data_ptr(), copies.data_ptr(), free_count_out.data_ptr(), n, R, maxb,
@@ -1035,14 +1050,16 @@ def kv_free_blocks(block_table, seq_lens, refs, free_blocks, free_count, request
     """The named requests (int32 [n], table rows) let go of their blocks: their
     entries become -1, their lengths 0, refs - 1 per block; blocks without a
     holder are pushed onto the free stack in ascending order.  Other arguments
-    as for kv_fork_blocks; free_blocks is written, too.  Returns
-    free_count_out."""
+    as for kv_fork_blocks; free_blocks is written, too.  Without names nothing is
+    done.  Returns free_count_out."""
     dev = _home(block_table, "block_table")
     R, maxb, nblk, nfree = _held(block_table, seq_lens, refs, free_blocks, free_count, dev)
     _want(requests, "requests", torch.int32, dev)
     if requests.dim() != 1:
         raise ValueError("requests must be [n]")
     free_count_out = _or_same(free_count_out, "free_count_out", free_count, dev)
+    if requests.shape[0] == 0:
+        return _pass_on(free_count, free_count_out, stream)
     _check(lib().kv_free_blocks(block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
                                 free_blocks.data_ptr(), free_count.data_ptr(), requests.data_ptr(),
                                 free_count_out.data_ptr(), requests.shape[0], R, maxb,
@@ -1082,7 +1099,7 @@ def kv_copy_blocks(k_pool, v_pool, copies, k_scale=None, v_scale=None, stream=No
 
     k_pool, v_pool: bf16, or uint8 codes of a paged 8-bit cache, [num_blocks,
     Hkv, block_size, D] (in place); copies: int32 [n, 2], as kv_fork_blocks and
-    kv_compact_blocks give them; k_scale, v_scale: the 8-bit cache's fp32
+    kv_compact_blocks give them (n = 0: nothing to do); k_scale, v_scale: the 8-bit cache's fp32
     [num_blocks, Hkv], copied too.
     """
     dev = _home(k_pool, "k_pool")
@@ -1102,6 +1119,9 @@ def kv_copy_blocks(k_pool, v_pool, copies, k_scale=None, v_scale=None, stream=No
     if k_scale is not None:
         _want(k_scale, "k_scale", torch.float32, dev, (nblk, Hkv))
         _want(v_scale, "v_scale", torch.float32, dev, (nblk, Hkv))
+    if n == 0:  # (as a pool of one block's moves are)
+        return
+    if k_scale is not None:
         _check(lib().kv_copy_blocks(k_scale.data_ptr(), v_scale.data_ptr(), copies.data_ptr(), n, nblk, 4 * Hkv, on))
     _check(lib().kv_copy_blocks(k_pool.data_ptr(), v_pool.data_ptr(), copies.data_ptr(), n, nblk,
                                 Hkv * bs * D * k_pool.element_size(), on))

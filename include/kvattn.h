@@ -794,7 +794,9 @@ KVATTN_API int kv_free_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *
  * held block at or past `used` moves to the k-th free one below it.
  *
  *   moves  : int32 [num_blocks / 2, 2], written in full: (from, to), for
- *            kv_copy_blocks in each layer's pools, (-1, -1) behind the last
+ *            kv_copy_blocks in each layer's pools, (-1, -1) behind the last.  (Of a
+ *            pool of one block nothing is written: any aligned pointer will do, and
+ *            there is no call of kv_copy_blocks to make, whose n is positive.)
  *   remap  : int32 [num_blocks] (16-byte aligned), written: each held block's
  *            new id, -1 for free blocks (to rewrite other tables by)
  *   *_out  : the tables, references, stack and count after the moves; each may

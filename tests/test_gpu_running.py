@@ -668,3 +668,57 @@ def test_on_another_stream_and_captured():
         gr.replay()
         for a, b in zip(state(), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("aside", [False, True])
+def test_empty_lists_and_a_pool_of_one_block(aside):
+    bs, Hkv, D = 16, 2, 64
+    pool = Pool(3, 4, 6, bs)
+    pool.grow(0, 40)
+    dev = Device(pool)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    more = dict(stream=torch.cuda.Stream()) if aside else {}
+    torch.cuda.synchronize()
+    # forks and drops of nobody: the count is passed on, all else stays
+    copies, count = g.kv_fork_blocks(*dev.args(), none, none, bs, **more)
+    assert copies.shape == (0, 2) and count is dev.count
+    assert g.kv_free_blocks(*dev.args(), none, bs, **more) is dev.count
+    for call in (lambda o: g.kv_fork_blocks(*dev.args(), none, none, bs, free_count_out=o, **more)[1],
+                 lambda o: g.kv_free_blocks(*dev.args(), none, bs, free_count_out=o, **more)):
+        out = _i32([-7])
+        torch.cuda.synchronize()
+        assert call(out) is out
+        torch.cuda.synchronize()
+        assert int(out) == 3
+    # their checks stay
+    with pytest.raises(ValueError):
+        g.kv_fork_blocks(*dev.args(), none, _i32([1]), bs)
+    with pytest.raises(TypeError):
+        g.kv_free_blocks(*dev.args(), none.long(), bs)
+    for dtype in (torch.bfloat16, torch.uint8):
+        pools = [torch.full((6, Hkv, bs, D), 3, dtype=dtype, device="cuda") for _ in range(2)]
+        scales = {}
+        if dtype is torch.uint8:
+            scales = {k: torch.ones(6, Hkv, device="cuda") for k in ("k_scale", "v_scale")}
+        torch.cuda.synchronize()
+        g.kv_copy_blocks(*pools, copies, **scales, **more)
+        with pytest.raises(ValueError):
+            g.kv_copy_blocks(pools[0], pools[1][:5], copies, **scales)
+        torch.cuda.synchronize()
+        assert all(bool((p == 3).all()) for p in pools)
+    g.check_device_error()
+    dev.same(pool)
+    # a pool of one block, free or held
+    for n in (0, 9):
+        one = Pool(1, 1, 1, bs)
+        one.grow(0, n)
+        dev = Device(one)
+        pools = [torch.ones((1, Hkv, bs, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        moves, remap = g.kv_compact_blocks(*dev.args(), bs, **more)
+        assert moves.shape == (0, 2)
+        g.kv_copy_blocks(*pools, moves, **more)
+        torch.cuda.synchronize()
+        g.check_device_error()
+        assert remap.tolist() == [0 if n else -1]
+        dev.same(one)
