@@ -14,7 +14,7 @@
 // m moves only when a score passes it by more than 2^8 (then O and l are
 // rescaled by 2^(m - m')), so O is rarely touched between products; p stays
 // below 2^8 and l in 32 bits.  p enters the second product as bf16 (the
-// output is bf16: the weights' rounding, at most 2^-9 each, averages out below
+// output is bf16: the weights' rounding, at most 2^-8 of each, averages out below
 // the output's own).
 //
 // Layout.  A tile is 128 query rows: hpg = gcd(G, 128) heads of one K/V head
@@ -83,8 +83,11 @@ struct PrefillParams {
     uint16_t *out;      // bf16 [N, Hq, D]
     unsigned int *err;
     int B, N, Hq, Hkv, G;
-    int hpg, hpg_lg;    // query heads of a tile, a power of two
-    int tpt;            // tokens of a tile, 128 / hpg
+    // query heads of a tile and their log2, and its tokens, 128 / hpg.  (Over a pool hpg
+    // may be a whole group of another size, with a power of two of tokens, and the tile
+    // have less than 128 rows; there is no log2 then.)
+    int hpg, hpg_lg;
+    int tpt;
     int passes;         // G / hpg
     int window;         // keys one query attends at most (N: all)
     float sl;           // |scale| log2(e), at least the smallest normal number
@@ -106,7 +109,7 @@ struct PagedPrefillParams : PrefillParams {
     // A unit of at most few_tok tokens (32 query rows) has them four times in
     // its tile, 32 lanes each, and every warp of the softmax takes a quarter of a
     // key tile's columns for its copy: four partial results that are joined.
-    int few_tok, few_bytes;  // (0: hpg > 32)
+    int few_tok, few_bytes;  // (0: no such units, as at D = 256 or hpg > 32)
     int tpu_lg;              // log2 of a unit's tokens
     int causal;              // token t sees up to itself; else the whole pool rows
     int w1, w2, cost_piece;  // costs, see UnitSeq
@@ -155,17 +158,15 @@ struct Ring {
     }
 };
 
-// The places of one of two copy warps that fill a ring of N slots from slot OFF
-// in turns (STEP 2), or of one that fills it alone.
-template <int N_, int OFF_, int STEP_>
+// The same for the copy warp that fills the ring, with its fills counted.
+template <int N_, int OFF_>
 struct CopyRing {
-    static constexpr int N = N_, OFF = OFF_, STEP = STEP_;
-    int slot, pos;  // pos: place counted on
+    static constexpr int N = N_, OFF = OFF_;
+    int slot = OFF_, pos = 0;
     uint32_t parity = 0;
-    __device__ __forceinline__ explicit CopyRing(int start) : slot(OFF_ + start), pos(start) {}
     __device__ __forceinline__ void next() {
-        pos += STEP;
-        if ((slot += STEP) >= OFF + N) {
+        ++pos;
+        if (++slot >= OFF + N) {
             slot -= N;
             parity ^= 1;
         }
@@ -208,8 +209,8 @@ struct PfCfg {
     using VRing = Ring<VN, NQ == 2 ? 0 : KN>;
     // Over a pool, where a slot's boxes are a lane's each (a copy warp each for K and
     // V at D = 64 and 128: 8192 tokens of 64 heads over 8 of 128 950 us for 800).
-    using KCopies = CopyRing<KN, 0, 1>;
-    using VCopies = CopyRing<VN, NQ == 2 ? 0 : KN, 1>;
+    using KCopies = CopyRing<KN, 0>;
+    using VCopies = CopyRing<VN, NQ == 2 ? 0 : KN>;
     static_assert(NS > 2 * CPT && NS >= 4, "the ring holds more than one K and one V tile");
     static_assert(alloc <= kSmemMax, "shared memory");
     // TMEM: S0, S1 (128 columns each; P over the first 64), then O per tile
@@ -758,7 +759,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         return true;
     };
     // (by a whole warp) one slot's copies: a uniform wait, then one lane issues
-    int fills = 0;  // slots filled by this warp
+    [[maybe_unused]] int fills = 0;  // (packed rows) slots filled by this warp
     auto issue = [&](const void *tm, int c, int head, int row, auto &r) -> bool {
         const int slot = r.slot;
         if (fills >= r.N && !mbar_wait_warp(&slot_empty[slot], r.parity ^ 1, abort_flag)) return false;
@@ -793,7 +794,6 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
                                       c * C::KC + sl * 64, t.row, t.z);
             }
             __syncwarp();
-            ++fills;
             r.next();
         }
         return true;
@@ -847,10 +847,10 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
         for (int i = fills > n ? fills - n : 0; i < fills; ++i)
             pf_wait(&slot_full[off + i % n], (uint32_t)((i / n) & 1), &never);
     };
-    // (paged, by one lane) the last fills of r's warp have landed
+    // (paged, by one lane) the last fills of r have landed
     [[maybe_unused]] auto landed_paged = [&](const auto &r) {
         volatile int never = 0;
-        for (int pos = r.pos - r.STEP, i = 0; pos >= 0 && i < (r.N + r.STEP - 1) / r.STEP; pos -= r.STEP, ++i)
+        for (int pos = r.pos - 1, i = 0; pos >= 0 && i < r.N; --pos, ++i)
             pf_wait(&slot_full[r.OFF + pos % r.N], (uint32_t)((pos / r.N) & 1), &never);
     };
     // A walk over the key tiles of all units (where a copy warp has K or V alone).
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             *done = true;
             return true;
         };
-        [[maybe_unused]] typename C::VCopies vcopies(0);
+        [[maybe_unused]] typename C::VCopies vcopies;
         Unit u = {};
         int k = 0;
         bool more = true, done;  // the last unit published does not end the list
@@ -1076,7 +1076,7 @@ __global__ void __launch_bounds__(PfCfg<D, PG>::THREADS, 1)
             }
             return true;
         };
-        [[maybe_unused]] typename C::KCopies kcopies(0);
+        [[maybe_unused]] typename C::KCopies kcopies;
         if constexpr (PG) {
             Walk w;
             ok = step(w);
