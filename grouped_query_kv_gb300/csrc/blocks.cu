@@ -20,7 +20,8 @@
 // large one, the counts of the CTAs exchanged through distributed shared memory; a
 // kernel per step would cost a launch each.  No workspace.  What bounds a call: the
 // chain of barriers and dependent loads; a pool of 65 536 blocks compacted 24 us, of
-// which the scattered marks, moves and table entries of eight SMs are 12.
+// which the scattered marks, moves and table entries of eight SMs are 12 (more SMs for
+// them, in a second launch, have not been tried).
 //
 // kv_copy_blocks is a copy of 16-byte vectors of K and V, four of each in flight
 // per thread, and bound by HBM: 7680 blocks of 16 x 8 x 128 150 us, 0.98 of the

@@ -22,8 +22,11 @@
 //
 // What bounds it.  Many tokens: what bounds prompt attention, the tensor pipe
 // between its turns (four prompts of 2048 tokens behind 6144, 64 heads over 8 of 128:
-// 1380 us, 1395 TFLOP/s, 0.74 of the cuBLAS rate), and the merge (7 to 10 us where
-// all CTAs leave units of 128 or 256 rows).  Short units: their starts and ends, some
+// 1377 us in a graph, 1397 TFLOP/s, 0.74 of the cuBLAS rate; called, 1412 to 1419), and
+// the merge (7 to 10 us where all CTAs leave units of 128 or 256 rows).  Beside prompt
+// attention of the same 8192 tokens: 764 us for 753 there (64 heads over 8 of 128; in a
+// window of 1024 275 for 228), 421 for 334 (16 over 1 of 256; 178 for 116), 182 for 162
+// (16 over 16 of 64; 85 for 67).  Short units: their starts and ends, some
 // 4 us each (eight requests of up to 511 tokens in a window of 1024, 16 heads over 1
 // of 256: 66 us, of which a CTA's first piece takes 13: instructions and the first
 // rows are far away).  Single tokens: memory, 5.5 TB/s (0.81 of
@@ -31,7 +34,8 @@
 // 16, 5.7 in larger ones; 3.9 for 64 of up to 2048 states, 16 heads of 64, whose units
 // are 1 to 16 key tiles long and take 2.5 us to begin and end.  A kernel's local
 // memory is L2 here (227 KB of shared memory leave little L1): a stack frame or a
-// spill in a loop cost some 1000 cycles a turn under load.
+// spill in a loop cost some 1000 cycles a turn under load.  (The form for few rows at
+// D = 128 still has two registers spilled, with 720 bytes of loads; where is not known.)
 #include <cfloat>
 #include <cmath>
 
@@ -255,6 +259,8 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     // Groups of no power of two: with up to two units' tokens a request on average,
     // all heads of a group in one tile, by a power of two of tokens, so that a
     // request's keys are read once for the group; beyond, every row of the tile counts.
+    // (The lengths are on the device; padding rows and requests without tokens count in
+    // the averages, too, and can have a call take the other form.)
     // 16 requests of 4096 positions, one pass / as many as it takes: 20 heads over 4
     // of 128 with 1 token 37 / 81 us, 64 tokens 72 / 125, 128 126 / 133; 24 over 2 of
     // 128 with 32 tokens 48 / 54, 64 75 / 67; 48 over 1 of 256 with 4 38 / 38, 8 50 / 46.
@@ -274,7 +280,10 @@ int run_extend(const void *q, const void *k_pool, const void *v_pool, const int3
     // Units of few rows in a form of their own where a request has few on average
     // (with it / without, 16 requests of 4096 positions: 16 heads of 64 56 / 91 us, 32
     // over 2 of 64 21 / 22, with 2 tokens 25 / 22; 64 over 8 of 128 56 / 59, with 2 60 /
-    // 60, 32 over 2 of 128 30 / 26; at D = 256 it loses).
+    // 60, 32 over 2 of 128 30 / 26; at D = 256 it loses).  An average that idle requests
+    // bring down is not borne out: 16 requests of 64 tokens behind 4032, 16 heads over 16
+    // of 64, 80 us, beside 240 without tokens 103; 64 single tokens of 64 over 8 of 128
+    // 100 us, with one row of padding 102.
     int few = 0;
     if (D < 256 && p.hpg <= 32 && (long long)N * p.hpg <= (D == 64 ? 16LL : 8LL) * B)
         for (few = 1; 2 * few * p.hpg <= 32;) few *= 2;  // tokens whose rows fit a quarter of the tile

@@ -704,7 +704,16 @@ KVATTN_API int kv_append_rope(const void *q, const void *k, const void *v,
  * request's keys are divided, and with it the rounding, depends on the others'
  * lengths.  The workspace (41 MB on a GPU of 152 SMs at D = 128 and 256, 21 MB at
  * D = 64) is the stream's, or of a captured call's own, as for
- * gqa_decode_attn_paged_fp8.
+ * gqa_decode_attn_paged_fp8: 64 and 32 MB then, or one of a graph that is gone, of
+ * twice that at most.
+ *
+ * Single tokens, one of each request, are gqa_decode_attn_paged's as well (D = 128
+ * and 256), which returns fp32 and keeps twice the bits of a weight.  This call is
+ * the faster one in blocks of 16 at D = 128 and some dozen requests (32 of 64 heads
+ * over 8 behind up to 8191: 103 us for 129) and for several tokens each at D = 256
+ * (4 of 48 heads over 1: 56 to 60 us for 107 to 109); that one in blocks of 64 and
+ * more (93 us for 101), at D = 256 (16 heads over 1: 29 us for 37, in blocks of 16 34
+ * for 39) and for a single request (8 us for 11).  In blocks of 32 they are even.
  * D in {64, 128, 256}; block_size a power of two in [16, 2^20]; 1 <= N <= 2^28.
  */
 KVATTN_API int gqa_extend_attn(const void *q, const void *k_pool, const void *v_pool,
@@ -719,8 +728,8 @@ KVATTN_API int gqa_extend_attn(const void *q, const void *k_pool, const void *v_
  * limit.  Every token of sequence b attends the positions 0 <= j < kv_lens[b] of
  * block table row b, whatever the number of its tokens; kv_lens[b] = 0 gives
  * zeros.  The states' K/V rows are written to their blocks once (kv_append_slots)
- * and may be shared (kv_fork_blocks, or the same ids in several rows).  The rest
- * as gqa_extend_attn.
+ * and may be shared (kv_fork_blocks, or the same ids in several rows, of which
+ * kv_free_blocks is to be given one).  The rest as gqa_extend_attn.
  */
 KVATTN_API int gqa_cross_attn(const void *q, const void *k_pool, const void *v_pool,
                               const int32_t *block_table, const int32_t *kv_lens,
@@ -780,7 +789,9 @@ KVATTN_API int kv_fork_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *
  * it is; an entry outside [0, num_blocks) is only cleared; a block freed more
  * often than it is held is pushed once; blocks that the stack has no room for
  * are dropped.  All of these set KVATTN_ERR_DEVICE_BOUNDS.  With free_count[0]
- * outside [0, num_free] nothing is freed.
+ * outside [0, num_free] nothing is freed.  The stack is not searched: an entry of a
+ * block that is on it already, as after a free of another row with the same ids that
+ * refs does not count, is taken for its last holder's and pushes it a second time.
  */
 KVATTN_API int kv_free_blocks(int32_t *block_table, int32_t *seq_lens, int32_t *refs,
                               int32_t *free_blocks, const int32_t *free_count,
