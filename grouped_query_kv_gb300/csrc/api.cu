@@ -1154,8 +1154,16 @@ void kvattn_release(void) {
     }
     int cur = 0;
     cudaGetDevice(&cur);
-    auto give_back = [](int dev, Workspace &w) {
+    unsigned long long quiet = 0;  // devices whose work has been waited for
+    auto at = [&](int dev) {
         cudaSetDevice(dev);
+        const unsigned long long bit = 1ULL << (dev & 63);
+        if (!(quiet & bit)) (void)cudaDeviceSynchronize();
+        quiet |= bit;
+    };
+    auto give_back = [&](int dev, Workspace &w) {
+        if (!w.ptr && w.retired.empty()) return;
+        at(dev);
         if (w.ptr) cudaFree(w.ptr);
         for (auto &old : w.retired) cudaFree(old.first);
         w = Workspace();
@@ -1163,11 +1171,14 @@ void kvattn_release(void) {
     for (auto &kv : g_ws) give_back(std::get<0>(kv.first), kv.second);
     g_ws.clear();
     // (a capture's record is deleted once its graph is gone)
-    collect_gone();
+    try {
+        collect_gone();
+    } catch (const std::bad_alloc &) {  // (no host memory for the list: what is left of it stays)
+    }
     for (auto &kv : g_ws_captured) give_back(std::get<0>(kv.first.first), kv.second->ws);
     g_ws_captured.clear();
     for (auto &kv : g_idle) {
-        cudaSetDevice(kv.first.first);
+        at(kv.first.first);
         cudaFree(kv.second);
     }
     g_idle.clear();

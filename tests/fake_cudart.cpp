@@ -97,6 +97,10 @@ cudaError_t cudaFree(void *) {
     note("free " + std::to_string(me));
     return cudaSuccess;
 }
+cudaError_t cudaDeviceSynchronize() {
+    note("sync " + std::to_string(me));
+    return cudaSuccess;
+}
 cudaError_t cudaGetDevice(int *d) {
     *d = 0;
     return cudaSuccess;

@@ -184,3 +184,17 @@ def test_the_stream_of_each_host_thread_has_a_workspace_of_its_own(lib, name, ca
         _joined_in_pairs([x for x in launches if x[1] == t])
     # and they do not wait for each other
     assert any(a[1] != b[1] for a, b in zip(launches[::2], launches[1::2])), launches
+
+
+def test_release_frees_nothing_beside_work(lib):
+    # (cudaFree waits for the device's work as well, but is kept from meeting any)
+    for name in ("gqa_extend_attn", "gqa_decode_attn"):
+        for s in (0x500, 0x600):
+            _call(lib, name, 4, s)
+    lib.fake_clear()
+    lib.kvattn_release()
+    words = [x[0] for x in _log(lib, "")]
+    assert words[0] == "sync" and words.count("free") >= 2 and set(words[1:]) == {"free"}
+    lib.fake_clear()
+    lib.kvattn_release()
+    assert not _log(lib, "")  # (nothing is held, nothing is waited for)
