@@ -1,6 +1,7 @@
 """Calls from several host threads on one stream: each gives the bits that it gives
 alone.  (What comes between a call's two launches, and that nothing does, is looked
 at without a GPU in test_threads_cpu.py.)"""
+import concurrent.futures
 import threading
 
 import pytest
@@ -71,6 +72,9 @@ def test_host_threads_on_one_stream():
             assert torch.equal(o, w)
 
 
+_WORKERS = concurrent.futures.ThreadPoolExecutor(max_workers=4)
+
+
 class _PerThread:
     """The stream of whichever host thread calls (cudaStreamPerThread)."""
     cuda_stream = 2
@@ -86,13 +90,17 @@ def test_the_streams_of_host_threads_side_by_side():
     torch.cuda.synchronize()
 
     def job(i):
+        gate.wait()
         for o in outs[i]:
             cases[i].run(out=o, stream=_PerThread)
-        g.check_device_error(_PerThread)  # (a thread ends when its stream's work has)
+        g.check_device_error(_PerThread)  # (its work is over before the thread is)
 
-    for _ in range(2):  # (the second time in other threads)
-        _together([lambda i=i: job(i) for i in range(len(cases))])
-        g.check_device_error()
+    # (threads that stay, and with them their streams)
+    gate = threading.Barrier(len(cases))
+    for _ in range(2):
+        for done in [_WORKERS.submit(job, i) for i in range(len(cases))]:
+            done.result()
+        torch.cuda.synchronize()
         for w, got in zip(want, outs):
             for o in got:
                 assert torch.equal(o, w)
